@@ -380,6 +380,178 @@ la_status la_gla_bwd(const la_dims *dims, int32_t dtype,
 size_t la_gla_workspace_size(const la_dims *dims, int32_t dtype,
                              const int32_t *cu_seqlens_host, int32_t with_forward_operands);
 
+/* ---- Operators beside the attention ------------------------------------------
+ * What stands next to la_fwd in a layer: the norms and the rotation of queries
+ * and keys, and the vector-state member of the family of recurrences.  The
+ * pages have no counterpart of either (they take q and k as given, and the
+ * state of `recurrent` is a matrix).  The conventions above hold; these calls
+ * copy nothing from the host (cu_seqlens_host is only checked), so they can be
+ * captured in a CUDA graph, packed or dense -- except when cu_seqlens is given
+ * without cu_seqlens_host, which copies it back and waits. */
+
+/* Gated linear recurrence: per sequence, head and channel, tokens in
+ * processing order,
+ *     s_t = exp(g_t) * s_{t-1} + x_t,      o_t = s_t
+ * s_0 = initial_state (or zero); final_state = s after the last token.
+ *   batch, seq_len, heads, num_seqs   as la_dims
+ *   dim         channels of a head, 1..256
+ *   gate_dtype  la_dtype of g and dg: the token dtype or LA_DTYPE_F32
+ *   *_strides   element strides (batch, token, head) of each token tensor;
+ *               the channels are contiguous.  An input may repeat a row
+ *               (stride 0); outputs must not.  la_gated_scan_fwd reads those
+ *               of x, g, o; la_gated_scan_bwd those of x, g, do, dx, dg. */
+typedef struct la_scan_dims {
+    int32_t batch;
+    int32_t seq_len;
+    int32_t heads;
+    int32_t dim;
+    int32_t num_seqs;
+    int32_t gate_dtype;
+    int64_t x_strides[3];
+    int64_t g_strides[3];
+    int64_t o_strides[3];
+    int64_t do_strides[3];
+    int64_t dx_strides[3];
+    int64_t dg_strides[3];
+} la_scan_dims;
+
+/* Forward.
+ *   x              [B,T,H,D] of `dtype`
+ *   g              [B,T,H,D] of gate_dtype: log-decay (values > 0 grow the state)
+ *   initial_state  [N,H,D] fp32, or NULL for zeros
+ *   reverse, cu_seqlens, cu_seqlens_host   as la_fwd
+ *   o              [B,T,H,D] of `dtype` (output)
+ *   final_state    [N,H,D] fp32 output, or NULL; may be initial_state itself
+ *   states         fp32 output of la_gated_scan_states_size bytes (16-byte
+ *                  aligned), or NULL: the states that la_gated_scan_bwd starts
+ *                  from, to be passed to it once or more
+ *   workspace      256-byte aligned, la_gated_scan_workspace_size(..., 0)
+ *                  bytes (LA_ERR_INVALID_ARG when smaller); that size may be 0 */
+la_status la_gated_scan_fwd(const la_scan_dims *dims, int32_t dtype, const void *x,
+                            const void *g, const float *initial_state, int32_t reverse,
+                            const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, void *o,
+                            float *final_state, float *states, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* Backward: gradients of sum(o * d_o) + sum(final_state * d_final_state).
+ * With K_t = exp(g_t) (d_o_t + K_{t+1}), K after the last token d_final_state:
+ *     dx_t = d_o_t + K_{t+1},   dg_t = K_t s_{t-1},   d_initial_state = K_1.
+ * s_{t-1} is computed again in fp32 from x, g and `states`, so dg takes no
+ * rounded o.
+ *   x, g, initial_state, reverse, cu_seqlens   as given to the forward call
+ *   d_o            [B,T,H,D] of `dtype`
+ *   d_final_state  [N,H,D] fp32, or NULL for zeros
+ *   states         what la_gated_scan_fwd wrote for the same arguments, or
+ *                  NULL: computed again in the workspace (one more pass over
+ *                  x and g)
+ *   dx             [B,T,H,D] of `dtype` (output)
+ *   dg             [B,T,H,D] of gate_dtype (output)
+ *   d_initial_state [N,H,D] fp32 output, or NULL
+ *   workspace      256-byte aligned, la_gated_scan_workspace_size bytes with
+ *                  backward = 1 (states given) or 2 (states NULL) */
+la_status la_gated_scan_bwd(const la_scan_dims *dims, int32_t dtype, const void *x,
+                            const void *g, const void *d_o, const float *initial_state,
+                            const float *d_final_state, int32_t reverse,
+                            const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                            const float *states, void *dx, void *dg, float *d_initial_state,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of la_gated_scan_fwd (backward = 0) or la_gated_scan_bwd
+ * (1: states given, 2: not); 0 for invalid sizes.  They do not depend on the
+ * sequences' lengths.  Pure host function. */
+size_t la_gated_scan_workspace_size(const la_scan_dims *dims, int32_t dtype, int32_t backward);
+
+/* Bytes of la_gated_scan_fwd's `states` (0 for invalid sizes, and where the
+ * backward needs none).  Pure host function. */
+size_t la_gated_scan_states_size(const la_scan_dims *dims);
+
+/* Norms of queries and keys for each head, with the position rotation:
+ *     y = R(n(x)),   n(x) = x * rsqrt(mean_c x_c^2 + eps) * weight
+ * for every row x of q [B,T,H,D] and of k [B,T,H_k,D].  R rotates pair j of
+ * the first rotary_dim channels by position * inv_freq[j]:
+ *     (y_a, y_b) = (n_a cos - n_b sin, n_a sin + n_b cos)
+ * and leaves the other channels.
+ *   batch, seq_len, num_seqs   as la_dims
+ *   q_heads, k_heads  0..65535, not both 0; a tensor with 0 heads is not there
+ *                 (its pointers are not read)
+ *   dim           D  1..256
+ *   rotary_dim    even, 0..D; 0: no rotation
+ *   num_axes      1..4 position axes (time, height, width, ...)
+ *   normalize     0: n(x) = x (the backward then reads neither q nor k)
+ *   interleaved   0: pair j is channels (j, j + rotary_dim/2); 1: (2j, 2j+1)
+ *   weight_dtype  la_dtype of the weights and of their gradients
+ *   position_bytes 4 (int32) or 8 (int64) per position
+ *   q_strides, k_strides     element strides (batch, token, head) of q, k
+ *   qo_strides, ko_strides   of the rotated outputs, and of d_qo, d_ko
+ *   dq_strides, dk_strides   of dq, dk (read by the backward only)
+ *   position_strides         of positions: (axis, batch, token); 0 repeats
+ *   pair_axis     the axis of each frequency pair j < rotary_dim/2 */
+typedef struct la_rope_dims {
+    int32_t batch;
+    int32_t seq_len;
+    int32_t q_heads;
+    int32_t k_heads;
+    int32_t dim;
+    int32_t rotary_dim;
+    int32_t num_seqs;
+    int32_t num_axes;
+    int32_t normalize;
+    int32_t interleaved;
+    int32_t weight_dtype;
+    int32_t position_bytes;
+    int64_t q_strides[3];
+    int64_t k_strides[3];
+    int64_t qo_strides[3];
+    int64_t ko_strides[3];
+    int64_t dq_strides[3];
+    int64_t dk_strides[3];
+    int64_t position_strides[3];
+    uint8_t pair_axis[128];
+} la_rope_dims;
+
+/* Forward.
+ *   q, k            [B,T,H,D], [B,T,H_k,D] of `dtype`
+ *   q_weight, k_weight  [D] of weight_dtype, or NULL for ones
+ *   inv_freq        [rotary_dim/2] fp64 (device): radians per position
+ *   positions       [num_axes,B,T] (device), or NULL: a token's index in its
+ *                   sequence (num_axes 1), plus position_offset
+ *   position_offset [N] int32 (device), or NULL for zeros; only without
+ *                   positions: where each sequence begins (decoding on)
+ *   cu_seqlens, cu_seqlens_host   as la_fwd; used only without positions
+ *   qo, ko          outputs of `dtype`; qo may be q itself and ko k itself
+ *                   (same pointer and strides)
+ * Angles keep their fraction of a turn to 2^-32 at every int32 position
+ * (positions beyond int32 wrap inv_freq's own rounding, 2^-53 of a radian per
+ * position, instead). */
+la_status la_qk_norm_rope_fwd(const la_rope_dims *dims, int32_t dtype, const void *q,
+                              const void *k, const void *q_weight, const void *k_weight,
+                              float eps, const double *inv_freq, const void *positions,
+                              const int32_t *position_offset, const int32_t *cu_seqlens,
+                              const int32_t *cu_seqlens_host, void *qo, void *ko, void *stream);
+
+/* Backward: with u = R^T(d_qo) and r = rsqrt(mean q^2 + eps),
+ *     dq = r (u w - q r^2 mean(q u w)),    d_q_weight = sum over rows of u q r
+ * and the same for k.
+ *   d_qo, d_ko      [B,T,H,D], [B,T,H_k,D] of `dtype` (qo_strides, ko_strides)
+ *   dq, dk          outputs of `dtype`
+ *   d_q_weight, d_k_weight  [D] of weight_dtype outputs, or NULL; the sums are
+ *                   formed in fp32 in a fixed order
+ *   workspace       256-byte aligned, la_qk_norm_rope_workspace_size bytes;
+ *                   needed when a weight's gradient is asked for
+ *   everything else as the forward call */
+la_status la_qk_norm_rope_bwd(const la_rope_dims *dims, int32_t dtype, const void *q,
+                              const void *k, const void *d_qo, const void *d_ko,
+                              const void *q_weight, const void *k_weight, float eps,
+                              const double *inv_freq, const void *positions,
+                              const int32_t *position_offset, const int32_t *cu_seqlens,
+                              const int32_t *cu_seqlens_host, void *dq, void *dk,
+                              void *d_q_weight, void *d_k_weight, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of la_qk_norm_rope_bwd (0 for invalid sizes and without
+ * normalize).  Host function (reads one device attribute, once per device). */
+size_t la_qk_norm_rope_workspace_size(const la_rope_dims *dims, int32_t dtype);
+
 /* Reads and clears the device-side error words that bounded on-device waits
  * set when they run out (LA_ERR_TIMEOUT), after synchronizing `stream`.
  * Returns LA_OK when no wait ran out, LA_ERR_TIMEOUT when one did, or

@@ -11,9 +11,15 @@ from .api import (alibi_g_gamma, get_device_error, gla_bwd, gla_fwd, kernel_fami
                   la_bwd_dkdv, la_bwd_dq, la_fwd, lightning_attn, lightning_attn_func,
                   lightning_g_gamma, recurrent, recurrent_gla)
 
+from .layer import (QkNorm, Rope, gated_scan, gated_scan_bwd, gated_scan_fwd, qk_norm_rope,
+                    qk_norm_rope_bwd, qk_norm_rope_fwd, rope_inv_freq, rotary, rotary_bwd,
+                    rotary_fwd)
+
 __all__ = [
     "LaDims", "LaError", "LaInvalidArgument", "LaUnsupported", "LA_DTYPE_BF16", "LA_DTYPE_F32",
     "lib", "alibi_g_gamma", "get_device_error", "gla_bwd", "gla_fwd", "kernel_family", "la_bwd",
     "la_bwd_dkdv", "la_bwd_dq", "la_fwd", "lightning_attn", "lightning_attn_func",
     "lightning_g_gamma", "recurrent", "recurrent_gla",
+    "QkNorm", "Rope", "gated_scan", "gated_scan_bwd", "gated_scan_fwd", "qk_norm_rope",
+    "qk_norm_rope_bwd", "qk_norm_rope_fwd", "rope_inv_freq", "rotary", "rotary_bwd", "rotary_fwd",
 ]

@@ -44,6 +44,29 @@ class LaDims(ctypes.Structure):
     ]
 
 
+_i64x3 = ctypes.c_int64 * 3
+
+
+class LaScanDims(ctypes.Structure):
+    """Mirror of `la_scan_dims` (include/la.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("batch", "seq_len", "heads", "dim", "num_seqs", "gate_dtype")] + \
+               [(n, _i64x3) for n in
+                ("x_strides", "g_strides", "o_strides", "do_strides", "dx_strides",
+                 "dg_strides")]
+
+
+class LaRopeDims(ctypes.Structure):
+    """Mirror of `la_rope_dims` (include/la.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("batch", "seq_len", "q_heads", "k_heads", "dim", "rotary_dim", "num_seqs",
+                 "num_axes", "normalize", "interleaved", "weight_dtype", "position_bytes")] + \
+               [(n, _i64x3) for n in
+                ("q_strides", "k_strides", "qo_strides", "ko_strides", "dq_strides",
+                 "dk_strides", "position_strides")] + \
+               [("pair_axis", ctypes.c_uint8 * 128)]
+
+
 class LaError(RuntimeError):
     def __init__(self, status, detail):
         self.status = status
@@ -63,6 +86,8 @@ _i32 = ctypes.c_int32
 _f32 = ctypes.c_float
 _sz = ctypes.c_size_t
 _dims_p = ctypes.POINTER(LaDims)
+_scan_p = ctypes.POINTER(LaScanDims)
+_rope_p = ctypes.POINTER(LaRopeDims)
 
 # name -> (restype, argtypes); mirrors include/la.h exactly (float* are passed
 # as void* addresses).
@@ -84,6 +109,17 @@ PROTOTYPES = {
     "la_gla_bwd": (_i32, [_dims_p, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _vp,
                           _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _sz, _vp]),
     "la_gla_workspace_size": (_sz, [_dims_p, _i32, _vp, _i32]),
+    "la_gated_scan_fwd": (_i32, [_scan_p, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
+                                 _vp, _sz, _vp]),
+    "la_gated_scan_bwd": (_i32, [_scan_p, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp,
+                                 _vp, _vp, _vp, _vp, _sz, _vp]),
+    "la_gated_scan_workspace_size": (_sz, [_scan_p, _i32, _i32]),
+    "la_gated_scan_states_size": (_sz, [_scan_p]),
+    "la_qk_norm_rope_fwd": (_i32, [_rope_p, _i32, _vp, _vp, _vp, _vp, _f32, _vp, _vp, _vp, _vp,
+                                   _vp, _vp, _vp, _vp]),
+    "la_qk_norm_rope_bwd": (_i32, [_rope_p, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _vp,
+                                   _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "la_qk_norm_rope_workspace_size": (_sz, [_rope_p, _i32]),
     "la_debug_withhold_next_handoff": (_i32, [_i32]),
     "la_debug_split_segments": (_i32, [_dims_p, _i32, _vp, _i32]),
     "la_fwd_noalloc": (_i32, [_dims_p, _i32, _vp, _vp, _vp, _vp, _f32, _vp, _i32, _vp, _vp,

@@ -497,11 +497,15 @@ def _scale_for(softmax_scale, head_dim):
 
 def recurrent(query: Tensor, key: Tensor, value: Tensor, g=None, g_gamma=None, gk=None, gv=None,
               softmax_scale: Optional[float] = None, initial_state: Optional[Tensor] = None,
-              reverse: bool = False, cu_seqlens=None):
+              reverse: bool = False, cu_seqlens=None, qk_norm=None, rope=None, positions=None,
+              position_offset=None):
     """ejkernel `recurrent` with the per-head `g_gamma` decay and the GLA-style gate `g`
     (a log-decay per key channel, [B,T,H,D]; gk / gv are not implemented).  Accepts
     [B,T,H,D] or packed [T_total,H,D] with cu_seqlens.  Returns (o, final_state);
-    differentiable in query, key, value, g and initial_state."""
+    differentiable in query, key, value, g and initial_state.
+    qk_norm (a QkNorm) and rope (a Rope, with positions or position_offset): norms of query
+    and key for each head and the position rotation, applied to both first in one pass
+    (`qk_norm_rope`); differentiable in the norms' weights too."""
     if gk is not None or gv is not None:
         raise NotImplementedError("the gk / gv gates are not implemented")
     squeeze = False
@@ -513,6 +517,12 @@ def recurrent(query: Tensor, key: Tensor, value: Tensor, g=None, g_gamma=None, g
         squeeze = True
     if cu_seqlens is not None and query.shape[0] != 1:
         raise ValueError(_packed_batch_msg(query.shape[0]))
+    if qk_norm is not None or rope is not None:
+        from .layer import qk_norm_rope
+        query, key = qk_norm_rope(query, key, qk_norm, rope, positions, position_offset,
+                                  cu_seqlens)
+    elif positions is not None or position_offset is not None:
+        raise ValueError("positions need rope")
     H = query.shape[2]
     if g_gamma is None:
         g_gamma = torch.zeros(H, dtype=torch.float32)
@@ -530,18 +540,22 @@ def recurrent(query: Tensor, key: Tensor, value: Tensor, g=None, g_gamma=None, g
 def recurrent_gla(query: Tensor, key: Tensor, value: Tensor, g: Optional[Tensor] = None,
                   g_gamma=None, softmax_scale: Optional[float] = None,
                   initial_state: Optional[Tensor] = None, reverse: bool = False,
-                  cu_seqlens=None):
+                  cu_seqlens=None, qk_norm=None, rope=None, positions=None,
+                  position_offset=None):
     """ejkernel `recurrent_gla` (the GLA page): the batch-1 / initial-state count
     checks of that page, the default scale from the key width, then `recurrent`."""
     _check_packing(query, cu_seqlens, initial_state)
     return recurrent(query, key, value, g=g, g_gamma=g_gamma,
                      softmax_scale=_scale_for(softmax_scale, key.shape[-1]),
-                     initial_state=initial_state, reverse=reverse, cu_seqlens=cu_seqlens)
+                     initial_state=initial_state, reverse=reverse, cu_seqlens=cu_seqlens,
+                     qk_norm=qk_norm, rope=rope, positions=positions,
+                     position_offset=position_offset)
 
 
 def lightning_attn(query: Tensor, key: Tensor, value: Tensor, layer_idx: int, num_layers: int,
                    softmax_scale: Optional[float] = None, initial_state: Optional[Tensor] = None,
-                   reverse: bool = False, cu_seqlens=None):
+                   reverse: bool = False, cu_seqlens=None, qk_norm=None, rope=None,
+                   positions=None, position_offset=None):
     """ejkernel `lightning_attn`: g_gamma from the layer position, then `recurrent`.
     Keys and values have the queries' shape (that page's docstring); grouped
     key/value heads go through `recurrent` or la_fwd / la_bwd."""
@@ -553,7 +567,9 @@ def lightning_attn(query: Tensor, key: Tensor, value: Tensor, layer_idx: int, nu
     H = query.shape[-2]
     return recurrent(query, key, value, g_gamma=lightning_g_gamma(H, layer_idx, num_layers),
                      softmax_scale=_scale_for(softmax_scale, key.shape[-1]),
-                     initial_state=initial_state, reverse=reverse, cu_seqlens=cu_seqlens)
+                     initial_state=initial_state, reverse=reverse, cu_seqlens=cu_seqlens,
+                     qk_norm=qk_norm, rope=rope, positions=positions,
+                     position_offset=position_offset)
 
 
 def lightning_attn_func(q: Tensor, k: Tensor, v: Tensor, s: Tensor) -> Tensor:

@@ -275,6 +275,58 @@ struct SplitScanArgs {
 };
 cudaError_t split_scan(const SplitScanArgs &a, cudaStream_t s);
 
+// The gated linear recurrence s_t = exp(g_t) s_{t-1} + x_t (la_scan.cu),
+// elementwise per (sequence, head, channel).  Tokens are numbered by their
+// processing position on one axis over all rows: p = row * T + j, j the place
+// in the row's processing order (dense), or p = t, from the end with reverse
+// (packed).  A tile is SCAN_TILE consecutive positions; states holds the fp32
+// state entering each tile, [tile][H][D] (unused where a sequence starts).
+constexpr int SCAN_TILE = 128;
+struct ScanArgs {
+    int B, T, H, D, N;
+    const int32_t *cu;          // device [N + 1], or nullptr (dense: N == B)
+    int reverse;
+    int bf16, gate_bf16;        // token and gate types: 1 bf16, 0 fp32
+    Tok x, g, d_o;
+    TokOut o, dx, dg;
+    const float *init;          // [N][H][D] or null
+    float *fin;                 // forward: final states, or null
+    const float *dfin;          // backward: their gradient, or null
+    float *dinit;               // backward: the initial states' gradient, or null
+    float *states;
+};
+// o may be null in the forward (states and final states alone).
+cudaError_t scan_forward(const ScanArgs &a, cudaStream_t s);
+cudaError_t scan_backward(const ScanArgs &a, cudaStream_t s);
+
+// Norms of queries and keys with the position rotation (la_qk_rope.cu).
+struct RopeTensor {
+    const void *x;              // [B][T][heads][D], or null where not read
+    const void *dy;             // backward: the outputs' gradient
+    void *y;                    // forward: the output; backward: dx
+    const void *w;              // [D] or null
+    void *dw;                   // backward: [D], or null
+    int heads;
+    int64_t xs[3], dys[3], ys[3];   // element strides (batch, token, head)
+};
+struct RopeArgs {
+    int B, T, N, D, R, axes;
+    int bf16, w_bf16, normalize, interleaved, pos64;
+    float eps;
+    const double *inv_freq;     // [R / 2]
+    const void *pos;            // int32 or int64, strides ps, or null
+    int64_t ps[3];
+    const int32_t *offset;      // [N] or null
+    const int32_t *cu;          // device [N + 1] or null
+    uint8_t axis[128];
+    RopeTensor t[2];            // q, k; heads == 0: not there
+    float *partial;             // backward: the CTAs' weight gradients
+};
+cudaError_t rope_forward(const RopeArgs &a, cudaStream_t s);
+cudaError_t rope_backward(const RopeArgs &a, cudaStream_t s);
+// Bytes of RopeArgs::partial.
+size_t rope_partial_bytes(int D);
+
 // Device error word of the tensor-core kernels (bounded waits that ran out).
 cudaError_t tc_read_and_clear_error(cudaStream_t s, int *err);
 
