@@ -392,7 +392,11 @@ size_t la_gla_workspace_size(const la_dims *dims, int32_t dtype,
 /* Gated linear recurrence: per sequence, head and channel, tokens in
  * processing order,
  *     s_t = exp(g_t) * s_{t-1} + x_t,      o_t = s_t
- * s_0 = initial_state (or zero); final_state = s after the last token.
+ * s_0 = initial_state (or zero); final_state = s after the last token.  The
+ * tokens are composed in parallel, so a product of consecutive decays must
+ * stay in fp32's range: gates <= 0 always do, and gates whose sum over
+ * consecutive tokens exceeds 88 may give infinities or NaN even where the
+ * state stays zero.
  *   batch, seq_len, heads, num_seqs   as la_dims
  *   dim         channels of a head, 1..256
  *   gate_dtype  la_dtype of g and dg: the token dtype or LA_DTYPE_F32
@@ -458,7 +462,7 @@ la_status la_gated_scan_bwd(const la_scan_dims *dims, int32_t dtype, const void 
 
 /* Workspace bytes of la_gated_scan_fwd (backward = 0) or la_gated_scan_bwd
  * (1: states given, 2: not); 0 for invalid sizes.  They do not depend on the
- * sequences' lengths.  Pure host function. */
+ * packed sequences' lengths.  Pure host function. */
 size_t la_gated_scan_workspace_size(const la_scan_dims *dims, int32_t dtype, int32_t backward);
 
 /* Bytes of la_gated_scan_fwd's `states` (0 for invalid sizes, and where the

@@ -285,6 +285,7 @@ constexpr int SCAN_TILE = 128;
 struct ScanArgs {
     int B, T, H, D, N;
     const int32_t *cu;          // device [N + 1], or nullptr (dense: N == B)
+    int some_empty;             // sequences without tokens are among them
     int reverse;
     int bf16, gate_bf16;        // token and gate types: 1 bf16, 0 fp32
     Tok x, g, d_o;
@@ -295,9 +296,15 @@ struct ScanArgs {
     float *dinit;               // backward: the initial states' gradient, or null
     float *states;
 };
-// o may be null in the forward (states and final states alone).
-cudaError_t scan_forward(const ScanArgs &a, cudaStream_t s);
-cudaError_t scan_backward(const ScanArgs &a, cudaStream_t s);
+// o may be null in the forward (the states alone).  ws: scan_link_bytes of
+// scratch (0 bytes: not needed), 256-byte aligned.
+cudaError_t scan_forward(const ScanArgs &a, void *ws, cudaStream_t s);
+cudaError_t scan_backward(const ScanArgs &a, void *ws, cudaStream_t s);
+size_t scan_link_bytes(int B, int T, int H, int D);
+// Reads (after synchronizing s) and clears the scan kernels' device error word.
+cudaError_t scan_read_and_clear_error(cudaStream_t s, int *err);
+// la_debug_withhold_next_handoff's switch of this host thread, reset by the read.
+int take_withheld();
 
 // Norms of queries and keys with the position rotation (la_qk_rope.cu).
 struct RopeTensor {

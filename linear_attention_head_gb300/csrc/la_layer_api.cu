@@ -75,11 +75,13 @@ la_status check_out(const int64_t *st, const char *name, int32_t B, int32_t T, i
     return e;
 }
 
-// The packed-sequence table, as la_fwd takes it; *N: the number of states.
+// The packed-sequence table, as la_fwd takes it; *N: the number of states,
+// *some_empty: sequences without tokens are among them.
 la_status check_packed(int32_t batch, int32_t seq_len, int32_t num_seqs, const int32_t *cu,
-                       const int32_t *cu_host, cudaStream_t stream, int *N)
+                       const int32_t *cu_host, cudaStream_t stream, int *N, int *some_empty)
 {
     *N = batch;
+    *some_empty = batch > 0 && seq_len == 0;
     if (!cu)
         return cu_host ? fail(LA_ERR_INVALID_ARG, "cu_seqlens_host given without cu_seqlens")
                        : LA_OK;
@@ -91,6 +93,7 @@ la_status check_packed(int32_t batch, int32_t seq_len, int32_t num_seqs, const i
     if (num_seqs < 0 || num_seqs > (1 << 30))
         return fail(LA_ERR_INVALID_ARG, "num_seqs = %d", num_seqs);
     *N = num_seqs;
+    *some_empty = 0;
     std::vector<int32_t> copy;
     if (!cu_host) {
         copy.resize((size_t)num_seqs + 1);
@@ -104,10 +107,12 @@ la_status check_packed(int32_t batch, int32_t seq_len, int32_t num_seqs, const i
     }
     if (cu_host[0] != 0)
         return fail(LA_ERR_INVALID_ARG, "cu_seqlens[0] = %d, expected 0", cu_host[0]);
-    for (int n = 0; n < num_seqs; ++n)
+    for (int n = 0; n < num_seqs; ++n) {
         if (cu_host[n + 1] < cu_host[n])
             return fail(LA_ERR_INVALID_ARG, "cu_seqlens decreases at %d (%d -> %d)", n,
                         cu_host[n], cu_host[n + 1]);
+        *some_empty |= cu_host[n + 1] == cu_host[n];
+    }
     if (cu_host[num_seqs] != seq_len)
         return fail(LA_ERR_INVALID_ARG, "cu_seqlens[%d] = %d but seq_len = %d", num_seqs,
                     cu_host[num_seqs], seq_len);
@@ -160,11 +165,26 @@ la_status scan_sizes(const la_scan_dims *d, int32_t dtype)
     return check_rows(d->batch, d->seq_len, d->dim);
 }
 
+// The states that enter the tiles; a single tile needs none.
 size_t states_bytes(const la_scan_dims *d)
 {
     const size_t tiles =
         ((size_t)d->batch * d->seq_len + la::SCAN_TILE - 1) / (size_t)la::SCAN_TILE;
-    return tiles * d->heads * d->dim * sizeof(float);
+    return tiles > 1 ? tiles * d->heads * d->dim * sizeof(float) : 0;
+}
+
+// A copy of the initial states (final_state being initial_state itself: the
+// kernel reads a sequence's initial state twice).
+size_t init_bytes(const la_scan_dims *d)
+{
+    const int32_t n = d->batch > d->num_seqs ? d->batch : d->num_seqs;
+    return (size_t)n * d->heads * d->dim * sizeof(float);
+}
+
+bool scan_sized(const la_scan_dims *d)
+{
+    return d && d->batch >= 0 && d->seq_len >= 0 && d->heads >= 1 && d->heads <= 65535 &&
+           d->dim >= 1 && d->dim <= 256;
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
@@ -178,7 +198,8 @@ la_status scan_args(const la_scan_dims *d, int32_t dtype, const void *x, const v
         (e = check_in(d->g_strides, "g")))
         return e;
     *a = la::ScanArgs{};
-    if ((e = check_packed(d->batch, d->seq_len, d->num_seqs, cu, cu_host, s, &a->N)))
+    if ((e = check_packed(d->batch, d->seq_len, d->num_seqs, cu, cu_host, s, &a->N,
+                          &a->some_empty)))
         return e;
     a->B = d->batch;
     a->T = d->seq_len;
@@ -234,7 +255,9 @@ la_status rope_args(const la_rope_dims *d, int32_t dtype, const void *qw, const 
     if (e)
         return e;
     *a = la::RopeArgs{};
-    if ((e = check_packed(d->batch, d->seq_len, d->num_seqs, cu, cu_host, s, &a->N)))
+    int some_empty;
+    if ((e = check_packed(d->batch, d->seq_len, d->num_seqs, cu, cu_host, s, &a->N,
+                          &some_empty)))
         return e;
     if (d->normalize && !(eps >= 0.f && std::isfinite(eps)))
         return fail(LA_ERR_INVALID_ARG, "eps = %g must be finite and not negative", (double)eps);
@@ -296,16 +319,18 @@ extern "C" {
 
 size_t la_gated_scan_states_size(const la_scan_dims *dims)
 {
-    return dims && dims->batch >= 0 && dims->seq_len >= 0 && dims->heads >= 1 &&
-                   dims->heads <= 65535 && dims->dim >= 1 && dims->dim <= 256
-               ? states_bytes(dims)
-               : 0;
+    return scan_sized(dims) ? states_bytes(dims) : 0;
 }
 
 size_t la_gated_scan_workspace_size(const la_scan_dims *dims, int32_t dtype, int32_t backward)
 {
     (void)dtype;
-    return backward == 2 ? round256(la_gated_scan_states_size(dims)) : 0;
+    if (!scan_sized(dims))
+        return 0;
+    return round256(la::scan_link_bytes(dims->batch, dims->seq_len, dims->heads, dims->dim)) +
+           (backward == 0   ? round256(init_bytes(dims))
+            : backward == 2 ? round256(states_bytes(dims))
+                            : 0);
 }
 
 la_status la_gated_scan_fwd(const la_scan_dims *dims, int32_t dtype, const void *x,
@@ -331,7 +356,18 @@ la_status la_gated_scan_fwd(const la_scan_dims *dims, int32_t dtype, const void 
         a.o = tok_out(o, dims->o_strides);
         a.fin = final_state;
         a.states = states;
-        return launched(la::scan_forward(a, s), "gated scan");
+        if (final_state && final_state == initial_state && (int64_t)a.B * a.T > 0) {
+            float *copy = reinterpret_cast<float *>(
+                static_cast<uint8_t *>(workspace) +
+                round256(la::scan_link_bytes(a.B, a.T, a.H, a.D)));
+            if ((e = launched(cudaMemcpyAsync(copy, initial_state,
+                                              (size_t)a.N * a.H * a.D * sizeof(float),
+                                              cudaMemcpyDeviceToDevice, s),
+                              "initial state")))
+                return e;
+            a.init = copy;
+        }
+        return launched(la::scan_forward(a, workspace, s), "gated scan");
     });
 }
 
@@ -361,8 +397,10 @@ la_status la_gated_scan_bwd(const la_scan_dims *dims, int32_t dtype, const void 
             return LA_OK;
         a.states = const_cast<float *>(states);
         if (!states && states_bytes(dims)) {
-            a.states = static_cast<float *>(workspace);
-            if ((e = launched(la::scan_forward(a, s), "gated scan states")))
+            a.states = reinterpret_cast<float *>(
+                static_cast<uint8_t *>(workspace) +
+                round256(la::scan_link_bytes(a.B, a.T, a.H, a.D)));
+            if ((e = launched(la::scan_forward(a, workspace, s), "gated scan states")))
                 return e;
         }
         a.d_o = tok(d_o, dims->do_strides);
@@ -370,7 +408,7 @@ la_status la_gated_scan_bwd(const la_scan_dims *dims, int32_t dtype, const void 
         a.dg = tok_out(dg, dims->dg_strides);
         a.dfin = d_final_state;
         a.dinit = d_initial_state;
-        return launched(la::scan_backward(a, s), "gated scan backward");
+        return launched(la::scan_backward(a, workspace, s), "gated scan backward");
     });
 }
 

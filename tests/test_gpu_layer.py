@@ -274,6 +274,28 @@ def test_scan_is_deterministic_and_takes_any_stream():
             assert torch.equal(a, b) and torch.equal(a, c)
 
 
+def test_scan_withheld_tile_reports_timeout_and_context_survives():
+    # the first tile does not publish its map: the tiles after it wait, at most two seconds,
+    # and the call reports it; the next call is right
+    import time
+    x, g, do, init, dfin = _cuda(*_scan_inputs(1, 6000, 1, 64, BF, BF, 1, 16))
+    want = la.gated_scan_fwd(x, g, init) + la.gated_scan_bwd(x, g, do, init, dfin)
+    la.get_device_error()
+    _, _, states = la.gated_scan_fwd(x, g, init, keep_states=True)
+    for call in (lambda: la.gated_scan_fwd(x, g, init),
+                 lambda: la.gated_scan_bwd(x, g, do, init, dfin, states=states)):
+        N.check(N.lib().la_debug_withhold_next_handoff(1))
+        t0 = time.time()
+        call()
+        with pytest.raises(N.LaError) as err:
+            la.get_device_error()
+        assert err.value.status == N.LA_ERR_TIMEOUT and time.time() - t0 < 30
+        la.get_device_error()
+        got = la.gated_scan_fwd(x, g, init) + la.gated_scan_bwd(x, g, do, init, dfin)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        la.get_device_error()
+
+
 def test_scan_refuses_foreign_states():
     x, g, do, init, dfin = _cuda(*_scan_inputs(1, 300, 1, 8, F32, F32, 1, 15))
     with pytest.raises(ValueError, match="states"):
