@@ -277,10 +277,11 @@ cudaError_t split_scan(const SplitScanArgs &a, cudaStream_t s);
 
 // The gated linear recurrence s_t = exp(g_t) s_{t-1} + x_t (la_scan.cu),
 // elementwise per (sequence, head, channel).  Tokens are numbered by their
-// processing position on one axis over all rows: p = row * T + j, j the place
-// in the row's processing order (dense), or p = t, from the end with reverse
-// (packed).  A tile is SCAN_TILE consecutive positions; states holds the fp32
-// state entering each tile, [tile][H][D] (unused where a sequence starts).
+// processing position on one axis over all rows: p = row * pitch + j, j the
+// place in the row's processing order (dense), or p = t, from the end with
+// reverse (packed).  A tile is SCAN_TILE consecutive positions; states holds
+// the fp32 state entering each of the scan_tiles tiles, [tile][H][D] (unused
+// where a sequence starts).
 constexpr int SCAN_TILE = 128;
 struct ScanArgs {
     int B, T, H, D, N;
@@ -295,7 +296,9 @@ struct ScanArgs {
     const float *dfin;          // backward: their gradient, or null
     float *dinit;               // backward: the initial states' gradient, or null
     float *states;
+    int pitch;                  // positions of a row: set by the launch
 };
+int64_t scan_tiles(int B, int T);
 // o may be null in the forward (the states alone).  ws: scan_link_bytes of
 // scratch (0 bytes: not needed), 256-byte aligned.
 cudaError_t scan_forward(const ScanArgs &a, void *ws, cudaStream_t s);

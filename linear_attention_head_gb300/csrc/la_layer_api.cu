@@ -168,8 +168,7 @@ la_status scan_sizes(const la_scan_dims *d, int32_t dtype)
 // The states that enter the tiles; a single tile needs none.
 size_t states_bytes(const la_scan_dims *d)
 {
-    const size_t tiles =
-        ((size_t)d->batch * d->seq_len + la::SCAN_TILE - 1) / (size_t)la::SCAN_TILE;
+    const size_t tiles = (size_t)la::scan_tiles(d->batch, d->seq_len);
     return tiles > 1 ? tiles * d->heads * d->dim * sizeof(float) : 0;
 }
 
