@@ -34,6 +34,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
@@ -1305,11 +1306,14 @@ cudaError_t run(const ScanArgs &a, Plan k, void *ws, cudaStream_t s)
     if (e != cudaSuccess)
         return e;
     // Segments where the chains (rows x parts of the channels) are fewer than
-    // a third of the teams, as many as there are teams for, of 4 tiles at least.
+    // a third of the teams: as many as there are teams for, unless the maps
+    // that a segment starts from cost more than its tiles (0.1 us a map, 4 us a
+    // tile for both passes: best at 7 sqrt(run)).
     const int64_t chains = (int64_t)k.rows * k.parts, slots = (int64_t)sms * teams;
     int64_t segments = 1;
     if (chains * 3 <= slots)
-        segments = std::min<int64_t>({slots / chains, k.run / 4, MAX_SEGMENTS});
+        segments = std::min<int64_t>({slots / chains, (int64_t)k.run,
+                                      (int64_t)(7.0 * std::sqrt((double)k.run)), MAX_SEGMENTS});
     segments = std::max<int64_t>(segments, 1);
     k.len = (int)((k.run + segments - 1) / segments);
     k.segments = (k.run + k.len - 1) / k.len;
@@ -1383,13 +1387,11 @@ int64_t scan_tiles(int B, int T) { return tiles_of(B, T); }
 
 size_t scan_link_bytes(int B, int T, int H, int D)
 {
-    // the segments' maps: at least 4 tiles each, and at most as many segments as
-    // teams for all rows together, or MAX_SEGMENTS a row
+    // the segments' maps: at most one a tile and MAX_SEGMENTS a row
     const int64_t tiles = tiles_of(B, T), rows = own_tiles(B, T) ? B : 1;
-    if (tiles < 8)
+    if (tiles == rows)
         return 0;
-    return (size_t)(std::min<int64_t>(tiles / 4, rows * MAX_SEGMENTS) + rows) * H * D *
-           sizeof(float2);
+    return (size_t)std::min<int64_t>(tiles, rows * MAX_SEGMENTS) * H * D * sizeof(float2);
 }
 
 cudaError_t scan_forward(const ScanArgs &a, void *ws, cudaStream_t s)
