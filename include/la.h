@@ -430,7 +430,8 @@ typedef struct la_scan_dims {
  *                  aligned), or NULL: the states that la_gated_scan_bwd starts
  *                  from, to be passed to it once or more
  *   workspace      256-byte aligned, la_gated_scan_workspace_size(..., 0)
- *                  bytes (LA_ERR_INVALID_ARG when smaller); that size may be 0 */
+ *                  bytes, or (..., 3) when final_state is initial_state
+ *                  (LA_ERR_INVALID_ARG when smaller); the size may be 0 */
 la_status la_gated_scan_fwd(const la_scan_dims *dims, int32_t dtype, const void *x,
                             const void *g, const float *initial_state, int32_t reverse,
                             const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, void *o,
@@ -460,8 +461,9 @@ la_status la_gated_scan_bwd(const la_scan_dims *dims, int32_t dtype, const void 
                             const float *states, void *dx, void *dg, float *d_initial_state,
                             void *workspace, size_t workspace_bytes, void *stream);
 
-/* Workspace bytes of la_gated_scan_fwd (backward = 0) or la_gated_scan_bwd
- * (1: states given, 2: not); 0 for invalid sizes.  They do not depend on the
+/* Workspace bytes of la_gated_scan_fwd (backward = 0; 3 when final_state is
+ * initial_state) or la_gated_scan_bwd (1: states given, 2: not); 0 for invalid
+ * sizes.  They do not depend on the
  * packed sequences' lengths.  Pure host function. */
 size_t la_gated_scan_workspace_size(const la_scan_dims *dims, int32_t dtype, int32_t backward);
 

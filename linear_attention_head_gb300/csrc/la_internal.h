@@ -332,8 +332,14 @@ struct RopeArgs {
     RopeTensor t[2];            // q, k; heads == 0: not there
     float *partial;             // backward: the CTAs' weight gradients
 };
-cudaError_t rope_forward(const RopeArgs &a, cudaStream_t s);
-cudaError_t rope_backward(const RopeArgs &a, cudaStream_t s);
+// The forward, or the backward (back).
+cudaError_t rope_run(bool back, const RopeArgs &a, cudaStream_t s);
+// Its kernels by direction and token type; *parts: the CTAs launched.
+cudaError_t rope_fwd_bf16(const RopeArgs &a, bool vec, int sms, cudaStream_t s, int *parts);
+cudaError_t rope_fwd_f32(const RopeArgs &a, bool vec, int sms, cudaStream_t s, int *parts);
+cudaError_t rope_bwd_bf16(const RopeArgs &a, bool vec, int sms, cudaStream_t s, int *parts);
+cudaError_t rope_bwd_f32(const RopeArgs &a, bool vec, int sms, cudaStream_t s, int *parts);
+constexpr int ROPE_MOST_CTAS = 768;
 // Bytes of RopeArgs::partial.
 size_t rope_partial_bytes(int D);
 

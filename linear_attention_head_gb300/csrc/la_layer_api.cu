@@ -327,7 +327,7 @@ size_t la_gated_scan_workspace_size(const la_scan_dims *dims, int32_t dtype, int
     if (!scan_sized(dims))
         return 0;
     return round256(la::scan_link_bytes(dims->batch, dims->seq_len, dims->heads, dims->dim)) +
-           (backward == 0   ? round256(init_bytes(dims))
+           (backward == 3   ? round256(init_bytes(dims))
             : backward == 2 ? round256(states_bytes(dims))
                             : 0);
 }
@@ -347,15 +347,16 @@ la_status la_gated_scan_fwd(const la_scan_dims *dims, int32_t dtype, const void 
             return e;
         if ((int64_t)a.B * a.T > 0 && (e = need(o, "o")))
             return e;
+        const bool in_place = final_state && final_state == initial_state;
         if ((e = check_workspace(workspace, workspace_bytes,
-                                 la_gated_scan_workspace_size(dims, dtype, 0))))
+                                 la_gated_scan_workspace_size(dims, dtype, in_place ? 3 : 0))))
             return e;
         if (a.N == 0)
             return LA_OK;
         a.o = tok_out(o, dims->o_strides);
         a.fin = final_state;
         a.states = states;
-        if (final_state && final_state == initial_state && (int64_t)a.B * a.T > 0) {
+        if (in_place && (int64_t)a.B * a.T > 0) {
             float *copy = reinterpret_cast<float *>(
                 static_cast<uint8_t *>(workspace) +
                 round256(la::scan_link_bytes(a.B, a.T, a.H, a.D)));
@@ -446,7 +447,7 @@ la_status la_qk_norm_rope_fwd(const la_rope_dims *dims, int32_t dtype, const voi
             put(t.xs, is[i]);
             put(t.ys, os[i]);
         }
-        return some ? launched(la::rope_forward(a, s), "norm and rotation") : LA_OK;
+        return some ? launched(la::rope_run(false, a, s), "norm and rotation") : LA_OK;
     });
 }
 
@@ -516,7 +517,7 @@ la_status la_qk_norm_rope_bwd(const la_rope_dims *dims, int32_t dtype, const voi
             return LA_OK;
         }
         a.partial = static_cast<float *>(workspace);
-        return launched(la::rope_backward(a, s), "norm and rotation backward");
+        return launched(la::rope_run(true, a, s), "norm and rotation backward");
     });
 }
 

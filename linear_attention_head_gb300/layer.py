@@ -16,29 +16,52 @@ while that graph lives a capture breaks off there.)
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import _native as N
-from .api import Tensor, _dtype_code, _packed_batch_msg, _ptr, _state, _stream, _traced
+from .api import Tensor, _packed_batch_msg, _state, _traced
 
-_I3 = ctypes.c_int64 * 3
+# The calls of a decoding step take a few microseconds on the GPU, so what the
+# host does for one counts: structures are packed in one go, pointers are plain
+# integers.
 _ref = ctypes.byref
+_scan_pack = struct.Struct("=6i18q").pack
+_rope_pack = struct.Struct("=12i21q128s").pack
+_scan_dims = N.LaScanDims.from_buffer_copy
+_rope_dims = N.LaRopeDims.from_buffer_copy
+_current_device = torch.cuda.current_device
+_CODES = {torch.bfloat16: N.LA_DTYPE_BF16, torch.float32: N.LA_DTYPE_F32}
+_NONE3 = (0, 0, 0)
+
+
+def _code(dtype) -> int:
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError("token tensors must be bfloat16 or float32, got %s" % dtype)
+    return code
+
+
+def _ptr(t: Optional[Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _strides(t: Optional[Tensor]):
-    return _I3(*t.stride()[:3]) if t is not None else _I3()
+    return _NONE3 if t is None else t.stride()[:3]
 
 
 def _call(device, fn, *args) -> None:
     """fn(*args) with `device` current, on its current stream (the last argument)."""
-    if device.index == torch.cuda.current_device():
-        N.check(fn(*args, _stream(device)))
+    if device.index == _current_device():
+        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
     else:
         with torch.cuda.device(device):
-            N.check(fn(*args, _stream(device)))
+            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if st:
+        N.check(st)
 
 
 def _workspace(nbytes: int, device) -> Tuple[Optional[Tensor], int]:
@@ -49,7 +72,7 @@ def _token(t: Tensor, name: str, like: Optional[Tensor] = None) -> Tensor:
     """A [B, T, H, D] token tensor with contiguous channels, on `like`'s device."""
     if t.ndim != 4:
         raise ValueError("%s must be [B, T, H, D], got %s" % (name, tuple(t.shape)))
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("token tensors must be CUDA tensors")
     if like is not None and t.device != like.device:
         raise ValueError("all tensors must be on one device")
@@ -146,10 +169,7 @@ class Rope:
         self.axes = tuple(axes)
         self.rotary_dim = 2 * pairs
         self.interleaved = bool(interleaved)
-        self._pair_axis = (ctypes.c_uint8 * 128)(*axes)
-
-
-_NO_AXES = (ctypes.c_uint8 * 128)()
+        self._pair_axis = bytes(axes).ljust(128, b"\0")
 
 
 class _RopeCall:
@@ -158,55 +178,49 @@ class _RopeCall:
     def __init__(self, q, k, q_weight, k_weight, eps, normalize, rope, positions,
                  position_offset, cu_seqlens, cu_seqlens_host, names=("q", "k")):
         q = _token(q, names[0])
-        dev = q.device
+        dev = self.device = q.device
+        B, T, H, D = q.shape
+        heads = 0
         if k is not None:
             k = _token(k, names[1], q)
-            if k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3]:
+            if k.shape[:2] != q.shape[:2] or k.shape[3] != D:
                 raise ValueError("%s must be [B, T, H, D] and %s [B, T, H_k, D] (got %s, %s)"
                                  % (names + (tuple(q.shape), tuple(k.shape))))
             if k.dtype != q.dtype:
                 raise TypeError("all token tensors must share one dtype")
-        B, T, H, D = q.shape
-        self.q, self.k, self.device = q, k, dev
-        self.dtype = _dtype_code(q)
-        ws = [w for w in (q_weight, k_weight) if w is not None]
-        for w in ws:
+            heads = k.shape[2]
+        elif k_weight is not None:
+            raise ValueError("k_weight needs %s" % names[1])
+        self.q, self.k = q, k
+        self.dtype = w_code = _code(q.dtype)
+        w_dtype = None
+        for w in (q_weight, k_weight):
+            if w is None:
+                continue
             if tuple(w.shape) != (D,) or w.device != dev:
                 raise ValueError("weights must be [%d] on %s" % (D, dev))
-            if w.dtype != ws[0].dtype:
+            if w.dtype != (w_dtype or w.dtype):
                 raise TypeError("the weights must share one dtype")
-        if k_weight is not None and k is None:
-            raise ValueError("k_weight needs %s" % names[1])
+            w_dtype, w_code = w.dtype, _code(w.dtype)
         self.qw = q_weight.contiguous() if q_weight is not None else None
         self.kw = k_weight.contiguous() if k_weight is not None else None
-        self.w_dtype = ws[0].dtype if ws else q.dtype
         self.eps = float(eps)
         self.cu = _cu(cu_seqlens, cu_seqlens_host, dev, B)
-        d = self.dims = N.LaRopeDims()
-        d.batch, d.seq_len, d.q_heads, d.dim = B, T, H, D
-        d.k_heads = k.shape[2] if k is not None else 0
-        d.num_seqs = self.cu.n
-        d.normalize = int(bool(normalize))
-        d.weight_dtype = _dtype_code(ws[0]) if ws else self.dtype
-        d.num_axes = 1
-        self.freq = None
+        rotary, axes, interleaved, pair_axis, self.freq = 0, 1, 0, b"", None
         if rope is not None:
-            if rope.rotary_dim > D:
-                raise ValueError("rotary_dim %d exceeds the %d channels" % (rope.rotary_dim, D))
-            if rope.inv_freq.device != dev:
+            rotary, axes, interleaved = rope.rotary_dim, rope.num_axes, int(rope.interleaved)
+            pair_axis, self.freq = rope._pair_axis, rope.inv_freq
+            if rotary > D:
+                raise ValueError("rotary_dim %d exceeds the %d channels" % (rotary, D))
+            if self.freq.device != dev:
                 raise ValueError("inv_freq is on %s, the tensors on %s"
-                                 % (rope.inv_freq.device, dev))
-            self.freq = rope.inv_freq
-            d.rotary_dim, d.num_axes = rope.rotary_dim, rope.num_axes
-            d.interleaved = int(rope.interleaved)
-            d.pair_axis = rope._pair_axis
+                                 % (self.freq.device, dev))
         elif positions is not None or position_offset is not None:
             raise ValueError("positions need rope")
+        pos_strides, pos_bytes = _NONE3, 0
         if positions is not None:
-            positions = self._positions(positions, B, T)
-            d.position_strides[0], d.position_strides[1], d.position_strides[2] = \
-                positions.stride()
-            d.position_bytes = positions.element_size()
+            positions, pos_strides = self._positions(positions, axes, B, T)
+            pos_bytes = positions.element_size()
         self.positions = positions
         if position_offset is not None:
             if positions is not None:
@@ -217,22 +231,31 @@ class _RopeCall:
                                  % (self.cu.n, tuple(off.shape)))
             position_offset = off.to(dev, torch.int32).contiguous()
         self.offset = position_offset
+        self._head = (B, T, H, heads, D, rotary, self.cu.n, axes, 1 if normalize else 0,
+                      interleaved, w_code, pos_bytes)
+        self._tail = tuple(pos_strides) + (pair_axis,)
 
-    def _positions(self, p, B, T):
-        """[axes, B, T] (or without the axes or the batch dimension where they are 1)."""
+    def _positions(self, p, axes, B, T):
+        """[axes, B, T] (or without the axes or the batch dimension where they are 1) and its
+        strides, 0 where one row serves the whole batch."""
         if p.dtype not in (torch.int32, torch.int64):
             raise TypeError("positions must be int32 or int64, got %s" % p.dtype)
         if p.device != self.device:
             raise ValueError("positions must be on %s" % self.device)
-        axes = self.dims.num_axes
-        if p.ndim == 1 and axes == 1:
-            p = p[None]
-        if p.ndim == 2:
-            p = p[None] if axes == 1 else p[:, None]
-        if p.ndim != 3 or p.shape[0] != axes or p.shape[1] not in (1, B) or p.shape[2] != T:
+        shape, st = tuple(p.shape), p.stride()
+        if len(shape) == 1 and axes == 1:
+            shape, st = (1, 1) + shape, (0, 0) + st
+        elif len(shape) == 2:
+            shape, st = (((1,) + shape, (0,) + st) if axes == 1 else
+                         ((shape[0], 1, shape[1]), (st[0], 0, st[1])))
+        if len(shape) != 3 or shape[0] != axes or shape[1] not in (1, B) or shape[2] != T:
             raise ValueError("positions must be [%d, %d, %d] (axes, batch, tokens), got %s"
                              % (axes, B, T, tuple(p.shape)))
-        return p.expand(axes, B, T)
+        return p, (st[0], st[1] if shape[1] > 1 else 0, st[2])
+
+    def dims(self, q, k, qo, ko, dq=None, dk=None):
+        return _rope_dims(_rope_pack(*self._head, *_strides(q), *_strides(k), *_strides(qo),
+                                     *_strides(ko), *_strides(dq), *_strides(dk), *self._tail))
 
     def tail(self):
         """The argument run (weights, eps, frequencies, positions, packing) of the C ABI."""
@@ -263,9 +286,7 @@ def qk_norm_rope_fwd(q: Tensor, k: Optional[Tensor] = None, q_weight: Optional[T
     qo, ko = _pair_of(out, "out")
     qo = _output(qo, c.q, "out")
     ko = _output(ko, c.k, "out") if c.k is not None else None
-    d = c.dims
-    d.q_strides, d.k_strides = _strides(c.q), _strides(c.k)
-    d.qo_strides, d.ko_strides = _strides(qo), _strides(ko)
+    d = c.dims(c.q, c.k, qo, ko)
     _call(c.device, N.lib().la_qk_norm_rope_fwd, _ref(d), c.dtype, _ptr(c.q), _ptr(c.k),
           *c.tail(), _ptr(qo), _ptr(ko))
     return (qo, ko) if c.k is not None else qo
@@ -273,7 +294,6 @@ def qk_norm_rope_fwd(q: Tensor, k: Optional[Tensor] = None, q_weight: Optional[T
 
 def _rope_bwd(c: _RopeCall, x, want_weights: bool):
     """Gradients for the call c, whose q and k are the outputs' gradients; x: the inputs."""
-    d = c.dims
     xq, xk = x
     dq = torch.empty(c.q.shape, dtype=c.q.dtype, device=c.device)
     dk = torch.empty(c.k.shape, dtype=c.k.dtype, device=c.device) if c.k is not None else None
@@ -281,9 +301,7 @@ def _rope_bwd(c: _RopeCall, x, want_weights: bool):
     if want_weights:
         dqw = torch.empty_like(c.qw) if c.qw is not None else None
         dkw = torch.empty_like(c.kw) if c.kw is not None else None
-    d.q_strides, d.k_strides = _strides(xq), _strides(xk)
-    d.qo_strides, d.ko_strides = _strides(c.q), _strides(c.k)
-    d.dq_strides, d.dk_strides = _strides(dq), _strides(dk)
+    d = c.dims(xq, xk, c.q, c.k, dq, dk)
     lib = N.lib()
     ws, nbytes = None, 0
     if dqw is not None or dkw is not None:
@@ -413,14 +431,13 @@ def _scan_call(x, g, initial_state, cu_seqlens, cu_seqlens_host):
     if g.shape != x.shape:
         raise ValueError("g must have x's shape %s, got %s" % (tuple(x.shape), tuple(g.shape)))
     g = _token(g, "g", x)
-    code = _dtype_code(x)
     if g.dtype not in (x.dtype, torch.float32):
         raise TypeError("g must have x's dtype %s or float32, got %s" % (x.dtype, g.dtype))
     B, T, H, D = x.shape
     cu = _cu(cu_seqlens, cu_seqlens_host, x.device, B)
     init = _state(initial_state, (cu.n, H, D), x.device, "initial_state")
-    d = N.LaScanDims(B, T, H, D, cu.n, _dtype_code(g), _strides(x), _strides(g))
-    return x, g, init, cu, d, code
+    head = (B, T, H, D, cu.n, _code(g.dtype)) + tuple(_strides(x)) + tuple(_strides(g))
+    return x, g, init, cu, head, _code(x.dtype)
 
 
 @_traced
@@ -434,7 +451,7 @@ def gated_scan_fwd(x: Tensor, g: Tensor, initial_state: Optional[Tensor] = None,
     keep_states=True (o, final_state, states): what gated_scan_bwd starts from, about 1% of x.
     final_state may be the initial_state tensor itself.  cu_seqlens, cu_seqlens_host and
     reverse as qk_norm_rope_fwd and la_fwd."""
-    x, g, init, cu, d, code = _scan_call(x, g, initial_state, cu_seqlens, cu_seqlens_host)
+    x, g, init, cu, head, code = _scan_call(x, g, initial_state, cu_seqlens, cu_seqlens_host)
     dev = x.device
     out = _output(out, x, "out")
     shape = (cu.n,) + tuple(x.shape[2:])
@@ -445,15 +462,18 @@ def gated_scan_fwd(x: Tensor, g: Tensor, initial_state: Optional[Tensor] = None,
                              % (shape, dev))
     elif want_final_state:
         final_state = torch.empty(shape, dtype=torch.float32, device=dev)
-    d.o_strides = _strides(out)
+    d = _scan_dims(_scan_pack(*head, *_strides(out), *_NONE3, *_NONE3, *_NONE3))
     lib = N.lib()
     states = None
     if keep_states:
         states = torch.empty(int(lib.la_gated_scan_states_size(_ref(d))) // 4,
                              dtype=torch.float32, device=dev)
-    ws, nbytes = _workspace(int(lib.la_gated_scan_workspace_size(_ref(d), code, 0)), dev)
+    in_place = init is not None and final_state is not None and \
+        init.data_ptr() == final_state.data_ptr()
+    ws, nbytes = _workspace(lib.la_gated_scan_workspace_size(_ref(d), code, 3 if in_place else 0),
+                            dev)
     _call(dev, lib.la_gated_scan_fwd, _ref(d), code, _ptr(x), _ptr(g), _ptr(init),
-          int(bool(reverse)), _ptr(cu.dev), _ptr(cu.host), _ptr(out), _ptr(final_state),
+          1 if reverse else 0, _ptr(cu.dev), _ptr(cu.host), _ptr(out), _ptr(final_state),
           _ptr(states), _ptr(ws), nbytes)
     return (out, final_state, states) if keep_states else (out, final_state)
 
@@ -467,7 +487,7 @@ def gated_scan_bwd(x: Tensor, g: Tensor, do: Tensor, initial_state: Optional[Ten
     sum(o * do) + sum(final_state * d_final_state); dg has g's dtype.  states: what
     gated_scan_fwd(..., keep_states=True) returned for the same arguments; without it they are
     computed again (one more pass over x and g)."""
-    x, g, init, cu, d, code = _scan_call(x, g, initial_state, cu_seqlens, cu_seqlens_host)
+    x, g, init, cu, head, code = _scan_call(x, g, initial_state, cu_seqlens, cu_seqlens_host)
     dev = x.device
     do = _token(do, "do", x)
     if do.shape != x.shape or do.dtype != x.dtype:
@@ -477,7 +497,7 @@ def gated_scan_bwd(x: Tensor, g: Tensor, do: Tensor, initial_state: Optional[Ten
     dg = torch.empty(x.shape, dtype=g.dtype, device=dev)
     dinit = (torch.empty((cu.n,) + tuple(x.shape[2:]), dtype=torch.float32, device=dev)
              if want_d_initial_state else None)
-    d.do_strides, d.dx_strides, d.dg_strides = _strides(do), _strides(dx), _strides(dg)
+    d = _scan_dims(_scan_pack(*head, *_NONE3, *_strides(do), *_strides(dx), *_strides(dg)))
     lib = N.lib()
     if states is not None:
         want = int(lib.la_gated_scan_states_size(_ref(d))) // 4
@@ -489,7 +509,7 @@ def gated_scan_bwd(x: Tensor, g: Tensor, do: Tensor, initial_state: Optional[Ten
     ws, nbytes = _workspace(int(lib.la_gated_scan_workspace_size(
         _ref(d), code, 1 if states is not None else 2)), dev)
     _call(dev, lib.la_gated_scan_bwd, _ref(d), code, _ptr(x), _ptr(g), _ptr(do), _ptr(init),
-          _ptr(dfin), int(bool(reverse)), _ptr(cu.dev), _ptr(cu.host), _ptr(states), _ptr(dx),
+          _ptr(dfin), 1 if reverse else 0, _ptr(cu.dev), _ptr(cu.host), _ptr(states), _ptr(dx),
           _ptr(dg), _ptr(dinit), _ptr(ws), nbytes)
     return dx, dg, dinit
 
