@@ -276,13 +276,12 @@ struct SplitScanArgs {
 cudaError_t split_scan(const SplitScanArgs &a, cudaStream_t s);
 
 // The gated linear recurrence s_t = exp(g_t) s_{t-1} + x_t (la_scan.cu),
-// elementwise per (sequence, head, channel).  Tokens are numbered by their
-// processing position on one axis over all rows: p = row * pitch + j, j the
-// place in the row's processing order (dense), or p = t, from the end with
-// reverse (packed).  A tile is SCAN_TILE consecutive positions; states holds
-// the fp32 state entering each of the scan_tiles tiles, [tile][H][D] (unused
-// where a sequence starts).
-constexpr int SCAN_TILE = 128;
+// elementwise per (sequence, head, channel).  A sequence's tokens in processing
+// order are cut into blocks, SCAN_TILE tokens each or, in the serial kernels,
+// SCAN_BLOCK; states holds the fp32 state that enters each block [block][H][D]
+// (of a sequence's first block it is not read).  Sequence n's blocks begin at
+// n * ceil(T / size) (dense) or cu[n] / size + n (packed).
+constexpr int SCAN_TILE = 128, SCAN_BLOCK = 8;
 struct ScanArgs {
     int B, T, H, D, N;
     const int32_t *cu;          // device [N + 1], or nullptr (dense: N == B)
@@ -296,14 +295,18 @@ struct ScanArgs {
     const float *dfin;          // backward: their gradient, or null
     float *dinit;               // backward: the initial states' gradient, or null
     float *states;
-    int pitch;                  // positions of a row: set by the launch
+    int64_t longest;            // scan_plan: the longest sequence's tokens,
+    int serial;                 // and the kernels that are used
 };
-int64_t scan_tiles(int B, int T);
-// o may be null in the forward (the states alone).  ws: scan_link_bytes of
+// tiles: of all sequences together.
+void scan_plan(ScanArgs *a, int64_t tiles, int64_t longest);
+// o may be null in the forward (the states alone).  ws: scan_maps_bytes of
 // scratch (0 bytes: not needed), 256-byte aligned.
 cudaError_t scan_forward(const ScanArgs &a, void *ws, cudaStream_t s);
 cudaError_t scan_backward(const ScanArgs &a, void *ws, cudaStream_t s);
-size_t scan_link_bytes(int B, int T, int H, int D);
+size_t scan_maps_bytes(int T);
+// Bytes of states; N > 0 with B == 1: enough for N packed sequences as well.
+size_t scan_states_bytes(int B, int T, int N, int H, int D);
 // Reads (after synchronizing s) and clears the scan kernels' device error word.
 cudaError_t scan_read_and_clear_error(cudaStream_t s, int *err);
 // la_debug_withhold_next_handoff's switch of this host thread, reset by the read.

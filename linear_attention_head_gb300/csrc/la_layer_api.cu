@@ -75,13 +75,21 @@ la_status check_out(const int64_t *st, const char *name, int32_t B, int32_t T, i
     return e;
 }
 
-// The packed-sequence table, as la_fwd takes it; *N: the number of states,
-// *some_empty: sequences without tokens are among them.
+// The packed-sequence table, as la_fwd takes it, and what it says (without one:
+// `batch` sequences of seq_len tokens).
+struct Sequences {
+    int n = 0;              // of states
+    int some_empty = 0;     // sequences without tokens are among them
+    int64_t tiles = 0;      // of la::SCAN_TILE tokens, of all sequences together
+    int64_t longest = 0;
+};
 la_status check_packed(int32_t batch, int32_t seq_len, int32_t num_seqs, const int32_t *cu,
-                       const int32_t *cu_host, cudaStream_t stream, int *N, int *some_empty)
+                       const int32_t *cu_host, cudaStream_t stream, Sequences *q)
 {
-    *N = batch;
-    *some_empty = batch > 0 && seq_len == 0;
+    q->n = batch;
+    q->some_empty = batch > 0 && seq_len == 0;
+    q->longest = seq_len;
+    q->tiles = (int64_t)batch * (((int64_t)seq_len + la::SCAN_TILE - 1) / la::SCAN_TILE);
     if (!cu)
         return cu_host ? fail(LA_ERR_INVALID_ARG, "cu_seqlens_host given without cu_seqlens")
                        : LA_OK;
@@ -92,8 +100,8 @@ la_status check_packed(int32_t batch, int32_t seq_len, int32_t num_seqs, const i
                     batch);
     if (num_seqs < 0 || num_seqs > (1 << 30))
         return fail(LA_ERR_INVALID_ARG, "num_seqs = %d", num_seqs);
-    *N = num_seqs;
-    *some_empty = 0;
+    *q = Sequences{};
+    q->n = num_seqs;
     std::vector<int32_t> copy;
     if (!cu_host) {
         copy.resize((size_t)num_seqs + 1);
@@ -108,10 +116,13 @@ la_status check_packed(int32_t batch, int32_t seq_len, int32_t num_seqs, const i
     if (cu_host[0] != 0)
         return fail(LA_ERR_INVALID_ARG, "cu_seqlens[0] = %d, expected 0", cu_host[0]);
     for (int n = 0; n < num_seqs; ++n) {
-        if (cu_host[n + 1] < cu_host[n])
+        const int64_t len = (int64_t)cu_host[n + 1] - cu_host[n];
+        if (len < 0)
             return fail(LA_ERR_INVALID_ARG, "cu_seqlens decreases at %d (%d -> %d)", n,
                         cu_host[n], cu_host[n + 1]);
-        *some_empty |= cu_host[n + 1] == cu_host[n];
+        q->some_empty |= len == 0;
+        q->longest = len > q->longest ? len : q->longest;
+        q->tiles += (len + la::SCAN_TILE - 1) / la::SCAN_TILE;
     }
     if (cu_host[num_seqs] != seq_len)
         return fail(LA_ERR_INVALID_ARG, "cu_seqlens[%d] = %d but seq_len = %d", num_seqs,
@@ -165,11 +176,9 @@ la_status scan_sizes(const la_scan_dims *d, int32_t dtype)
     return check_rows(d->batch, d->seq_len, d->dim);
 }
 
-// The states that enter the tiles; a single tile needs none.
 size_t states_bytes(const la_scan_dims *d)
 {
-    const size_t tiles = (size_t)la::scan_tiles(d->batch, d->seq_len);
-    return tiles > 1 ? tiles * d->heads * d->dim * sizeof(float) : 0;
+    return la::scan_states_bytes(d->batch, d->seq_len, d->num_seqs, d->heads, d->dim);
 }
 
 // A copy of the initial states (final_state being initial_state itself: the
@@ -197,9 +206,11 @@ la_status scan_args(const la_scan_dims *d, int32_t dtype, const void *x, const v
         (e = check_in(d->g_strides, "g")))
         return e;
     *a = la::ScanArgs{};
-    if ((e = check_packed(d->batch, d->seq_len, d->num_seqs, cu, cu_host, s, &a->N,
-                          &a->some_empty)))
+    Sequences q;
+    if ((e = check_packed(d->batch, d->seq_len, d->num_seqs, cu, cu_host, s, &q)))
         return e;
+    a->N = q.n;
+    a->some_empty = q.some_empty;
     a->B = d->batch;
     a->T = d->seq_len;
     a->H = d->heads;
@@ -211,6 +222,7 @@ la_status scan_args(const la_scan_dims *d, int32_t dtype, const void *x, const v
     a->x = tok(x, d->x_strides);
     a->g = tok(g, d->g_strides);
     a->init = init;
+    la::scan_plan(a, q.tiles, q.longest);
     if ((int64_t)a->B * a->T > 0 && ((e = need(x, "x")) || (e = need(g, "g"))))
         return e;
     return LA_OK;
@@ -254,10 +266,10 @@ la_status rope_args(const la_rope_dims *d, int32_t dtype, const void *qw, const 
     if (e)
         return e;
     *a = la::RopeArgs{};
-    int some_empty;
-    if ((e = check_packed(d->batch, d->seq_len, d->num_seqs, cu, cu_host, s, &a->N,
-                          &some_empty)))
+    Sequences q;
+    if ((e = check_packed(d->batch, d->seq_len, d->num_seqs, cu, cu_host, s, &q)))
         return e;
+    a->N = q.n;
     if (d->normalize && !(eps >= 0.f && std::isfinite(eps)))
         return fail(LA_ERR_INVALID_ARG, "eps = %g must be finite and not negative", (double)eps);
     if (!d->normalize && (qw || kw))
@@ -326,7 +338,7 @@ size_t la_gated_scan_workspace_size(const la_scan_dims *dims, int32_t dtype, int
     (void)dtype;
     if (!scan_sized(dims))
         return 0;
-    return round256(la::scan_link_bytes(dims->batch, dims->seq_len, dims->heads, dims->dim)) +
+    return round256(la::scan_maps_bytes(dims->seq_len)) +
            (backward == 3   ? round256(init_bytes(dims))
             : backward == 2 ? round256(states_bytes(dims))
                             : 0);
@@ -359,7 +371,7 @@ la_status la_gated_scan_fwd(const la_scan_dims *dims, int32_t dtype, const void 
         if (in_place && (int64_t)a.B * a.T > 0) {
             float *copy = reinterpret_cast<float *>(
                 static_cast<uint8_t *>(workspace) +
-                round256(la::scan_link_bytes(a.B, a.T, a.H, a.D)));
+                round256(la::scan_maps_bytes(a.T)));
             if ((e = launched(cudaMemcpyAsync(copy, initial_state,
                                               (size_t)a.N * a.H * a.D * sizeof(float),
                                               cudaMemcpyDeviceToDevice, s),
@@ -399,7 +411,7 @@ la_status la_gated_scan_bwd(const la_scan_dims *dims, int32_t dtype, const void 
         if (!states && states_bytes(dims)) {
             a.states = reinterpret_cast<float *>(
                 static_cast<uint8_t *>(workspace) +
-                round256(la::scan_link_bytes(a.B, a.T, a.H, a.D)));
+                round256(la::scan_maps_bytes(a.T)));
             if ((e = launched(la::scan_forward(a, workspace, s), "gated scan states")))
                 return e;
         }

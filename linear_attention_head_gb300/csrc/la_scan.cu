@@ -8,29 +8,27 @@
 //
 // Both are chains of maps s -> A s + B, which compose:
 //     (A2, B2) o (A1, B1) = (A2 A1, A2 B1 + B2).
-// So a team of threads takes a tile of SCAN_TILE tokens x CT channels at once:
-// its token groups compose their L tokens, the groups are composed through
-// shared memory, and the state then goes through the tokens again.  Teams walk
-// along the tokens, tile by tile, with the state in registers; x, g (and do) are
-// read once and o (dx, dg) written once.
+// So a team of threads takes a tile of SCAN_TILE tokens of a sequence x CT
+// channels at once: its token groups compose their L tokens, the groups are
+// composed through shared memory, and the state then goes through the tokens
+// again.  Teams walk along a sequence, tile by tile, with the state in registers;
+// x, g (and do) are read once and o (dx, dg) written once.
 // A CTA per SM: a warp has the teams' tiles copied to a ring of stages by TMA, so
-// that copies are under way at all times.  (Tiles that lie in two batch rows are
-// copied a row of theirs at a time, 18 cycles a copy: 2.4 us a tile against 1.1.)
+// that copies are under way at all times.
 //
-// Where there are too few rows and channels for the teams, the tokens are cut
-// into segments: a first pass composes each segment's map s -> A s + B (it reads
-// the inputs and writes nothing else), and a segment starts from the maps of
-// those before it.  That pass adds 2/3 of the reads; the alternative, tiles that
-// wait for the state of the tile before them, was measured at 143 us against
-// PLACEHOLDER (b1 h8 n65536 forward): every tile of the GPU then waits at once,
-// two to four microseconds a round.
+// Where there are too few sequences and channels for the teams, the sequences are
+// cut into segments: a first pass composes each segment's map s -> A s + B (it
+// reads the inputs and writes nothing else), and a segment starts from the maps
+// of those before it.  That pass adds 2/3 of the reads; the alternative, tiles
+// that wait for the state of the tile before them, measured 143 us against 123
+// (b1 h8 n65536 forward): every tile of the GPU then waits at once, two to four
+// microseconds a round.
 //
-// All rows form one axis of processing positions (la_internal.h), so short and
-// packed sequences fill tiles like long ones.  A sequence's first token is a
-// reset: what comes before it is dropped by a select, never multiplied by zero,
-// so that a NaN or an infinity stays in its sequence.
+// Short sequences (a few tokens of many rows, decoding) take a thread per four
+// channels, which walks its sequence alone (serial, below).
 //
-// Bound: HBM, 6 (bf16 gate) or 8 bytes a value forward, 10 or 14 backward.
+// Bound: HBM, 6 (bf16 gate) or 8 bytes a value forward, 10 or 14 backward, and
+// close to it the issue rate: 20 instructions a value forward, 39 backward.
 
 #include <algorithm>
 #include <atomic>
@@ -69,7 +67,7 @@ using Bwd = Shape<8>;
 constexpr int FEEDERS = 128, CTA = 512 + FEEDERS;
 constexpr int RING = 196608;                       // bytes of all stages
 
-constexpr int MAX_SEGMENTS = 256;
+constexpr int MAX_SEGMENTS = 256, MAX_UNITS = 1024;   // units: where there are segments
 constexpr unsigned long long WAIT_NS = 2000000000ull;
 constexpr unsigned ALL = 0xffffffffu;
 
@@ -183,16 +181,6 @@ __device__ __forceinline__ float times(float a, float b)
     const float r = a * b;
     return r == 0.f && a != 0.f && b != 0.f ? 1.4e-45f : r;
 }
-// The state after tokens with the map (A, B); r: a sequence starts among them
-// (what came before is dropped, A is not used).
-__device__ __forceinline__ float through(float A, float B, int r, float s)
-{
-    return r ? B : fmaf(A, s, B);
-}
-__device__ __forceinline__ Val through(const Val &A, const Val &B, int r, const Val &s)
-{
-    return r ? B : fma2(A, s, B);
-}
 
 // ---- tokens and channels -------------------------------------------------------
 
@@ -254,7 +242,30 @@ template <typename T, bool VEC> struct Col {
                 off[v] = o;
         }
     }
-    __device__ T *row(int2 at, int64_t sb, int64_t st) const { return q + at.x * sb + at.y * st; }
+    // four consecutive channels from c0 on
+    __device__ Col(const void *base, int64_t sh, unsigned D, bool flat, unsigned c0, unsigned on)
+        : q(const_cast<T *>(static_cast<const T *>(base)))
+    {
+#pragma unroll
+        for (int v = 0; v < (VEC ? 1 : V); ++v) {
+            const unsigned c = on >> v & 1 ? c0 + v : c0;   // (the others are not accessed)
+            const int64_t o = flat ? c : c / D * sh + c % D;
+            if constexpr (VEC)
+                q += o;
+            else
+                off[v] = o;
+        }
+    }
+    __device__ Four<T> four(const T *r, unsigned on) const
+    {
+        Four<T> x;
+        if constexpr (VEC)
+            x.r = *reinterpret_cast<const decltype(x.r) *>(r);
+        else
+            x.set(load(r, on));
+        return x;
+    }
+    __device__ T *row(int b, int t, int64_t sb, int64_t st) const { return q + b * sb + t * st; }
     // one channel after the other, of rows that are not wide
     __device__ Val load(const T *r, unsigned on) const
     {
@@ -284,75 +295,25 @@ template <typename T, bool VEC> struct Col {
     }
 };
 
-// The tile's tokens: (batch row, token), the number of the sequence, and bits
-// of those that are their sequence's first or last.
-struct Tokens {
-    int2 at[SCAN_TILE];
-    int seq[SCAN_TILE];
-    unsigned starts[SCAN_TILE / 32], ends[SCAN_TILE / 32];
-};
-
-// A processing position: where its token is, its sequence, the first and the
-// last position of the sequence.
-struct At {
-    int b, t, n;
-    int64_t first, last;
-};
-__device__ __forceinline__ At position(const ScanArgs &a, int64_t P, int64_t p)
+// A state vector's values at four consecutive channels (0 where absent).
+__device__ __forceinline__ Val get_state(const float *from, int64_t n, int64_t C, unsigned c0,
+                                         unsigned on)
 {
-    const int pitch = a.pitch;
-    At r;
-    if (a.cu) {
-        r.b = 0;
-        r.t = (int)(a.reverse ? a.T - 1 - p : p);
-        r.n = 0;
-        for (int hi = a.N; hi - r.n > 1;) {   // cu[n] <= t < cu[hi]
-            const int m = (r.n + hi) / 2;
-            if (a.cu[m] <= r.t)
-                r.n = m;
-            else
-                hi = m;
-        }
-        const int before = r.t - a.cu[r.n], after = a.cu[r.n + 1] - 1 - r.t;
-        r.first = p - (a.reverse ? after : before);
-        r.last = p + (a.reverse ? before : after);
-    } else {
-        int j;
-        if (P <= 0x7fffffff) {
-            r.b = (int)((unsigned)p / (unsigned)pitch);
-            j = (int)((unsigned)p - (unsigned)r.b * (unsigned)pitch);
-        } else {
-            r.b = (int)(p / pitch);
-            j = (int)(p - (int64_t)r.b * pitch);
-        }
-        r.t = a.reverse ? a.T - 1 - j : j;
-        r.n = r.b;
-        r.first = p - j;
-        r.last = p + a.T - 1 - j;
-    }
-    return r;
+    float s[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        s[v] = from && (on >> v & 1) ? from[n * C + c0 + v] : 0.f;
+    return val(s[0], s[1], s[2], s[3]);
 }
-
-// Fills the w-th 32 entries of the table of the tile that begins at position
-// p0, by one warp.
-__device__ __forceinline__ void look_up(const ScanArgs &a, Tokens &tk, int64_t P, int64_t p0,
-                                        int count, int w)
+__device__ __forceinline__ void put_state(float *to, int64_t n, int64_t C, unsigned c0,
+                                          unsigned on, const Val &x)
 {
-    const int lane = threadIdx.x % 32, i = w * 32 + lane;
-    bool start = false, end = false;
-    if (i < count) {
-        const At r = position(a, P, p0 + i);
-        start = r.first == p0 + i;
-        end = r.last == p0 + i;
-        tk.at[i] = make_int2(r.b, r.t);
-        tk.seq[i] = r.n;
-    }
-    const unsigned ss = __ballot_sync(ALL, start), es = __ballot_sync(ALL, end);
-    if (lane == 0) {
-        tk.starts[w] = ss;
-        tk.ends[w] = es;
-    }
-    __syncwarp();
+    const float4 f = x.f();
+    const float s[V] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        if (on >> v & 1)
+            to[n * C + c0 + v] = s[v];
 }
 
 // The barrier of a team.
@@ -373,41 +334,13 @@ template <int N> struct Team {
     }
 };
 
-// A state vector's values at the thread's channels (0 where absent).
-template <bool VEC>
-__device__ __forceinline__ Val get_state(const float *from, int64_t n, int64_t C, unsigned c0,
-                                         int lane, unsigned on)
-{
-    float s[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        s[v] = from && (on >> v & 1) ? from[n * C + c0 + local_channel<VEC>(lane, v)] : 0.f;
-    return val(s[0], s[1], s[2], s[3]);
-}
-template <bool VEC>
-__device__ __forceinline__ void put_state(float *to, int64_t n, int64_t C, unsigned c0, int lane,
-                                          unsigned on, const Val &x)
-{
-    const float4 f = x.f();
-    float *p = to + n * C + c0;
-    if (on & 1)
-        p[local_channel<VEC>(lane, 0)] = f.x;
-    if (on & 2)
-        p[local_channel<VEC>(lane, 1)] = f.y;
-    if (on & 4)
-        p[local_channel<VEC>(lane, 2)] = f.z;
-    if (on & 8)
-        p[local_channel<VEC>(lane, 3)] = f.w;
-}
-
 // ---- what a call is cut into ------------------------------------------------
 
 struct Plan {
-    int rows, run;      // `rows` rows of `run` tiles
     int parts;          // of the channels
-    int segments, len;  // of a row, of `len` tiles; in the order of the chain
-    int units;          // rows * segments * parts: what a team takes
-    float2 *maps;       // [row][segment][C]: (A, B); A < 0: a sequence starts in the segment
+    int segments;       // of a sequence, in the order of the chain
+    int units;          // sequences * segments * parts: what a team takes
+    float2 *maps;       // [sequence][segment][C]: (A, B); A < 0: the state B itself
     int map;            // this launch forms them
     int flat;           // every tensor's heads are D apart
     int small;          // no token stride is beyond 2^24
@@ -422,32 +355,41 @@ __device__ __forceinline__ unsigned long long now_ns()
     return t;
 }
 
+// A sequence: its batch row, first token and tokens, and the first of its blocks
+// of SIZE tokens among all sequences' (ScanArgs::states).
+struct Row {
+    int b, bos, len;
+    int64_t block;
+};
+template <int SIZE> __device__ __forceinline__ Row row_of(const ScanArgs &a, int n)
+{
+    if (!a.cu)
+        return Row{n, 0, a.T, (int64_t)n * ((a.T + SIZE - 1) / SIZE)};
+    // (within the tokens, whatever the table says by now)
+    const int lo = min(max(a.cu[n], 0), a.T), hi = min(max(a.cu[n + 1], lo), a.T);
+    return Row{0, lo, hi - lo, (int64_t)lo / SIZE + n};
+}
+
 // What a team needs to know of a tile.
 struct Item {
     int stage;              // its place in the ring; < 0: no more
-    int tile;
+    int count;              // its tokens
     unsigned c0;            // its first channel
-    int whole;              // all positions are there, in one sequence, neither its first nor last
-    int straight;           // in one batch row
-    int count;              // positions
+    int seq, segment;
     int begin, end;         // it is its unit's first, last
-    int unit_row, segment;  // of the unit
-    int2 at;                // the token of the first position
-    int64_t p0;             // the tile's first position
-    int64_t first;          // the sequence of p0 begins there
+    int first, last;        // it holds its sequence's first, last token
+    int b, t;               // of its first processed token
+    int64_t block;          // its place in ScanArgs::states
 };
 
 template <class S, bool BACK> struct Maps {
     float A[S::WARPS][ROW], B[S::WARPS][ROW];   // the warps' maps
     float S_[S::WARPS][ROW];                    // the state that enters the warp
-    int reset[S::WARPS];                        // whether a sequence starts in its tokens
-    // the backward's forward chain: B of the maps (A is the same), states, resets
+    // the backward's forward chain: B of the maps (A is the same), states
     float fB[BACK ? S::WARPS : 1][ROW], fS[BACK ? S::WARPS : 1][ROW];
-    int freset[S::WARPS];
 };
 template <class S, bool BACK, int NS> struct Shared {
     Maps<S, BACK> maps[S::TEAMS];
-    Tokens tk[NS];                // where not whole
     Item item[S::TEAMS][2];       // a team's, in turn
     // at most two items of a team are under way: the feeding warps hand over the
     // next when one of the two barriers says that the last but one was worked off
@@ -459,33 +401,25 @@ template <class S, bool BACK, int NS> struct Shared {
 // A team's way through its units: one lane's state.
 struct Walk {
     int unit, step;     // the next unit; units apart
-    int row, seg, jj, end;   // the present one: jj of the chain's order, up to end
+    int seq, seg, jj, end, run;   // the present one: jj of the chain's order, up to end
     unsigned c0;
+    Row row;
 };
-template <bool BACK>
-__device__ __forceinline__ bool enter_unit(const ScanArgs &a, const Plan &k, int64_t P, Walk *w)
+__device__ __forceinline__ bool enter_unit(const ScanArgs &a, const Plan &k, Walk *w)
 {
     for (; w->unit < k.units; w->unit += w->step) {
         const int u = w->unit / k.parts;
         w->c0 = (unsigned)(w->unit - u * k.parts) * CT;
-        w->row = u / k.segments;
-        w->seg = u - w->row * k.segments;
-        w->jj = w->seg * k.len;
-        w->end = min(w->jj + k.len, k.run);
-        if (w->jj >= w->end)
+        w->seq = u / k.segments;
+        w->seg = u - w->seq * k.segments;
+        w->row = row_of<SCAN_TILE>(a, w->seq);
+        w->run = (w->row.len + SCAN_TILE - 1) / SCAN_TILE;
+        const int len = (w->run + k.segments - 1) / k.segments;
+        w->jj = w->seg * len;
+        w->end = min(w->jj + len, w->run);
+        // (of the last segment nobody needs the map)
+        if (w->jj >= w->end || (k.map && w->end == w->run))
             continue;
-        if (k.map) {
-            if (w->end == k.run)   // nobody starts from the last
-                continue;
-            // from the tile in which the sequence that leaves the segment starts
-            const int64_t last = (int64_t)w->row * k.run + (BACK ? k.run - w->end : w->end - 1);
-            const int64_t p = BACK ? last * SCAN_TILE : min(P, (last + 1) * SCAN_TILE) - 1;
-            const At x = position(a, P, p);
-            const int64_t at = (BACK ? x.last : x.first) / SCAN_TILE - (int64_t)w->row * k.run;
-            const int64_t jj = BACK ? k.run - 1 - at : at;
-            if (jj > w->jj)
-                w->jj = (int)jj;
-        }
         w->unit += w->step;
         return true;
     }
@@ -493,32 +427,28 @@ __device__ __forceinline__ bool enter_unit(const ScanArgs &a, const Plan &k, int
 }
 
 template <bool BACK>
-__device__ __forceinline__ Item next_item(const ScanArgs &a, const Plan &k, int64_t P, Walk *w)
+__device__ __forceinline__ Item next_item(const ScanArgs &a, const Plan &k, Walk *w)
 {
     Item d;
     d.stage = -1;
     d.begin = 0;
     if (w->jj >= w->end) {
-        if (!enter_unit<BACK>(a, k, P, w))
+        if (!enter_unit(a, k, w))
             return d;
         d.begin = 1;
     }
     d.stage = 0;
-    const int j = BACK ? k.run - 1 - w->jj : w->jj;
-    d.tile = w->row * k.run + j;
+    const int j = BACK ? w->run - 1 - w->jj : w->jj, p = j * SCAN_TILE;
+    d.count = min(w->row.len - p, SCAN_TILE);
     d.c0 = w->c0;
-    d.unit_row = w->row;
+    d.seq = w->seq;
     d.segment = w->seg;
     d.end = ++w->jj == w->end;
-    d.p0 = (int64_t)d.tile * SCAN_TILE;
-    d.count = (int)min(P - d.p0, (int64_t)SCAN_TILE);
-    const At x = position(a, P, d.p0);
-    if (k.rows > 1)   // rows of their own tiles: the last ends early
-        d.count = (int)min((int64_t)d.count, x.last + 1 - d.p0);
-    d.first = x.first;
-    d.at = make_int2(x.b, x.t);
-    d.whole = x.first < d.p0 && d.p0 + SCAN_TILE <= x.last;
-    d.straight = a.cu || d.p0 + d.count - 1 <= x.last;
+    d.first = j == 0;
+    d.last = j == w->run - 1;
+    d.b = w->row.b;
+    d.t = w->row.bos + (a.reverse ? w->row.len - 1 - p : p);
+    d.block = w->row.block + j;
     return d;
 }
 
@@ -526,16 +456,12 @@ __device__ __forceinline__ Item next_item(const ScanArgs &a, const Plan &k, int6
 // the warps 2p and 2p + 1 in the order of the chain (BACK: the last warp first).
 struct Run {
     float A0, B0;   // the first warp's map
-    int r0;
     float eA, eB;   // the map of all warps before it
-    int er;
     float A, B;     // the map of the tile (in every lane)
-    int r;
 };
 template <class S, bool BACK>
 __device__ __forceinline__ Run run_of(const float (&A)[S::WARPS][ROW],
-                                      const float (&B)[S::WARPS][ROW],
-                                      const int (&reset)[S::WARPS])
+                                      const float (&B)[S::WARPS][ROW])
 {
     constexpr int PARTS = S::PARTS;
     const int c = threadIdx.x % S::THREADS / PARTS, part = threadIdx.x % PARTS;
@@ -543,29 +469,23 @@ __device__ __forceinline__ Run run_of(const float (&A)[S::WARPS][ROW],
     Run q;
     q.A0 = A[w0][c];
     q.B0 = B[w0][c];
-    q.r0 = reset[w0];
     q.A = times(q.A0, A[w1][c]);
-    q.B = through(A[w1][c], B[w1][c], reset[w1], q.B0);
-    q.r = q.r0 | reset[w1];
+    q.B = fmaf(A[w1][c], q.B0, B[w1][c]);
 #pragma unroll
     for (int i = 1; i < PARTS; i *= 2) {
         const float x = __shfl_up_sync(ALL, q.A, i), y = __shfl_up_sync(ALL, q.B, i);
-        const int r = __shfl_up_sync(ALL, q.r, i);
         if (part >= i) {
-            q.B = through(q.A, q.B, q.r, y);
+            q.B = fmaf(q.A, y, q.B);
             q.A = times(q.A, x);
-            q.r |= r;
         }
     }
     q.eA = __shfl_up_sync(ALL, q.A, 1);
     q.eB = __shfl_up_sync(ALL, q.B, 1);
-    q.er = __shfl_up_sync(ALL, q.r, 1);
     if (part == 0)
-        q.eA = 1.f, q.eB = 0.f, q.er = 0;
+        q.eA = 1.f, q.eB = 0.f;
     const int last = threadIdx.x % 32 / PARTS * PARTS + PARTS - 1;
     q.A = __shfl_sync(ALL, q.A, last);
     q.B = __shfl_sync(ALL, q.B, last);
-    q.r = __shfl_sync(ALL, q.r, last);
     return q;
 }
 // The states that enter the warps, from the one that enters the tile.
@@ -574,66 +494,61 @@ __device__ __forceinline__ void spread(float (&to)[S::WARPS][ROW], const Run &q,
 {
     const int c = threadIdx.x % S::THREADS / S::PARTS, part = threadIdx.x % S::PARTS;
     const int w0 = BACK ? S::WARPS - 1 - 2 * part : 2 * part, w1 = BACK ? w0 - 1 : w0 + 1;
-    const float in = through(q.eA, q.eB, q.er, s);
+    const float in = fmaf(q.eA, s, q.eB);
     to[w0][c] = in;
-    to[w1][c] = through(q.A0, q.B0, q.r0, in);
-}
-
-// The state that enters the unit at channel c: the maps of the row's segments
-// before it, in their order.
-__device__ __forceinline__ float entering(const Plan &k, int64_t C, int64_t c, int row, int segment)
-{
-    const float2 *m = k.maps + (int64_t)row * k.segments * C + c;
-    float s = 0.f;
-    constexpr int BATCH = 8;
-    for (int i = 0; i < segment; i += BATCH) {
-        float2 v[BATCH];
-#pragma unroll
-        for (int u = 0; u < BATCH; ++u)
-            v[u] = i + u < segment ? m[(i + u) * C] : make_float2(1.f, 0.f);
-#pragma unroll
-        for (int u = 0; u < BATCH; ++u)
-            s = through(v[u].x, v[u].y, v[u].x < 0.f, s);
-    }
-    return s;
+    to[w1][c] = fmaf(q.A0, in, q.B0);
 }
 
 // What the PARTS lanes of a channel carry from tile to tile: the state, or in the
-// first pass the map from the unit's start.
+// first pass the map from the unit's start (which for a sequence's first segment
+// is the state as well).
 struct Carry {
-    float s, A, B;
-    int r;
+    float s, A;
 };
-// The unit's first tile: what it starts from.
-__device__ __forceinline__ void start(const Plan &k, const Item &it, int64_t C, unsigned c,
-                                      Carry *x)
+// The unit's first tile: what it starts from; init: the sequence's.
+__device__ __forceinline__ void start(const Plan &k, const Item &it, const float *init, int64_t C,
+                                      int64_t c, Carry *x)
 {
-    if (k.map) {
-        x->A = 1.f;
-        x->B = 0.f;
-        x->r = 0;
-    } else {
-        x->s = it.segment && c < C ? entering(k, C, c, it.unit_row, it.segment) : 0.f;
+    const bool on = c < C;
+    if (it.segment == 0) {
+        x->s = init && on ? init[it.seq * C + c] : 0.f;
+        x->A = -1.f;
+        return;
+    }
+    x->s = 0.f;
+    x->A = 1.f;
+    if (k.map || !on)
+        return;
+    const float2 *m = k.maps + (int64_t)it.seq * k.segments * C + c;
+    constexpr int BATCH = 8;
+    for (int i = 0; i < it.segment; i += BATCH) {
+        float2 v[BATCH];
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u)
+            v[u] = i + u < it.segment ? m[(i + u) * C] : make_float2(1.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u)
+            x->s = v[u].x < 0.f ? v[u].y : fmaf(v[u].x, x->s, v[u].y);
     }
 }
 // The tile's map is known: hands the state that enters it to the warps and steps
-// over the tile.
+// over the tile; after the unit's last tile the segment's map, after the chain's
+// last tile its state.
 template <class S, bool BACK>
 __device__ __forceinline__ void step(const Plan &k, const Item &it, Maps<S, BACK> &maps, int64_t C,
-                                     unsigned c, Carry *x)
+                                     int64_t c, float *fin, Carry *x)
 {
-    const Run q = run_of<S, BACK>(maps.A, maps.B, maps.reset);
-    if (k.map) {
-        x->B = through(q.A, q.B, q.r, x->B);
-        x->A = times(q.A, x->A);
-        x->r |= q.r;
-        if (it.end && threadIdx.x % S::PARTS == 0 && c < C)
-            k.maps[((int64_t)it.unit_row * k.segments + it.segment) * C + c] =
-                make_float2(x->r ? -1.f : x->A, x->B);
-    } else {
+    const Run q = run_of<S, BACK>(maps.A, maps.B);
+    const bool speaks = threadIdx.x % S::PARTS == 0 && c < C;
+    if (!k.map)
         spread<S, BACK>(maps.S_, q, x->s);
-        x->s = through(q.A, q.B, q.r, x->s);
-    }
+    x->s = fmaf(q.A, x->s, q.B);
+    if (x->A >= 0.f)
+        x->A = times(q.A, x->A);
+    if (k.map && it.end && speaks)
+        k.maps[((int64_t)it.seq * k.segments + it.segment) * C + c] = make_float2(x->A, x->s);
+    if (!k.map && (BACK ? it.first : it.last) && fin && speaks)
+        fin[it.seq * C + c] = x->s;
 }
 
 // ---- the ring ---------------------------------------------------------------
@@ -659,7 +574,7 @@ __device__ __forceinline__ bool stage_wait(uint64_t *bar, unsigned parity)
     return true;
 }
 
-// Bytes from a row to the next position's row (Plan::small).
+// Bytes from a token's row to the next processed token's (Plan::small).
 template <typename T> __device__ __forceinline__ int step_of(const ScanArgs &a, int64_t st)
 {
     const int b = (int)st * (int)sizeof(T);
@@ -681,11 +596,11 @@ __device__ __forceinline__ void expect(uint64_t *bar, unsigned bytes)
 // A feeding lane copies token i's row of the tile, of one tensor: one copy, or
 // one for each head where the heads are apart.
 template <typename T>
-__device__ __forceinline__ void copy_row(const ScanArgs &a, const Tok &x, const Item &it,
-                                             int2 at, bool flat, unsigned C, int row,
-                                         uint8_t *to, uint64_t *full)
+__device__ __forceinline__ void copy_row(const ScanArgs &a, const Tok &x, const Item &it, int t,
+                                         bool flat, unsigned C, int row, uint8_t *to,
+                                         uint64_t *full)
 {
-    const T *q = static_cast<const T *>(x.p) + at.x * x.sb + at.y * x.st;
+    const T *q = static_cast<const T *>(x.p) + it.b * x.sb + t * x.st;
     const unsigned end = min(it.c0 + CT, C);
     uint32_t dst = sm100::smem_u32(to) + row * CT * (unsigned)sizeof(T);
     for (unsigned c = it.c0; c < end;) {
@@ -706,11 +621,11 @@ struct Boxes {
     CUtensorMap x, g, d;
 };
 
-// The feeding warps: FLIP (reverse): the tile's last position is its first row.
+// The feeding warps: FLIP (reverse): the tile's last token is its first row.
 template <class S, bool BACK, typename T, typename TG, bool VEC, bool FLIP>
 __device__ __forceinline__ void feed(const ScanArgs &a, const Plan &k, const Boxes &boxes,
                                      Shared<S, BACK, Stage<BACK, T, TG>::NS> &sm, uint8_t *ring,
-                                     unsigned C, int64_t P)
+                                     unsigned C)
 {
     using St = Stage<BACK, T, TG>;
     const Team<FEEDERS> team{15};
@@ -723,7 +638,7 @@ __device__ __forceinline__ void feed(const ScanArgs &a, const Plan &k, const Box
     unsigned ended = 0;          // bit i: team i has been told so
     for (unsigned n = 0; ended != (1u << S::TEAMS) - 1; ++n) {   // every team's n-th tile
         if (w == 0 && lane < S::TEAMS)
-            sm.taken[n & 1][lane] = next_item<BACK>(a, k, P, &walk);
+            sm.taken[n & 1][lane] = next_item<BACK>(a, k, &walk);
         team.sync();
         for (int i = 0; i < S::TEAMS; ++i) {
             if (ended >> i & 1)
@@ -747,27 +662,21 @@ __device__ __forceinline__ void feed(const ScanArgs &a, const Plan &k, const Box
             } else {
                 ++q;
                 uint8_t *to = ring + st * St::BYTES;
-                if (!VEC || !it.whole)
-                    look_up(a, sm.tk[st], P, it.p0, it.count, w);
                 const int t = threadIdx.x - 512;   // the lane's token
                 // the bytes are announced first: they may land before the arrival
-                if (VEC && k.boxed && it.straight) {
+                if (VEC && k.boxed) {
                     if (t == 0) {
                         const int h = k.flat ? 0 : it.c0 / a.D, c = it.c0 - h * a.D;
-                        const int t0 = FLIP ? it.at.y - (SCAN_TILE - 1) : it.at.y;
+                        const int t0 = FLIP ? it.t - (SCAN_TILE - 1) : it.t;
                         expect(full, St::BYTES - (needs_x ? 0 : St::X));
                         if (needs_x)
-                            sm100::tma_load_4d(to, &boxes.x, full, c, h, t0, it.at.x);
-                        sm100::tma_load_4d(to + St::X, &boxes.g, full, c, h, t0, it.at.x);
+                            sm100::tma_load_4d(to, &boxes.x, full, c, h, t0, it.b);
+                        sm100::tma_load_4d(to + St::X, &boxes.g, full, c, h, t0, it.b);
                         if (BACK)
-                            sm100::tma_load_4d(to + St::X + St::G, &boxes.d, full, c, h, t0,
-                                               it.at.x);
+                            sm100::tma_load_4d(to + St::X + St::G, &boxes.d, full, c, h, t0, it.b);
                     }
                 } else if (VEC && t < it.count) {
-                    int2 at = make_int2(it.at.x, it.at.y + (FLIP ? -t : t));
-                    if (!it.whole)
-                        at = sm.tk[st].at[t];
-                    const int row = FLIP ? SCAN_TILE - 1 - t : t;
+                    const int row = FLIP ? SCAN_TILE - 1 - t : t, at = it.t + (FLIP ? -t : t);
                     const int per = (int)(sizeof(TG) + (needs_x ? sizeof(T) : 0) +
                                           (BACK ? sizeof(T) : 0));
                     expect(full, (min(it.c0 + CT, C) - it.c0) * per);
@@ -785,43 +694,6 @@ __device__ __forceinline__ void feed(const ScanArgs &a, const Plan &k, const Box
     // copies under way end before the CTA does: every one is waited for by the
     // team that it is for, unless a wait ran out, long after they have landed
 }
-
-// What a thread of a team knows of its tile.
-template <bool VEC> struct Mine {
-    unsigned on;             // bit v: channel v is there
-    int count;               // tokens of the thread's group
-    unsigned starts, ends;   // bit e: token e is its sequence's first, last
-    bool plain;              // all tokens, neighbours in one row, no first or last among them
-    int2 at;                 // plain: the group's first token
-    template <int L>
-    __device__ static Mine of(const ScanArgs &a, const Plan &k, const Item &it, const Tokens &tk,
-                              unsigned C, int lane, int slot)
-    {
-        Mine t;
-        t.on = present<VEC>(it.c0, lane, C);
-        t.count = t.on ? max(0, min(L, it.count - slot)) : 0;
-        t.starts = t.ends = 0;
-        t.plain = VEC && it.whole && k.small;
-        t.at = make_int2(it.at.x, it.at.y + (a.reverse ? -slot : slot));
-        if (!VEC || !it.whole) {
-            t.starts = tk.starts[slot / 32] >> slot % 32 & ((1u << L) - 1);
-            t.ends = tk.ends[slot / 32] >> slot % 32 & ((1u << L) - 1);
-            t.plain = VEC && k.small && t.count == L && !(t.starts | t.ends);
-            t.at = tk.at[slot];
-        }
-        if (!t.on)
-            t.plain = false;
-        return t;
-    }
-    // where token e of the group is
-    __device__ int2 where(const ScanArgs &a, const Item &it, const Tokens &tk, int slot,
-                          int e) const
-    {
-        if (VEC && it.whole)
-            return make_int2(at.x, at.y + (a.reverse ? -e : e));
-        return tk.at[slot + e];
-    }
-};
 
 // The thread's values in a stage: token e of the group at [e * pitch].
 template <typename T, bool FLIP>
@@ -869,20 +741,19 @@ __global__ void __launch_bounds__(CTA, 1)
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ Shared<S, false, St::NS> sm;
     const unsigned C = (unsigned)a.H * (unsigned)a.D;
-    const int64_t P = (int64_t)a.B * a.pitch;
     set_up(sm);
     if (threadIdx.x >= 512) {
         fewer_registers();
-        feed<S, false, T, TG, VEC, FLIP>(a, k, boxes, sm, ring, C, P);
+        feed<S, false, T, TG, VEC, FLIP>(a, k, boxes, sm, ring, C);
         return;
     }
     more_registers();
     const int me = threadIdx.x % S::THREADS, lane = me % LANES, slot = me / LANES * L;
-    const int warp = me / 32;
+    const int warp = me / 32, dir = a.reverse ? -1 : 1;
     const bool odd = me & LANES;   // the second group of the warp
     const Team<S::THREADS> team{1 + (int)threadIdx.x / S::THREADS};
     Maps<S, false> &maps = sm.maps[team.id - 1];
-    Carry carry{0.f, 1.f, 0.f, 0};
+    Carry carry{0.f, 1.f};
     for (unsigned n = 0;; ++n) {
         if (!team.all(stage_wait(&sm.full[team.id - 1][n & 1], n / 2 & 1)))
             break;
@@ -890,21 +761,23 @@ __global__ void __launch_bounds__(CTA, 1)
         const int st = it.stage;
         if (st < 0)
             break;
-        const Tokens &tk = sm.tk[st];
         const unsigned c0 = it.c0, ch = c0 + me / PARTS;   // ch: the channel of step
         if (it.begin)
-            start(k, it, C, ch, &carry);
+            start(k, it, a.init, C, ch, &carry);
         uint8_t *tile = ring + st * St::BYTES;
         Four<T> *xs = values<T, FLIP>(tile, lane, slot);
         Four<TG> *gs = values<TG, FLIP>(tile + St::X, lane, slot);
-        const Mine<VEC> t = Mine<VEC>::template of<L>(a, k, it, tk, C, lane, slot);
+        const unsigned on = present<VEC>(c0, lane, C);
+        const int count = on ? max(0, min(L, it.count - slot)) : 0;
+        const bool plain = VEC && k.small && count == L;
+        const int b = it.b, t0 = it.t + dir * slot;   // the group's first token
         if (!VEC) {
-            const Col<T, VEC> x(a.x.p, a.x.sh, a.D, k.flat, c0, lane, t.on);
-            const Col<TG, VEC> g(a.g.p, a.g.sh, a.D, k.flat, c0, lane, t.on);
+            const Col<T, VEC> x(a.x.p, a.x.sh, a.D, k.flat, c0, lane, on);
+            const Col<TG, VEC> g(a.g.p, a.g.sh, a.D, k.flat, c0, lane, on);
 #pragma unroll 4
-            for (int e = 0; e < t.count; ++e) {
-                xs[e * PITCH].set(x.load(x.row(tk.at[slot + e], a.x.sb, a.x.st), t.on));
-                gs[e * PITCH].set(g.load(g.row(tk.at[slot + e], a.g.sb, a.g.st), t.on));
+            for (int e = 0; e < count; ++e) {
+                xs[e * PITCH].set(x.load(x.row(b, t0 + dir * e, a.x.sb, a.x.st), on));
+                gs[e * PITCH].set(g.load(g.row(b, t0 + dir * e, a.g.sb, a.g.st), on));
             }
         }
         // the thread's tokens composed to s -> A s + B.  Their decays are kept
@@ -914,7 +787,7 @@ __global__ void __launch_bounds__(CTA, 1)
         constexpr bool KEEP = sizeof(TG) == 2;
         Four<T> keep[KEEP ? L : 1];
         Val A = val(1.f, 1.f, 1.f, 1.f), B = val(0.f, 0.f, 0.f, 0.f);
-        if (t.plain) {
+        if (plain) {
 #pragma unroll
             for (int e = 0; e < L; ++e) {
                 const Val d = decay(gs[e * PITCH].get());
@@ -931,58 +804,46 @@ __global__ void __launch_bounds__(CTA, 1)
             }
         } else {
 #pragma unroll 1
-            for (int e = 0; e < t.count; ++e) {
-                if (t.starts >> e & 1)   // from here on A is not used
-                    B = get_state<VEC>(a.init, tk.seq[slot + e], C, c0, lane, t.on);
+            for (int e = 0; e < count; ++e) {
                 const Val d = decay(gs[e * PITCH].get());
                 B = fma2(d, B, xs[e * PITCH].get());
                 A = mul2(A, d);
             }
         }
         // the two groups of a warp, then the warps
-        const int r = t.starts != 0, er = __shfl_xor_sync(ALL, r, LANES);
         const Val eA = shuffled(A), eB = shuffled(B);   // the other group's map
         if (odd) {
             put_row<VEC>(maps.A[warp], lane, mul2(A, eA));
-            put_row<VEC>(maps.B[warp], lane, through(A, B, r, eB));
-            if (lane == 0)
-                maps.reset[warp] = r | er;
+            put_row<VEC>(maps.B[warp], lane, fma2(A, eB, B));
         }
         team.sync();
-        if (a.states && !k.map && me % PARTS == 0 && ch < C)
-            a.states[(int64_t)it.tile * C + ch] = carry.s;
-        step<S, false>(k, it, maps, C, ch, &carry);
+        if (a.states && !it.first && !k.map && me % PARTS == 0 && ch < C)
+            a.states[it.block * C + ch] = carry.s;
+        step<S, false>(k, it, maps, C, ch, a.fin, &carry);
         team.sync();
-        if (t.count && !k.map && (a.o.p || a.fin)) {
+        if (count && !k.map && a.o.p) {
             Val s = get_row<VEC>(maps.S_[warp], lane);
             if (odd)
-                s = through(eA, eB, er, s);
-            const Col<T, VEC> o(a.o.p, a.o.sh, a.D, k.flat, c0, lane, t.on);
-            if (t.plain) {
-                if (a.o.p) {   // (no last token is among a plain group's)
-                    T *const row = o.row(t.at, a.o.sb, a.o.st);
-                    const int step = step_of<T>(a, a.o.st);
+                s = fma2(eA, s, eB);
+            const Col<T, VEC> o(a.o.p, a.o.sh, a.D, k.flat, c0, lane, on);
+            if (plain) {
+                T *const row = o.row(b, t0, a.o.sb, a.o.st);
+                const int by = step_of<T>(a, a.o.st);
 #pragma unroll
-                    for (int e = 0; e < L; ++e) {
-                        if constexpr (KEEP)
-                            s = fma2(Val{{reinterpret_cast<unsigned long long *>(xs)[e * PITCH]},
-                                         {reinterpret_cast<unsigned long long *>(gs)[e * PITCH]}},
-                                     s, keep[e].get());
-                        else
-                            s = fma2(gs[e * PITCH].get(), s, xs[e * PITCH].get());
-                        o.store(stepped(row, e, step), t.on, s);
-                    }
+                for (int e = 0; e < L; ++e) {
+                    if constexpr (KEEP)
+                        s = fma2(Val{{reinterpret_cast<unsigned long long *>(xs)[e * PITCH]},
+                                     {reinterpret_cast<unsigned long long *>(gs)[e * PITCH]}},
+                                 s, keep[e].get());
+                    else
+                        s = fma2(gs[e * PITCH].get(), s, xs[e * PITCH].get());
+                    o.store(stepped(row, e, by), on, s);
                 }
             } else {
 #pragma unroll 1
-                for (int e = 0; e < t.count; ++e) {
-                    if (t.starts >> e & 1)
-                        s = get_state<VEC>(a.init, tk.seq[slot + e], C, c0, lane, t.on);
+                for (int e = 0; e < count; ++e) {
                     s = fma2(decay(gs[e * PITCH].get()), s, xs[e * PITCH].get());
-                    if (a.o.p)
-                        o.store(o.row(t.where(a, it, tk, slot, e), a.o.sb, a.o.st), t.on, s);
-                    if (a.fin && (t.ends >> e & 1))
-                        put_state<VEC>(a.fin, tk.seq[slot + e], C, c0, lane, t.on, s);
+                    o.store(o.row(b, t0 + dir * e, a.o.sb, a.o.st), on, s);
                 }
             }
         }
@@ -993,8 +854,8 @@ __global__ void __launch_bounds__(CTA, 1)
 }
 
 // ---- backward -----------------------------------------------------------------
-// The chain runs from the last position to the first; s_{t-1} comes from the
-// states that entered the tiles in the forward.
+// The chain runs from the last token to the first; s_{t-1} comes from the states
+// that entered the tiles in the forward.
 
 template <typename T, typename TG, bool VEC, bool FLIP>
 __global__ void __launch_bounds__(CTA, 1)
@@ -1006,20 +867,19 @@ __global__ void __launch_bounds__(CTA, 1)
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ Shared<S, true, St::NS> sm;
     const unsigned C = (unsigned)a.H * (unsigned)a.D;
-    const int64_t P = (int64_t)a.B * a.pitch;
     set_up(sm);
     if (threadIdx.x >= 512) {
         fewer_registers();
-        feed<S, true, T, TG, VEC, FLIP>(a, k, boxes, sm, ring, C, P);
+        feed<S, true, T, TG, VEC, FLIP>(a, k, boxes, sm, ring, C);
         return;
     }
     more_registers();
     const int me = threadIdx.x % S::THREADS, lane = me % LANES, slot = me / LANES * L;
-    const int warp = me / 32;
+    const int warp = me / 32, dir = a.reverse ? -1 : 1;
     const bool odd = me & LANES;
     const Team<S::THREADS> team{1 + (int)threadIdx.x / S::THREADS};
     Maps<S, true> &maps = sm.maps[team.id - 1];
-    Carry carry{0.f, 1.f, 0.f, 0};
+    Carry carry{0.f, 1.f};
     for (unsigned n = 0;; ++n) {
         if (!team.all(stage_wait(&sm.full[team.id - 1][n & 1], n / 2 & 1)))
             break;
@@ -1027,131 +887,99 @@ __global__ void __launch_bounds__(CTA, 1)
         const int st = it.stage;
         if (st < 0)
             break;
-        const Tokens &tk = sm.tk[st];
         const unsigned c0 = it.c0, ch = c0 + me / PARTS;   // ch: the channel of step
         if (it.begin)
-            start(k, it, C, ch, &carry);
+            start(k, it, a.dfin, C, ch, &carry);
         uint8_t *tile = ring + st * St::BYTES;
         Four<T> *xs = values<T, FLIP>(tile, lane, slot);
         Four<TG> *gs = values<TG, FLIP>(tile + St::X, lane, slot);
         Four<T> *ds = values<T, FLIP>(tile + St::X + St::G, lane, slot);
         // the forward state that enters the tile
         float fs = 0.f;
-        if (!k.map && it.first < it.p0 && ch < C)
-            fs = a.states[(int64_t)it.tile * C + ch];
-        const Mine<VEC> t = Mine<VEC>::template of<L>(a, k, it, tk, C, lane, slot);
+        if (!k.map && ch < C) {
+            if (!it.first)
+                fs = a.states[it.block * C + ch];
+            else if (a.init)
+                fs = a.init[(int64_t)it.seq * C + ch];
+        }
+        const unsigned on = present<VEC>(c0, lane, C);
+        const int count = on ? max(0, min(L, it.count - slot)) : 0;
+        const bool plain = VEC && k.small && count == L;
+        const int b = it.b, t0 = it.t + dir * slot;   // the group's first token
         if (!VEC) {
-            const Col<T, VEC> xc(a.x.p, a.x.sh, a.D, k.flat, c0, lane, t.on);
-            const Col<T, VEC> dc(a.d_o.p, a.d_o.sh, a.D, k.flat, c0, lane, t.on);
-            const Col<TG, VEC> gc(a.g.p, a.g.sh, a.D, k.flat, c0, lane, t.on);
+            const Col<T, VEC> xc(a.x.p, a.x.sh, a.D, k.flat, c0, lane, on);
+            const Col<T, VEC> dc(a.d_o.p, a.d_o.sh, a.D, k.flat, c0, lane, on);
+            const Col<TG, VEC> gc(a.g.p, a.g.sh, a.D, k.flat, c0, lane, on);
 #pragma unroll 4
-            for (int e = 0; e < t.count; ++e) {
-                const int2 at = tk.at[slot + e];
-                xs[e * PITCH].set(xc.load(xc.row(at, a.x.sb, a.x.st), t.on));
-                gs[e * PITCH].set(gc.load(gc.row(at, a.g.sb, a.g.st), t.on));
-                ds[e * PITCH].set(dc.load(dc.row(at, a.d_o.sb, a.d_o.st), t.on));
+            for (int e = 0; e < count; ++e) {
+                const int t = t0 + dir * e;
+                xs[e * PITCH].set(xc.load(xc.row(b, t, a.x.sb, a.x.st), on));
+                gs[e * PITCH].set(gc.load(gc.row(b, t, a.g.sb, a.g.st), on));
+                ds[e * PITCH].set(dc.load(dc.row(b, t, a.d_o.sb, a.d_o.st), on));
             }
         }
         // the thread's maps of the forward chain (A, fB) and of the backward
-        // chain (A, B): the same decays, one product
+        // chain (A, B): the same decays, one product.  B from the first token
+        // on: K = A K' + B with A = d_0 .. d_e, B = sum_i d_0 .. d_i do_i
         Val d[L], A = val(1.f, 1.f, 1.f, 1.f), B = val(0.f, 0.f, 0.f, 0.f), fB = B;
-        if (t.plain) {
 #pragma unroll
-            for (int e = 0; e < L; ++e) {
-                // B from the first token on: K = A K' + B with A = d_0 .. d_e,
-                // B = sum_i d_0 .. d_i do_i
+        for (int e = 0; e < L; ++e) {
+            if (e < count) {
                 d[e] = decay(gs[e * PITCH].get());
                 fB = fma2(d[e], fB, xs[e * PITCH].get());
                 A = mul2(A, d[e]);
                 B = fma2(A, ds[e * PITCH].get(), B);
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < L; ++e) {
-                if (e < t.count) {
-                    if (t.starts >> e & 1)
-                        fB = get_state<VEC>(a.init, tk.seq[slot + e], C, c0, lane, t.on);
-                    d[e] = decay(gs[e * PITCH].get());
-                    fB = fma2(d[e], fB, xs[e * PITCH].get());
-                    A = mul2(A, d[e]);
-                }
-            }
-#pragma unroll
-            for (int e = L - 1; e >= 0; --e) {
-                if (e < t.count) {
-                    if (t.ends >> e & 1)
-                        B = get_state<VEC>(a.dfin, tk.seq[slot + e], C, c0, lane, t.on);
-                    B = mul2(d[e], add2(ds[e * PITCH].get(), B));
-                }
-            }
         }
         // the other group's maps: the even group's forward one for the odd, the
         // odd group's backward one for the even
-        const int fr = t.starts != 0, r = t.ends != 0;
-        const int orr = __shfl_xor_sync(ALL, odd ? r : fr, LANES);
         const Val oA = shuffled(A), oB = shuffled(odd ? B : fB);
         if (odd) {
-            put_row<VEC>(maps.fB[warp], lane, through(A, fB, fr, oB));
-            if (lane == 0)
-                maps.freset[warp] = fr | orr;
+            put_row<VEC>(maps.fB[warp], lane, fma2(A, oB, fB));
         } else {
             put_row<VEC>(maps.A[warp], lane, mul2(A, oA));
-            put_row<VEC>(maps.B[warp], lane, through(A, B, r, oB));
-            if (lane == 0)
-                maps.reset[warp] = r | orr;
+            put_row<VEC>(maps.B[warp], lane, fma2(A, oB, B));
         }
         team.sync();
         if (!k.map)
-            spread<S, false>(maps.fS, run_of<S, false>(maps.A, maps.fB, maps.freset), fs);
-        step<S, true>(k, it, maps, C, ch, &carry);
+            spread<S, false>(maps.fS, run_of<S, false>(maps.A, maps.fB), fs);
+        step<S, true>(k, it, maps, C, ch, a.dinit, &carry);
         team.sync();
-        if (t.count && !k.map) {
+        if (count && !k.map) {
             Val s = get_row<VEC>(maps.fS[warp], lane), K = get_row<VEC>(maps.S_[warp], lane);
             if (odd)
-                s = through(oA, oB, orr, s);
+                s = fma2(oA, s, oB);
             else
-                K = through(oA, oB, orr, K);
-            const Col<T, VEC> dx(a.dx.p, a.dx.sh, a.D, k.flat, c0, lane, t.on);
-            const Col<TG, VEC> dg(a.dg.p, a.dg.sh, a.D, k.flat, c0, lane, t.on);
+                K = fma2(oA, K, oB);
+            const Col<T, VEC> dx(a.dx.p, a.dx.sh, a.D, k.flat, c0, lane, on);
+            const Col<TG, VEC> dg(a.dg.p, a.dg.sh, a.D, k.flat, c0, lane, on);
             Val x[L];   // the states before the thread's tokens
-            if (t.plain) {
 #pragma unroll
-                for (int e = 0; e < L; ++e) {
+            for (int e = 0; e < L; ++e) {
+                if (e < count) {
                     x[e] = s;
                     s = fma2(d[e], s, xs[e * PITCH].get());
                 }
-                T *const xr = dx.row(t.at, a.dx.sb, a.dx.st);
-                TG *const gr = dg.row(t.at, a.dg.sb, a.dg.st);
+            }
+            T *const xr = dx.row(b, t0, a.dx.sb, a.dx.st);
+            TG *const gr = dg.row(b, t0, a.dg.sb, a.dg.st);
+            if (plain) {
                 const int xd = step_of<T>(a, a.dx.st), gd = step_of<TG>(a, a.dg.st);
 #pragma unroll
                 for (int e = L - 1; e >= 0; --e) {
                     const Val G = add2(ds[e * PITCH].get(), K);
                     K = mul2(d[e], G);
-                    dx.store(stepped(xr, e, xd), t.on, G);
-                    dg.store(stepped(gr, e, gd), t.on, mul2(K, x[e]));
+                    dx.store(stepped(xr, e, xd), on, G);
+                    dg.store(stepped(gr, e, gd), on, mul2(K, x[e]));
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < L; ++e) {
-                    if (e < t.count) {
-                        if (t.starts >> e & 1)
-                            s = get_state<VEC>(a.init, tk.seq[slot + e], C, c0, lane, t.on);
-                        x[e] = s;
-                        s = fma2(d[e], s, xs[e * PITCH].get());
-                    }
-                }
-#pragma unroll
                 for (int e = L - 1; e >= 0; --e) {
-                    if (e < t.count) {
-                        if (t.ends >> e & 1)
-                            K = get_state<VEC>(a.dfin, tk.seq[slot + e], C, c0, lane, t.on);
+                    if (e < count) {
                         const Val G = add2(ds[e * PITCH].get(), K);
                         K = mul2(d[e], G);
-                        const int2 at = t.where(a, it, tk, slot, e);
-                        dx.store(dx.row(at, a.dx.sb, a.dx.st), t.on, G);
-                        dg.store(dg.row(at, a.dg.sb, a.dg.st), t.on, mul2(K, x[e]));
-                        if (a.dinit && (t.starts >> e & 1))
-                            put_state<VEC>(a.dinit, tk.seq[slot + e], C, c0, lane, t.on, K);
+                        dx.store(xr + dir * e * a.dx.st, on, G);
+                        dg.store(gr + dir * e * a.dg.st, on, mul2(K, x[e]));
                     }
                 }
             }
@@ -1159,6 +987,104 @@ __global__ void __launch_bounds__(CTA, 1)
         sm100::mbar_arrive(&sm.empty[st]);
         sm100::mbar_arrive(&sm.done[team.id - 1][n & 1]);
     }
+}
+
+// ---- serial ---------------------------------------------------------------------
+// A thread takes four channels of a sequence and walks it alone, SCAN_BLOCK
+// tokens at a time, whose loads are under way together.
+
+template <typename T, typename TG, bool VEC>
+__global__ void __launch_bounds__(128) scan_fwd_serial(const ScanArgs a, int flat)
+{
+    const unsigned C = (unsigned)a.H * (unsigned)a.D, quads = (C + V - 1) / V;
+    const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    if (i >= (int64_t)a.N * quads)
+        return;
+    const int n = (int)(i / quads), dir = a.reverse ? -1 : 1;
+    const unsigned c0 = (unsigned)(i - (int64_t)n * quads) * V;
+    const Row w = row_of<SCAN_BLOCK>(a, n);
+    const unsigned on = (1u << min(C - c0, (unsigned)V)) - 1;
+    const Col<T, VEC> x(a.x.p, a.x.sh, a.D, flat, c0, on), o(a.o.p, a.o.sh, a.D, flat, c0, on);
+    const Col<TG, VEC> g(a.g.p, a.g.sh, a.D, flat, c0, on);
+    Val s = get_state(a.init, n, C, c0, on);
+    const int t0 = w.bos + (a.reverse ? w.len - 1 : 0);
+    for (int p = 0; p < w.len; p += SCAN_BLOCK) {
+        Four<T> xr[SCAN_BLOCK];
+        Four<TG> gr[SCAN_BLOCK];
+#pragma unroll
+        for (int e = 0; e < SCAN_BLOCK; ++e) {
+            if (p + e < w.len) {
+                const int t = t0 + dir * (p + e);
+                xr[e] = x.four(x.row(w.b, t, a.x.sb, a.x.st), on);
+                gr[e] = g.four(g.row(w.b, t, a.g.sb, a.g.st), on);
+            }
+        }
+        if (a.states && p)
+            put_state(a.states, w.block + p / SCAN_BLOCK, C, c0, on, s);
+#pragma unroll
+        for (int e = 0; e < SCAN_BLOCK; ++e) {
+            if (p + e < w.len) {
+                s = fma2(decay(gr[e].get()), s, xr[e].get());
+                if (a.o.p)
+                    o.store(o.row(w.b, t0 + dir * (p + e), a.o.sb, a.o.st), on, s);
+            }
+        }
+    }
+    if (a.fin)
+        put_state(a.fin, n, C, c0, on, s);
+}
+
+template <typename T, typename TG, bool VEC>
+__global__ void __launch_bounds__(128) scan_bwd_serial(const ScanArgs a, int flat)
+{
+    const unsigned C = (unsigned)a.H * (unsigned)a.D, quads = (C + V - 1) / V;
+    const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    if (i >= (int64_t)a.N * quads)
+        return;
+    const int n = (int)(i / quads), dir = a.reverse ? -1 : 1;
+    const unsigned c0 = (unsigned)(i - (int64_t)n * quads) * V;
+    const Row w = row_of<SCAN_BLOCK>(a, n);
+    const unsigned on = (1u << min(C - c0, (unsigned)V)) - 1;
+    const Col<T, VEC> x(a.x.p, a.x.sh, a.D, flat, c0, on), d(a.d_o.p, a.d_o.sh, a.D, flat, c0, on);
+    const Col<T, VEC> dx(a.dx.p, a.dx.sh, a.D, flat, c0, on);
+    const Col<TG, VEC> g(a.g.p, a.g.sh, a.D, flat, c0, on), dg(a.dg.p, a.dg.sh, a.D, flat, c0, on);
+    Val K = get_state(a.dfin, n, C, c0, on);
+    const int t0 = w.bos + (a.reverse ? w.len - 1 : 0);
+    for (int p = (w.len - 1) / SCAN_BLOCK * SCAN_BLOCK; p >= 0 && w.len > 0; p -= SCAN_BLOCK) {
+        Val dec[SCAN_BLOCK], prev[SCAN_BLOCK], grad[SCAN_BLOCK];
+#pragma unroll
+        for (int e = 0; e < SCAN_BLOCK; ++e) {
+            if (p + e < w.len) {
+                const int t = t0 + dir * (p + e);
+                prev[e] = x.four(x.row(w.b, t, a.x.sb, a.x.st), on).get();
+                dec[e] = g.four(g.row(w.b, t, a.g.sb, a.g.st), on).get();
+                grad[e] = d.four(d.row(w.b, t, a.d_o.sb, a.d_o.st), on).get();
+            }
+        }
+        Val s = p ? get_state(a.states, w.block + p / SCAN_BLOCK, C, c0, on)
+                  : get_state(a.init, n, C, c0, on);
+#pragma unroll
+        for (int e = 0; e < SCAN_BLOCK; ++e) {
+            if (p + e < w.len) {
+                dec[e] = decay(dec[e]);
+                const Val y = fma2(dec[e], s, prev[e]);
+                prev[e] = s;
+                s = y;
+            }
+        }
+#pragma unroll
+        for (int e = SCAN_BLOCK - 1; e >= 0; --e) {
+            if (p + e < w.len) {
+                const int t = t0 + dir * (p + e);
+                const Val G = add2(grad[e], K);
+                K = mul2(dec[e], G);
+                dx.store(dx.row(w.b, t, a.dx.sb, a.dx.st), on, G);
+                dg.store(dg.row(w.b, t, a.dg.sb, a.dg.st), on, mul2(K, prev[e]));
+            }
+        }
+    }
+    if (a.dinit)
+        put_state(a.dinit, n, C, c0, on, K);
 }
 
 // Sequences without tokens: their state (or its gradient) passes through.
@@ -1189,17 +1115,19 @@ bool wide(const void *p, int64_t sb, int64_t st, int64_t sh, int bf16)
 bool wide(const Tok &t, int bf16) { return wide(t.p, t.sb, t.st, t.sh, bf16); }
 bool wide(const TokOut &t, int bf16) { return wide(t.p, t.sb, t.st, t.sh, bf16); }
 
-// Batch rows that are long get tiles of their own (their last one is not full):
-// then no tile lies in two rows, and the rows' chains proceed side by side
-// instead of one after the other (b4 h32 n8192 forward: 226 -> 160 us).  Short
-// rows share tiles.
-bool own_tiles(int B, int T) { return B > 1 && T >= 4 * SCAN_TILE; }
-
-int64_t tiles_of(int B, int T)
+// Whether a thread walks a sequence alone, by the times that were measured (us):
+// alone 0.25 a token of the longest, teams 2.2 a tile of the 608 at once, both
+// no faster than HBM (64 rows of 16 tokens, 4096 channels, forward: 10 against
+// 19; 4 rows of 100: 27 against 8).  Only where that costs little: ScanArgs::
+// states has a state for each SCAN_BLOCK tokens then.
+bool serial(int64_t tiles, int64_t longest, int64_t tokens, int64_t C)
 {
-    if (own_tiles(B, T))
-        return (int64_t)B * ((T + SCAN_TILE - 1) / SCAN_TILE);
-    return ((int64_t)B * T + SCAN_TILE - 1) / SCAN_TILE;
+    if (longest > 8 * SCAN_TILE)
+        return false;
+    const double hbm = (double)tokens * C * 6 / 5e6;
+    const double alone = 0.25 * longest + hbm;
+    const double teams = 2.0 + std::max(2.2 * tiles * ((C + CT - 1) / CT) / 608, hbm);
+    return alone < teams;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder()
@@ -1272,18 +1200,20 @@ cudaError_t run(const ScanArgs &a, Plan k, void *ws, cudaStream_t s)
     cudaError_t e = sms_for<BACK, T, TG, VEC, FLIP>(kernel, &sms);
     if (e != cudaSuccess)
         return e;
-    // Segments where the chains (rows x parts of the channels) are fewer than
-    // a third of the teams: as many as there are teams for, unless the maps
+    // Segments where the chains (sequences x parts of the channels) are fewer
+    // than a third of the teams: as many as there are teams for, unless the maps
     // that a segment starts from cost more than its tiles (0.1 us a map, 4 us a
     // tile for both passes: best at 7 sqrt(run)).
-    const int64_t chains = (int64_t)k.rows * k.parts, slots = (int64_t)sms * teams;
+    const int64_t chains = (int64_t)a.N * k.parts;
+    const int64_t slots = std::min<int64_t>((int64_t)sms * teams, MAX_UNITS);
+    const int64_t run = (a.longest + SCAN_TILE - 1) / SCAN_TILE;
     int64_t segments = 1;
     if (chains * 3 <= slots)
-        segments = std::min<int64_t>({slots / chains, (int64_t)k.run,
-                                      (int64_t)(7.0 * std::sqrt((double)k.run)), MAX_SEGMENTS});
-    segments = std::max<int64_t>(segments, 1);
-    k.len = (int)((k.run + segments - 1) / segments);
-    k.segments = (k.run + k.len - 1) / k.len;
+        segments = std::min<int64_t>(
+            {slots / chains, run, (int64_t)(7.0 * std::sqrt((double)run)), MAX_SEGMENTS});
+    k.segments = (int)std::max<int64_t>(segments, 1);
+    if (chains * k.segments > 0x7fffffff)
+        return cudaErrorNotSupported;
     k.units = (int)(chains * k.segments);
     const int grid = (int)std::min<int64_t>(k.units, sms);
     Boxes boxes;
@@ -1303,69 +1233,87 @@ cudaError_t run(const ScanArgs &a, Plan k, void *ws, cudaStream_t s)
     return cudaGetLastError();
 }
 
-template <typename T, typename TG>
-cudaError_t launch(bool back, bool vec, ScanArgs a, void *ws, cudaStream_t s)
+template <bool BACK, typename T, typename TG>
+cudaError_t launch(bool vec, const ScanArgs &a, void *ws, cudaStream_t s)
 {
-    const int64_t C = (int64_t)a.H * a.D, tiles = tiles_of(a.B, a.T);
-    const int64_t parts = (C + CT - 1) / CT;
-    const bool own = own_tiles(a.B, a.T);
-    if (tiles * parts > 0x7fffffff)
-        return cudaErrorNotSupported;
-    a.pitch = own ? (a.T + SCAN_TILE - 1) / SCAN_TILE * SCAN_TILE : a.T;
-    Plan k{};
-    k.rows = own ? a.B : 1;
-    k.run = (int)(tiles / k.rows);
-    k.parts = (int)parts;
-    // (an absent tensor's strides are 0; one head's distance is not used)
-    const int64_t sh[5] = {a.x.sh, a.g.sh, back ? a.d_o.sh : a.D, back ? a.dx.sh : a.D,
-                           back ? a.dg.sh : a.o.p ? a.o.sh : a.D};
+    const int64_t C = (int64_t)a.H * a.D;
+    // (one head's distance is not used)
+    const int64_t sh[5] = {a.x.sh, a.g.sh, BACK ? a.d_o.sh : a.D, BACK ? a.dx.sh : a.D,
+                           BACK ? a.dg.sh : a.o.p ? a.o.sh : a.D};
     const int64_t st[6] = {a.x.st, a.g.st, a.d_o.st, a.dx.st, a.dg.st, a.o.st};
+    Plan k{};
+    k.parts = (int)((C + CT - 1) / CT);
     k.flat = 1;
     for (int64_t v : sh)
         k.flat &= a.H == 1 || v == a.D;
     k.small = 1;
     for (int64_t v : st)
         k.small &= v <= (1 << 24);
+    if (a.serial) {
+        const int64_t ctas = (a.N * ((C + V - 1) / V) + 127) / 128;
+        if (ctas > 0x7fffffff)
+            return cudaErrorNotSupported;
+        if (BACK && vec)
+            scan_bwd_serial<T, TG, true><<<(unsigned)ctas, 128, 0, s>>>(a, k.flat);
+        else if (BACK)
+            scan_bwd_serial<T, TG, false><<<(unsigned)ctas, 128, 0, s>>>(a, k.flat);
+        else if (vec)
+            scan_fwd_serial<T, TG, true><<<(unsigned)ctas, 128, 0, s>>>(a, k.flat);
+        else
+            scan_fwd_serial<T, TG, false><<<(unsigned)ctas, 128, 0, s>>>(a, k.flat);
+        note_launch();
+        return cudaGetLastError();
+    }
     if (!vec)
-        return back ? run<true, T, TG, false, false>(a, k, ws, s)
-                    : run<false, T, TG, false, false>(a, k, ws, s);
-    if (a.reverse)
-        return back ? run<true, T, TG, true, true>(a, k, ws, s)
-                    : run<false, T, TG, true, true>(a, k, ws, s);
-    return back ? run<true, T, TG, true, false>(a, k, ws, s)
-                : run<false, T, TG, true, false>(a, k, ws, s);
+        return run<BACK, T, TG, false, false>(a, k, ws, s);
+    return a.reverse ? run<BACK, T, TG, true, true>(a, k, ws, s)
+                     : run<BACK, T, TG, true, false>(a, k, ws, s);
 }
 
-cudaError_t dispatch(bool back, const ScanArgs &a, bool vec, void *ws, cudaStream_t s)
+template <bool BACK> cudaError_t dispatch(const ScanArgs &a, bool vec, void *ws, cudaStream_t s)
 {
     using bf = __nv_bfloat16;
     if ((int64_t)a.B * a.T == 0)
         return cudaSuccess;
     if (a.bf16 && a.gate_bf16)
-        return launch<bf, bf>(back, vec, a, ws, s);
+        return launch<BACK, bf, bf>(vec, a, ws, s);
     if (a.bf16)
-        return launch<bf, float>(back, vec, a, ws, s);
-    return launch<float, float>(back, vec, a, ws, s);
+        return launch<BACK, bf, float>(vec, a, ws, s);
+    return launch<BACK, float, float>(vec, a, ws, s);
 }
 
 }  // namespace
 
-int64_t scan_tiles(int B, int T) { return tiles_of(B, T); }
-
-size_t scan_link_bytes(int B, int T, int H, int D)
+void scan_plan(ScanArgs *a, int64_t tiles, int64_t longest)
 {
-    // the segments' maps: at most one a tile and MAX_SEGMENTS a row
-    const int64_t tiles = tiles_of(B, T), rows = own_tiles(B, T) ? B : 1;
-    if (tiles == rows)
-        return 0;
-    return (size_t)std::min<int64_t>(tiles, rows * MAX_SEGMENTS) * H * D * sizeof(float2);
+    a->longest = longest;
+    a->serial = serial(tiles, longest, (int64_t)a->B * a->T, (int64_t)a->H * a->D) &&
+                (!a->cu || (int64_t)a->T <= (int64_t)a->N * SCAN_TILE);
 }
+
+size_t scan_states_bytes(int B, int T, int N, int H, int D)
+{
+    const int64_t C = (int64_t)H * D;
+    auto blocks = [&](int64_t rows, int64_t size) { return rows * ((T + size - 1) / size); };
+    // dense: B rows of T tokens
+    const bool alone = serial(blocks(B, SCAN_TILE), T, (int64_t)B * T, C);
+    int64_t n = T <= (alone ? SCAN_BLOCK : SCAN_TILE) ? 0 : blocks(B, alone ? SCAN_BLOCK : SCAN_TILE);
+    // packed: the lengths are not known, so for either kernel
+    if (B == 1 && N > 0) {
+        n = std::max(n, (int64_t)T / SCAN_TILE + N);
+        if ((int64_t)T <= (int64_t)N * SCAN_TILE)
+            n = std::max(n, (int64_t)T / SCAN_BLOCK + N);
+    }
+    return (size_t)n * C * sizeof(float);
+}
+
+size_t scan_maps_bytes(int T) { return T > SCAN_TILE ? (size_t)MAX_UNITS * CT * sizeof(float2) : 0; }
 
 cudaError_t scan_forward(const ScanArgs &a, void *ws, cudaStream_t s)
 {
     const bool vec = a.D % (a.bf16 ? 8 : 4) == 0 && wide(a.x, a.bf16) && wide(a.g, a.gate_bf16) &&
                      (!a.o.p || wide(a.o, a.bf16));
-    cudaError_t e = dispatch(false, a, vec, ws, s);
+    cudaError_t e = dispatch<false>(a, vec, ws, s);
     return e != cudaSuccess ? e : pass_empty(a, a.init, a.fin, s);
 }
 
@@ -1373,7 +1321,7 @@ cudaError_t scan_backward(const ScanArgs &a, void *ws, cudaStream_t s)
 {
     const bool vec = a.D % (a.bf16 ? 8 : 4) == 0 && wide(a.x, a.bf16) && wide(a.g, a.gate_bf16) &&
                      wide(a.d_o, a.bf16) && wide(a.dx, a.bf16) && wide(a.dg, a.gate_bf16);
-    cudaError_t e = dispatch(true, a, vec, ws, s);
+    cudaError_t e = dispatch<true>(a, vec, ws, s);
     return e != cudaSuccess ? e : pass_empty(a, a.dfin, a.dinit, s);
 }
 
