@@ -234,7 +234,7 @@ template <typename T, bool VEC> struct Col {
 #pragma unroll
         for (int v = 0; v < (VEC ? 1 : V); ++v) {
             unsigned c = c0 + local_channel<VEC>(lane, v);
-            c = on >> v & 1 ? c : 0;   // not accessed
+            c = on >> v & 1 ? c : 0;
             const int64_t o = flat ? c : c / D * sh + c % D;
             if constexpr (VEC)
                 q += o;
@@ -703,6 +703,32 @@ __device__ __forceinline__ Four<T> *values(uint8_t *tile, int lane, int slot)
            lane;
 }
 
+// Rows that no wide access fits: the team itself loads them, eight tokens of a
+// thread at a time.  Without conditions (absent channels and tokens are read from
+// another's place), so that the loads are under way together.
+template <int PITCH, typename T>
+__device__ __forceinline__ void fill(Four<T> *to, const Col<T, false> &c, const T *row, int64_t by,
+                                     int count)
+{
+    constexpr int AT = 8;
+#pragma unroll 1
+    for (int e0 = 0; e0 < count; e0 += AT) {
+        T v[AT][V];
+#pragma unroll
+        for (int e = 0; e < AT; ++e) {
+            const T *r = row + min(e0 + e, count - 1) * by;
+#pragma unroll
+            for (int u = 0; u < V; ++u)
+                v[e][u] = r[c.off[u]];
+        }
+#pragma unroll
+        for (int e = 0; e < AT; ++e)
+            if (e0 + e < count)
+                to[(e0 + e) * PITCH].set(val(ldt(&v[e][0]), ldt(&v[e][1]), ldt(&v[e][2]),
+                                             ldt(&v[e][3])));
+    }
+}
+
 template <class S, bool BACK, int NS> __device__ __forceinline__ void set_up(Shared<S, BACK, NS> &sm)
 {
     if (threadIdx.x == 0) {
@@ -769,16 +795,13 @@ __global__ void __launch_bounds__(CTA, 1)
         Four<TG> *gs = values<TG, FLIP>(tile + St::X, lane, slot);
         const unsigned on = present<VEC>(c0, lane, C);
         const int count = on ? max(0, min(L, it.count - slot)) : 0;
-        const bool plain = VEC && k.small && count == L;
+        const bool plain = k.small && count == L;
         const int b = it.b, t0 = it.t + dir * slot;   // the group's first token
-        if (!VEC) {
+        if constexpr (!VEC) {
             const Col<T, VEC> x(a.x.p, a.x.sh, a.D, k.flat, c0, lane, on);
             const Col<TG, VEC> g(a.g.p, a.g.sh, a.D, k.flat, c0, lane, on);
-#pragma unroll 4
-            for (int e = 0; e < count; ++e) {
-                xs[e * PITCH].set(x.load(x.row(b, t0 + dir * e, a.x.sb, a.x.st), on));
-                gs[e * PITCH].set(g.load(g.row(b, t0 + dir * e, a.g.sb, a.g.st), on));
-            }
+            fill<PITCH>(xs, x, x.row(b, t0, a.x.sb, a.x.st), dir * a.x.st, count);
+            fill<PITCH>(gs, g, g.row(b, t0, a.g.sb, a.g.st), dir * a.g.st, count);
         }
         // the thread's tokens composed to s -> A s + B.  Their decays are kept
         // for the second pass, in the stage: the registers for them would cost
@@ -904,19 +927,15 @@ __global__ void __launch_bounds__(CTA, 1)
         }
         const unsigned on = present<VEC>(c0, lane, C);
         const int count = on ? max(0, min(L, it.count - slot)) : 0;
-        const bool plain = VEC && k.small && count == L;
+        const bool plain = k.small && count == L;
         const int b = it.b, t0 = it.t + dir * slot;   // the group's first token
-        if (!VEC) {
+        if constexpr (!VEC) {
             const Col<T, VEC> xc(a.x.p, a.x.sh, a.D, k.flat, c0, lane, on);
             const Col<T, VEC> dc(a.d_o.p, a.d_o.sh, a.D, k.flat, c0, lane, on);
             const Col<TG, VEC> gc(a.g.p, a.g.sh, a.D, k.flat, c0, lane, on);
-#pragma unroll 4
-            for (int e = 0; e < count; ++e) {
-                const int t = t0 + dir * e;
-                xs[e * PITCH].set(xc.load(xc.row(b, t, a.x.sb, a.x.st), on));
-                gs[e * PITCH].set(gc.load(gc.row(b, t, a.g.sb, a.g.st), on));
-                ds[e * PITCH].set(dc.load(dc.row(b, t, a.d_o.sb, a.d_o.st), on));
-            }
+            fill<PITCH>(xs, xc, xc.row(b, t0, a.x.sb, a.x.st), dir * a.x.st, count);
+            fill<PITCH>(gs, gc, gc.row(b, t0, a.g.sb, a.g.st), dir * a.g.st, count);
+            fill<PITCH>(ds, dc, dc.row(b, t0, a.d_o.sb, a.d_o.st), dir * a.d_o.st, count);
         }
         // the thread's maps of the forward chain (A, fB) and of the backward
         // chain (A, B): the same decays, one product.  B from the first token
@@ -1106,15 +1125,6 @@ cudaError_t pass_empty(const ScanArgs &a, const float *from, float *to, cudaStre
     return cudaGetLastError();
 }
 
-// 16-byte aligned rows, channels in whole 16-byte pieces.
-bool wide(const void *p, int64_t sb, int64_t st, int64_t sh, int bf16)
-{
-    const int n = bf16 ? 8 : 4;
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && sb % n == 0 && st % n == 0 && sh % n == 0;
-}
-bool wide(const Tok &t, int bf16) { return wide(t.p, t.sb, t.st, t.sh, bf16); }
-bool wide(const TokOut &t, int bf16) { return wide(t.p, t.sb, t.st, t.sh, bf16); }
-
 // Whether a thread walks a sequence alone, by the times that were measured (us):
 // alone 0.25 a token of the longest, teams 2.2 a tile of the 608 at once, both
 // no faster than HBM (64 rows of 16 tokens, 4096 channels, forward: 10 against
@@ -1233,8 +1243,17 @@ cudaError_t run(const ScanArgs &a, Plan k, void *ws, cudaStream_t s)
     return cudaGetLastError();
 }
 
+// The tensors' rows are in whole 16-byte pieces: wide accesses and copies.  Of
+// tensors whose heads are D apart (flat) all heads' channels are one row.
+template <typename TT> bool wide(const TT &t, int bf16, bool flat, int64_t C, int D)
+{
+    const int n = bf16 ? 8 : 4;
+    return reinterpret_cast<uintptr_t>(t.p) % 16 == 0 && t.sb % n == 0 && t.st % n == 0 &&
+           (flat ? C % n == 0 : D % n == 0 && t.sh % n == 0);
+}
+
 template <bool BACK, typename T, typename TG>
-cudaError_t launch(bool vec, const ScanArgs &a, void *ws, cudaStream_t s)
+cudaError_t launch(const ScanArgs &a, void *ws, cudaStream_t s)
 {
     const int64_t C = (int64_t)a.H * a.D;
     // (one head's distance is not used)
@@ -1249,6 +1268,10 @@ cudaError_t launch(bool vec, const ScanArgs &a, void *ws, cudaStream_t s)
     k.small = 1;
     for (int64_t v : st)
         k.small &= v <= (1 << 24);
+    auto fits = [&](const auto &t, int bf16) { return wide(t, bf16, k.flat, C, a.D); };
+    const bool vec = fits(a.x, a.bf16) && fits(a.g, a.gate_bf16) &&
+                     (BACK ? fits(a.d_o, a.bf16) && fits(a.dx, a.bf16) && fits(a.dg, a.gate_bf16)
+                           : !a.o.p || fits(a.o, a.bf16));
     if (a.serial) {
         const int64_t ctas = (a.N * ((C + V - 1) / V) + 127) / 128;
         if (ctas > 0x7fffffff)
@@ -1270,16 +1293,16 @@ cudaError_t launch(bool vec, const ScanArgs &a, void *ws, cudaStream_t s)
                      : run<BACK, T, TG, true, false>(a, k, ws, s);
 }
 
-template <bool BACK> cudaError_t dispatch(const ScanArgs &a, bool vec, void *ws, cudaStream_t s)
+template <bool BACK> cudaError_t dispatch(const ScanArgs &a, void *ws, cudaStream_t s)
 {
     using bf = __nv_bfloat16;
     if ((int64_t)a.B * a.T == 0)
         return cudaSuccess;
     if (a.bf16 && a.gate_bf16)
-        return launch<BACK, bf, bf>(vec, a, ws, s);
+        return launch<BACK, bf, bf>(a, ws, s);
     if (a.bf16)
-        return launch<BACK, bf, float>(vec, a, ws, s);
-    return launch<BACK, float, float>(vec, a, ws, s);
+        return launch<BACK, bf, float>(a, ws, s);
+    return launch<BACK, float, float>(a, ws, s);
 }
 
 }  // namespace
@@ -1311,17 +1334,13 @@ size_t scan_maps_bytes(int T) { return T > SCAN_TILE ? (size_t)MAX_UNITS * CT * 
 
 cudaError_t scan_forward(const ScanArgs &a, void *ws, cudaStream_t s)
 {
-    const bool vec = a.D % (a.bf16 ? 8 : 4) == 0 && wide(a.x, a.bf16) && wide(a.g, a.gate_bf16) &&
-                     (!a.o.p || wide(a.o, a.bf16));
-    cudaError_t e = dispatch<false>(a, vec, ws, s);
+    cudaError_t e = dispatch<false>(a, ws, s);
     return e != cudaSuccess ? e : pass_empty(a, a.init, a.fin, s);
 }
 
 cudaError_t scan_backward(const ScanArgs &a, void *ws, cudaStream_t s)
 {
-    const bool vec = a.D % (a.bf16 ? 8 : 4) == 0 && wide(a.x, a.bf16) && wide(a.g, a.gate_bf16) &&
-                     wide(a.d_o, a.bf16) && wide(a.dx, a.bf16) && wide(a.dg, a.gate_bf16);
-    cudaError_t e = dispatch<true>(a, vec, ws, s);
+    cudaError_t e = dispatch<true>(a, ws, s);
     return e != cudaSuccess ? e : pass_empty(a, a.dfin, a.dinit, s);
 }
 

@@ -27,13 +27,15 @@ from .api import Tensor, _packed_batch_msg, _state, _traced
 
 # The calls of a decoding step take a few microseconds on the GPU, so what the
 # host does for one counts: structures are packed in one go, pointers are plain
-# integers.
+# integers, the stream is asked for as one (torch.cuda.current_stream makes an
+# object for it: 2 us of a call's 20).
 _ref = ctypes.byref
 _scan_pack = struct.Struct("=6i18q").pack
 _rope_pack = struct.Struct("=12i21q128s").pack
 _scan_dims = N.LaScanDims.from_buffer_copy
 _rope_dims = N.LaRopeDims.from_buffer_copy
-_current_device = torch.cuda.current_device
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 _CODES = {torch.bfloat16: N.LA_DTYPE_BF16, torch.float32: N.LA_DTYPE_F32}
 _NONE3 = (0, 0, 0)
 
@@ -55,11 +57,12 @@ def _strides(t: Optional[Tensor]):
 
 def _call(device, fn, *args) -> None:
     """fn(*args) with `device` current, on its current stream (the last argument)."""
-    if device.index == _current_device():
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if index == _current_device():
+        st = fn(*args, _current_stream(index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            st = fn(*args, _current_stream(index))
     if st:
         N.check(st)
 
@@ -76,18 +79,32 @@ def _token(t: Tensor, name: str, like: Optional[Tensor] = None) -> Tensor:
         raise ValueError("token tensors must be CUDA tensors")
     if like is not None and t.device != like.device:
         raise ValueError("all tensors must be on one device")
-    return t if t.stride(3) == 1 or t.shape[3] == 1 else t.contiguous()
+    return t if t.is_contiguous() or t.stride(3) == 1 or t.shape[3] == 1 else t.contiguous()
 
 
-def _output(t: Optional[Tensor], like: Tensor, name: str, dtype=None) -> Tensor:
+def _new(like: Tensor) -> Tensor:
+    """A dense tensor with the shape and the type of `like`."""
+    if like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+
+
+def _state_of(x: Optional[Tensor], shape, device, name) -> Optional[Tensor]:
+    """_state, without its conversions where x is as the call wants it."""
+    if x is not None and x.dtype is torch.float32 and x.shape == shape and x.device == device \
+            and x.is_contiguous():
+        return x
+    return _state(x, shape, device, name)
+
+
+def _output(t: Optional[Tensor], like: Tensor, name: str) -> Tensor:
     """The caller's output, checked, or a dense new one with the shape of `like`."""
-    dtype = dtype or like.dtype
     if t is None:
-        return torch.empty(like.shape, dtype=dtype, device=like.device)
-    if t.shape != like.shape or t.dtype != dtype or t.device != like.device or \
+        return _new(like)
+    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device or \
             (t.shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError("%s must be a %s tensor of shape %s with contiguous channels on %s"
-                         % (name, dtype, tuple(like.shape), like.device))
+                         % (name, like.dtype, tuple(like.shape), like.device))
     return t
 
 
@@ -197,7 +214,7 @@ class _RopeCall:
         for w in (q_weight, k_weight):
             if w is None:
                 continue
-            if tuple(w.shape) != (D,) or w.device != dev:
+            if w.shape != (D,) or w.device != dev:
                 raise ValueError("weights must be [%d] on %s" % (D, dev))
             if w.dtype != (w_dtype or w.dtype):
                 raise TypeError("the weights must share one dtype")
@@ -295,8 +312,8 @@ def qk_norm_rope_fwd(q: Tensor, k: Optional[Tensor] = None, q_weight: Optional[T
 def _rope_bwd(c: _RopeCall, x, want_weights: bool):
     """Gradients for the call c, whose q and k are the outputs' gradients; x: the inputs."""
     xq, xk = x
-    dq = torch.empty(c.q.shape, dtype=c.q.dtype, device=c.device)
-    dk = torch.empty(c.k.shape, dtype=c.k.dtype, device=c.device) if c.k is not None else None
+    dq = _new(c.q)
+    dk = _new(c.k) if c.k is not None else None
     dqw = dkw = None
     if want_weights:
         dqw = torch.empty_like(c.qw) if c.qw is not None else None
@@ -435,7 +452,7 @@ def _scan_call(x, g, initial_state, cu_seqlens, cu_seqlens_host):
         raise TypeError("g must have x's dtype %s or float32, got %s" % (x.dtype, g.dtype))
     B, T, H, D = x.shape
     cu = _cu(cu_seqlens, cu_seqlens_host, x.device, B)
-    init = _state(initial_state, (cu.n, H, D), x.device, "initial_state")
+    init = _state_of(initial_state, (cu.n, H, D), x.device, "initial_state")
     head = (B, T, H, D, cu.n, _code(g.dtype)) + tuple(_strides(x)) + tuple(_strides(g))
     return x, g, init, cu, head, _code(x.dtype)
 
@@ -448,7 +465,8 @@ def gated_scan_fwd(x: Tensor, g: Tensor, initial_state: Optional[Tensor] = None,
                    keep_states: bool = False):
     """s_t = exp(g_t) s_{t-1} + x_t for every channel of x [B,T,H,D]; g, the log-decay, has x's
     shape and its dtype or fp32.  Returns (o, final_state [N,H,D] fp32), and with
-    keep_states=True (o, final_state, states): what gated_scan_bwd starts from, about 1% of x.
+    keep_states=True (o, final_state, states): what gated_scan_bwd starts from, 4 bytes a
+    channel for every 128 tokens (every 8 where the sequences are short and many).
     final_state may be the initial_state tensor itself.  cu_seqlens, cu_seqlens_host and
     reverse as qk_norm_rope_fwd and la_fwd."""
     x, g, init, cu, head, code = _scan_call(x, g, initial_state, cu_seqlens, cu_seqlens_host)
@@ -492,9 +510,8 @@ def gated_scan_bwd(x: Tensor, g: Tensor, do: Tensor, initial_state: Optional[Ten
     do = _token(do, "do", x)
     if do.shape != x.shape or do.dtype != x.dtype:
         raise ValueError("do must have x's shape and dtype")
-    dfin = _state(d_final_state, (cu.n,) + tuple(x.shape[2:]), dev, "d_final_state")
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dg = torch.empty(x.shape, dtype=g.dtype, device=dev)
+    dfin = _state_of(d_final_state, (cu.n,) + tuple(x.shape[2:]), dev, "d_final_state")
+    dx, dg = _new(x), _new(g)
     dinit = (torch.empty((cu.n,) + tuple(x.shape[2:]), dtype=torch.float32, device=dev)
              if want_d_initial_state else None)
     d = _scan_dims(_scan_pack(*head, *_NONE3, *_strides(do), *_strides(dx), *_strides(dg)))
