@@ -428,7 +428,8 @@ typedef struct la_scan_dims {
  *   final_state    [N,H,D] fp32 output, or NULL; may be initial_state itself
  *   states         fp32 output of la_gated_scan_states_size bytes (16-byte
  *                  aligned), or NULL: the states that la_gated_scan_bwd starts
- *                  from, to be passed to it once or more
+ *                  from, to be passed to it once or more (their number and
+ *                  places go by the sequences' lengths; not all are written)
  *   workspace      256-byte aligned, la_gated_scan_workspace_size(..., 0)
  *                  bytes, or (..., 3) when final_state is initial_state
  *                  (LA_ERR_INVALID_ARG when smaller); the size may be 0 */
@@ -463,8 +464,8 @@ la_status la_gated_scan_bwd(const la_scan_dims *dims, int32_t dtype, const void 
 
 /* Workspace bytes of la_gated_scan_fwd (backward = 0; 3 when final_state is
  * initial_state) or la_gated_scan_bwd (1: states given, 2: not); 0 for invalid
- * sizes.  They do not depend on the
- * packed sequences' lengths.  Pure host function. */
+ * sizes.  They do not depend on the packed sequences' lengths.  Pure host
+ * function. */
 size_t la_gated_scan_workspace_size(const la_scan_dims *dims, int32_t dtype, int32_t backward);
 
 /* Bytes of la_gated_scan_fwd's `states` (0 for invalid sizes, and where the

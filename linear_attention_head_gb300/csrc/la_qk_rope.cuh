@@ -31,8 +31,8 @@ namespace {
 
 constexpr int V = 8;                           // channels per lane
 constexpr int WARPS = 8, THREADS = WARPS * 32;
-// How a kernel rotates: not at all, halves or neighbours (wide accesses, see
-// rope_vec), or as the arguments say, with any alignment.
+// How a kernel rotates: not at all, halves or neighbours (wide accesses: dispatch,
+// below, and rope_run), or as the arguments say, with any alignment.
 enum { NONE, HALVES, NEIGHBOURS, ANY };
 // Loads of a lane under way at once (bf16: 4 x 16 bytes, fp32: 2 x 32), and CTAs
 // an SM, which bound the registers.  60000 tokens of 40 heads of 128, bf16,

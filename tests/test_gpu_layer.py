@@ -4,14 +4,17 @@ backward, each alone and in a run together with the attention.
 
 Tolerances.  An output rounded to its type is off by at most half a step (bf16 2^-8, fp32
 2^-24, relative to the value).  Before it, the recurrence in fp32 makes at most 8 relative
-roundings of 2^-24 a token of the running magnitude: the decay (2: below one unit in the last
-place), the product of decays and the sum of each of the two levels a token passes (its thread's
-tokens, its tile) and the final step (6 together); layer_reference.scan carries them on as the
-recurrence does (the *_e scales).  The rotation: sin and cos within 2^-22 (the angle's
-fraction of a turn rounded to 2^-25 turns is 2 pi 2^-25 < 2^-22 radians, sincospi below two
-units in the last place), the norm's factor within 2^-22 (a sum of up to 256 squares by 8 and
-then pairwise, the root, the quotient: 13 + 2 roundings of 2^-24), three products: together
-below 2^-20 of the pair's magnitude, which the row's largest value times sqrt 2 bounds.
+roundings of u = 2^-24 a token of the running magnitude.  The decay a enters with a times its
+relative error: for |g| < 1/4 below 2 u (a series whose last addition rounds); else 2^x within
+4 u and its argument's rounding, |g| u, so a (4 + |g|) u <= 3.4 u, the most at |g| = 1/4.  The
+token's own sum in each of the two passes over it, the product of decays: 3 u.  The joins of
+16 (or 8) tokens to a thread's map, of those to a tile's and to the state: fewer than 12 for
+those tokens together, below 1.5 u each.  layer_reference.scan carries them on as the
+recurrence does (the *_e scales).  The rotation: sin and cos within 2^-22 (the angle's fraction
+of a turn kept to 2^-32; its remainder as fp32 and the series' last steps 3 u), the norm's
+factor within 2^-22 (a sum of up to 256 squares by 8 and then pairwise, the root, the product:
+13 + 2 roundings of 2^-24), three products: together below 2^-20 of the pair's magnitude, which
+the row's largest value times sqrt 2 bounds.
 """
 import math
 
@@ -97,7 +100,7 @@ def test_scan_dense(B, T, H, D, dt, gt):
 @pytest.mark.parametrize("dt,gt", TYPES)
 @pytest.mark.parametrize("reverse", [False, True])
 def test_scan_long(dt, gt, reverse):
-    # dozens of tiles, far beyond one window of neighbouring tiles
+    # dozens of tiles, in segments: the maps of those before a segment give its state
     x, g, do, init, dfin = _scan_inputs(1, 9001, 1, 8, dt, gt, 1, 3)
     _scan_check(x, g, do, init, dfin, reverse, label="long")
 
@@ -137,6 +140,97 @@ def test_scan_many_short_sequences():
     for t, name, scale in ((o, "o", "o_e"), (fin, "final", "final_e"), (dx, "dx", "dx_e"),
                            (dg, "dg", "dg_e"), (dinit, "dinit", "dinit_e")):
         _close(t, ref[name], SCAN_U * ref[scale], F32, name)
+
+
+@pytest.mark.parametrize("D,dt,gt,reverse", [
+    (3, BF, F32, False), (8, BF, BF, True), (8, F32, F32, False), (3, F32, F32, True)])
+def test_scan_many_sequences_of_some_tokens(D, dt, gt, reverse):
+    # so many that a thread takes a sequence alone, in several blocks of tokens: whole blocks,
+    # a last one of one token, sequences without tokens; dense too
+    lens = [0, 1, 8, 9, 16, 17, 20] * 220
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    x, g, do, init, dfin = _scan_inputs(1, cu[-1], 1, D, dt, gt, len(lens), 21)
+    _scan_check(x, g, do, init, dfin, reverse, cu, label="packed")
+    x, g, do, init, dfin = _scan_inputs(1400, 17, 1, D, dt, gt, 1400, 22, state=not reverse)
+    _scan_check(x, g, do, init, dfin, reverse, label="dense")
+
+
+@pytest.mark.parametrize("B,T,H,D", [
+    (2, 1500, 2, 64), (3, 300, 4, 6), (2, 140, 8, 250), (1, 2500, 1, 200), (2, 400, 3, 33)])
+@pytest.mark.parametrize("dt,gt", TYPES)
+@pytest.mark.parametrize("reverse", [False, True])
+def test_scan_rows_of_all_heads(B, T, H, D, dt, gt, reverse):
+    # heads whose channels are one row together, whatever a head's own width; several rows
+    x, g, do, init, dfin = _scan_inputs(B, T, H, D, dt, gt, B, 23)
+    _scan_check(x, g, do, init, dfin, reverse, label="%s" % ((B, T, H, D),))
+
+
+@pytest.mark.parametrize("dt,gt", [(BF, F32), (F32, F32)])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("D", [64, 72, 192])
+def test_scan_head_major_in_segments(D, dt, gt, reverse):
+    # heads apart, in tiles that are whole heads' parts (64, 192) or cross them (72), packed
+    cu = [0, 700, 701, 2000]
+    x, g, do, init, dfin = _scan_inputs(1, 2000, 2, D, dt, gt, 3, 24)
+    dev = [_relayout(t, "head_major") for t in (x, g, do)] + _cuda(init, dfin)
+    _scan_check(x, g, do, init, dfin, reverse, cu, label="head major", dev=dev)
+
+
+def test_scan_rows_far_apart():
+    # offsets beyond 2^31 elements, between batch rows and between tokens (whose distance is
+    # beyond the steps that fit 32 bits of bytes)
+    x, g, do, init, dfin = _scan_inputs(2, 150, 1, 64, BF, BF, 2, 25)
+    far = 1 << 31
+    big = torch.empty(far + 150 * 64, dtype=BF, device="cuda")
+    xd = big.as_strided((2, 150, 1, 64), (far, 64, 64, 1))
+    xd.copy_(x)
+    _scan_check(x, g, do, init, dfin, label="rows", dev=[xd] + _cuda(g, do, init, dfin))
+    del xd, big
+    step = (1 << 24) + 8
+    big = torch.empty(149 * step + 64, dtype=BF, device="cuda")
+    out = big.as_strided((1, 150, 1, 64), (0, step, 64, 1))
+    for reverse in (False, True):
+        want, _ = la.gated_scan_fwd(x[:1].cuda(), g[:1].cuda(), reverse=reverse)
+        got, _ = la.gated_scan_fwd(x[:1].cuda(), g[:1].cuda(), reverse=reverse, out=out)
+        assert torch.equal(got, want)
+    out.copy_(x[:1])
+    for reverse in (False, True):
+        want, _ = la.gated_scan_fwd(x[:1].cuda(), g[:1].cuda(), reverse=reverse)
+        got, _ = la.gated_scan_fwd(out, g[:1].cuda(), reverse=reverse)
+        assert torch.equal(got, want)
+
+
+def test_scan_and_norms_from_threads():
+    # two host threads, each on its own stream, the same inputs: the results of one alone
+    import threading
+    x, g, do, init, dfin = _cuda(*_scan_inputs(1, 3000, 2, 64, BF, F32, 1, 26))
+    q, k, dq, dk, qw, kw = _cuda(*_rope_inputs(1, 700, 4, 2, 64, BF, 27))
+    rope = la.Rope(la.rope_inv_freq(64))
+
+    def calls():
+        y = la.gated_scan_fwd(x, g, init, keep_states=True)
+        z = la.qk_norm_rope_bwd(q, k, dq, dk, qw, kw, rope=rope)
+        return y + la.gated_scan_bwd(x, g, do, init, dfin, states=y[2])[:2] + z
+    want = calls()
+    torch.cuda.synchronize()
+    got, threads = [None, None], []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got[i] = calls()
+    for i in range(2):
+        threads.append(threading.Thread(target=work, args=(i,)))
+        threads[-1].start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    la.get_device_error()
+    for r in got:
+        # (the states of first tiles are not written)
+        assert all(torch.equal(a, b) for i, (a, b) in enumerate(zip(r, want)) if i != 2)
 
 
 def _relayout(t, kind):
@@ -275,8 +369,8 @@ def test_scan_is_deterministic_and_takes_any_stream():
 
 
 def test_scan_withheld_tile_reports_timeout_and_context_survives():
-    # the first tile does not publish its map: the tiles after it wait, at most two seconds,
-    # and the call reports it; the next call is right
+    # a CTA's first tile is not handed over: its team waits, at most two seconds, and the call
+    # reports it; the next call is right
     import time
     x, g, do, init, dfin = _cuda(*_scan_inputs(1, 6000, 1, 64, BF, BF, 1, 16))
     want = la.gated_scan_fwd(x, g, init) + la.gated_scan_bwd(x, g, do, init, dfin)
@@ -355,8 +449,9 @@ def _rope_check(q, k, dqo, dko, qw, kw, rope, pos, kwargs, normalize=True, eps=1
         size = _row_scale(dy.double()) * wmax * rr * (1 + n * n)
         _close(got[i], grads[0], 4 * ROT_U * size, dt, label + " d" + name)
         if w is not None and normalize:
-            # fp32 sums of every row's term: each term's own roundings, and at most 64 + 24
-            # additions on any path from a term to the sum
+            # fp32 sums of every row's term: each term's own roundings, and at most 88
+            # additions on any path from a term to the sum (a lane's rows: 12, the CTA's lanes:
+            # 32, a slice's CTAs: 4, the slices: 32)
             terms = (_row_scale(dy.double()) * (xr.detach() * rr).abs()).sum((0, 1, 2))
             _close(got[2 + i], grads[1], (ROT_U + 88 * R.U) * terms, w.dtype,
                    label + " d%s_weight" % name)
@@ -508,6 +603,49 @@ def test_norm_rotation_keeps_rows_apart():
         keep[1, 3, 0] = False
         assert torch.equal(g[0][keep], cg[0][keep]) and torch.equal(g[1], cg[1])
         assert torch.equal(g[3], cg[3])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,rot", [(64, 32), (36, 10)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_rotation_leaves_the_other_channels_alone(D, rot, interleaved, dt):
+    # NaN and infinities in rotated channels stay in their pair, so do those of the others
+    q, k, dq, dk, _, _ = _cuda(*_rope_inputs(1, 9, 3, 2, D, dt, 12))
+    rope = la.Rope(la.rope_inv_freq(rot), interleaved=interleaved)
+    for call, x, y in ((la.rotary_fwd, q, k), (la.rotary_bwd, dq, dk)):
+        clean = call(x, y, rope=rope)[0]
+        for c in (0, rot - 1, rot, D - 1):
+            for bad in (float("nan"), float("inf")):
+                z = x.clone()
+                z[0, 4, 1, c] = bad
+                got = call(z, y, rope=rope)[0]
+                keep = torch.ones_like(z, dtype=torch.bool)
+                keep[0, 4, 1, c] = False
+                if c < rot:
+                    keep[0, 4, 1, c ^ 1 if interleaved else (c + rot // 2) % rot] = False
+                assert torch.equal(got[keep], clean[keep]), (c, bad)
+
+
+def test_norm_rotation_rows_far_apart():
+    # offsets beyond 2^31 elements, between batch rows and between heads
+    q, k, dqo, dko, qw, kw = _rope_inputs(2, 6, 2, 2, 64, BF, 13)
+    rope = la.Rope(la.rope_inv_freq(64))
+    far = 1 << 31
+    big = torch.empty(far + 6 * 2 * 64, dtype=BF, device="cuda")
+    args = dict(q_weight=qw.cuda(), k_weight=kw.cuda(), rope=rope)
+    want = la.qk_norm_rope_fwd(q.cuda(), k.cuda(), **args)
+    wantg = la.qk_norm_rope_bwd(q.cuda(), k.cuda(), dqo.cuda(), dko.cuda(), **args)
+    for shape, strides in (((2, 6, 2, 64), (far, 128, 64, 1)), ((2, 6, 2, 64), (384, 64, far, 1))):
+        if strides[2] == far:
+            big = torch.empty(far + 2 * 384, dtype=BF, device="cuda")
+        qd = big.as_strided(shape, strides)
+        qd.copy_(q)
+        got = la.qk_norm_rope_fwd(qd, k.cuda(), **args)
+        gotg = la.qk_norm_rope_bwd(qd, k.cuda(), dqo.cuda(), dko.cuda(), **args)
+        for a, b in zip(got + gotg, want + wantg):
+            assert torch.equal(a, b)
+        got = la.qk_norm_rope_fwd(qd, k.cuda(), out=(qd, None), **args)   # in place
+        assert torch.equal(got[0], want[0]) and torch.equal(qd, want[0])
 
 
 def test_weight_gradients_are_deterministic_and_empty_sums_are_zero():
@@ -728,3 +866,33 @@ def test_decoding_continues_the_prompt():
     got = torch.cat(parts, 1)
     err = float((got.float() - whole.float()).abs().max() / whole.float().abs().max())
     assert err <= 2e-2, err
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_attention_calls_take_norms_and_rotation(gated):
+    # recurrent_gla and lightning_attn with qk_norm= and rope= are the calls on normalised and
+    # rotated inputs, gradients included
+    B, T, H, D = 2, 70, 2, 64
+    gen = torch.Generator().manual_seed(60)
+    r = lambda *s: torch.randn(s, generator=gen).to(BF).cuda()
+    leaves = [r(B, T, H, D).requires_grad_() for _ in range(3)]
+    w = [(1 + 0.1 * r(D)).requires_grad_() for _ in range(2)]
+    gate = torch.nn.functional.logsigmoid(r(B, T, H, D).float() + 2)
+    norm, rope = la.QkNorm(w[0], w[1]), la.Rope(la.rope_inv_freq(D))
+    pos = torch.randint(0, 1000, (B, T), generator=gen).cuda()
+    gg = la.alibi_g_gamma(H)
+
+    def attend(q, k, v, **kw):
+        if gated:
+            return la.recurrent_gla(q, k, v, g=gate, g_gamma=gg, **kw)[0]
+        return la.lightning_attn(q, k, v, 1, 4, **kw)
+    q, k, v = leaves
+    o = attend(q, k, v, qk_norm=norm, rope=rope, positions=pos)
+    q2, k2 = la.qk_norm_rope(q, k, norm, rope, pos)
+    want = attend(q2, k2, v)
+    o, want = (t[0] if isinstance(t, tuple) else t for t in (o, want))
+    assert torch.equal(o, want)
+    do = r(*o.shape)
+    for a, b in zip(torch.autograd.grad(o, leaves + w, do),
+                    torch.autograd.grad(want, leaves + w, do)):
+        assert torch.equal(a, b)

@@ -143,6 +143,27 @@ def test_scan_workspace_is_checked(lib):
     assert lib.la_gated_scan_states_size(ctypes.byref(_scan_dims(D=0))) == 0
 
 
+def test_scan_sizes_of_states_and_workspaces(lib):
+    states = lambda d: lib.la_gated_scan_states_size(ctypes.byref(d))
+    ws = lambda d, mode: lib.la_gated_scan_workspace_size(ctypes.byref(d), 0, mode)
+    row = 3 * 8 * 4
+    # a tile's tokens or fewer: no states; one more, two of them a row (few rows: no threads
+    # of their own); many rows of some tokens: a state for every 8
+    assert states(_scan_dims(B=2, T=128, H=3, D=8)) == 0
+    assert states(_scan_dims(B=2, T=129, H=3, D=8)) == 2 * 2 * row
+    assert states(_scan_dims(B=5000, T=9, H=3, D=8)) == 5000 * 2 * row
+    assert states(_scan_dims(B=5000, T=8, H=3, D=8)) == 0
+    # packed: enough for any lengths, whichever kernels they get
+    for T in (5, 100, 1000, 5000):
+        assert states(_scan_dims(B=1, T=T, H=3, D=8, n=6)) >= (T // 128 + 6) * row
+    assert states(_scan_dims(B=1, T=700, H=3, D=8, n=6)) >= (700 // 8 + 6) * row
+    # in place: a copy of every sequence's initial state besides
+    d = _scan_dims(B=1, T=700, H=3, D=8, n=6)
+    assert ws(d, 3) >= ws(d, 0) + 6 * row
+    assert ws(d, 2) >= ws(d, 1) + states(d)
+    assert ws(_scan_dims(B=4, T=128), 0) == 0
+
+
 def test_empty_scans_enqueue_nothing(lib):
     assert _scan_fwd(lib, _scan_dims(B=0), x=None, o=None) == N.LA_OK
     assert _scan_fwd(lib, _scan_dims(B=1, T=0, n=0), x=None, o=None, cu=FAKE,
