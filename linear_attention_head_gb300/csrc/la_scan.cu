@@ -401,7 +401,8 @@ template <class S, bool BACK, int NS> struct Shared {
 // A team's way through its units: one lane's state.
 struct Walk {
     int unit, step;     // the next unit; units apart
-    int seq, seg, jj, end, run;   // the present one: jj of the chain's order, up to end
+    int seq, seg, run;  // the present one
+    int lo, jj, end;    // its tiles in the chain's order: [lo, end), jj done or next
     unsigned c0;
     Row row;
 };
@@ -415,7 +416,7 @@ __device__ __forceinline__ bool enter_unit(const ScanArgs &a, const Plan &k, Wal
         w->row = row_of<SCAN_TILE>(a, w->seq);
         w->run = (w->row.len + SCAN_TILE - 1) / SCAN_TILE;
         const int len = (w->run + k.segments - 1) / k.segments;
-        w->jj = w->seg * len;
+        w->lo = w->jj = w->seg * len;
         w->end = min(w->jj + len, w->run);
         // (of the last segment nobody needs the map)
         if (w->jj >= w->end || (k.map && w->end == w->run))
@@ -438,7 +439,10 @@ __device__ __forceinline__ Item next_item(const ScanArgs &a, const Plan &k, Walk
         d.begin = 1;
     }
     d.stage = 0;
-    const int j = BACK ? w->run - 1 - w->jj : w->jj, p = j * SCAN_TILE;
+    // the first pass goes through a segment backwards: what it reads last, the
+    // second pass reads first, while L2 still has it
+    const int jj = k.map ? w->lo + w->end - 1 - w->jj : w->jj;
+    const int j = BACK ? w->run - 1 - jj : jj, p = j * SCAN_TILE;
     d.count = min(w->row.len - p, SCAN_TILE);
     d.c0 = w->c0;
     d.seq = w->seq;
@@ -500,8 +504,7 @@ __device__ __forceinline__ void spread(float (&to)[S::WARPS][ROW], const Run &q,
 }
 
 // What the PARTS lanes of a channel carry from tile to tile: the state, or in the
-// first pass the map from the unit's start (which for a sequence's first segment
-// is the state as well).
+// first pass the map (A, s) of the tiles from here to the segment's end.
 struct Carry {
     float s, A;
 };
@@ -509,16 +512,15 @@ struct Carry {
 __device__ __forceinline__ void start(const Plan &k, const Item &it, const float *init, int64_t C,
                                       int64_t c, Carry *x)
 {
-    const bool on = c < C;
-    if (it.segment == 0) {
-        x->s = init && on ? init[it.seq * C + c] : 0.f;
-        x->A = -1.f;
-        return;
-    }
     x->s = 0.f;
     x->A = 1.f;
-    if (k.map || !on)
+    if (k.map || c >= C)
         return;
+    if (it.segment == 0) {
+        if (init)
+            x->s = init[it.seq * C + c];
+        return;
+    }
     const float2 *m = k.maps + (int64_t)it.seq * k.segments * C + c;
     constexpr int BATCH = 8;
     for (int i = 0; i < it.segment; i += BATCH) {
@@ -532,22 +534,29 @@ __device__ __forceinline__ void start(const Plan &k, const Item &it, const float
     }
 }
 // The tile's map is known: hands the state that enters it to the warps and steps
-// over the tile; after the unit's last tile the segment's map, after the chain's
-// last tile its state.
+// over the tile; after the chain's last tile its state.  First pass: takes the
+// tile in front of the map, which it writes after the segment's last tile (for a
+// sequence's first segment the state at its end).
 template <class S, bool BACK>
 __device__ __forceinline__ void step(const Plan &k, const Item &it, Maps<S, BACK> &maps, int64_t C,
-                                     int64_t c, float *fin, Carry *x)
+                                     int64_t c, const float *init, float *fin, Carry *x)
 {
     const Run q = run_of<S, BACK>(maps.A, maps.B);
     const bool speaks = threadIdx.x % S::PARTS == 0 && c < C;
-    if (!k.map)
-        spread<S, BACK>(maps.S_, q, x->s);
+    if (k.map) {
+        x->s = fmaf(x->A, q.B, x->s);
+        x->A = times(x->A, q.A);
+        if (it.end && speaks) {
+            float2 m = make_float2(x->A, x->s);
+            if (it.segment == 0)
+                m = make_float2(-1.f, init ? fmaf(x->A, init[it.seq * C + c], x->s) : x->s);
+            k.maps[((int64_t)it.seq * k.segments + it.segment) * C + c] = m;
+        }
+        return;
+    }
+    spread<S, BACK>(maps.S_, q, x->s);
     x->s = fmaf(q.A, x->s, q.B);
-    if (x->A >= 0.f)
-        x->A = times(q.A, x->A);
-    if (k.map && it.end && speaks)
-        k.maps[((int64_t)it.seq * k.segments + it.segment) * C + c] = make_float2(x->A, x->s);
-    if (!k.map && (BACK ? it.first : it.last) && fin && speaks)
+    if ((BACK ? it.first : it.last) && fin && speaks)
         fin[it.seq * C + c] = x->s;
 }
 
@@ -842,7 +851,7 @@ __global__ void __launch_bounds__(CTA, 1)
         team.sync();
         if (a.states && !it.first && !k.map && me % PARTS == 0 && ch < C)
             a.states[it.block * C + ch] = carry.s;
-        step<S, false>(k, it, maps, C, ch, a.fin, &carry);
+        step<S, false>(k, it, maps, C, ch, a.init, a.fin, &carry);
         team.sync();
         if (count && !k.map && a.o.p) {
             Val s = get_row<VEC>(maps.S_[warp], lane);
@@ -962,7 +971,7 @@ __global__ void __launch_bounds__(CTA, 1)
         team.sync();
         if (!k.map)
             spread<S, false>(maps.fS, run_of<S, false>(maps.A, maps.fB), fs);
-        step<S, true>(k, it, maps, C, ch, a.dinit, &carry);
+        step<S, true>(k, it, maps, C, ch, a.dfin, a.dinit, &carry);
         team.sync();
         if (count && !k.map) {
             Val s = get_row<VEC>(maps.fS[warp], lane), K = get_row<VEC>(maps.S_[warp], lane);
