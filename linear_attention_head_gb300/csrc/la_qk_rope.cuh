@@ -19,6 +19,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -37,8 +38,7 @@ enum { NONE, HALVES, NEIGHBOURS, ANY };
 // Loads of a lane under way at once (bf16: 4 x 16 bytes, fp32: 2 x 32), and CTAs
 // an SM, which bound the registers.  60000 tokens of 40 heads of 128, bf16,
 // forward: 190 us with 4 CTAs, 199 with 3 (HBM's rate: 181); the rotation alone,
-// 32760 tokens of 32 heads: 94 and 85 (79).  Backward with the norms: 336 us with
-// 2 CTAs (272), 395 with half the loads.
+// 32760 tokens of 32 heads: 94 and 85 (79).
 template <typename T, bool VEC> constexpr int rounds_of()
 {
     return !VEC ? 1 : sizeof(T) == 2 ? 4 : 2;
@@ -434,6 +434,19 @@ __device__ __forceinline__ void turn(const RopeArgs &a, int c0, const Vals &p, c
 struct Work {
     int64_t items;
     int blocks, rows;   // blocks of a token, rows of a block
+    // the item's token (batch row, place) and first row
+    __device__ __forceinline__ void at(const RopeArgs &a, int64_t it, int *b, int *t, int *r0) const
+    {
+        const int64_t tok = blocks == 1 ? it : it / blocks;
+        *r0 = (int)(it - tok * blocks) * rows;
+        if (tok <= 0xffffffffll) {
+            *b = (int)((unsigned)tok / (unsigned)a.T);
+            *t = (int)((unsigned)tok - (unsigned)*b * (unsigned)a.T);
+        } else {
+            *b = (int)(tok / a.T);
+            *t = (int)(tok - (int64_t)*b * a.T);
+        }
+    }
 };
 
 // What a lane needs for the rows of one tensor of a token.
@@ -479,17 +492,105 @@ __device__ __forceinline__ Vals one_row(const RopeArgs &a, const Lane &k, const 
     return v;
 }
 
+// bf16's backward with the norms holds too much to have enough loads under way in
+// registers: a warp's rounds are copied to a ring in shared memory, each lane's
+// values to a place of its own, so that nobody else is waited for.  60000 tokens
+// of 40 heads of 128: 298 us (HBM's rate: 272), 335 from registers; 300 tokens:
+// 11 us, 10.  fp32 from registers: 302 us (296) at 32768 tokens, 484 through the
+// ring, whose copies are 16 bytes of a lane's 32.
+template <typename T, bool BACK, bool NORM, int ROT> constexpr bool ringed()
+{
+    return BACK && NORM && ROT != ANY && sizeof(T) == 2;
+}
+constexpr int STAGES = 3, ROUND = 4096;   // bytes of a warp's round
+constexpr int RING_BYTES = WARPS * STAGES * ROUND;
+
+__device__ __forceinline__ void slot_copy(uint32_t to, const void *from, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+template <typename T> __device__ __forceinline__ Eight<T> slot_load(uint32_t from)
+{
+    constexpr int N = sizeof(Eight<T>) / 16;
+    union {
+        Eight<T> x;
+        uint4 r[N];
+    } v;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.r[i].x), "=r"(v.r[i].y), "=r"(v.r[i].z), "=r"(v.r[i].w)
+                     : "r"(from + i * 512));
+    return v.x;
+}
+
+// The rounds of a warp in the order that it takes them.
+template <typename T> struct Ahead {
+    int64_t it;
+    int which, h0, hi;
+    const T *xp, *gp;
+
+    // asks for the next round's values (none are left: for nothing)
+    template <int SUBS, int U>
+    __device__ __forceinline__ void next(const RopeArgs &a, const Work &wk, uint32_t to, int c0,
+                                         int n, int sub)
+    {
+        constexpr int PIECE = (int)sizeof(Eight<T>) * 32;
+        while (h0 >= hi && it < wk.items) {
+            if (++which == 2) {
+                which = 0;
+                it += (int64_t)gridDim.x * WARPS;
+                if (it >= wk.items)
+                    break;
+            }
+            const RopeTensor &q = a.t[which];
+            int b, t, r0;
+            wk.at(a, it, &b, &t, &r0);
+            r0 -= which ? a.t[0].heads : 0;
+            h0 = max(r0, 0);
+            hi = min(r0 + wk.rows, q.heads);
+            xp = static_cast<const T *>(q.x) + b * q.xs[0] + t * q.xs[1] + (h0 + sub) * q.xs[2] + c0;
+            gp = static_cast<const T *>(q.dy) + b * q.dys[0] + t * q.dys[1] +
+                 (h0 + sub) * q.dys[2] + c0;
+        }
+        if (it < wk.items) {
+            const RopeTensor &q = a.t[which];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool there = n && h0 + u * SUBS + sub < hi;
+                const T *x = there ? xp : static_cast<const T *>(q.x);
+                const T *g = there ? gp : static_cast<const T *>(q.dy);
+#pragma unroll
+                for (int i = 0; i < (int)sizeof(Eight<T>) / 16; ++i) {
+                    slot_copy(to + 2 * u * PIECE + i * 512, x + i * (16 / sizeof(T)), there);
+                    slot_copy(to + (2 * u + 1) * PIECE + i * 512, g + i * (16 / sizeof(T)), there);
+                }
+                xp += SUBS * q.xs[2];
+                gp += SUBS * q.dys[2];
+            }
+            h0 += SUBS * U;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+};
+
 template <typename T, int LPR, bool BACK, bool NORM, int ROT>
 __global__ void __launch_bounds__(THREADS, ctas_of(BACK, NORM))
     rope(const RopeArgs a, const Work wk)
 {
     constexpr bool VEC = ROT != ANY;
     constexpr int SUBS = 32 / LPR, U = rounds_of<T, VEC>();
+    constexpr int PIECE = (int)sizeof(Eight<T>) * 32;   // a warp's values of one row group
+    static_assert(!VEC || 2 * U * PIECE == ROUND, "ring");
+    constexpr bool RING = ringed<T, BACK, NORM, ROT>();
     __shared__ Table tab;
     // a warp's cos and sin, ANY: then its rows' partners; at the end the sums
     __shared__ __align__(16) float exchange[WARPS][32 * V + (VEC ? 0 : 32 * V)];
     const int lane = threadIdx.x % 32, l = lane % LPR, sub = lane / LPR, warp = threadIdx.x / 32;
     const bool norm = VEC ? NORM : a.normalize;
+    extern __shared__ __align__(16) uint8_t slots[];
     Lane k;
     k.c0 = l * V;
     k.n = max(0, min(V, a.D - k.c0));
@@ -511,18 +612,23 @@ __global__ void __launch_bounds__(THREADS, ctas_of(BACK, NORM))
     }
     __syncthreads();
     Vals dw[2] = {zeros(), zeros()};
+    // RING: the warp's rounds, asked for STAGES - 1 ahead
+    Ahead<T> f;
+    const uint32_t slot = RING ? (uint32_t)__cvta_generic_to_shared(slots) +
+                                     warp * (STAGES * ROUND) + lane * 16
+                               : 0;
+    unsigned round = 0;
+    if constexpr (RING) {
+        f.it = (int64_t)blockIdx.x * WARPS + warp;
+        f.which = -1;
+        f.h0 = f.hi = 0;
+        for (int i = 0; i < STAGES - 1; ++i)
+            f.template next<SUBS, U>(a, wk, slot + i * ROUND, k.c0, k.n, sub);
+    }
     for (int64_t it = (int64_t)blockIdx.x * WARPS + warp; it < wk.items;
          it += (int64_t)gridDim.x * WARPS) {
-        const int64_t tok = wk.blocks == 1 ? it : it / wk.blocks;
-        const int r0 = (int)(it - tok * wk.blocks) * wk.rows;
-        int b, t;
-        if (tok <= 0xffffffffll) {
-            b = (int)((unsigned)tok / (unsigned)a.T);
-            t = (int)((unsigned)tok - (unsigned)b * (unsigned)a.T);
-        } else {
-            b = (int)(tok / a.T);
-            t = (int)(tok - (int64_t)b * a.T);
-        }
+        int b, t, r0;
+        wk.at(a, it, &b, &t, &r0);
         float *cs = exchange[warp], *sn = cs + 128;
         bool known = ROT == NONE;   // the angles
 #pragma unroll 1
@@ -552,7 +658,8 @@ __global__ void __launch_bounds__(THREADS, ctas_of(BACK, NORM))
                     gp += gd;
                 }
             };
-            fetch(lo);   // on their way while the angles are formed
+            if constexpr (!RING)
+                fetch(lo);   // on their way while the angles are formed
             if (!known) {
                 angles(a, tab, b, t, cs, sn);
                 known = true;
@@ -570,23 +677,46 @@ __global__ void __launch_bounds__(THREADS, ctas_of(BACK, NORM))
             }
             Vals sum = zeros();
             for (int h0 = lo;;) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (h0 + u * SUBS >= hi)
-                        break;
+                uint32_t from = 0;
+                if constexpr (RING) {
+                    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+                    from = slot + round % STAGES * ROUND;
+                    // (to the stage of the round before this one)
+                    f.template next<SUBS, U>(a, wk, slot + (round + STAGES - 1) % STAGES * ROUND,
+                                             k.c0, k.n, sub);
+                    ++round;
+                }
+                auto row = [&](int u) {
                     const int m = h0 + u * SUBS + sub < hi ? k.n : 0;
+                    if constexpr (RING) {
+                        xr[u] = slot_load<T>(from + 2 * u * PIECE);
+                        gr[u] = slot_load<T>(from + (2 * u + 1) * PIECE);
+                    }
                     const Vals before = sum;
-                    const Vals y =
-                        one_row<T, LPR, BACK, NORM, ROT>(a, k, xr[u], gr[u], &sum);
+                    const Vals y = one_row<T, LPR, BACK, NORM, ROT>(a, k, xr[u], gr[u], &sum);
                     if (BACK && !m)   // (with eps 0 a row that is not there has no finite norm)
                         sum = before;
                     store<T, VEC>(yp, m, y);
                     yp += yd;
+                };
+                // whole rounds without a branch: their rows' sums overlap then
+                if (RING && h0 + SUBS * U <= hi) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        row(u);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (h0 + u * SUBS >= hi)
+                            break;
+                        row(u);
+                    }
                 }
                 h0 += SUBS * U;
                 if (h0 >= hi)
                     break;
-                fetch(h0);
+                if constexpr (!RING)
+                    fetch(h0);
             }
             if (BACK && norm) {
 #pragma unroll
@@ -642,7 +772,23 @@ cudaError_t launch(const RopeArgs &a, int sms, cudaStream_t s, int *parts)
     wk.blocks = (heads + wk.rows - 1) / wk.rows;
     wk.items = tokens * wk.blocks;
     *parts = (int)std::min<int64_t>((wk.items + WARPS - 1) / WARPS, most);
-    rope<T, LPR, BACK, NORM, ROT><<<*parts, THREADS, 0, s>>>(a, wk);
+    constexpr int ring = ringed<T, BACK, NORM, ROT>() ? RING_BYTES : 0;
+    constexpr auto kernel = rope<T, LPR, BACK, NORM, ROT>;
+    if constexpr (ring > 0) {   // once per device
+        static std::atomic<uint64_t> known;
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess)
+            return e;
+        if (dev > 63 || !(known.load() >> dev & 1)) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
+            if (e != cudaSuccess)
+                return e;
+            if (dev < 64)
+                known.fetch_or((uint64_t)1 << dev);
+        }
+    }
+    kernel<<<*parts, THREADS, ring, s>>>(a, wk);
     note_launch();
     return cudaGetLastError();
 }
