@@ -20,15 +20,18 @@
 // cut into segments: a first pass composes each segment's map s -> A s + B (it
 // reads the inputs and writes nothing else), and a segment starts from the maps
 // of those before it.  That pass adds 2/3 of the reads; the alternative, tiles
-// that wait for the state of the tile before them, measured 143 us against 123
-// (b1 h8 n65536 forward): every tile of the GPU then waits at once, two to four
-// microseconds a round.
+// that wait for the state of the tile before them, measured 143 us against 108
+// (b1 h8 d128 n65536 forward): every tile of the GPU then waits at once, two to
+// four microseconds a round.
 //
 // Short sequences (a few tokens of many rows, decoding) take a thread per four
 // channels, which walks its sequence alone (serial, below).
 //
 // Bound: HBM, 6 (bf16 gate) or 8 bytes a value forward, 10 or 14 backward, and
-// close to it the issue rate: 20 instructions a value forward, 39 backward.
+// close to it the issue rate: 19 instructions a value forward, 38 backward, half
+// of the issue slots.  bf16, b4 h32 d128 n8192 (134 M values): forward 142 us, 0.84
+// of HBM's rate, backward 238 us, 0.83.  In segments (b1 h8 n262144, 268 M):
+// forward 410 us, 0.58 (0.97 of the 10 bytes that it moves), backward 666, 0.59.
 
 #include <algorithm>
 #include <atomic>
