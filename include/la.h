@@ -396,7 +396,8 @@ size_t la_gla_workspace_size(const la_dims *dims, int32_t dtype,
  * tokens are composed in parallel, so a product of consecutive decays must
  * stay in fp32's range: gates <= 0 always do, and gates whose sum over
  * consecutive tokens exceeds 88 may give infinities or NaN even where the
- * state stays zero.
+ * state stays zero.  What is left of a state after decays whose product is
+ * below 2^-126 counts as nothing.
  *   batch, seq_len, heads, num_seqs   as la_dims
  *   dim         channels of a head, 1..256
  *   gate_dtype  la_dtype of g and dg: the token dtype or LA_DTYPE_F32
@@ -556,7 +557,7 @@ la_status la_qk_norm_rope_bwd(const la_rope_dims *dims, int32_t dtype, const voi
                               size_t workspace_bytes, void *stream);
 
 /* Workspace bytes of la_qk_norm_rope_bwd (0 for invalid sizes and without
- * normalize).  Host function (reads one device attribute, once per device). */
+ * normalize).  Pure host function. */
 size_t la_qk_norm_rope_workspace_size(const la_rope_dims *dims, int32_t dtype);
 
 /* Reads and clears the device-side error words that bounded on-device waits

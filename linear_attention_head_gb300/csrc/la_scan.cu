@@ -364,10 +364,15 @@ struct Row {
     int b, bos, len;
     int64_t block;
 };
+// ceil(n / SIZE), at every n
+template <int SIZE> __device__ __forceinline__ int blocks_of(int n)
+{
+    return n / SIZE + (n % SIZE != 0);
+}
 template <int SIZE> __device__ __forceinline__ Row row_of(const ScanArgs &a, int n)
 {
     if (!a.cu)
-        return Row{n, 0, a.T, (int64_t)n * ((a.T + SIZE - 1) / SIZE)};
+        return Row{n, 0, a.T, (int64_t)n * blocks_of<SIZE>(a.T)};
     // (within the tokens, whatever the table says by now)
     const int lo = min(max(a.cu[n], 0), a.T), hi = min(max(a.cu[n + 1], lo), a.T);
     return Row{0, lo, hi - lo, (int64_t)lo / SIZE + n};
@@ -417,7 +422,7 @@ __device__ __forceinline__ bool enter_unit(const ScanArgs &a, const Plan &k, Wal
         w->seq = u / k.segments;
         w->seg = u - w->seq * k.segments;
         w->row = row_of<SCAN_TILE>(a, w->seq);
-        w->run = (w->row.len + SCAN_TILE - 1) / SCAN_TILE;
+        w->run = blocks_of<SCAN_TILE>(w->row.len);
         const int len = (w->run + k.segments - 1) / k.segments;
         w->lo = w->jj = w->seg * len;
         w->end = min(w->jj + len, w->run);
@@ -1234,7 +1239,7 @@ cudaError_t run(const ScanArgs &a, Plan k, void *ws, cudaStream_t s)
         segments = std::min<int64_t>(
             {slots / chains, run, (int64_t)(7.0 * std::sqrt((double)run)), MAX_SEGMENTS});
     k.segments = (int)std::max<int64_t>(segments, 1);
-    if (chains * k.segments > 0x7fffffff)
+    if (chains * k.segments > 0x7f000000)   // (a team steps beyond the last unit)
         return cudaErrorNotSupported;
     k.units = (int)(chains * k.segments);
     const int grid = (int)std::min<int64_t>(k.units, sms);
