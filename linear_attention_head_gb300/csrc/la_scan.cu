@@ -16,20 +16,25 @@
 // A CTA per SM: a warp has the teams' tiles copied to a ring of stages by TMA, so
 // that copies are under way at all times.
 //
-// Where there are too few sequences and channels for the teams, the sequences are
-// cut into segments: a first pass composes each segment's map s -> A s + B (it
-// reads the inputs and writes nothing else), and a segment starts from the maps
-// of those before it.  That pass adds 2/3 of the reads; the alternative, tiles
-// that wait for the state of the tile before them, measured 143 us against 108
-// (b1 h8 d128 n65536 forward): every tile of the GPU then waits at once, two to
-// four microseconds a round.
+// A tile takes a team 1.6 us (backward 2.8) however fast its data come.  Where
+// there are fewer sequences x channels than teams, two or four teams of a CTA take
+// the tiles of a chain in turn, and only the step from the state before a tile to
+// the one after it goes from team to team (0.95 us a tile with four, 128 chains of
+// 64 tiles: 68 us, 106 with one).
+// Where there are fewer still, the sequences are cut into segments: a first pass
+// composes each segment's map s -> A s + B (it reads the inputs and writes nothing
+// else), and a segment starts from the maps of those before it.  That pass adds
+// 2/3 of the reads; the alternative, tiles that wait for the state of the tile
+// before them in another CTA, measured 143 us against 108 (b1 h8 d128 n65536
+// forward): every tile of the GPU then waits at once, two to four microseconds a
+// round.
 //
 // Short sequences (a few tokens of many rows, decoding) take a thread per four
 // channels, which walks its sequence alone (serial, below).
 //
 // Bound: HBM, 6 (bf16 gate) or 8 bytes a value forward, 10 or 14 backward, and
 // close to it the issue rate: 19 instructions a value forward, 38 backward, half
-// of the issue slots.  bf16, b4 h32 d128 n8192 (134 M values): forward 142 us, 0.84
+// of the issue slots.  bf16, b4 h32 d128 n8192 (134 M values): forward 129 us, 0.92
 // of HBM's rate, backward 238 us, 0.83.  In segments (b1 h8 n262144, 268 M):
 // forward 410 us, 0.58 (0.97 of the 10 bytes that it moves), backward 666, 0.59.
 
@@ -345,6 +350,8 @@ struct Plan {
     int units;          // sequences * segments * parts: what a team takes
     float2 *maps;       // [sequence][segment][C]: (A, B); A < 0: the state B itself
     int map;            // this launch forms them
+    int group;          // GROUPED: teams that take a unit's tiles in turn (each a unit of its
+                        // own); else 1
     int flat;           // every tensor's heads are D apart
     int small;          // no token stride is beyond 2^24
     int boxed;          // the tensors have their Boxes
@@ -403,10 +410,14 @@ template <class S, bool BACK, int NS> struct Shared {
     // next when one of the two barriers says that the last but one was worked off
     uint64_t full[S::TEAMS][2], done[S::TEAMS][2];
     uint64_t empty[NS];
+    // of a group: the state after a tile, for the next one's team (a place for each
+    // team: the tile that had the place before is then done)
+    uint64_t passed[S::TEAMS / 2][S::TEAMS];
+    float state[S::TEAMS / 2][S::TEAMS][CT];
     Item taken[2][S::TEAMS];      // by the feeders, in turn
 };
 
-// A team's way through its units: one lane's state.
+// A group's way through its units: one lane's state.
 struct Walk {
     int unit, step;     // the next unit; units apart
     int seq, seg, run;  // the present one
@@ -432,6 +443,7 @@ __device__ __forceinline__ bool enter_unit(const ScanArgs &a, const Plan &k, Wal
         w->unit += w->step;
         return true;
     }
+    w->jj = w->end = 0;
     return false;
 }
 
@@ -591,6 +603,28 @@ __device__ __forceinline__ bool stage_wait(uint64_t *bar, unsigned parity)
     return true;
 }
 
+// The group's tile number m: takes the state over from the team of the tile
+// before it.
+template <class S, bool BACK, int NS>
+__device__ __forceinline__ bool taken_over(Shared<S, BACK, NS> &sm, int group, unsigned m, Carry *x)
+{
+    if (m == 0)
+        return true;
+    --m;
+    if (!stage_wait(&sm.passed[group][m % S::TEAMS], m / S::TEAMS & 1))
+        return false;
+    x->s = sm.state[group][m % S::TEAMS][threadIdx.x % S::THREADS / S::PARTS];
+    return true;
+}
+template <class S, bool BACK, int NS>
+__device__ __forceinline__ void pass_on(Shared<S, BACK, NS> &sm, int group, unsigned m,
+                                        const Carry &x)
+{
+    if (threadIdx.x % S::PARTS == 0)
+        sm.state[group][m % S::TEAMS][threadIdx.x % S::THREADS / S::PARTS] = x.s;
+    sm100::mbar_arrive(&sm.passed[group][m % S::TEAMS]);
+}
+
 // Bytes from a token's row to the next processed token's (Plan::small).
 template <typename T> __device__ __forceinline__ int step_of(const ScanArgs &a, int64_t st)
 {
@@ -648,14 +682,16 @@ __device__ __forceinline__ void feed(const ScanArgs &a, const Plan &k, const Box
     const Team<FEEDERS> team{15};
     const int lane = threadIdx.x % 32, w = (threadIdx.x - 512) / 32;
     const bool needs_x = !BACK || !k.map;
-    Walk walk{};   // of team `lane`
+    const int groups = S::TEAMS / k.group;
+    Walk walk{};   // of group `lane`
     walk.unit = blockIdx.x + lane * gridDim.x;
-    walk.step = gridDim.x * S::TEAMS;
+    walk.step = gridDim.x * groups;
     unsigned q = 0;              // stages handed out
     unsigned ended = 0;          // bit i: team i has been told so
     for (unsigned n = 0; ended != (1u << S::TEAMS) - 1; ++n) {   // every team's n-th tile
-        if (w == 0 && lane < S::TEAMS)
-            sm.taken[n & 1][lane] = next_item<BACK>(a, k, &walk);
+        if (w == 0 && lane < groups)
+            for (int i = 0; i < k.group; ++i)
+                sm.taken[n & 1][lane * k.group + i] = next_item<BACK>(a, k, &walk);
         team.sync();
         for (int i = 0; i < S::TEAMS; ++i) {
             if (ended >> i & 1)
@@ -746,7 +782,8 @@ __device__ __forceinline__ void fill(Four<T> *to, const Col<T, false> &c, const 
     }
 }
 
-template <class S, bool BACK, int NS> __device__ __forceinline__ void set_up(Shared<S, BACK, NS> &sm)
+template <class S, bool BACK, int NS>
+__device__ __forceinline__ void set_up(Shared<S, BACK, NS> &sm)
 {
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::TEAMS; ++i) {
@@ -754,6 +791,8 @@ template <class S, bool BACK, int NS> __device__ __forceinline__ void set_up(Sha
                 sm100::mbar_init(&sm.full[i][u], FEEDERS);
                 sm100::mbar_init(&sm.done[i][u], S::THREADS);
             }
+            for (int u = 0; u < S::TEAMS / 2; ++u)
+                sm100::mbar_init(&sm.passed[u][i], S::THREADS);
         }
         for (int i = 0; i < NS; ++i)
             sm100::mbar_init(&sm.empty[i], S::THREADS);
@@ -774,7 +813,7 @@ __device__ __forceinline__ void more_registers()
 
 // ---- forward ----------------------------------------------------------------
 
-template <typename T, typename TG, bool VEC, bool FLIP>
+template <typename T, typename TG, bool VEC, bool FLIP, bool GROUPED>
 __global__ void __launch_bounds__(CTA, 1)
     scan_fwd_tiles(const ScanArgs a, const Plan k, const __grid_constant__ Boxes boxes)
 {
@@ -796,6 +835,7 @@ __global__ void __launch_bounds__(CTA, 1)
     const bool odd = me & LANES;   // the second group of the warp
     const Team<S::THREADS> team{1 + (int)threadIdx.x / S::THREADS};
     Maps<S, false> &maps = sm.maps[team.id - 1];
+    const int group = (team.id - 1) / k.group, place = (team.id - 1) % k.group;
     Carry carry{0.f, 1.f};
     for (unsigned n = 0;; ++n) {
         if (!team.all(stage_wait(&sm.full[team.id - 1][n & 1], n / 2 & 1)))
@@ -856,10 +896,17 @@ __global__ void __launch_bounds__(CTA, 1)
             put_row<VEC>(maps.A[warp], lane, mul2(A, eA));
             put_row<VEC>(maps.B[warp], lane, fma2(A, eB, B));
         }
-        team.sync();
+        if (GROUPED) {
+            if (!team.all(taken_over(sm, group, n * k.group + place, &carry)))
+                break;
+        } else {
+            team.sync();
+        }
         if (a.states && !it.first && !k.map && me % PARTS == 0 && ch < C)
             a.states[it.block * C + ch] = carry.s;
         step<S, false>(k, it, maps, C, ch, a.init, a.fin, &carry);
+        if (GROUPED)
+            pass_on(sm, group, n * k.group + place, carry);
         team.sync();
         if (count && !k.map && a.o.p) {
             Val s = get_row<VEC>(maps.S_[warp], lane);
@@ -897,7 +944,7 @@ __global__ void __launch_bounds__(CTA, 1)
 // The chain runs from the last token to the first; s_{t-1} comes from the states
 // that entered the tiles in the forward.
 
-template <typename T, typename TG, bool VEC, bool FLIP>
+template <typename T, typename TG, bool VEC, bool FLIP, bool GROUPED>
 __global__ void __launch_bounds__(CTA, 1)
     scan_bwd_tiles(const ScanArgs a, const Plan k, const __grid_constant__ Boxes boxes)
 {
@@ -919,6 +966,7 @@ __global__ void __launch_bounds__(CTA, 1)
     const bool odd = me & LANES;
     const Team<S::THREADS> team{1 + (int)threadIdx.x / S::THREADS};
     Maps<S, true> &maps = sm.maps[team.id - 1];
+    const int group = (team.id - 1) / k.group, place = (team.id - 1) % k.group;
     Carry carry{0.f, 1.f};
     for (unsigned n = 0;; ++n) {
         if (!team.all(stage_wait(&sm.full[team.id - 1][n & 1], n / 2 & 1)))
@@ -976,10 +1024,17 @@ __global__ void __launch_bounds__(CTA, 1)
             put_row<VEC>(maps.A[warp], lane, mul2(A, oA));
             put_row<VEC>(maps.B[warp], lane, fma2(A, oB, B));
         }
-        team.sync();
+        if (GROUPED) {
+            if (!team.all(taken_over(sm, group, n * k.group + place, &carry)))
+                break;
+        } else {
+            team.sync();
+        }
         if (!k.map)
             spread<S, false>(maps.fS, run_of<S, false>(maps.A, maps.fB), fs);
         step<S, true>(k, it, maps, C, ch, a.dfin, a.dinit, &carry);
+        if (GROUPED)
+            pass_on(sm, group, n * k.group + place, carry);
         team.sync();
         if (count && !k.map) {
             Val s = get_row<VEC>(maps.fS[warp], lane), K = get_row<VEC>(maps.S_[warp], lane);
@@ -1197,10 +1252,7 @@ bool box_of(CUtensorMap *m, const ScanArgs &a, const Tok &x, int bf16, bool flat
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The device's SMs; sets the kernel's shared memory up on the first call per
-// device.
-template <bool BACK, typename T, typename TG, bool VEC, bool FLIP, typename K>
-cudaError_t sms_for(K kernel, int *sms)
+cudaError_t sms_of(int *sms)
 {
     static std::atomic<int> known[64];
     int dev = 0;
@@ -1209,33 +1261,55 @@ cudaError_t sms_for(K kernel, int *sms)
         return e;
     if (dev < 64 && (*sms = known[dev].load()) > 0)
         return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING);
-    if (e == cudaSuccess)
-        e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess && dev < 64)
         known[dev].store(*sms);
     return e;
 }
 
+// Launches the kernel, whose shared memory is set up on the first call per device.
+template <bool BACK, typename T, typename TG, bool VEC, bool FLIP, bool GROUPED>
+cudaError_t tiles(const ScanArgs &a, const Plan &k, const Boxes &boxes, int grid, cudaStream_t s)
+{
+    constexpr auto kernel = BACK ? scan_bwd_tiles<T, TG, VEC, FLIP, GROUPED>
+                                 : scan_fwd_tiles<T, TG, VEC, FLIP, GROUPED>;
+    static std::atomic<uint64_t> known;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev > 63 || !(known.load() >> dev & 1)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING);
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            known.fetch_or((uint64_t)1 << dev);
+    }
+    kernel<<<grid, CTA, RING, s>>>(a, k, boxes);
+    note_launch();
+    return cudaGetLastError();
+}
+
 template <bool BACK, typename T, typename TG, bool VEC, bool FLIP>
 cudaError_t run(const ScanArgs &a, Plan k, void *ws, cudaStream_t s)
 {
-    constexpr auto kernel =
-        BACK ? scan_bwd_tiles<T, TG, VEC, FLIP> : scan_fwd_tiles<T, TG, VEC, FLIP>;
     constexpr int teams = BACK ? Bwd::TEAMS : Fwd::TEAMS;
     int sms = 0;
-    cudaError_t e = sms_for<BACK, T, TG, VEC, FLIP>(kernel, &sms);
+    cudaError_t e = sms_of(&sms);
     if (e != cudaSuccess)
         return e;
-    // Segments where the chains (sequences x parts of the channels) are fewer
-    // than a third of the teams: as many as there are teams for, unless the maps
-    // that a segment starts from cost more than its tiles (0.1 us a map, 4 us a
-    // tile for both passes: best at 7 sqrt(run)).
+    // Chains: sequences x parts of the channels.  Few: segments, as many as there
+    // are teams for, unless the maps that a segment starts from cost more than its
+    // tiles (0.1 us a map, 4 us a tile for both passes: best at 7 sqrt(run)).
+    // More: several teams for one chain, a unit to a group.  The measured border
+    // (64 tiles a chain, us, segments and groups): forward 32 chains 32 and 62, 64
+    // chains 61 and 64, 128 chains 115 and 68; backward 64 chains 106 and 138, 128
+    // chains 180 and 137.
     const int64_t chains = (int64_t)a.N * k.parts;
     const int64_t slots = std::min<int64_t>((int64_t)sms * teams, MAX_UNITS);
     const int64_t run = (a.longest + SCAN_TILE - 1) / SCAN_TILE;
     int64_t segments = 1;
-    if (chains * 3 <= slots)
+    if (BACK ? 7 * chains <= 4 * sms : 5 * chains <= 2 * sms)
         segments = std::min<int64_t>(
             {slots / chains, run, (int64_t)(7.0 * std::sqrt((double)run)), MAX_SEGMENTS});
     k.segments = (int)std::max<int64_t>(segments, 1);
@@ -1243,21 +1317,23 @@ cudaError_t run(const ScanArgs &a, Plan k, void *ws, cudaStream_t s)
         return cudaErrorNotSupported;
     k.units = (int)(chains * k.segments);
     const int grid = (int)std::min<int64_t>(k.units, sms);
-    Boxes boxes;
+    k.group = 1;
+    while (k.segments == 1 && k.group < teams && chains * k.group * 2 <= slots)
+        k.group *= 2;
+    Boxes boxes{};
     k.boxed = VEC && box_of(&boxes.x, a, a.x, a.bf16, k.flat) &&
               box_of(&boxes.g, a, a.g, a.gate_bf16, k.flat) &&
               (!BACK || box_of(&boxes.d, a, a.d_o, a.bf16, k.flat));
     if (k.segments > 1) {
         k.maps = static_cast<float2 *>(ws);
         k.map = 1;
-        kernel<<<grid, CTA, RING, s>>>(a, k, boxes);
-        note_launch();
+        if ((e = tiles<BACK, T, TG, VEC, FLIP, false>(a, k, boxes, grid, s)) != cudaSuccess)
+            return e;
         k.map = 0;
     }
     k.withhold = take_withheld();
-    kernel<<<grid, CTA, RING, s>>>(a, k, boxes);
-    note_launch();
-    return cudaGetLastError();
+    return k.group > 1 ? tiles<BACK, T, TG, VEC, FLIP, true>(a, k, boxes, grid, s)
+                       : tiles<BACK, T, TG, VEC, FLIP, false>(a, k, boxes, grid, s);
 }
 
 // The tensors' rows are in whole 16-byte pieces: wide accesses and copies.  Of
@@ -1337,7 +1413,8 @@ size_t scan_states_bytes(int B, int T, int N, int H, int D)
     auto blocks = [&](int64_t rows, int64_t size) { return rows * ((T + size - 1) / size); };
     // dense: B rows of T tokens
     const bool alone = serial(blocks(B, SCAN_TILE), T, (int64_t)B * T, C);
-    int64_t n = T <= (alone ? SCAN_BLOCK : SCAN_TILE) ? 0 : blocks(B, alone ? SCAN_BLOCK : SCAN_TILE);
+    const int64_t size = alone ? SCAN_BLOCK : SCAN_TILE;
+    int64_t n = T <= size ? 0 : blocks(B, size);
     // packed: the lengths are not known, so for either kernel
     if (B == 1 && N > 0) {
         n = std::max(n, (int64_t)T / SCAN_TILE + N);
@@ -1347,7 +1424,10 @@ size_t scan_states_bytes(int B, int T, int N, int H, int D)
     return (size_t)n * C * sizeof(float);
 }
 
-size_t scan_maps_bytes(int T) { return T > SCAN_TILE ? (size_t)MAX_UNITS * CT * sizeof(float2) : 0; }
+size_t scan_maps_bytes(int T)
+{
+    return T > SCAN_TILE ? (size_t)MAX_UNITS * CT * sizeof(float2) : 0;
+}
 
 cudaError_t scan_forward(const ScanArgs &a, void *ws, cudaStream_t s)
 {

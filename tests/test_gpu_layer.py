@@ -167,6 +167,17 @@ def test_scan_rows_of_all_heads(B, T, H, D, dt, gt, reverse):
     _scan_check(x, g, do, init, dfin, reverse, label="%s" % ((B, T, H, D),))
 
 
+@pytest.mark.parametrize("H,dt,gt", [(40, BF, BF), (50, F32, F32), (80, BF, F32), (100, BF, BF)])
+@pytest.mark.parametrize("cu", [None, [0, 900], [0, 1, 130, 130, 900]])
+def test_scan_chains_of_several_teams(H, dt, gt, cu):
+    # 64 to 300 chains (sequences x 64 channels): two or four teams take a chain's tiles in
+    # turn, whole and ragged runs, rows of 16-byte pieces and (D 127) others
+    B, T, D = (1, 900, 128) if H != 50 else (1, 900, 127)
+    n = 1 if cu is None else len(cu) - 1
+    x, g, do, init, dfin = _scan_inputs(B, T, H if n == 1 else H // 2, D, dt, gt, n, 28)
+    _scan_check(x, g, do, init, dfin, H == 80, cu, label="%d heads" % H)
+
+
 @pytest.mark.parametrize("dt,gt", [(BF, F32), (F32, F32)])
 @pytest.mark.parametrize("reverse", [False, True])
 @pytest.mark.parametrize("D", [64, 72, 192])
