@@ -401,6 +401,21 @@ def test_scan_withheld_tile_reports_timeout_and_context_survives():
         la.get_device_error()
 
 
+def test_scan_withheld_tile_among_teams_that_wait_for_one_another():
+    # the same where several teams take a chain's tiles in turn: all of them stop
+    x, g, do, init, dfin = _cuda(*_scan_inputs(1, 900, 50, 128, BF, BF, 1, 17))
+    want = la.gated_scan_fwd(x, g, init)
+    la.get_device_error()
+    N.check(N.lib().la_debug_withhold_next_handoff(1))
+    la.gated_scan_fwd(x, g, init)
+    with pytest.raises(N.LaError) as err:
+        la.get_device_error()
+    assert err.value.status == N.LA_ERR_TIMEOUT
+    got = la.gated_scan_fwd(x, g, init)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    la.get_device_error()
+
+
 def test_scan_refuses_foreign_states():
     x, g, do, init, dfin = _cuda(*_scan_inputs(1, 300, 1, 8, F32, F32, 1, 15))
     with pytest.raises(ValueError, match="states"):
