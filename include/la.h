@@ -576,9 +576,10 @@ la_status la_get_device_error(void *stream);
  * a kernel with internal hand-offs (the tensor-core sweeps, the streamed
  * decode kernel, the tiles of la_gated_scan_fwd and _bwd) made from this host
  * thread withholds one of them -- between its warps, or the copy of a state
- * block -- so that a bounded on-device wait runs out (after about 2 s); the kernel then stops, frees what it holds and returns,
- * its outputs are undefined, and la_get_device_error reports LA_ERR_TIMEOUT.
- * The switch resets itself after that launch and is off by default. */
+ * block -- so that a bounded on-device wait runs out (after about 2 s); the
+ * kernel then stops, frees what it holds and returns, its outputs are
+ * undefined, and la_get_device_error reports LA_ERR_TIMEOUT.  The switch
+ * resets itself after that launch and is off by default. */
 la_status la_debug_withhold_next_handoff(int32_t on);
 
 /* Diagnostic, for testing the sequence split's planning without a device:

@@ -415,7 +415,8 @@ __device__ __forceinline__ Vals partners(const RopeArgs &a, const Eight<T> &x, c
 
 // Adds the partners' part to the rotated channels; the others keep what they
 // are, whatever NaN or infinity stands in the row's rotated ones.
-__device__ __forceinline__ void turn(const RopeArgs &a, int c0, const Vals &p, const Vals &s, Vals *v)
+__device__ __forceinline__ void turn(const RopeArgs &a, int c0, const Vals &p, const Vals &s,
+                                     Vals *v)
 {
     if (a.R >= a.D) {
         *v = fma(p, s, *v);
@@ -551,9 +552,9 @@ template <typename T> struct Ahead {
             r0 -= which ? a.t[0].heads : 0;
             h0 = max(r0, 0);
             hi = min(r0 + wk.rows, q.heads);
-            xp = static_cast<const T *>(q.x) + b * q.xs[0] + t * q.xs[1] + (h0 + sub) * q.xs[2] + c0;
-            gp = static_cast<const T *>(q.dy) + b * q.dys[0] + t * q.dys[1] +
-                 (h0 + sub) * q.dys[2] + c0;
+            const int h = h0 + sub;
+            xp = static_cast<const T *>(q.x) + b * q.xs[0] + t * q.xs[1] + h * q.xs[2] + c0;
+            gp = static_cast<const T *>(q.dy) + b * q.dys[0] + t * q.dys[1] + h * q.dys[2] + c0;
         }
         if (it < wk.items) {
             const RopeTensor &q = a.t[which];
