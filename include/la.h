@@ -530,9 +530,9 @@ typedef struct la_rope_dims {
  *   cu_seqlens, cu_seqlens_host   as la_fwd; used only without positions
  *   qo, ko          outputs of `dtype`; qo may be q itself and ko k itself
  *                   (same pointer and strides)
- * Angles keep their fraction of a turn to 2^-32 at every int32 position
- * (positions beyond int32 wrap inv_freq's own rounding, 2^-53 of a radian per
- * position, instead). */
+ * Angles are those of the fp64 numbers inv_freq: their fraction of a turn is
+ * within 2^-32 + |position| * 2^-63 of the exact product's (2^-31 at every
+ * int32 position), whatever the frequency. */
 la_status la_qk_norm_rope_fwd(const la_rope_dims *dims, int32_t dtype, const void *q,
                               const void *k, const void *q_weight, const void *k_weight,
                               float eps, const double *inv_freq, const void *positions,

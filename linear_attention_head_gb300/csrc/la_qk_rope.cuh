@@ -5,10 +5,11 @@
 //   u = R^T(dy);  dx = r (z - x r^2 mean(z x)), z = u w;  dw = sum u x r
 //
 // Angles: inv_freq / 2 pi is kept as a 64-bit fixed-point fraction of a turn
-// F, so position * F mod 2^64 is the angle's fraction of a turn, wrapped
-// exactly, at every position; its upper 32 bits are kept (2^-32 of a turn), and
-// sin and cos are taken of the remainder to the nearest quarter turn.  An fp32
-// product position * inv_freq would be off by 0.06 radians at position 10^6.
+// F, so position * F mod 2^64 is the angle's fraction of a turn, whole turns
+// wrapped exactly; F is within 2^-63, so the fraction within |position| 2^-63;
+// its upper 32 bits are kept (2^-32 of a turn), and sin and cos are taken of the
+// remainder to the nearest quarter turn.  An fp32 product position * inv_freq
+// would be off by 0.06 radians at position 10^6.
 //
 // Bound: HBM, two accesses of a value forward and three backward (two without
 // the norms).  A row (one head of one token) belongs to LPR lanes, 8 channels
@@ -217,11 +218,20 @@ template <int LPR> __device__ __forceinline__ float row_sum(float x)
 
 // ---- angles ------------------------------------------------------------------
 
+// A turn's fraction of x as 64-bit fixed point, to the nearest (whole turns wrap).
+__device__ __forceinline__ uint64_t fixed_turn(double x)
+{
+    return (uint64_t)__double2ll_rn((x - rint(x)) * 18446744073709551616.0);
+}
+// inv_freq / 2 pi.  1 / 2 pi in two parts: the product with the first one and its
+// rounding exactly, so that the fraction has all its 64 bits, which a far
+// position multiplies up (one rounded fp64 product: 55 of them, 2^-25 of a turn
+// at position 2^31).
 __device__ __forceinline__ uint64_t turn_of(double inv_freq)
 {
-    double f = inv_freq * 0.15915494309189535;   // 1 / 2 pi
-    f -= floor(f);
-    return f >= 1.0 ? 0 : (uint64_t)(f * 18446744073709551616.0);
+    constexpr double HI = 0x1.45f306dc9c883p-3, LO = -0x1.6b01ec5417056p-57;
+    const double p = __dmul_rn(inv_freq, HI);   // (rounded by itself, in no fma)
+    return fixed_turn(p) + fixed_turn(__fma_rn(inv_freq, LO, __fma_rn(inv_freq, HI, -p)));
 }
 
 // sin and cos of f / 2^32 of a turn: Taylor series of the remainder x to the

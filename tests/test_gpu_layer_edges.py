@@ -1,5 +1,7 @@
 """The operators beside the attention where fp32 runs out: infinite states under gates that
-forget.  The tolerances are those of test_gpu_layer.py unless a test derives its own."""
+forget, angles at far positions and of any frequency.  The tolerances are those of
+test_gpu_layer.py unless a test derives its own."""
+from fractions import Fraction
 import math
 
 import pytest
@@ -55,3 +57,61 @@ def test_scan_infinite_states_stay_infinite_under_strong_gates(B, T, H, D, dt, g
     for name, t, d in zip(("dx", "dg", "dinit"), got, (dt, gt, F32)):
         _same(t, ref[name], ref[name + "_e"], d, name)
     la.get_device_error()
+
+
+# ---------------------------------------------------------------------------
+# angles
+
+_PI = Fraction(31415926535897932384626433832795028841971693993751058209749445923,
+               10 ** 64)
+
+
+def _turn(position, freq):
+    """The fraction of a turn in (-1/2, 1/2] of position * freq radians, freq the fp64 number
+    itself, with 60 digits of pi."""
+    t = Fraction(position) * Fraction(freq) / (2 * _PI)
+    return float(t - round(t))
+
+
+def _angles(positions, freqs):
+    """cos and sin [position, frequency] of the kernel: pairs (1, 0) rotated."""
+    n, R_ = len(freqs), len(positions)
+    q = torch.zeros(1, R_, 1, 2 * n)
+    q[..., :n] = 1
+    rope = la.Rope(torch.tensor(freqs, dtype=torch.float64).cuda())
+    y = la.rotary_fwd(q.cuda(), rope=rope,
+                      positions=torch.tensor(positions, dtype=torch.int64).cuda())
+    y = y[0, :, 0].cpu().double()
+    return y[:, :n], y[:, n:]
+
+
+FAR = [2 ** 31 - 1, -2 ** 31, 123456789, -77777777, 2 ** 28 + 1, 2 ** 24 + 1, 131071, 7, 0, -1]
+
+
+def test_rotation_angles_of_any_frequency():
+    # frequencies above 1 and below, negative ones and 0 too: cos and sin within 2^-22 of those
+    # of the exact product (the angle itself: the next test)
+    freqs = [1.0, 2.0, 3.7, 100.0, 12345.678, -5.5, 1e-4, 0.1, 0.0, 1e6]
+    cos, sin = _angles(FAR, freqs)
+    for i, p in enumerate(FAR):
+        for j, f in enumerate(freqs):
+            a = 2 * math.pi * _turn(p, f)
+            assert abs(float(cos[i, j]) - math.cos(a)) <= 2.0 ** -22, (p, f)
+            assert abs(float(sin[i, j]) - math.sin(a)) <= 2.0 ** -22, (p, f)
+
+
+@pytest.mark.parametrize("position", [2 ** 31 - 1, -2 ** 31, 2 ** 28 + 1, 2 ** 24 + 1])
+def test_rotation_angle_keeps_its_fraction_of_a_turn(position):
+    # frequencies that take this position to almost whole turns: there the sine, a small number,
+    # shows the angle itself.  The fraction of a turn is within 2^-32 (its lower bits are cut off)
+    # and |position| 2^-64 <= 2^-33 (the two roundings of a frequency's fraction); sine and the
+    # remainder as fp32 are within 2^-22 of their value.
+    freqs = [2 * math.pi * round(abs(position) * f / (2 * math.pi)) / abs(position)
+             for f in (1.0, 0.7, 0.3, 0.01, 2.0, 17.0)]
+    _, sin = _angles([position], freqs)
+    for j, f in enumerate(freqs):
+        turn = _turn(position, f)
+        assert abs(turn) < 2.0 ** -16       # (of these frequencies)
+        want = math.sin(2 * math.pi * turn)
+        bound = 2 * math.pi * 1.5 * 2.0 ** -32 + 2.0 ** -22 * abs(want)
+        assert abs(float(sin[0, j]) - want) <= bound, (f, turn, float(sin[0, j]), want)
