@@ -399,7 +399,8 @@ size_t la_gla_workspace_size(const la_dims *dims, int32_t dtype,
  * state stays zero.  What is left of a state after decays whose product is
  * below 2^-126 counts as nothing (an error of at most 2^-126 of that state).
  * An infinite state stays infinite under any decays above 2^-126 (gates above
- * -87.3); a smaller decay is 0, and 0 times infinity NaN.
+ * -87.3); a smaller decay is 0, and 0 times infinity NaN.  A decay is within
+ * (4 + 1.25 |g|) * 2^-24 of exp(g), relative to it.
  *   batch, seq_len, heads, num_seqs   as la_dims
  *   dim         channels of a head, 1..256
  *   gate_dtype  la_dtype of g and dg: the token dtype or LA_DTYPE_F32

@@ -98,8 +98,10 @@ __device__ __forceinline__ float ex2(float x)
 // the only rounding of the size of the result, and it has no preferred sign.
 // The hardware's 2^x has one (as has expf), and a channel that remembers
 // thousands of tokens adds it up once a token: 1.1e-5 of the final state at
-// 8192 tokens against 2e-6.  Larger |g| forget within four tokens; there 2^x
-// is within 2^-22.
+// 8192 tokens against 2e-6.  Elsewhere it is 2^x, which is within 2^-22, of
+// g log2(e) rounded twice, the constant and the product: together within
+// (4 + 1.25 |g|) 2^-24 of exp(g).  Gates below -1/4 forget within four tokens,
+// so little of that adds up; gates above 1/4 do add it up while the state grows.
 __device__ __forceinline__ F2 decay(F2 g)
 {
     F2 p = fma2(g, f2(1.f / 720.f), f2(1.f / 120.f));

@@ -1,6 +1,6 @@
 """The operators beside the attention where fp32 runs out: infinite states under gates that
-forget, angles at far positions and of any frequency.  The tolerances are those of
-test_gpu_layer.py unless a test derives its own."""
+forget, decays over their range, angles at far positions and of any frequency.  The tolerances are
+those of test_gpu_layer.py unless a test derives its own."""
 from fractions import Fraction
 import math
 
@@ -57,6 +57,32 @@ def test_scan_infinite_states_stay_infinite_under_strong_gates(B, T, H, D, dt, g
     for name, t, d in zip(("dx", "dg", "dinit"), got, (dt, gt, F32)):
         _same(t, ref[name], ref[name + "_e"], d, name)
     la.get_device_error()
+
+
+# ---------------------------------------------------------------------------
+# decays
+
+@pytest.mark.parametrize("T", [1, 300])
+def test_scan_decays_over_their_range(T):
+    # a state under one gate (and then gates of 0, whose decay is 1 itself): exp(g) within
+    # 4 u (2^x within 2^-22; near 0 the series, 2 u) and, from the argument's product with a
+    # rounded log2 e, 1.25 |g| u; below 2^-126 it is 0.  T = 1: a thread alone, 300: a tile.
+    H, D = 64, 256
+    gate = torch.linspace(-110.0, 88.0, H * D, dtype=torch.float64).float()
+    near = torch.linspace(-0.5, 0.5, 4096, dtype=torch.float64).float()
+    gate[:4096] = near
+    g = torch.zeros(1, T, H, D)
+    g[0, 0] = gate.reshape(H, D)
+    x, init = torch.zeros(1, T, H, D), torch.ones(1, H, D)
+    o, fin = la.gated_scan_fwd(*_cuda(x, g, init))
+    want = gate.double().exp()
+    for got in (o[0, T - 1], fin[0]):
+        got = got.cpu().double().reshape(-1)
+        gone = want < 2.0 ** -126 * (1 + 2.0 ** -16)    # (to where the argument may round)
+        assert bool((got[gone] <= 2.0 ** -125).all())
+        err = (got - want).abs()[~gone] / want[~gone]
+        bound = (4 + 1.25 * gate.double().abs()[~gone]) * R.U
+        assert bool((err <= bound).all()), float((err / bound).max())
 
 
 # ---------------------------------------------------------------------------
