@@ -636,16 +636,19 @@ __device__ __forceinline__ bool stage_wait(uint64_t *bar, unsigned parity)
 }
 
 // The group's tile number m: takes the state over from the team of the tile
-// before it.
+// before it.  A unit's first tile (begin) has its own state to start from and
+// only waits, so that the places keep their order.
 template <class S, bool BACK, int NS>
-__device__ __forceinline__ bool taken_over(Shared<S, BACK, NS> &sm, int group, unsigned m, Carry *x)
+__device__ __forceinline__ bool taken_over(Shared<S, BACK, NS> &sm, int group, unsigned m,
+                                           int begin, Carry *x)
 {
     if (m == 0)
         return true;
     --m;
     if (!stage_wait(&sm.passed[group][m % S::TEAMS], m / S::TEAMS & 1))
         return false;
-    x->s = sm.state[group][m % S::TEAMS][threadIdx.x % S::THREADS / S::PARTS];
+    if (!begin)
+        x->s = sm.state[group][m % S::TEAMS][threadIdx.x % S::THREADS / S::PARTS];
     return true;
 }
 template <class S, bool BACK, int NS>
@@ -944,7 +947,8 @@ __global__ void __launch_bounds__(CTA, 1)
             put_row<VEC>(maps.B[warp], lane, fma2(A, eB, B));
         }
         if (GROUPED) {
-            if (!team.all(taken_over(sm, group, n * k.group + place, &carry)))
+            if (!team.all(taken_over(sm, group, n * k.group + place, it.begin,
+                                     &carry)))
                 break;
         } else {
             team.sync();
@@ -1085,7 +1089,8 @@ __global__ void __launch_bounds__(CTA, 1)
             put_row<VEC>(maps.B[warp], lane, fma2(A, oB, B));
         }
         if (GROUPED) {
-            if (!team.all(taken_over(sm, group, n * k.group + place, &carry)))
+            if (!team.all(taken_over(sm, group, n * k.group + place, it.begin,
+                                     &carry)))
                 break;
         } else {
             team.sync();
