@@ -1,6 +1,8 @@
 """The operators beside the attention where fp32 runs out: infinite states under gates that
-forget, decays over their range, angles at far positions and of any frequency.  The tolerances are
-those of test_gpu_layer.py unless a test derives its own."""
+forget, decays over their range, angles at far positions and of any frequency; and the launches of
+the gated recurrence that depend on the number of chains.  The tolerances are those of
+test_gpu_layer.py unless a test derives its own."""
+import ctypes
 from fractions import Fraction
 import math
 
@@ -9,7 +11,9 @@ import torch
 
 import layer_reference as R
 import linear_attention_head_gb300 as la
-from test_gpu_layer import BF, F32, SCAN_U, _close, _cuda, _scan_inputs
+from linear_attention_head_gb300 import _native as N
+from test_gpu_layer import (BF, F32, SCAN_U, _close, _cuda, _relayout, _scan_check,
+                            _scan_inputs)
 
 pytestmark = pytest.mark.gpu
 
@@ -141,3 +145,85 @@ def test_rotation_angle_keeps_its_fraction_of_a_turn(position):
         want = math.sin(2 * math.pi * turn)
         bound = 2 * math.pi * 1.5 * 2.0 ** -32 + 2.0 ** -22 * abs(want)
         assert abs(float(sin[0, j]) - want) <= bound, (f, turn, float(sin[0, j]), want)
+
+
+# ---------------------------------------------------------------------------
+# teams that take a chain's tiles in turn, backward
+
+def _chains():
+    """Chains for which both directions have their teams take turns: fewer than the teams of
+    the backward by half, more than are cut into segments."""
+    return int(0.8 * torch.cuda.get_device_properties(0).multi_processor_count)
+
+
+@pytest.mark.parametrize("dt,gt", TYPES)
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("cu", [None, [0, 1, 130, 900], [0, 512, 512, 900]])
+def test_scan_backward_of_teams_in_turn(dt, gt, reverse, cu):
+    n = 1 if cu is None else len(cu) - 1
+    x, g, do, init, dfin = _scan_inputs(1, 900, _chains() // n, 64, dt, gt, n, 33)
+    _scan_check(x, g, do, init, dfin, reverse, cu, label="in turn")
+
+
+@pytest.mark.parametrize("dt,gt,layout,D", [
+    (BF, F32, "head_major", 72), (F32, F32, "head_major", 72), (BF, BF, "dense", 63),
+    (F32, F32, "odd_rows", 64)])
+@pytest.mark.parametrize("reverse", [False, True])
+def test_scan_backward_of_teams_in_turn_by_rows(dt, gt, layout, D, reverse):
+    # tiles that cross heads which are apart (copied row by row), rows that no wide access fits
+    H = _chains() * 64 // D - 1
+    x, g, do, init, dfin = _scan_inputs(1, 700, H, D, dt, gt, 1, 34)
+    dev = [_relayout(t, layout) for t in (x, g, do)] + _cuda(init, dfin)
+    _scan_check(x, g, do, init, dfin, reverse, label=layout, dev=dev)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_scan_withheld_tile_among_backward_teams_that_wait_for_one_another(dt):
+    x, g, do, init, dfin = _cuda(*_scan_inputs(1, 900, _chains(), 64, dt, dt, 1, 35))
+    _, _, states = la.gated_scan_fwd(x, g, init, keep_states=True)
+    want = la.gated_scan_bwd(x, g, do, init, dfin, states=states)
+    la.get_device_error()
+    N.check(N.lib().la_debug_withhold_next_handoff(1))
+    la.gated_scan_bwd(x, g, do, init, dfin, states=states)
+    with pytest.raises(N.LaError) as err:
+        la.get_device_error()
+    assert err.value.status == N.LA_ERR_TIMEOUT
+    la.get_device_error()
+    got = la.gated_scan_bwd(x, g, do, init, dfin, states=states)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    la.get_device_error()
+
+
+@pytest.mark.parametrize("H", [1, 121])
+def test_scan_backward_of_tokens_far_apart(H):
+    # tokens further apart than the steps of whole groups that fit 32 bits of bytes, read and
+    # (C call) written; one chain in segments, many in turn
+    x, g, do, init, dfin = _cuda(*_scan_inputs(1, 140, H, 64, BF, BF, 1, 36))
+    step = (1 << 24) + 64 * H
+    room = 139 * step + 64 * H
+    far = lambda buf: buf.as_strided((1, 140, H, 64), (0, step, 64, 1))
+    for reverse in (False, True):
+        want = la.gated_scan_bwd(x, g, do, init, dfin, reverse)
+        for i in range(3):
+            buf = torch.empty(room, dtype=BF, device="cuda")
+            args = [x, g, do]
+            args[i] = far(buf).copy_(args[i])
+            got = la.gated_scan_bwd(*args, init, dfin, reverse)
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), (i, reverse)
+            del buf, args
+        # dx far apart
+        lib, dg, dinit = N.lib(), torch.empty_like(g), torch.empty_like(init)
+        buf = torch.zeros(room, dtype=BF, device="cuda")
+        dx = far(buf)
+        near = (ctypes.c_int64 * 3)(*x.stride()[:3])
+        apart = (ctypes.c_int64 * 3)(0, step, 64)
+        d = N.LaScanDims(1, 140, H, 64, 1, N.LA_DTYPE_BF16, near, near, near, near, apart, near)
+        ws = torch.empty(int(lib.la_gated_scan_workspace_size(ctypes.byref(d), N.LA_DTYPE_BF16, 2)),
+                         dtype=torch.uint8, device="cuda")
+        ptr = [t.data_ptr() for t in (x, g, do, init, dfin, dx, dg, dinit, ws)]
+        N.check(lib.la_gated_scan_bwd(ctypes.byref(d), N.LA_DTYPE_BF16, *ptr[:5], int(reverse),
+                                      None, None, None, *ptr[5:9], ws.numel(),
+                                      torch.cuda.current_stream().cuda_stream))
+        assert all(torch.equal(a, b) for a, b in zip((dx, dg, dinit), want)), reverse
+        del buf, dx
+    la.get_device_error()
