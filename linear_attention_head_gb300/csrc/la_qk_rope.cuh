@@ -513,7 +513,8 @@ template <typename T, bool BACK, bool NORM, int ROT> constexpr bool ringed()
 {
     return BACK && NORM && ROT != ANY && sizeof(T) == 2;
 }
-constexpr int STAGES = 3, ROUND = 4096;   // bytes of a warp's round
+// Bytes of a warp's round, and of one tensor's values of a row group in it.
+constexpr int STAGES = 3, ROUND = 4096, PIECE = 512;
 constexpr int RING_BYTES = WARPS * STAGES * ROUND;
 
 __device__ __forceinline__ void slot_copy(uint32_t to, const void *from, bool there)
@@ -522,23 +523,18 @@ __device__ __forceinline__ void slot_copy(uint32_t to, const void *from, bool th
                  "r"(there ? 16 : 0)
                  : "memory");
 }
-template <typename T> __device__ __forceinline__ Eight<T> slot_load(uint32_t from)
+__device__ __forceinline__ Eight<__nv_bfloat16> slot_load(uint32_t from)
 {
-    constexpr int N = sizeof(Eight<T>) / 16;
-    union {
-        Eight<T> x;
-        uint4 r[N];
-    } v;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v.r[i].x), "=r"(v.r[i].y), "=r"(v.r[i].z), "=r"(v.r[i].w)
-                     : "r"(from + i * 512));
-    return v.x;
+    Eight<__nv_bfloat16> x;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.r.x), "=r"(x.r.y), "=r"(x.r.z), "=r"(x.r.w)
+                 : "r"(from));
+    return x;
 }
 
 // The rounds of a warp in the order that it takes them.
-template <typename T> struct Ahead {
+struct Ahead {
+    using T = __nv_bfloat16;
     int64_t it;
     int which, h0, hi;
     const T *xp, *gp;
@@ -548,7 +544,6 @@ template <typename T> struct Ahead {
     __device__ __forceinline__ void next(const RopeArgs &a, const Work &wk, uint32_t to, int c0,
                                          int n, int sub)
     {
-        constexpr int PIECE = (int)sizeof(Eight<T>) * 32;
         while (h0 >= hi && it < wk.items) {
             if (++which == 2) {
                 which = 0;
@@ -573,11 +568,8 @@ template <typename T> struct Ahead {
                 const bool there = n && h0 + u * SUBS + sub < hi;
                 const T *x = there ? xp : static_cast<const T *>(q.x);
                 const T *g = there ? gp : static_cast<const T *>(q.dy);
-#pragma unroll
-                for (int i = 0; i < (int)sizeof(Eight<T>) / 16; ++i) {
-                    slot_copy(to + 2 * u * PIECE + i * 512, x + i * (16 / sizeof(T)), there);
-                    slot_copy(to + (2 * u + 1) * PIECE + i * 512, g + i * (16 / sizeof(T)), there);
-                }
+                slot_copy(to + 2 * u * PIECE, x, there);
+                slot_copy(to + (2 * u + 1) * PIECE, g, there);
                 xp += SUBS * q.xs[2];
                 gp += SUBS * q.dys[2];
             }
@@ -593,9 +585,8 @@ __global__ void __launch_bounds__(THREADS, ctas_of(BACK, NORM))
 {
     constexpr bool VEC = ROT != ANY;
     constexpr int SUBS = 32 / LPR, U = rounds_of<T, VEC>();
-    constexpr int PIECE = (int)sizeof(Eight<T>) * 32;   // a warp's values of one row group
-    static_assert(!VEC || 2 * U * PIECE == ROUND, "ring");
     constexpr bool RING = ringed<T, BACK, NORM, ROT>();
+    static_assert(!RING || (sizeof(Eight<T>) * 32 == PIECE && 2 * U * PIECE == ROUND), "ring");
     __shared__ Table tab;
     // a warp's cos and sin, ANY: then its rows' partners; at the end the sums
     __shared__ __align__(16) float exchange[WARPS][32 * V + (VEC ? 0 : 32 * V)];
@@ -624,7 +615,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of(BACK, NORM))
     __syncthreads();
     Vals dw[2] = {zeros(), zeros()};
     // RING: the warp's rounds, asked for STAGES - 1 ahead
-    Ahead<T> f;
+    Ahead f;
     const uint32_t slot = RING ? (uint32_t)__cvta_generic_to_shared(slots) +
                                      warp * (STAGES * ROUND) + lane * 16
                                : 0;
@@ -634,7 +625,7 @@ __global__ void __launch_bounds__(THREADS, ctas_of(BACK, NORM))
         f.which = -1;
         f.h0 = f.hi = 0;
         for (int i = 0; i < STAGES - 1; ++i)
-            f.template next<SUBS, U>(a, wk, slot + i * ROUND, k.c0, k.n, sub);
+            f.next<SUBS, U>(a, wk, slot + i * ROUND, k.c0, k.n, sub);
     }
     for (int64_t it = (int64_t)blockIdx.x * WARPS + warp; it < wk.items;
          it += (int64_t)gridDim.x * WARPS) {
@@ -693,15 +684,15 @@ __global__ void __launch_bounds__(THREADS, ctas_of(BACK, NORM))
                     asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
                     from = slot + round % STAGES * ROUND;
                     // (to the stage of the round before this one)
-                    f.template next<SUBS, U>(a, wk, slot + (round + STAGES - 1) % STAGES * ROUND,
+                    f.next<SUBS, U>(a, wk, slot + (round + STAGES - 1) % STAGES * ROUND,
                                              k.c0, k.n, sub);
                     ++round;
                 }
                 auto row = [&](int u) {
                     const int m = h0 + u * SUBS + sub < hi ? k.n : 0;
                     if constexpr (RING) {
-                        xr[u] = slot_load<T>(from + 2 * u * PIECE);
-                        gr[u] = slot_load<T>(from + (2 * u + 1) * PIECE);
+                        xr[u] = slot_load(from + 2 * u * PIECE);
+                        gr[u] = slot_load(from + (2 * u + 1) * PIECE);
                     }
                     const Vals before = sum;
                     const Vals y = one_row<T, LPR, BACK, NORM, ROT>(a, k, xr[u], gr[u], &sum);
