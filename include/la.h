@@ -473,7 +473,8 @@ la_status la_gated_scan_bwd(const la_scan_dims *dims, int32_t dtype, const void 
 size_t la_gated_scan_workspace_size(const la_scan_dims *dims, int32_t dtype, int32_t backward);
 
 /* Bytes of la_gated_scan_fwd's `states` (0 for invalid sizes, and where the
- * backward needs none).  Pure host function. */
+ * backward needs none; with batch 1 and num_seqs > 0 enough for any lengths of
+ * that many packed sequences).  Pure host function. */
 size_t la_gated_scan_states_size(const la_scan_dims *dims);
 
 /* Norms of queries and keys for each head, with the position rotation:

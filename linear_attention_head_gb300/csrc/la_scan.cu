@@ -16,11 +16,11 @@
 // A CTA per SM: a warp has the teams' tiles copied to a ring of stages by TMA, so
 // that copies are under way at all times.
 //
-// A tile takes a team 1.6 us (backward 2.8) however fast its data come.  Where
+// A tile takes a team 1.8 us (backward 2.8) however fast its data come.  Where
 // there are fewer sequences x channels than teams, two or four teams of a CTA take
 // the tiles of a chain in turn, and only the step from the state before a tile to
-// the one after it goes from team to team (0.95 us a tile with four, 128 chains of
-// 64 tiles: 68 us, 106 with one).
+// the one after it goes from team to team (1.1 us a tile with four, 128 chains of
+// 64 tiles: 68 us, 116 with one; backward, with two: 134 and 183).
 // Where there are fewer still, the sequences are cut into segments: a first pass
 // composes each segment's map s -> A s + B (it reads the inputs and writes nothing
 // else), and a segment starts from the maps of those before it.  That pass adds
@@ -33,10 +33,12 @@
 // channels, which walks its sequence alone (serial, below).
 //
 // Bound: HBM, 6 (bf16 gate) or 8 bytes a value forward, 10 or 14 backward, and
-// close to it the issue rate: 19 instructions a value forward, 38 backward, half
-// of the issue slots.  bf16, b4 h32 d128 n8192 (134 M values): forward 129 us, 0.92
-// of HBM's rate, backward 238 us, 0.83.  In segments (b1 h8 n262144, 268 M):
-// forward 410 us, 0.58 (0.97 of the 10 bytes that it moves), backward 666, 0.59.
+// close to it the issue rate: 20 instructions a value forward, 38 backward, half
+// of the issue slots.  bf16, b4 h32 d128 n8192 (134 M values): forward 128 us, 0.93
+// of HBM's rate, backward 242 us, 0.82.  In segments (b1 h8 n262144, 268 M):
+// forward 408 us, 0.58 (0.97 of the 10 bytes that it moves), backward 673, 0.59.
+// Segments and teams are chosen by the number of sequences, not by their lengths:
+// one of 262144 tokens beside 64 of one token is not cut (forward 3.5 ms).
 
 #include <algorithm>
 #include <atomic>
@@ -211,9 +213,9 @@ __device__ __forceinline__ Val times(const Val &x, const Val &y)
 // The same for A, the product of decays of which `least` are the smallest.
 __device__ __forceinline__ Val above_zero(const Val &A, float4 least)
 {
+    auto at = [](float a, float l) { return a == 0.f && l != 0.f ? LEAST : a; };
     const float4 a = A.f();
-    return val(a.x == 0.f && least.x != 0.f ? LEAST : a.x, a.y == 0.f && least.y != 0.f ? LEAST : a.y,
-               a.z == 0.f && least.z != 0.f ? LEAST : a.z, a.w == 0.f && least.w != 0.f ? LEAST : a.w);
+    return val(at(a.x, least.x), at(a.y, least.y), at(a.z, least.z), at(a.w, least.w));
 }
 __device__ __forceinline__ void lower(float4 *least, const Val &d)
 {
@@ -1266,7 +1268,9 @@ cudaError_t pass_empty(const ScanArgs &a, const float *from, float *to, cudaStre
 // alone 0.25 a token of the longest, teams 2.2 a tile of the 608 at once, both
 // no faster than HBM (64 rows of 16 tokens, 4096 channels, forward: 10 against
 // 19; 4 rows of 100: 27 against 8).  Only where that costs little: ScanArgs::
-// states has a state for each SCAN_BLOCK tokens then.
+// states has a state for each SCAN_BLOCK tokens then.  By the sizes alone, with
+// the 6 bytes a value of bf16's forward for all: the backward has to choose as its
+// forward did.
 bool serial(int64_t tiles, int64_t longest, int64_t tokens, int64_t C)
 {
     if (longest > 8 * SCAN_TILE)
@@ -1367,9 +1371,9 @@ cudaError_t run(const ScanArgs &a, Plan k, void *ws, cudaStream_t s)
     // are teams for, unless the maps that a segment starts from cost more than its
     // tiles (0.1 us a map, 4 us a tile for both passes: best at 7 sqrt(run)).
     // More: several teams for one chain, a unit to a group.  The measured border
-    // (64 tiles a chain, us, segments and groups): forward 32 chains 32 and 62, 64
-    // chains 61 and 64, 128 chains 115 and 68; backward 64 chains 106 and 138, 128
-    // chains 180 and 137.
+    // (64 tiles a chain, us, segments and groups): forward 32 chains 33 and 62, 64
+    // chains 56 and 63, 128 chains 106 and 68; backward 64 chains 107 and 133, 128
+    // chains 182 and 134.
     const int64_t chains = (int64_t)a.N * k.parts;
     const int64_t slots = std::min<int64_t>((int64_t)sms * teams, MAX_UNITS);
     const int64_t run = (a.longest + SCAN_TILE - 1) / SCAN_TILE;
