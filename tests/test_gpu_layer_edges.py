@@ -73,8 +73,7 @@ def test_scan_decays_over_their_range(T):
     # rounded log2 e, 1.25 |g| u; below 2^-126 it is 0.  T = 1: a thread alone, 300: a tile.
     H, D = 64, 256
     gate = torch.linspace(-110.0, 88.0, H * D, dtype=torch.float64).float()
-    near = torch.linspace(-0.5, 0.5, 4096, dtype=torch.float64).float()
-    gate[:4096] = near
+    gate[::4] = torch.linspace(-0.5, 0.5, 4096, dtype=torch.float64).float()
     g = torch.zeros(1, T, H, D)
     g[0, 0] = gate.reshape(H, D)
     x, init = torch.zeros(1, T, H, D), torch.ones(1, H, D)
@@ -83,6 +82,7 @@ def test_scan_decays_over_their_range(T):
     for got in (o[0, T - 1], fin[0]):
         got = got.cpu().double().reshape(-1)
         gone = want < 2.0 ** -126 * (1 + 2.0 ** -16)    # (to where the argument may round)
+        assert 0 < int(gone.sum()) < gone.numel()
         assert bool((got[gone] <= 2.0 ** -125).all())
         err = (got - want).abs()[~gone] / want[~gone]
         bound = (4 + 1.25 * gate.double().abs()[~gone]) * R.U
