@@ -361,7 +361,7 @@ def _delta_plain(st):
         outs.append(scale * eG[:, :, c] * (q[:, :, c] @ S) + P[:, :, c] @ Z)
         S = gC[:, :, c] * S + kC[:, :, c].transpose(-1, -2) @ Z
         writes.append(Z)
-    dt, gt = st["q"].dtype, st["g"].dtype
+    dt = st["q"].dtype
     out = (_unpadded(st, torch.cat(outs, 2), dt), S)
     if not both:
         return out
@@ -393,8 +393,8 @@ def _delta_plain(st):
     g = {n: torch.cat(x, 2) for n, x in grads.items()}
     for n in ("q", "k"):
         g[n] = g[n].unflatten(1, (case["qk_heads"], group)).sum(2)
-    out += tuple(_unpadded(st, g[n], dt) for n in ("q", "k", "v"))
-    out += tuple(_unpadded(st, g[n], gt) for n in ("g", "beta"))
+    # the gates' gradients come in the tokens' type, whatever the gates' own
+    out += tuple(_unpadded(st, g[n], dt) for n in ("q", "k", "v", "g", "beta"))
     return out + ((K,) if case["state"] else ())
 
 
@@ -416,7 +416,7 @@ def work(case):
     states = (case["packed"] or B) * H * D * E * 4
     qk, v, gates = 2 * B * T * Hk * D * e, B * T * H * E * e, 2 * B * T * H * f
     if both:    # q, k, v, do, gates, states in; o, gradients out
-        return {"bytes": 2 * (qk + 2 * v + gates) + states * (4 if case["state"] else 1),
+        return {"bytes": 2 * (qk + 2 * v) + gates + 2 * B * T * H * e + states * (4 if case["state"] else 1),
                 "flops": 20 * B * T * H * D * E}
     return {"bytes": qk + 2 * v + gates + states * (2 if case["state"] else 1),
             "flops": 6 * B * T * H * D * E}
