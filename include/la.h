@@ -564,6 +564,104 @@ la_status la_qk_norm_rope_bwd(const la_rope_dims *dims, int32_t dtype, const voi
  * normalize).  Pure host function. */
 size_t la_qk_norm_rope_workspace_size(const la_rope_dims *dims, int32_t dtype);
 
+/* Gated delta rule: the member of the family whose state forgets what it is
+ * about to write over.  Per sequence and value head, tokens in order, S a
+ * D x E fp32 state,
+ *     S' = exp(g_t) S,   e_t = v_t - S'^T k_t,   S = S' + beta_t k_t e_t^T,
+ *     o_t = scale * S^T q_t.
+ * Keys of length 1 and beta in 0..1 keep S from growing; nothing checks it
+ * (la_qk_norm_rope_fwd with weights D^-1/2 normalises q and k so).  g <= 0;
+ * -inf forgets everything (the chunked kernels take gates below -100 as -100).
+ *   batch, seq_len, num_seqs   as la_dims
+ *   heads       H  1..65535 value heads (v, g, beta, o, the states)
+ *   qk_heads    a divisor of H: value head h reads query and key head
+ *               h / (H / qk_heads); dq and dk sum over a group's value heads
+ *   dim_qk      D  1..256;  dim_v  E  1..256
+ *   gate_dtype  la_dtype of g and beta: the token dtype or LA_DTYPE_F32
+ *   *_strides   element strides (batch, token, head); channels are contiguous;
+ *               g and beta are [B,T,H], their strides the same three.  Inputs
+ *               may repeat rows (stride 0), outputs not.  la_gated_delta_fwd
+ *               reads those of q, k, v, g, beta, o; la_gated_delta_bwd all but
+ *               o's. */
+typedef struct la_delta_dims {
+    int32_t batch;
+    int32_t seq_len;
+    int32_t heads;
+    int32_t qk_heads;
+    int32_t dim_qk;
+    int32_t dim_v;
+    int32_t num_seqs;
+    int32_t gate_dtype;
+    int64_t q_strides[3];
+    int64_t k_strides[3];
+    int64_t v_strides[3];
+    int64_t g_strides[3];
+    int64_t beta_strides[3];
+    int64_t o_strides[3];
+    int64_t do_strides[3];
+    int64_t dq_strides[3];
+    int64_t dk_strides[3];
+    int64_t dv_strides[3];
+} la_delta_dims;
+
+/* Forward.
+ *   q, k           [B,T,H_qk,D] of `dtype`;  v [B,T,H,E] of `dtype`
+ *   g, beta        [B,T,H] of gate_dtype: log-decay, and the write's strength
+ *   initial_state  [N,H,D,E] fp32, or NULL for zeros
+ *   cu_seqlens, cu_seqlens_host   as la_fwd
+ *   o              [B,T,H,E] of `dtype` (output)
+ *   final_state    [N,H,D,E] fp32 output, or NULL; may be initial_state itself
+ *   saved          la_gated_delta_saved_size bytes, 256-byte aligned, or NULL:
+ *                  what la_gated_delta_bwd starts from, to be passed to it once
+ *                  or more; then o's rows must lie as v's (below)
+ *   workspace      256-byte aligned, la_gated_delta_workspace_size(..., 0) bytes,
+ *                  (..., 3) with saved (LA_ERR_INVALID_ARG when smaller); may be 0
+ * Kernels: bf16 with D and E multiples of 8 up to 128, strides of q, k, v that
+ * are multiples of 8 elements (and positive where the axis is longer than 1),
+ * and a sequence of more than 16 tokens: chunks of 64 tokens on the tensor
+ * cores, in which every operand that is not an input is split in two bf16
+ * (16 bits of it: the states come out as fp32 arithmetic gives them).  Then q, k,
+ * v and o must start on 16-byte boundaries, or (without saved) the call runs as
+ * every other one: token by token in fp32. */
+la_status la_gated_delta_fwd(const la_delta_dims *dims, int32_t dtype, const void *q,
+                             const void *k, const void *v, const void *g, const void *beta,
+                             float scale, const float *initial_state, const int32_t *cu_seqlens,
+                             const int32_t *cu_seqlens_host, void *o, float *final_state,
+                             void *saved, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/* Backward: gradients of sum(o * d_o) + sum(final_state * d_final_state).
+ *   q ... cu_seqlens   as given to the forward call
+ *   d_o            [B,T,H,E] of `dtype`
+ *   d_final_state  [N,H,D,E] fp32, or NULL for zeros
+ *   saved          what la_gated_delta_fwd wrote for the same arguments, or
+ *                  NULL: computed again in the workspace
+ *   dq, dk         [B,T,H_qk,D] of `dtype`;  dv [B,T,H,E] of `dtype` (outputs)
+ *   dg, dbeta      [B,T,H] dense, of `dtype` whatever gate_dtype is: they carry
+ *                  what products of token-type numbers do
+ *   d_initial_state [N,H,D,E] fp32 output, or NULL
+ *   workspace      256-byte aligned, la_gated_delta_workspace_size bytes with
+ *                  backward = 1 (saved given) or 2 (saved NULL)
+ * Where the forward's sizes and strides give the tensor-core kernels, so do the
+ * backward's; the strides of d_o, dq, dk, dv must then be multiples of 8 too and
+ * every token tensor start on a 16-byte boundary (LA_ERR_INVALID_ARG). */
+la_status la_gated_delta_bwd(const la_delta_dims *dims, int32_t dtype, const void *q,
+                             const void *k, const void *v, const void *g, const void *beta,
+                             const void *d_o, float scale, const float *initial_state,
+                             const float *d_final_state, const int32_t *cu_seqlens,
+                             const int32_t *cu_seqlens_host, const void *saved, void *dq,
+                             void *dk, void *dv, void *dg, void *dbeta, float *d_initial_state,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of la_gated_delta_fwd (backward = 0; 3 with saved) or
+ * la_gated_delta_bwd (1: saved given, 2: not), and bytes of `saved` (0 where the
+ * backward takes none; NULL will do then); 0 for invalid sizes.  cu_seqlens_host:
+ * host copy of cu_seqlens for packed sequences, else NULL.  Pure host functions. */
+size_t la_gated_delta_workspace_size(const la_delta_dims *dims, int32_t dtype,
+                                     const int32_t *cu_seqlens_host, int32_t backward);
+size_t la_gated_delta_saved_size(const la_delta_dims *dims, int32_t dtype,
+                                 const int32_t *cu_seqlens_host);
+
 /* Reads and clears the device-side error words that bounded on-device waits
  * set when they run out (LA_ERR_TIMEOUT), after synchronizing `stream`.
  * Returns LA_OK when no wait ran out, LA_ERR_TIMEOUT when one did, or

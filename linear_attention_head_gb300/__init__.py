@@ -11,6 +11,7 @@ from .api import (alibi_g_gamma, get_device_error, gla_bwd, gla_fwd, kernel_fami
                   la_bwd_dkdv, la_bwd_dq, la_fwd, lightning_attn, lightning_attn_func,
                   lightning_g_gamma, recurrent, recurrent_gla)
 
+from .delta import gated_delta, gated_delta_bwd, gated_delta_fwd
 from .layer import (QkNorm, Rope, gated_scan, gated_scan_bwd, gated_scan_fwd, qk_norm_rope,
                     qk_norm_rope_bwd, qk_norm_rope_fwd, rope_inv_freq, rotary, rotary_bwd,
                     rotary_fwd)
@@ -20,6 +21,7 @@ __all__ = [
     "lib", "alibi_g_gamma", "get_device_error", "gla_bwd", "gla_fwd", "kernel_family", "la_bwd",
     "la_bwd_dkdv", "la_bwd_dq", "la_fwd", "lightning_attn", "lightning_attn_func",
     "lightning_g_gamma", "recurrent", "recurrent_gla",
+    "gated_delta", "gated_delta_bwd", "gated_delta_fwd",
     "QkNorm", "Rope", "gated_scan", "gated_scan_bwd", "gated_scan_fwd", "qk_norm_rope",
     "qk_norm_rope_bwd", "qk_norm_rope_fwd", "rope_inv_freq", "rotary", "rotary_bwd", "rotary_fwd",
 ]

@@ -67,6 +67,16 @@ class LaRopeDims(ctypes.Structure):
                [("pair_axis", ctypes.c_uint8 * 128)]
 
 
+class LaDeltaDims(ctypes.Structure):
+    """Mirror of `la_delta_dims` (include/la.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("batch", "seq_len", "heads", "qk_heads", "dim_qk", "dim_v", "num_seqs",
+                 "gate_dtype")] + \
+               [(n, _i64x3) for n in
+                ("q_strides", "k_strides", "v_strides", "g_strides", "beta_strides", "o_strides",
+                 "do_strides", "dq_strides", "dk_strides", "dv_strides")]
+
+
 class LaError(RuntimeError):
     def __init__(self, status, detail):
         self.status = status
@@ -88,6 +98,7 @@ _sz = ctypes.c_size_t
 _dims_p = ctypes.POINTER(LaDims)
 _scan_p = ctypes.POINTER(LaScanDims)
 _rope_p = ctypes.POINTER(LaRopeDims)
+_delta_p = ctypes.POINTER(LaDeltaDims)
 
 # name -> (restype, argtypes); mirrors include/la.h exactly (float* are passed
 # as void* addresses).
@@ -120,6 +131,12 @@ PROTOTYPES = {
     "la_qk_norm_rope_bwd": (_i32, [_rope_p, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _vp,
                                    _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "la_qk_norm_rope_workspace_size": (_sz, [_rope_p, _i32]),
+    "la_gated_delta_fwd": (_i32, [_delta_p, _i32, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _vp, _vp,
+                                  _vp, _vp, _vp, _vp, _sz, _vp]),
+    "la_gated_delta_bwd": (_i32, [_delta_p, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _vp,
+                                  _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "la_gated_delta_workspace_size": (_sz, [_delta_p, _i32, _vp, _i32]),
+    "la_gated_delta_saved_size": (_sz, [_delta_p, _i32, _vp]),
     "la_debug_withhold_next_handoff": (_i32, [_i32]),
     "la_debug_split_segments": (_i32, [_dims_p, _i32, _vp, _i32]),
     "la_fwd_noalloc": (_i32, [_dims_p, _i32, _vp, _vp, _vp, _vp, _f32, _vp, _i32, _vp, _vp,

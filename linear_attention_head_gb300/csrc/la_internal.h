@@ -312,6 +312,42 @@ cudaError_t scan_read_and_clear_error(cudaStream_t s, int *err);
 // la_debug_withhold_next_handoff's switch of this host thread, reset by the read.
 int take_withheld();
 
+// The gated delta rule (la_delta_token.cu, la_delta_tc.cu): per sequence n and
+// value head h (query and key head h / (H / HK)), S a D x E fp32 state,
+//     S' = exp(g) S,  e = v - S'^T k,  S = S' + beta k e^T,  o = scale S^T q.
+struct DeltaArgs {
+    int B, T, H, HK, D, E, N;
+    const int32_t *cu;          // device [N + 1], or nullptr (dense: N == B)
+    int bf16, gate_bf16;        // token type; type of g and beta
+    float scale;
+    Tok q, k, v, d_o;           // hdiv of q and k: H / HK
+    Tok g, beta;                // [B][T][H]
+    TokOut o, dq, dk, dv;
+    void *dg, *dbeta;           // dense [B][T][H] of the token type
+    const float *init;          // [N][H][D][E] or null
+    float *fin;                 // forward: final states, or null
+    const float *dfin;          // backward: their gradient, or null
+    float *dinit;               // backward: the initial states' gradient, or null
+    int64_t longest;            // tokens of the longest sequence
+    uint8_t *saved;             // tensor-core kernels: what the backward starts from
+    uint8_t *ws;                // scratch, 256-byte aligned
+    int withhold_handoff;       // diagnostic: one hand-off is left out
+};
+// Token by token: every size and type.
+cudaError_t delta_token_forward(const DeltaArgs &a, cudaStream_t s);
+cudaError_t delta_token_backward(const DeltaArgs &a, cudaStream_t s);
+size_t delta_token_bwd_bytes(const DeltaArgs &a);
+// Chunks on the tensor cores: bf16, D and E multiples of 8 up to 128, q, k, v
+// rows on 16-byte boundaries, sequences of more than SHORT_MAX_T tokens.
+bool delta_tc_sized(const DeltaArgs &a);
+bool delta_tc_row_ok(const void *p, const int64_t *strides, int B, int T, int heads);
+size_t delta_tc_saved_bytes(const DeltaArgs &a);
+size_t delta_tc_fwd_bytes(const DeltaArgs &a, bool keep);
+size_t delta_tc_bwd_bytes(const DeltaArgs &a);
+cudaError_t delta_tc_forward(const DeltaArgs &a, cudaStream_t s);
+cudaError_t delta_tc_backward(const DeltaArgs &a, cudaStream_t s);
+
+
 // Norms of queries and keys with the position rotation (la_qk_rope.cu).
 struct RopeTensor {
     const void *x;              // [B][T][heads][D], or null where not read

@@ -1,7 +1,7 @@
 // la_layer_api.cu -- the C entry points of the operators beside the attention
-// (include/la.h): the gated linear recurrence and the norms of queries and
-// keys with the position rotation.  Argument checks, then the launches of
-// la_scan.cu and la_qk_rope.cu.
+// (include/la.h): the gated linear recurrence, the norms of queries and keys
+// with the position rotation, and the gated delta rule.  Argument checks, then
+// the launches of la_scan.cu, la_qk_rope.cu, la_delta_token.cu and la_delta_tc.cu.
 
 #include <climits>
 #include <cmath>
@@ -324,6 +324,118 @@ bool same(const int64_t *x, const int64_t *y)
     return x[0] == y[0] && x[1] == y[1] && x[2] == y[2];
 }
 
+// ---- gated delta rule --------------------------------------------------------
+
+la_status delta_sizes(const la_delta_dims *d, int32_t dtype)
+{
+    if (!d)
+        return fail(LA_ERR_INVALID_ARG, "dims is NULL");
+    if (!known_dtype(dtype))
+        return fail(LA_ERR_INVALID_ARG, "dtype %d is neither LA_DTYPE_BF16 nor LA_DTYPE_F32",
+                    dtype);
+    if (d->gate_dtype != dtype && d->gate_dtype != LA_DTYPE_F32)
+        return fail(LA_ERR_INVALID_ARG, "gate_dtype %d is neither the token dtype nor LA_DTYPE_F32",
+                    d->gate_dtype);
+    if (d->heads < 1 || d->heads > 65535)
+        return fail(LA_ERR_INVALID_ARG, "heads = %d outside 1..65535", d->heads);
+    if (d->qk_heads < 1 || d->qk_heads > d->heads || d->heads % d->qk_heads)
+        return fail(LA_ERR_INVALID_ARG, "qk_heads = %d does not divide heads = %d", d->qk_heads,
+                    d->heads);
+    if (d->dim_v < 1 || d->dim_v > 256)
+        return fail(LA_ERR_UNSUPPORTED, "dim_v = %d: supported range is 1..256", d->dim_v);
+    return check_rows(d->batch, d->seq_len, d->dim_qk);
+}
+
+// Sizes and strides; q.longest as check_packed found it.
+la::DeltaArgs delta_args(const la_delta_dims *d, int32_t dtype, const Sequences &q)
+{
+    la::DeltaArgs a{};
+    a.B = d->batch;
+    a.T = d->seq_len;
+    a.H = d->heads;
+    a.HK = d->qk_heads;
+    a.D = d->dim_qk;
+    a.E = d->dim_v;
+    a.N = q.n;
+    a.longest = q.longest;
+    a.bf16 = dtype == LA_DTYPE_BF16;
+    a.gate_bf16 = d->gate_dtype == LA_DTYPE_BF16;
+    a.q = tok(nullptr, d->q_strides);
+    a.k = tok(nullptr, d->k_strides);
+    a.v = tok(nullptr, d->v_strides);
+    a.q.hdiv = a.k.hdiv = a.H / a.HK;
+    a.g = tok(nullptr, d->g_strides);
+    a.beta = tok(nullptr, d->beta_strides);
+    return a;
+}
+
+// The sequences as a size query sees them; false: not a valid table.
+bool delta_query(const la_delta_dims *d, int32_t dtype, const int32_t *cu_host, la::DeltaArgs *a)
+{
+    if (delta_sizes(d, dtype) != LA_OK)
+        return false;
+    Sequences q;
+    if (cu_host) {
+        // cu_host stands for both tables: only the host's is read
+        if (check_packed(d->batch, d->seq_len, d->num_seqs, cu_host, cu_host, nullptr, &q) != LA_OK)
+            return false;
+    } else {
+        q.n = d->batch;
+        q.longest = d->seq_len;
+    }
+    *a = delta_args(d, dtype, q);
+    a->cu = cu_host;
+    return true;
+}
+
+size_t delta_workspace(const la::DeltaArgs &a, int backward)
+{
+    const bool tc = la::delta_tc_sized(a);
+    if (backward == 0 || backward == 3)
+        return tc ? round256(la::delta_tc_fwd_bytes(a, backward == 3)) : 0;
+    if (!tc)
+        return round256(la::delta_token_bwd_bytes(a));
+    const size_t again = round256(la::delta_tc_saved_bytes(a)) +
+                         round256(la::delta_tc_fwd_bytes(a, true));
+    return round256(la::delta_tc_bwd_bytes(a)) + (backward == 2 ? again : 0);
+}
+
+la_status delta_inputs(const la_delta_dims *d, int32_t dtype, const void *q, const void *k,
+                       const void *v, const void *g, const void *beta, float scale,
+                       const float *init, const int32_t *cu, const int32_t *cu_host,
+                       cudaStream_t s, la::DeltaArgs *a)
+{
+    la_status e = delta_sizes(d, dtype);
+    Sequences sq;
+    if (e || (e = check_in(d->q_strides, "q")) || (e = check_in(d->k_strides, "k")) ||
+        (e = check_in(d->v_strides, "v")) || (e = check_in(d->g_strides, "g")) ||
+        (e = check_in(d->beta_strides, "beta")))
+        return e;
+    if (!std::isfinite(scale))
+        return fail(LA_ERR_INVALID_ARG, "scale is not finite");
+    if ((e = check_packed(d->batch, d->seq_len, d->num_seqs, cu, cu_host, s, &sq)))
+        return e;
+    if ((int64_t)d->batch * d->seq_len > 0 &&
+        ((e = need(q, "q")) || (e = need(k, "k")) || (e = need(v, "v")) || (e = need(g, "g")) ||
+         (e = need(beta, "beta"))))
+        return e;
+    *a = delta_args(d, dtype, sq);
+    a->cu = cu;
+    a->scale = scale;
+    a->q.p = q;
+    a->k.p = k;
+    a->v.p = v;
+    a->g.p = g;
+    a->beta.p = beta;
+    a->init = init;
+    return LA_OK;
+}
+
+bool delta_row(const void *p, const int64_t *st, const la::DeltaArgs &a, int heads)
+{
+    return la::delta_tc_row_ok(p, st, a.B, a.T, heads);
+}
+
 }  // namespace
 
 extern "C" {
@@ -530,6 +642,127 @@ la_status la_qk_norm_rope_bwd(const la_rope_dims *dims, int32_t dtype, const voi
         }
         a.partial = static_cast<float *>(workspace);
         return launched(la::rope_run(true, a, s), "norm and rotation backward");
+    });
+}
+
+size_t la_gated_delta_workspace_size(const la_delta_dims *dims, int32_t dtype,
+                                     const int32_t *cu_seqlens_host, int32_t backward)
+{
+    la::DeltaArgs a;
+    return delta_query(dims, dtype, cu_seqlens_host, &a) ? delta_workspace(a, backward) : 0;
+}
+
+size_t la_gated_delta_saved_size(const la_delta_dims *dims, int32_t dtype,
+                                 const int32_t *cu_seqlens_host)
+{
+    la::DeltaArgs a;
+    if (!delta_query(dims, dtype, cu_seqlens_host, &a) || !la::delta_tc_sized(a))
+        return 0;
+    return round256(la::delta_tc_saved_bytes(a));
+}
+
+la_status la_gated_delta_fwd(const la_delta_dims *dims, int32_t dtype, const void *q,
+                             const void *k, const void *v, const void *g, const void *beta,
+                             float scale, const float *initial_state, const int32_t *cu_seqlens,
+                             const int32_t *cu_seqlens_host, void *o, float *final_state,
+                             void *saved, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return guarded([&]() -> la_status {
+        cudaStream_t s = (cudaStream_t)stream;
+        la::DeltaArgs a;
+        la_status e = delta_inputs(dims, dtype, q, k, v, g, beta, scale, initial_state,
+                                   cu_seqlens, cu_seqlens_host, s, &a);
+        if (e || (e = check_out(dims->o_strides, "o", a.B, a.T, a.H)))
+            return e;
+        if ((int64_t)a.B * a.T > 0 && (e = need(o, "o")))
+            return e;
+        bool tc = la::delta_tc_sized(a);
+        if (tc && !(delta_row(q, dims->q_strides, a, a.HK) &&
+                    delta_row(k, dims->k_strides, a, a.HK) &&
+                    delta_row(v, dims->v_strides, a, a.H) &&
+                    delta_row(o, dims->o_strides, a, a.H))) {
+            if (saved)
+                return fail(LA_ERR_INVALID_ARG, "with saved, q, k, v and o must start on 16-byte "
+                                                "boundaries, with strides of whole 16 bytes");
+            tc = false;
+        }
+        if ((e = check_workspace(workspace, workspace_bytes,
+                                 delta_workspace(a, saved ? 3 : 0))))
+            return e;
+        if (saved && (reinterpret_cast<uintptr_t>(saved) & 255))
+            return fail(LA_ERR_INVALID_ARG, "saved is not 256-byte aligned");
+        a.o = tok_out(o, dims->o_strides);
+        a.fin = final_state;
+        a.saved = static_cast<uint8_t *>(saved);
+        a.ws = static_cast<uint8_t *>(workspace);
+        if (tc) {
+            a.withhold_handoff = la::take_withheld();
+            return launched(la::delta_tc_forward(a, s), "gated delta rule");
+        }
+        return launched(la::delta_token_forward(a, s), "gated delta rule");
+    });
+}
+
+la_status la_gated_delta_bwd(const la_delta_dims *dims, int32_t dtype, const void *q,
+                             const void *k, const void *v, const void *g, const void *beta,
+                             const void *d_o, float scale, const float *initial_state,
+                             const float *d_final_state, const int32_t *cu_seqlens,
+                             const int32_t *cu_seqlens_host, const void *saved, void *dq,
+                             void *dk, void *dv, void *dg, void *dbeta, float *d_initial_state,
+                             void *workspace, size_t workspace_bytes, void *stream)
+{
+    return guarded([&]() -> la_status {
+        cudaStream_t s = (cudaStream_t)stream;
+        la::DeltaArgs a;
+        la_status e = delta_inputs(dims, dtype, q, k, v, g, beta, scale, initial_state,
+                                   cu_seqlens, cu_seqlens_host, s, &a);
+        if (e || (e = check_in(dims->do_strides, "d_o")) ||
+            (e = check_out(dims->dq_strides, "dq", a.B, a.T, a.HK)) ||
+            (e = check_out(dims->dk_strides, "dk", a.B, a.T, a.HK)) ||
+            (e = check_out(dims->dv_strides, "dv", a.B, a.T, a.H)))
+            return e;
+        if ((int64_t)a.B * a.T > 0 &&
+            ((e = need(d_o, "d_o")) || (e = need(dq, "dq")) || (e = need(dk, "dk")) ||
+             (e = need(dv, "dv")) || (e = need(dg, "dg")) || (e = need(dbeta, "dbeta"))))
+            return e;
+        const bool tc = la::delta_tc_sized(a);
+        if (tc && !(delta_row(q, dims->q_strides, a, a.HK) &&
+                    delta_row(k, dims->k_strides, a, a.HK) &&
+                    delta_row(v, dims->v_strides, a, a.H) &&
+                    delta_row(d_o, dims->do_strides, a, a.H) &&
+                    delta_row(dq, dims->dq_strides, a, a.HK) &&
+                    delta_row(dk, dims->dk_strides, a, a.HK) &&
+                    delta_row(dv, dims->dv_strides, a, a.H)))
+            return fail(LA_ERR_INVALID_ARG,
+                        "q, k, v, d_o, dq, dk and dv must start on 16-byte boundaries, with "
+                        "strides of whole 16 bytes");
+        if ((e = check_workspace(workspace, workspace_bytes, delta_workspace(a, saved ? 1 : 2))))
+            return e;
+        if (saved && (reinterpret_cast<uintptr_t>(saved) & 255))
+            return fail(LA_ERR_INVALID_ARG, "saved is not 256-byte aligned");
+        a.d_o = tok(d_o, dims->do_strides);
+        a.dq = tok_out(dq, dims->dq_strides);
+        a.dk = tok_out(dk, dims->dk_strides);
+        a.dv = tok_out(dv, dims->dv_strides);
+        a.dg = dg;
+        a.dbeta = dbeta;
+        a.dfin = d_final_state;
+        a.dinit = d_initial_state;
+        a.ws = static_cast<uint8_t *>(workspace);
+        if (!tc)
+            return launched(la::delta_token_backward(a, s), "gated delta rule backward");
+        a.withhold_handoff = la::take_withheld();
+        a.saved = static_cast<uint8_t *>(const_cast<void *>(saved));
+        if (!saved) {   // the forward again, without its outputs
+            la::DeltaArgs f = a;
+            const size_t own = round256(la::delta_tc_bwd_bytes(a));
+            f.withhold_handoff = 0;
+            f.saved = a.saved = a.ws + own;
+            f.ws = f.saved + round256(la::delta_tc_saved_bytes(a));
+            if ((e = launched(la::delta_tc_forward(f, s), "gated delta rule states")))
+                return e;
+        }
+        return launched(la::delta_tc_backward(a, s), "gated delta rule backward");
     });
 }
 
