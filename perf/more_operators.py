@@ -221,7 +221,7 @@ def _norm_own(st):
     h, y = la.block_norm_fwd(st["x"], **kw)
     if case["direction"] == "forward":
         return (h, y) if y is not None else h
-    g = la.block_norm_bwd(st["x"], st["dh"], st["dy"], h=h, **kw)
+    g = la.block_norm_bwd(st["x"], st["dh"], st["dy"], **kw)
     return tuple(t for t in (h, y) + tuple(g) if t is not None)
 
 
