@@ -798,7 +798,7 @@ la_status la_get_device_error(void *stream)
     cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
     if (e == cudaSuccess)
         e = la::tc_read_and_clear_error((cudaStream_t)stream, &err);
-    int err2 = 0, err3 = 0, err4 = 0, err5 = 0;
+    int err2 = 0, err3 = 0, err4 = 0, err5 = 0, err6 = 0;
     if (e == cudaSuccess)
         e = la::token_read_and_clear_error((cudaStream_t)stream, &err2);
     if (e == cudaSuccess)
@@ -807,10 +807,12 @@ la_status la_get_device_error(void *stream)
         e = la::decode_read_and_clear_error((cudaStream_t)stream, &err4);
     if (e == cudaSuccess)
         e = la::scan_read_and_clear_error((cudaStream_t)stream, &err5);
+    if (e == cudaSuccess)
+        e = la::delta_read_and_clear_error((cudaStream_t)stream, &err6);
     if (e != cudaSuccess)
         return cuda_fail(e, "la_get_device_error");
     if (!err)
-        err = err2 ? err2 : err3 ? err3 : err4 ? err4 : err5;
+        err = err2 ? err2 : err3 ? err3 : err4 ? err4 : err5 ? err5 : err6;
     else if ((err & 0xff) != LA_ERR_BOUNDS && (err3 & 0xff) == LA_ERR_BOUNDS)
         err = err3;
     if ((err & 0xff) == LA_ERR_BOUNDS)

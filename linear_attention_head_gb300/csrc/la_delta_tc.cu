@@ -1,15 +1,1464 @@
-// la_delta_tc.cu -- the gated delta rule in chunks on the tensor cores (none yet:
-// every call runs token by token).
-#include "la_internal.h"
+// la_delta_tc.cu -- the gated delta rule in chunks of 64 tokens on the tensor
+// cores (tcgen05, TMA, TMEM): bf16, D and E multiples of 8 up to 128.
+//
+// Per sequence and value head, S (D x E) entering a chunk, G the running sums of
+// g in it, M_ij = exp(G_i - G_j) for j <= i, token i's write beta_i k_i e_i^T:
+//
+//     A = strictly lower part of M * (K K^T),   (I + A beta) B = A
+//     X = V - e^G K S,                          Eps = X - B (beta X)
+//     O = scale e^G Q S + P (beta Eps),         P = scale M * (Q K^T)
+//     S' = e^G_C S + K^T (kappa beta Eps),      kappa_j = exp(G_C - G_j)
+//
+// and back, K' = dL/dS' (called G below where no confusion arises):
+//
+//     W = P^T dO + kappa K K',                  R = W - B^T (beta W)
+//     dV = beta R,  dbeta_i = R_i . Eps_i
+//     dL/dS = e^G_C K' + (scale e^G Q)^T dO - (e^G K)^T dV
+//     dQ = scale e^G dO S^T + W1 K,             W1 = scale M * (dO Eps^T) beta
+//     dK = -e^G dV S^T + W2 K                   (row: as the one that reads S)
+//        + W1^T Q + W2^T K + kappa beta Eps K'^T    (col: as the one that writes)
+//        with W2 = -M * (dV Eps^T) beta, strictly lower
+//     dg_t = sum over i >= t in the chunk of (q_i.dq_i + k_i.(row_i - col_i)) + <S', K'>.
+//
+// B needs neither S nor a division by beta.  Four kernels:
+//   delta_prep     B of every chunk, all chunks in parallel (fp32, mma.sync for K K^T)
+//   delta_sweep    <false>: the forward, a CTA a (sequence, head), chunk by chunk
+//                  <true>: the backward's K', from the last chunk to the first
+//   delta_grads    dQ, dK, dg, dbeta, all chunks in parallel
+//
+// The sweeps work transposed: the 128 TMEM lanes are the value channels, the
+// columns tokens or key channels.  So S^T, X^T, Eps^T come out of one product and
+// go into the next as its A operand through TMEM, and K, Q, B are B operands as
+// they lie.  A chunk is a chain: K S -> X -> B (beta X) -> Eps -> K^T Eps -> S.
+// Chunks of 64: B costs a quarter of what 128 would, and half the bytes a token.
+//
+// Precision: inputs are exact in bf16; every other operand of the chain (S, X,
+// Eps, B, P) is held as two bf16, hi + lo, 16 bits of it, and multiplied
+// hi hi + hi lo + lo hi with fp32 sums: the states stay within 2^-17 a factor
+// instead of 2^-9.  The tensor cores have room: the chain's latency is what a
+// chunk takes.  delta_grads rounds its operands (S, K', Eps, R, W1, W2) to bf16
+// once: its outputs are bf16 gradients that no later chunk depends on.
+
+#include <climits>
+
+#include "la_tc_common.cuh"
 
 namespace la {
+namespace {
 
-bool delta_tc_sized(const DeltaArgs &) { return false; }
-bool delta_tc_row_ok(const void *, const int64_t *, int, int, int) { return false; }
-size_t delta_tc_saved_bytes(const DeltaArgs &) { return 0; }
-size_t delta_tc_fwd_bytes(const DeltaArgs &, bool) { return 0; }
-size_t delta_tc_bwd_bytes(const DeltaArgs &) { return 0; }
-cudaError_t delta_tc_forward(const DeltaArgs &, cudaStream_t) { return cudaErrorNotSupported; }
-cudaError_t delta_tc_backward(const DeltaArgs &, cudaStream_t) { return cudaErrorNotSupported; }
+constexpr int C = 64;                           // tokens a chunk
+constexpr int BTILE = 16384;                    // B hi, B lo: [64][64] bf16 each
+constexpr int STILE = 32768;                    // S^T or K'^T: [2][128 e][64 d] bf16
+constexpr int ETILE = 16384;                    // Eps or R: [2][64 tokens][64 e] bf16
+constexpr int TAB = C * 16;                     // {e^G, beta, kappa, G} a token
+constexpr float LEAST_GATE = -100.f;            // e^-100 is 0 beside anything kept
+
+// Where a chunk lies.  Chunk slots: ceil(T / 64) a dense row; cu[n] / 64 + n on
+// packed, which leaves every sequence room for its ceil(len / 64).
+__host__ __device__ inline int64_t slots_of(int N, int T, bool packed)
+{
+    return packed ? (int64_t)T / C + N : (int64_t)N * ((T + C - 1) / C);
+}
+struct Seq {
+    int n;
+    int64_t row, bos, len, slot;        // slot: of the sequence's first chunk
+};
+__device__ __forceinline__ Seq sequence(const int32_t *cu, int T, int n)
+{
+    Seq q;
+    q.n = n;
+    if (cu) {
+        q.row = 0;
+        q.bos = cu[n];
+        q.len = (int64_t)cu[n + 1] - q.bos;
+        q.slot = q.bos / C + n;
+    } else {
+        q.row = n;
+        q.bos = 0;
+        q.len = T;
+        q.slot = (int64_t)n * ((T + C - 1) / C);
+    }
+    return q;
+}
+// The sequence that slot belongs to (the last one whose first slot is not above).
+__device__ __forceinline__ Seq sequence_of_slot(const int32_t *cu, int T, int N, int64_t slot)
+{
+    if (!cu)
+        return sequence(nullptr, T, (int)(slot / ((T + C - 1) / C)));
+    int lo = 0, hi = N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (cu[mid] / C + mid <= slot)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return sequence(cu, T, lo);
+}
+
+struct Scratch {
+    uint8_t *b;         // [slot][H] BTILE
+    float4 *tab;        // [slot][H][64]
+    uint8_t *s, *e;     // [slot][H] STILE, ETILE (kept for the backward; or null)
+    uint8_t *k, *r;     // backward: [slot][H] STILE, ETILE
+    float *dqp, *dkp;   // backward, shared heads: [B][T][H][D] fp32
+};
+
+__device__ __forceinline__ float gate_at(const Tok &g, int bf16, int64_t row, int64_t t, int h)
+{
+    const int64_t at = row * g.sb + t * g.st + (int64_t)h * g.sh;
+    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(g.p)[at])
+                : static_cast<const float *>(g.p)[at];
+}
+
+// (x0, x1) as hi + lo, each two bf16.
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo)
+{
+    hi = pack_bf16x2(x0, x1);
+    lo = pack_bf16x2(x0 - bf16lo(hi), x1 - bf16hi(hi));
+}
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// ---- B of every chunk -----------------------------------------------------------
+//
+// K K^T by mma.sync (bf16 exact, fp32 sums), then the triangular system in fp32:
+// diagonal blocks of 16 by substitution, a thread a column, then blocks joined
+// 16 -> 32 -> 64:  B21 = (I - B22 beta) A21 (I - beta B11).
+
+constexpr int PREP = 128;
+constexpr int KP = 136;         // bf16 a row of K in shared memory
+constexpr int AP = 68;          // floats a row of A
+
+__device__ __forceinline__ void ldm_x4(uint32_t (&r)[4], const void *p)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_u32(p))
+                 : "memory");
+}
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3},"
+                 " {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The join of blocks of W rows: `first` is the pair's first row; M holds the second
+// blocks' rows alone.  Threads of the pair: t of n.
+template <int W>
+__device__ __forceinline__ void join_first(const float (*A)[AP], const float *beta, float (*M)[AP],
+                                           int first, int t, int n)
+{
+    for (int x = t; x < W * W / 4; x += n) {
+        const int i = first + W + x / (W / 4), j = first + 4 * (x % (W / 4));
+        float4 m = *reinterpret_cast<const float4 *>(&A[i][j]);
+#pragma unroll 4
+        for (int k = j + 1 - first; k < W; ++k) {       // B11 is strictly lower
+            const float f = A[i][first + k] * beta[first + k];
+            const float4 b = *reinterpret_cast<const float4 *>(&A[first + k][j]);
+            m.x = fmaf(-f, b.x, m.x);
+            m.y = fmaf(-f, b.y, m.y);
+            m.z = fmaf(-f, b.z, m.z);
+            m.w = fmaf(-f, b.w, m.w);
+        }
+        *reinterpret_cast<float4 *>(&M[i - W - first / 2][j]) = m;
+    }
+}
+template <int W>
+__device__ __forceinline__ void join_second(float (*A)[AP], const float *beta,
+                                            const float (*M)[AP], int first, int t, int n)
+{
+    for (int x = t; x < W * W / 4; x += n) {
+        const int ii = x / (W / 4), i = first + W + ii, j = first + 4 * (x % (W / 4));
+        float4 m = *reinterpret_cast<const float4 *>(&M[first / 2 + ii][j]);
+#pragma unroll 4
+        for (int k = 0; k < ii; ++k) {                  // B22 is strictly lower
+            const float f = A[i][first + W + k] * beta[first + W + k];
+            const float4 b = *reinterpret_cast<const float4 *>(&M[first / 2 + k][j]);
+            m.x = fmaf(-f, b.x, m.x);
+            m.y = fmaf(-f, b.y, m.y);
+            m.z = fmaf(-f, b.z, m.z);
+            m.w = fmaf(-f, b.w, m.w);
+        }
+        *reinterpret_cast<float4 *>(&A[i][j]) = m;
+    }
+}
+
+__global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, const Scratch sc)
+{
+    __shared__ __align__(16) __nv_bfloat16 ks[C][KP];
+    __shared__ __align__(16) float A[C][AP], M[C / 2][AP];
+    __shared__ float G[C], beta[C], part[2];
+    const int h = blockIdx.x % a.H;
+    const int64_t slot = blockIdx.x / a.H;
+    const Seq q = sequence_of_slot(a.cu, a.T, a.N, slot);
+    const int64_t t0 = (slot - q.slot) * C;
+    if (t0 >= q.len)
+        return;
+    const int n = (int)min((int64_t)C, q.len - t0);     // tokens of this chunk
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t tile = slot * a.H + h;
+
+    const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k.p) + q.row * a.k.sb +
+                             (q.bos + t0) * a.k.st + (int64_t)(h / a.k.hdiv) * a.k.sh;
+    const int ksteps = (a.D + 15) / 16;
+    for (int x = tid; x < C * 2 * ksteps; x += PREP) {
+        const int i = x / (2 * ksteps), c = x % (2 * ksteps);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (i < n && 8 * c < a.D)
+            v = *reinterpret_cast<const uint4 *>(k + i * a.k.st + 8 * c);
+        *reinterpret_cast<uint4 *>(&ks[i][8 * c]) = v;
+    }
+    if (tid < C) {
+        float g = 0.f, b = 0.f;
+        if (tid < n) {
+            g = fmaxf(gate_at(a.g, a.gate_bf16, q.row, q.bos + t0 + tid, h), LEAST_GATE);
+            b = gate_at(a.beta, a.gate_bf16, q.row, q.bos + t0 + tid, h);
+        }
+#pragma unroll
+        for (int m = 1; m < 32; m *= 2) {
+            const float y = __shfl_up_sync(0xffffffffu, g, m);
+            if (lane >= m)
+                g += y;
+        }
+        if (lane == 31)
+            part[warp] = g;
+        G[tid] = g;
+        beta[tid] = b;
+    }
+    __syncthreads();
+    if (tid < C) {
+        const float g = tid < 32 ? G[tid] : G[tid] + part[0];
+        const float all = part[0] + part[1];
+        sc.tab[tile * C + tid] = make_float4(expf(g), beta[tid], expf(all - g), g);
+        __syncwarp();
+        G[tid] = g;
+    }
+    __syncthreads();
+
+    // rows 16 warp .. of K K^T, columns up to the diagonal block
+    {
+        const int r = lane & 15, half = lane >> 4;
+        float acc[8][4] = {};
+        for (int kk = 0; kk < ksteps; ++kk) {
+            uint32_t x[4];
+            ldm_x4(x, &ks[16 * warp + r][16 * kk + 8 * half]);
+#pragma unroll
+            for (int jb = 0; jb < 4; ++jb)
+                if (jb <= warp) {
+                    uint32_t y[4];      // columns 16 jb: 0, 2 its first eight, 1, 3 the others
+                    ldm_x4(y, &ks[16 * jb + r][16 * kk + 8 * half]);
+                    mma_16816(acc[2 * jb], x, y[0], y[2]);
+                    mma_16816(acc[2 * jb + 1], x, y[1], y[3]);
+                }
+        }
+#pragma unroll
+        for (int nb = 0; nb < 8; ++nb)
+            if (nb < 2 * (warp + 1))
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int i = 16 * warp + (lane >> 2) + 8 * (v >> 1);
+                    const int j = 8 * nb + 2 * (lane & 3) + (v & 1);
+                    A[i][j] = j < i ? expf(G[i] - G[j]) * acc[nb][v] : 0.f;
+                }
+    }
+    __syncthreads();
+    // diagonal blocks: column lane of block warp
+    {
+        const int b0 = 16 * warp, c = lane & 15;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s = A[b0 + i][b0 + c];
+#pragma unroll
+            for (int m = 0; m < i; ++m)
+                s = fmaf(-A[b0 + i][b0 + m] * beta[b0 + m], x[m], s);
+            x[i] = s;
+        }
+        __syncwarp();
+        if (lane < 16)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                A[b0 + i][b0 + c] = x[i];
+    }
+    __syncthreads();
+    join_first<16>(A, beta, M, 32 * (tid >> 6), tid & 63, 64);
+    __syncthreads();
+    join_second<16>(A, beta, M, 32 * (tid >> 6), tid & 63, 64);
+    __syncthreads();
+    join_first<32>(A, beta, M, 0, tid, PREP);
+    __syncthreads();
+    join_second<32>(A, beta, M, 0, tid, PREP);
+    __syncthreads();
+    // hi and lo as 128B-swizzled rows, the shared-memory image that the sweeps load
+    {
+        const int i = tid >> 1, half = tid & 1;
+        uint8_t *to = sc.b + tile * BTILE + i * 128;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int c16 = 4 * half + x;
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int j = 8 * c16 + 2 * p;
+                split2(j < i ? A[i][j] : 0.f, j + 1 < i ? A[i][j + 1] : 0.f, hi[p], lo[p]);
+            }
+            uint8_t *at = to + ((c16 ^ (i & 7)) << 4);
+            *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(at + BTILE / 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+    }
+}
+
+// ---- the sweeps -----------------------------------------------------------------
+//
+// 448 threads: warp 0 loads, warp 1 issues the products, warps 2-9 ("chain") carry
+// X, Eps (or W, R) and the state between products, each a quarter of the lanes and
+// half of the columns, warps 10-13 ("side") make P and O (or P and scale e^G Q).
+// Q and K of a chunk lie as one 128-row tile: [Q; K] K^T gives the scores in lanes
+// 0-63 (lanes 64-127, K K^T, are not used).
+
+constexpr int SWEEP = 448;
+constexpr int CHAIN = 256, SIDE = 128;
+constexpr int NS = 2;                           // stages
+constexpr int QK = 0, VD = 32768, BB = 49152, STAGE = 65536;
+constexpr int POFF = NS * STAGE;                // P hi, lo: [64][64] bf16 each
+constexpr int QOFF = POFF + 16384;              // backward: scale e^G Q, hi, lo
+constexpr int Q2 = 16384;                       // bytes of one of them: [2][64][64] bf16
+template <bool BWD> struct SweepLayout {
+    static constexpr int TOFF = QOFF + (BWD ? 2 * Q2 : 0);
+    static constexpr int MOFF = TOFF + NS * TAB;
+    static constexpr int NBAR = 4 * NS + 11;
+    static constexpr int SLOT = MOFF + NBAR * 8;
+    static constexpr int ABORT = SLOT + 4;
+    static constexpr int RANK = ABORT + 4;
+    static constexpr int DYN = RANK + 4 + 1024;
+    static_assert(DYN <= 232448, "shared memory per CTA");
+};
+// TMEM columns: the state fp32, its hi and lo; the chain's accumulator; a second
+// one (O's inter term; back: P^T dO); scores, then O's intra term; the chain's
+// operand (beta X, then kappa beta Eps), hi and lo
+constexpr uint32_t TS = 0, TSH = 128, T1 = 256, T2 = 320, TR = 384, TY = 448, TCOLS = 512;
+// an operand of 64 tokens in 64 columns: for each half of the tokens 16 columns of
+// hi, 16 of lo, so that the threads of a half write among columns of their own
+__device__ __forceinline__ uint32_t tok_col(int kk, int lo)
+{
+    return 32 * (kk >> 1) + 8 * (kk & 1) + 16 * lo;
+}
+
+struct SweepParams {
+    CUtensorMap mq, mk, mv;     // mv: v, or back: do
+    DeltaArgs a;
+    Scratch sc;
+};
+
+// 32 values a lane (this lane's channel, tokens 32 half ..) to bf16 rows, a token
+// a row: neighbouring lanes trade, each stores a pair of channels of every other
+// token.  at(token) gives the place of channel 0 or null.
+template <typename F>
+__device__ __forceinline__ void store_tokens(const float (&x)[32], int half, int e, int E, F at)
+{
+    const bool odd = e & 1;
+#pragma unroll
+    for (int m = 0; m < 16; ++m) {
+        const float mine = odd ? x[2 * m + 1] : x[2 * m], other = odd ? x[2 * m] : x[2 * m + 1];
+        const float got = __shfl_xor_sync(0xffffffffu, other, 1);
+        const uint32_t pair = odd ? pack_bf16x2(got, mine) : pack_bf16x2(mine, got);
+        const int j = 32 * half + 2 * m + odd;
+        if (uint8_t *p = at(j); p && e < E)
+            *reinterpret_cast<uint32_t *>(p) = pair;
+    }
+}
+// place of the pair of channels of e in row j of a [2][rows][64] swizzled tile
+__device__ __forceinline__ uint32_t image_pair(int rows, int j, int e)
+{
+    return (uint32_t)((e >> 6) * rows * 128 + j * 128 + ((((e & 63) >> 3) ^ (j & 7)) << 4) +
+                      (e & 6) * 2);
+}
+
+template <bool BWD>
+__global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_constant__ SweepParams P)
+{
+    using L = SweepLayout<BWD>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+    const DeltaArgs &a = P.a;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::MOFF);    // Q, K, table
+    uint64_t *fullv = full + NS, *fullb = full + 2 * NS, *empty = full + 3 * NS;
+    uint64_t *bars = full + 4 * NS;
+    uint64_t *sc_full = bars;           // scores
+    uint64_t *ks_full = bars + 1;       // K S (back: K K', and P^T dO)
+    uint64_t *e_full = bars + 2;        // Eps (R)
+    uint64_t *s_full = bars + 3;        // the state
+    uint64_t *o_full = bars + 4;        // O
+    uint64_t *s_ready = bars + 5;       // the state's hi, lo and its decayed fp32
+    uint64_t *y_ready = bars + 6;       // X and beta X
+    uint64_t *w_ready = bars + 7;       // what the state takes, and beta Eps
+    uint64_t *p_ready = bars + 8;       // P (back: the Q lanes' part is q_ready)
+    uint64_t *q_ready = bars + 9;       // forward: O read; back: scale e^G Q
+    uint64_t *drain = bars + 10;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::SLOT);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::ABORT);
+    volatile int *rank_slot = reinterpret_cast<volatile int *>(sm + L::RANK);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&fullv[i], 1);
+            mbar_init(&fullb[i], 1);
+            mbar_init(&empty[i], 1 + CHAIN / 32 + SIDE / 32);
+        }
+        for (int i = 0; i < 5; ++i)
+            mbar_init(&bars[i], 1);
+        mbar_init(s_ready, CHAIN);
+        mbar_init(y_ready, CHAIN);
+        mbar_init(w_ready, CHAIN);
+        mbar_init(p_ready, C);
+        mbar_init(q_ready, BWD ? C : SIDE);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        *rank_slot = blockIdx.x / a.H;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tslot, TCOLS);
+        tmem_relinquish();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&P.mq);
+        prefetch_tmap(&P.mk);
+        prefetch_tmap(&P.mv);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = *tslot;
+    const int h = blockIdx.x % a.H;
+    // packed sequences the longest first: a late long one would run alone.  Each
+    // CTA counts for itself which it is (N * N compares over 448 threads).
+    if (a.cu && a.N > 1 && a.N <= 256) {
+        const int rank = blockIdx.x / a.H;
+        for (int n = threadIdx.x; n < a.N; n += SWEEP) {
+            const int len = a.cu[n + 1] - a.cu[n];
+            int before = 0;
+            for (int m = 0; m < a.N; ++m) {
+                const int other = a.cu[m + 1] - a.cu[m];
+                before += other > len || (other == len && m < n);
+            }
+            if (before == rank)
+                *rank_slot = n;
+        }
+        __syncthreads();
+    }
+    const Seq sq = sequence(a.cu, a.T, *rank_slot);
+    const int nc = (int)((sq.len + C - 1) / C);
+    // c counts chunks in the order of the sweep
+    auto chunk = [&](int c) { return BWD ? nc - 1 - c : c; };
+    auto tokens = [&](int c) { return (int)min((int64_t)C, sq.len - (int64_t)chunk(c) * C); };
+    auto tile_of = [&](int c) { return (sq.slot + chunk(c)) * a.H + h; };
+    const float4 *tabs = reinterpret_cast<const float4 *>(sm + L::TOFF);
+
+    if (warp == 0) {
+        // ------------------------------------------------------------- loads
+        if (lane == 0) {
+            const int hq = h / a.q.hdiv;
+            int issued = 0;
+            for (int c = 0; c < nc; ++c) {
+                const int s = c % NS;
+                if (c >= NS && !bwait(&empty[s], (c / NS - 1) & 1, abort_flag))
+                    break;
+                const int t = (int)(sq.bos + (int64_t)chunk(c) * C);
+                uint8_t *st = sm + s * STAGE;
+                mbar_arrive_expect_tx(&full[s], 32768 + TAB);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    tma_load_4d(st + QK + b * 16384, &P.mq, &full[s], 64 * b, hq, t, (int)sq.row);
+                    tma_load_4d(st + QK + b * 16384 + 8192, &P.mk, &full[s], 64 * b, hq, t,
+                                (int)sq.row);
+                }
+                bulk_load(sm + L::TOFF + s * TAB, P.sc.tab + tile_of(c) * C, TAB, &full[s]);
+                mbar_arrive_expect_tx(&fullv[s], 16384);
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    tma_load_4d(st + VD + b * 8192, &P.mv, &fullv[s], 64 * b, h, t, (int)sq.row);
+                mbar_arrive_expect_tx(&fullb[s], BTILE);
+                bulk_load(st + BB, P.sc.b + tile_of(c) * BTILE, BTILE, &fullb[s]);
+                ++issued;
+            }
+            for (int c = issued > NS ? issued - NS : 0; c < issued; ++c) {
+                drain_wait(&full[c % NS], (c / NS) & 1);
+                drain_wait(&fullv[c % NS], (c / NS) & 1);
+                drain_wait(&fullb[c % NS], (c / NS) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------- products
+        const uint32_t sb = smem_u32(sm);
+        constexpr uint32_t id64 = idesc_bf16_f32(128, 64, 0, 0);       // B K-major
+        constexpr uint32_t id64mn = idesc_bf16_f32(128, 64, 0, 1);     // B MN-major
+        constexpr uint32_t id128mn = idesc_bf16_f32(128, 128, 0, 1);
+        constexpr uint32_t id64mm = idesc_bf16_f32(128, 64, 1, 1);     // both MN-major
+        constexpr uint32_t id128mm = idesc_bf16_f32(128, 128, 1, 1);
+        const uint32_t ph = sb + POFF, pl = ph + 8192;
+        auto stage = [&](int c) { return sb + (uint32_t)((c % NS) * STAGE); };
+        // rows `row` .. of the [Q; K] tile as the K-major B operand, k-step kk of D
+        auto rows_desc = [&](uint32_t st, int row, int kk) {
+            return sdesc_sw128(st + QK + row * 128 + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024);
+        };
+        // as an MN-major operand (D along M or N), k-step kk of the tokens
+        auto cols_desc = [&](uint32_t st, int row, int kk) {
+            return sdesc_sw128(st + QK + row * 128 + kk * 2048, 16384, 1024);
+        };
+        auto scores = [&](int c) {      // [Q; K] K^T
+            const uint32_t st = stage(c);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+                mma_ss(tm + TR, rows_desc(st, 0, kk), rows_desc(st, 64, kk), id64, kk > 0);
+            mma_commit(sc_full);
+        };
+        auto state_times = [&](uint32_t d, int c, int row) {
+            const uint32_t st = stage(c);
+#pragma unroll
+            for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_ts(tm + d, tm + TSH + 64 * lo + 8 * kk, rows_desc(st, row, kk), id64,
+                           lo + kk > 0);
+        };
+        // The tokens past a packed sequence's end are another's: zeros in their
+        // place (the loads fill with zeros past the tensor's end).
+        auto clear_tail = [&](int c) {
+            const int n = tokens(c);
+            if (!a.cu || n == C)
+                return true;
+            if (!warp_all(bwait(&fullv[c % NS], (c / NS) & 1, abort_flag)))
+                return false;
+            uint8_t *st = sm + (c % NS) * STAGE;
+            const uint4 z = make_uint4(0, 0, 0, 0);
+            for (int x = lane; x < (C - n) * 8; x += 32) {
+                const int off = (n + x / 8) * 128 + (x % 8) * 16;
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    *reinterpret_cast<uint4 *>(st + QK + b * 8192 + off) = z;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    *reinterpret_cast<uint4 *>(st + VD + b * 8192 + off) = z;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            return true;
+        };
+        auto stage_in = [&](int c) {
+            return warp_all(bwait(&full[c % NS], (c / NS) & 1, abort_flag)) && clear_tail(c);
+        };
+        auto both = [&](uint64_t *bar, int c) {
+            const bool ok = warp_all(bwait(bar, c & 1, abort_flag));
+            tc_fence_after();
+            return ok;
+        };
+        const bool one = lane == 0;
+        bool any = false;
+        if (BWD && nc > 0 && stage_in(0)) {
+            any = true;
+            if (one)
+                scores(0);
+            __syncwarp();
+            auto prior = [&](int c) {   // P^T dO
+                if (!both(p_ready, c) ||
+                    !warp_all(bwait(&fullv[c % NS], (c / NS) & 1, abort_flag)))
+                    return false;
+                if (one) {
+                    const uint32_t st = stage(c);
+#pragma unroll
+                    for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ss(tm + T2, sdesc_sw128(st + VD + kk * 2048, 8192, 1024),
+                                   sdesc_sw128((lo ? pl : ph) + kk * 2048, 8192, 1024), id64mm,
+                                   lo + kk > 0);
+                }
+                __syncwarp();
+                return true;
+            };
+            bool ok = prior(0);
+            for (int c = 0; ok && c < nc; ++c) {
+                const uint32_t st = stage(c);
+                if (!(ok = both(s_ready, c)))
+                    break;
+                if (one) {
+                    state_times(T1, c, 64);
+                    mma_commit(ks_full);
+                }
+                __syncwarp();
+                if (!(ok = both(q_ready, c)))
+                    break;
+                if (one)    // dO^T (scale e^G Q)
+#pragma unroll
+                    for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ss(tm + TS, sdesc_sw128(st + VD + kk * 2048, 8192, 1024),
+                                   sdesc_sw128(sb + QOFF + lo * Q2 + kk * 2048, 8192, 1024),
+                                   id128mm, 1);
+                __syncwarp();
+                if (c + 1 < nc) {
+                    if (!(ok = stage_in(c + 1)))
+                        break;
+                    if (one)
+                        scores(c + 1);
+                    __syncwarp();
+                }
+                if (!(ok = warp_all(bwait(&fullb[c % NS], (c / NS) & 1, abort_flag)) &&
+                           both(y_ready, c)))
+                    break;
+                if (one) {
+#pragma unroll
+                    for (int x = 0; x < 3; ++x)     // hi hi, lo hi, hi lo
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ts(tm + T1, tm + TY + tok_col(kk, x == 1),
+                                   sdesc_sw128(st + BB + (x == 2 ? BTILE / 2 : 0) + kk * 2048, 8192,
+                                               1024),
+                                   id64mn, 1);
+                    mma_commit(e_full);
+                }
+                __syncwarp();
+                if (!(ok = both(w_ready, c)))
+                    break;
+                if (one) {
+#pragma unroll
+                    for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ts(tm + TS, tm + TY + tok_col(kk, lo), cols_desc(st, 64, kk),
+                                   id128mn, 1);
+                    mma_commit(s_full);
+                    mma_commit(&empty[c % NS]);
+                }
+                __syncwarp();
+                if (c + 1 < nc)
+                    ok = prior(c + 1);
+            }
+        } else if (!BWD) {
+            for (int c = 0; c < nc; ++c) {
+                const uint32_t st = stage(c);
+                if (!stage_in(c) || !both(s_ready, c))
+                    break;
+                any = true;
+                if (one) {
+                    state_times(T1, c, 64);
+                    mma_commit(ks_full);
+                }
+                __syncwarp();
+                if (c > 0 && !both(q_ready, c - 1))     // O of the chunk before is read
+                    break;
+                if (one) {
+                    scores(c);
+                    state_times(T2, c, 0);
+                }
+                __syncwarp();
+                if (!warp_all(bwait(&fullb[c % NS], (c / NS) & 1, abort_flag)) ||
+                    !both(y_ready, c))
+                    break;
+                if (one) {
+#pragma unroll
+                    for (int x = 0; x < 3; ++x)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ts(tm + T1, tm + TY + tok_col(kk, x == 1),
+                                   sdesc_sw128(st + BB + (x == 2 ? BTILE / 2 : 0) + kk * 32, 16,
+                                               1024),
+                                   id64, 1);
+                    mma_commit(e_full);
+                }
+                __syncwarp();
+                if (!both(w_ready, c))
+                    break;
+                if (one) {
+#pragma unroll
+                    for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ts(tm + TS, tm + TY + tok_col(kk, lo), cols_desc(st, 64, kk),
+                                   id128mn, 1);
+                    mma_commit(s_full);
+                }
+                __syncwarp();
+                if (!both(p_ready, c))
+                    break;
+                if (one) {  // (beta Eps)^T P^T; beta Eps lies in T1, as tok_col
+#pragma unroll
+                    for (int x = 0; x < 3; ++x)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ts(tm + TR, tm + T1 + tok_col(kk, x == 1),
+                                   sdesc_sw128((x == 2 ? pl : ph) + kk * 32, 16, 1024), id64,
+                                   x + kk > 0);
+                    mma_commit(o_full);
+                    mma_commit(&empty[c % NS]);
+                }
+                __syncwarp();
+            }
+        }
+        if (any && one) {   // every product is done before TMEM is released
+            mma_commit(drain);
+            drain_wait(drain, 0);
+        }
+        __syncwarp();
+    } else if (warp < 10) {
+        // ------------------------------------------------------------- chain
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        const int e = 32 * q + lane;
+        const uint32_t lanes = tm + ((uint32_t)(32 * q) << 16);
+        const int64_t sbase = ((int64_t)sq.n * a.H + h) * a.D * a.E;
+        const float *in = BWD ? a.dfin : a.init;
+        float *out = BWD ? a.dinit : a.fin;
+        uint8_t *simg = BWD ? P.sc.k : P.sc.s, *eimg = BWD ? P.sc.r : P.sc.e;
+        const int mine = threadIdx.x - 64;
+        bool ok = true;
+        for (int c = 0; ok && c < nc; ++c) {
+            const int s = c % NS, n = tokens(c);
+            const uint8_t *st = sm + s * STAGE;
+            const float4 *tab = tabs + s * C;
+            const int64_t tile = tile_of(c);
+            if (!(ok = warp_all(bwait(&full[s], (c / NS) & 1, abort_flag))))
+                break;
+            // ---- the state
+            if (c > 0 && !(ok = warp_all(bwait(s_full, (c - 1) & 1, abort_flag))))
+                break;
+            tc_fence_after();
+            const float gC = tab[C - 1].x;
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int d0 = 64 * half + 32 * p;
+                uint32_t r[32];
+                if (c == 0) {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        r[x] = in && e < a.E && d0 + x < a.D
+                                   ? __float_as_uint(in[sbase + (int64_t)(d0 + x) * a.E + e])
+                                   : 0u;
+                } else {
+                    tmem_ld32(lanes + TS + d0, r);
+                }
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    split2(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1]), hi[x], lo[x]);
+                    r[2 * x] = __float_as_uint(gC * __uint_as_float(r[2 * x]));
+                    r[2 * x + 1] = __float_as_uint(gC * __uint_as_float(r[2 * x + 1]));
+                }
+                tmem_st16_issue(lanes + TSH + d0 / 2, hi);
+                tmem_st16_issue(lanes + TSH + 64 + d0 / 2, lo);
+                tmem_st32_issue(lanes + TS + d0, r);
+                if (simg) {
+                    uint8_t *to = simg + tile * STILE + half * 16384 + e * 128;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        *reinterpret_cast<uint4 *>(to + (((4 * p + x) ^ (e & 7)) << 4)) =
+                            make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
+                }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(s_ready);
+            // ---- X (W)
+            const int j0 = 32 * half;
+            uint32_t v[16];
+            if constexpr (!BWD) {
+                if (!(ok = warp_all(bwait(&fullv[s], (c / NS) & 1, abort_flag))))
+                    break;
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                    const int j = j0 + x;
+                    const uint32_t b = *reinterpret_cast<const uint16_t *>(
+                        st + VD + image_pair(C, j, e) + (e & 1) * 2);
+                    v[x / 2] = x & 1 ? v[x / 2] | b << 16 : b;
+                }
+            }
+            if (!(ok = warp_all(bwait(ks_full, c & 1, abort_flag))))
+                break;
+            tc_fence_after();
+            uint32_t r[32], hi[16], lo[16];
+            if constexpr (BWD) {
+                uint32_t p[32];
+                tmem_ld32_issue(lanes + T1 + j0, r);
+                tmem_ld32_issue(lanes + T2 + j0, p);
+                tmem_wait_ld(r, p);
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                    r[x] = __float_as_uint(fmaf(tab[j0 + x].z, __uint_as_float(r[x]),
+                                                __uint_as_float(p[x])));
+            } else {
+                tmem_ld32(lanes + T1 + j0, r);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                    const float vv = x & 1 ? bf16hi(v[x / 2]) : bf16lo(v[x / 2]);
+                    r[x] = __float_as_uint(fmaf(-tab[j0 + x].x, __uint_as_float(r[x]), vv));
+                }
+            }
+            if (n < C)
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                    if (j0 + x >= n)
+                        r[x] = 0u;
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+                split2(-tab[j0 + 2 * x].y * __uint_as_float(r[2 * x]),
+                       -tab[j0 + 2 * x + 1].y * __uint_as_float(r[2 * x + 1]), hi[x], lo[x]);
+            tmem_st32_issue(lanes + T1 + j0, r);
+            tmem_st16_issue(lanes + TY + 32 * half, hi);
+            tmem_st16_issue(lanes + TY + 32 * half + 16, lo);
+            tmem_wait_st();
+            tc_fence_before();
+            if (!(a.withhold_handoff && c == 0 && mine == 0))
+                mbar_arrive(y_ready);
+            // ---- Eps (R)
+            if (!(ok = warp_all(bwait(e_full, c & 1, abort_flag))))
+                break;
+            tc_fence_after();
+            float x32[32];
+            tmem_ld32(lanes + T1 + j0, r);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                const float4 t0 = tab[j0 + 2 * x], t1 = tab[j0 + 2 * x + 1];
+                const float x0 = __uint_as_float(r[2 * x]), x1 = __uint_as_float(r[2 * x + 1]);
+                x32[2 * x] = x0;
+                x32[2 * x + 1] = x1;
+                split2((BWD ? -t0.x : t0.z) * t0.y * x0, (BWD ? -t1.x : t1.z) * t1.y * x1, hi[x],
+                       lo[x]);
+            }
+            tmem_st16_issue(lanes + TY + 32 * half, hi);
+            tmem_st16_issue(lanes + TY + 32 * half + 16, lo);
+            if constexpr (!BWD) {
+                // beta Eps over this half's own columns of T1
+#pragma unroll
+                for (int x = 0; x < 16; ++x)
+                    split2(tab[j0 + 2 * x].y * x32[2 * x], tab[j0 + 2 * x + 1].y * x32[2 * x + 1],
+                           hi[x], lo[x]);
+                tmem_st16_issue(lanes + T1 + 32 * half, hi);
+                tmem_st16_issue(lanes + T1 + 32 * half + 16, lo);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(w_ready);
+            // ---- off the chain: what delta_grads starts from, dv
+            if (eimg)
+                store_tokens(x32, half, e, 128, [&](int j) {
+                    return eimg + tile * ETILE + image_pair(C, j, e);
+                });
+            if constexpr (BWD) {
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                    x32[x] *= tab[j0 + x].y;
+                uint8_t *to = reinterpret_cast<uint8_t *>(
+                    static_cast<__nv_bfloat16 *>(a.dv.p) + sq.row * a.dv.sb +
+                    (sq.bos + (int64_t)chunk(c) * C) * a.dv.st + (int64_t)h * a.dv.sh + (e & ~1));
+                store_tokens(x32, half, e, a.E, [&](int j) -> uint8_t * {
+                    return j < n ? to + 2 * j * a.dv.st : nullptr;
+                });
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&empty[s]);
+        }
+        if (ok && nc > 0)
+            ok = warp_all(bwait(s_full, (nc - 1) & 1, abort_flag));
+        tc_fence_after();
+        if (ok && out)
+#pragma unroll 1
+            for (int p = 0; p < 2; ++p) {
+                const int d0 = 64 * half + 32 * p;
+                uint32_t r[32];
+                if (nc > 0)
+                    tmem_ld32(lanes + TS + d0, r);
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                    if (e < a.E && d0 + x < a.D) {
+                        const int64_t at = sbase + (int64_t)(d0 + x) * a.E + e;
+                        out[at] = nc > 0 ? __uint_as_float(r[x]) : in ? in[at] : 0.f;
+                    }
+            }
+    } else {
+        // -------------------------------------------------------------- side
+        const int q = warp & 3;
+        const int row = 32 * q + lane;
+        const uint32_t lanes = tm + ((uint32_t)(32 * q) << 16);
+        for (int c = 0; c < nc; ++c) {
+            const int s = c % NS, n = tokens(c);
+            const float4 *tab = tabs + s * C;
+            if (!warp_all(bwait(&full[s], (c / NS) & 1, abort_flag)) ||
+                !warp_all(bwait(sc_full, c & 1, abort_flag)))
+                break;
+            tc_fence_after();
+            if (q < 2) {    // row i of P
+                const int i = row;
+                const float gi = tab[i].w;
+                uint8_t *to = sm + POFF + i * 128;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    uint32_t r[32];
+                    tmem_ld32(lanes + TR + 32 * p, r);
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        const int j = 32 * p + x;
+                        r[x] = j <= i ? __float_as_uint(a.scale * __expf(gi - tab[j].w) *
+                                                        __uint_as_float(r[x]))
+                                      : 0u;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            split2(__uint_as_float(r[8 * x + 2 * y]),
+                                   __uint_as_float(r[8 * x + 2 * y + 1]), hi[y], lo[y]);
+                        uint8_t *at = to + (((4 * p + x) ^ (i & 7)) << 4);
+                        *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(at + 8192) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                mbar_arrive(p_ready);
+            } else if (BWD) {   // row i of scale e^G Q
+                const int i = row - 64;
+                const float f = i < n ? a.scale * tab[i].x : 0.f;
+                const uint8_t *from = sm + s * STAGE + QK + i * 128;
+                uint8_t *to = sm + QOFF + i * 128;
+#pragma unroll 4
+                for (int x = 0; x < 16; ++x) {
+                    const int off = ((x & 7) ^ (i & 7)) << 4;
+                    uint4 v = *reinterpret_cast<const uint4 *>(from + (x >> 3) * 16384 + off);
+                    if (i >= n)
+                        v = make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        split2(f * bf16lo(w[y]), f * bf16hi(w[y]), hi[y], lo[y]);
+                    uint8_t *at = to + (x >> 3) * 8192 + off;
+                    *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(at + Q2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(q_ready);
+            }
+            if constexpr (!BWD) {
+                if (!warp_all(bwait(o_full, c & 1, abort_flag)))
+                    break;
+                tc_fence_after();
+                uint8_t *to = a.o.p ? reinterpret_cast<uint8_t *>(
+                                          static_cast<__nv_bfloat16 *>(a.o.p) + sq.row * a.o.sb +
+                                          (sq.bos + (int64_t)c * C) * a.o.st +
+                                          (int64_t)h * a.o.sh + (row & ~1))
+                                    : nullptr;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    uint32_t r[32], w[32];
+                    tmem_ld32_issue(lanes + T2 + 32 * p, r);
+                    tmem_ld32_issue(lanes + TR + 32 * p, w);
+                    tmem_wait_ld(r, w);
+                    if (p == 1) {
+                        tc_fence_before();
+                        mbar_arrive(q_ready);
+                    }
+                    float y[32];
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        y[x] = fmaf(a.scale * tab[32 * p + x].x, __uint_as_float(r[x]),
+                                    __uint_as_float(w[x]));
+                    if (to)
+                        store_tokens(y, p, row, a.E, [&](int j) -> uint8_t * {
+                            return j < n ? to + 2 * j * a.o.st : nullptr;
+                        });
+                }
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&empty[s]);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tm, TCOLS);
+    }
+}
+
+// ---- dQ, dK, dg, dbeta -----------------------------------------------------------
+//
+// A CTA a (chunk, head), two of them an SM: 112 KB of tiles, 256 TMEM columns.
+// Transposed as the sweeps: lanes are key channels, columns tokens.  [dO; R] lie as
+// one 128-row tile, so one product with Eps^T gives dO Eps^T in lanes 0-63 and
+// R Eps^T in lanes 64-127.  K'^T takes S^T's place once the products with S are done.
+
+constexpr int GRADS = 256;
+constexpr int GQ = 0, GK = 16384, GE = 32768, GD = 49152, GS = 81920, GBAR = 114688;
+constexpr int GDYN = GBAR + 64;
+constexpr uint32_t UW = 0, UQ = 64, UR = 128, UC = 192, UCOLS = 256;
+
+struct GradParams {
+    CUtensorMap mq, mk, mdo;
+    DeltaArgs a;
+    Scratch sc;
+};
+
+// 16 tokens' values of this lane's channel to rows of bf16 or, f32, fp32.
+template <typename F>
+__device__ __forceinline__ void store_16(const float (&x)[16], int j0, int d, int D, F at)
+{
+    const bool odd = d & 1;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+        const float mine = odd ? x[2 * m + 1] : x[2 * m], other = odd ? x[2 * m] : x[2 * m + 1];
+        const float got = __shfl_xor_sync(0xffffffffu, other, 1);
+        const uint32_t pair = odd ? pack_bf16x2(got, mine) : pack_bf16x2(mine, got);
+        if (uint32_t *p = at(j0 + 2 * m + odd); p && d < D)
+            *p = pair;
+    }
+}
+
+__global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_constant__ GradParams P)
+{
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const DeltaArgs &a = P.a;
+    const int h = blockIdx.x % a.H;
+    const int64_t slot = blockIdx.x / a.H;
+    const Seq sq = sequence_of_slot(a.cu, a.T, a.N, slot);
+    const int64_t t0 = (slot - sq.slot) * C;
+    if (t0 >= sq.len)
+        return;
+    // the tiles' swizzle goes by address: dynamic shared memory starts on 1024 bytes
+    // where a kernel has no other (two CTAs leave no room to round up)
+    if (smem_u32(sm) & 1023) {
+        if (threadIdx.x == 0)
+            atomicExch(&g_tc_error, TC_ERR_TIMEOUT);
+        return;
+    }
+    const int n = (int)min((int64_t)C, sq.len - t0);
+    const int64_t tile = slot * a.H + h;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int q = warp & 3, half = warp >> 2;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + GBAR);
+    uint64_t *in_full = bars, *one_full = bars + 1, *k_full = bars + 2, *two_full = bars + 3;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 4);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 5);
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i)
+            mbar_init(&bars[i], 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(tslot, UCOLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = *tslot;
+    const uint32_t lanes = tm + ((uint32_t)(32 * q) << 16);
+    const float4 *tab = P.sc.tab + tile * C;
+
+    if (tid == 0) {
+        const int hq = h / a.q.hdiv, t = (int)(sq.bos + t0), row = (int)sq.row;
+        mbar_arrive_expect_tx(in_full, 3 * 16384 + 2 * ETILE + STILE);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            tma_load_4d(sm + GD + b * 16384, &P.mdo, in_full, 64 * b, h, t, row);
+            bulk_load(sm + GD + b * 16384 + 8192, P.sc.r + tile * ETILE + b * 8192, 8192, in_full);
+            tma_load_4d(sm + GQ + b * 8192, &P.mq, in_full, 64 * b, hq, t, row);
+            tma_load_4d(sm + GK + b * 8192, &P.mk, in_full, 64 * b, hq, t, row);
+        }
+        bulk_load(sm + GE, P.sc.e + tile * ETILE, ETILE, in_full);
+        bulk_load(sm + GS, P.sc.s + tile * STILE, STILE, in_full);
+    }
+    __syncwarp();
+    bool ok = warp_all(bwait(in_full, 0, abort_flag));
+    if (a.cu && n < C) {    // another sequence's tokens: zeros
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        for (int x = tid; x < (C - n) * 8; x += GRADS) {
+            const int off = (n + x / 8) * 128 + (x % 8) * 16;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                *reinterpret_cast<uint4 *>(sm + GQ + b * 8192 + off) = z;
+                *reinterpret_cast<uint4 *>(sm + GK + b * 8192 + off) = z;
+                *reinterpret_cast<uint4 *>(sm + GD + b * 16384 + off) = z;
+            }
+        }
+        fence_proxy_async_smem();
+    }
+    __syncthreads();
+    const uint32_t sb = smem_u32(sm);
+    constexpr uint32_t id_kk = idesc_bf16_f32(128, 64, 0, 0), id_mk = idesc_bf16_f32(128, 64, 1, 0),
+                       id_mm = idesc_bf16_f32(128, 64, 1, 1);
+    if (tid == 0 && ok) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t rows = (kk >> 2) * 16384 + (kk & 3) * 32;
+            const uint64_t de = sdesc_sw128(sb + GE + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024);
+            const uint64_t ddo = sdesc_sw128(sb + GD + rows, 16, 1024);
+            const uint64_t dr = sdesc_sw128(sb + GD + 8192 + rows, 16, 1024);
+            const uint64_t ds = sdesc_sw128(sb + GS + kk * 2048, 16384, 1024);
+            mma_ss(tm + UW, ddo, de, id_kk, kk > 0);        // [dO; R] Eps^T
+            mma_ss(tm + UQ, ds, ddo, id_mk, kk > 0);        // S dO^T
+            mma_ss(tm + UR, ds, dr, id_mk, kk > 0);         // S R^T
+        }
+        mma_commit(one_full);
+    }
+    __syncwarp();
+    // this thread's share of S for <S, K'>
+    uint4 sv[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+        sv[x] = *reinterpret_cast<const uint4 *>(sm + GS + tid * 16 + x * 4096);
+    ok = warp_all(bwait(one_full, 0, abort_flag)) && ok;
+    tc_fence_after();
+    __syncthreads();    // S has been read, by the products and by every thread
+    if (tid == 0 && ok) {
+        mbar_arrive_expect_tx(k_full, STILE);
+        bulk_load(sm + GS, P.sc.k + tile * STILE, STILE, k_full);
+    }
+    __syncwarp();
+    const int j0 = 32 * half;
+    {   // W1, W2 as bf16 rows over dO and R (both read); S dO^T, S R^T scaled
+        const int i = 32 * (q & 1) + lane;
+        const float4 ti = tab[i];
+        uint32_t r[32];
+        tmem_ld32(lanes + UW + j0, r);
+        uint8_t *to = sm + GD + (q < 2 ? 0 : 8192) + i * 128;
+        // one branch a warp: dO's lanes, R's lanes
+        const float f = q < 2 ? a.scale : -ti.y;
+        const int last = q < 2 ? i : i - 1;
+        if (q >= 2 && i >= j0 && i < j0 + 32 && i < n) {
+            float d = 0.f;
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+                d = j0 + x == i ? __uint_as_float(r[x]) : d;
+            static_cast<__nv_bfloat16 *>(a.dbeta)[((sq.row * a.T) + sq.bos + t0 + i) * a.H + h] =
+                __float2bfloat16_rn(d);
+        }
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+            const float4 tj = tab[j0 + x];
+            r[x] = j0 + x <= last ? __float_as_uint(f * tj.y * __expf(ti.w - tj.w) *
+                                                    __uint_as_float(r[x]))
+                                  : 0u;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<uint4 *>(to + (((4 * half + x) ^ (i & 7)) << 4)) = make_uint4(
+                pack_bf16x2(__uint_as_float(r[8 * x]), __uint_as_float(r[8 * x + 1])),
+                pack_bf16x2(__uint_as_float(r[8 * x + 2]), __uint_as_float(r[8 * x + 3])),
+                pack_bf16x2(__uint_as_float(r[8 * x + 4]), __uint_as_float(r[8 * x + 5])),
+                pack_bf16x2(__uint_as_float(r[8 * x + 6]), __uint_as_float(r[8 * x + 7])));
+        tmem_ld32(lanes + UQ + j0, r);
+#pragma unroll
+        for (int x = 0; x < 32; ++x)
+            r[x] = __float_as_uint(a.scale * tab[j0 + x].x * __uint_as_float(r[x]));
+        tmem_st32_issue(lanes + UQ + j0, r);
+        uint32_t w[32];
+        tmem_ld32(lanes + UR + j0, w);
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+            const float4 tj = tab[j0 + x];
+            w[x] = __float_as_uint(-tj.x * tj.y * __uint_as_float(w[x]));
+        }
+        tmem_st32_issue(lanes + UR + j0, w);
+        tmem_wait_st();
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    ok = warp_all(bwait(k_full, 0, abort_flag)) && ok;
+    if (tid == 0 && ok) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t kt = sdesc_sw128(sb + GK + kk * 2048, 8192, 1024);
+            const uint64_t qt = sdesc_sw128(sb + GQ + kk * 2048, 8192, 1024);
+            const uint32_t w1 = sb + GD, w2 = sb + GD + 8192;
+            mma_ss(tm + UQ, kt, sdesc_sw128(w1 + kk * 32, 16, 1024), id_mk, 1);     // K^T W1^T
+            mma_ss(tm + UR, kt, sdesc_sw128(w2 + kk * 32, 16, 1024), id_mk, 1);     // K^T W2^T
+            mma_ss(tm + UC, qt, sdesc_sw128(w1 + kk * 2048, 8192, 1024), id_mm, kk > 0);
+            mma_ss(tm + UC, kt, sdesc_sw128(w2 + kk * 2048, 8192, 1024), id_mm, 1);
+        }
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)      // K' Eps^T
+            mma_ss(tm + UW, sdesc_sw128(sb + GS + kk * 2048, 16384, 1024),
+                   sdesc_sw128(sb + GE + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024), id_mk,
+                   kk > 0);
+        mma_commit(two_full);
+    }
+    __syncwarp();
+    float end = 0.f;    // <S', K'>
+    if (ok) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const uint4 kv = *reinterpret_cast<const uint4 *>(sm + GS + tid * 16 + x * 4096);
+            const uint32_t u[4] = {sv[x].x, sv[x].y, sv[x].z, sv[x].w};
+            const uint32_t w[4] = {kv.x, kv.y, kv.z, kv.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                end = fmaf(bf16lo(u[y]), bf16lo(w[y]), end);
+                end = fmaf(bf16hi(u[y]), bf16hi(w[y]), end);
+            }
+        }
+        end *= tab[C - 1].x;
+    }
+    ok = warp_all(bwait(two_full, 0, abort_flag)) && ok;
+    tc_fence_after();
+    float *red = reinterpret_cast<float *>(sm + GD + 16384);    // [4][64], then 8 sums
+    const int d = 32 * q + lane;
+    if (ok) {
+#pragma unroll 1
+        for (int p = 0; p < 2; ++p) {
+            const int jp = j0 + 16 * p;
+            uint32_t dq[16], dr[16], dc[16], dw[16];
+            tmem_ld16_issue(lanes + UQ + jp, dq);
+            tmem_ld16_issue(lanes + UR + jp, dr);
+            tmem_wait_ld16x2(dq, dr);
+            tmem_ld16_issue(lanes + UC + jp, dc);
+            tmem_ld16_issue(lanes + UW + jp, dw);
+            tmem_wait_ld16x2(dc, dw);
+            float oq[16], ok_[16], t[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                const float4 tj = tab[jp + x];
+                const uint32_t at = image_pair(C, jp + x, d) + (d & 1) * 2;
+                const float qv = __uint_as_float(
+                    (uint32_t)*reinterpret_cast<const uint16_t *>(sm + GQ + at) << 16);
+                const float kv = __uint_as_float(
+                    (uint32_t)*reinterpret_cast<const uint16_t *>(sm + GK + at) << 16);
+                const float into = tj.z * tj.y * __uint_as_float(dw[x]);
+                const float row = __uint_as_float(dr[x]), col = __uint_as_float(dc[x]) + into;
+                oq[x] = __uint_as_float(dq[x]);
+                ok_[x] = row + col;
+                t[x] = fmaf(qv, oq[x], kv * (row - col));
+                end = fmaf(kv, into, end);
+            }
+            if (P.sc.dqp) {
+                float *pq = P.sc.dqp + ((sq.row * a.T + sq.bos + t0) * a.H + h) * a.D + d;
+                float *pk = P.sc.dkp + (pq - P.sc.dqp);
+#pragma unroll
+                for (int x = 0; x < 16; ++x)
+                    if (jp + x < n && d < a.D) {
+                        pq[(int64_t)(jp + x) * a.H * a.D] = oq[x];
+                        pk[(int64_t)(jp + x) * a.H * a.D] = ok_[x];
+                    }
+            } else {
+                auto rows = [&](const TokOut &o) {
+                    return static_cast<__nv_bfloat16 *>(o.p) + sq.row * o.sb +
+                           (sq.bos + t0) * o.st + (int64_t)h * o.sh + (d & ~1);
+                };
+                __nv_bfloat16 *pq = rows(a.dq), *pk = rows(a.dk);
+                store_16(oq, jp, d, a.D, [&](int j) {
+                    return j < n ? reinterpret_cast<uint32_t *>(pq + j * a.dq.st) : nullptr;
+                });
+                store_16(ok_, jp, d, a.D, [&](int j) {
+                    return j < n ? reinterpret_cast<uint32_t *>(pk + j * a.dk.st) : nullptr;
+                });
+            }
+            // t summed over the lanes: halves traded, each lane ends with one token
+#pragma unroll
+            for (int m = 16, w = 8; w >= 1; m /= 2, w /= 2) {
+                const bool up = lane & m;
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    if (x < w) {
+                        const float keep = up ? t[x + w] : t[x], send = up ? t[x] : t[x + w];
+                        t[x] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+                    }
+            }
+            t[0] += __shfl_xor_sync(0xffffffffu, t[0], 1);
+            if (!(lane & 1))
+                red[64 * q + jp + (lane >> 1)] = t[0];
+        }
+#pragma unroll
+        for (int m = 1; m < 32; m *= 2)
+            end += __shfl_xor_sync(0xffffffffu, end, m);
+        if (lane == 0)
+            red[256 + warp] = end;
+    }
+    if (tid == 0 && !ok) {  // a wait ran out: what is in flight ends before the CTA does
+        drain_wait(in_full, 0);
+        drain_wait(one_full, 0);
+        drain_wait(k_full, 0);
+        drain_wait(two_full, 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) {
+        tmem_dealloc(tm, UCOLS);
+        // dg: running sums from the chunk's last token
+        float run = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w)
+            run += red[256 + w];
+#pragma unroll
+        for (int p = 1; p >= 0; --p) {
+            const int i = 32 * p + 31 - lane;
+            float x = red[i] + red[64 + i] + red[128 + i] + red[192 + i];
+#pragma unroll
+            for (int m = 1; m < 32; m *= 2) {
+                const float y = __shfl_up_sync(0xffffffffu, x, m);
+                if (lane >= m)
+                    x += y;
+            }
+            if (i < n && ok)
+                static_cast<__nv_bfloat16 *>(a.dg)[((sq.row * a.T) + sq.bos + t0 + i) * a.H + h] =
+                    __float2bfloat16_rn(run + x);
+            run += __shfl_sync(0xffffffffu, x, 31);
+        }
+    }
+}
+
+// ---- host -------------------------------------------------------------------------
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+size_t tiles_of(const DeltaArgs &a)
+{
+    return (size_t)slots_of(a.N, a.T, a.cu != nullptr) * a.H;
+}
+size_t prep_bytes(const DeltaArgs &a) { return tiles_of(a) * (BTILE + TAB); }
+
+void put_saved(const DeltaArgs &a, uint8_t *p, bool keep, Scratch *sc)
+{
+    const size_t t = tiles_of(a);
+    sc->b = p;
+    sc->tab = reinterpret_cast<float4 *>(p + t * BTILE);
+    sc->s = keep ? p + prep_bytes(a) : nullptr;
+    sc->e = keep ? sc->s + t * STILE : nullptr;
+}
+
+bool token_map(CUtensorMap *m, const DeltaArgs &a, const Tok &x, int heads, int width)
+{
+    SweepArgs s{};
+    s.B = a.B;
+    s.T = a.T;
+    s.H = heads;
+    return make_map(m, x.p, width, s, x.sb, x.st, x.sh, C);
+}
+
+template <bool BWD> cudaError_t sweep(const DeltaArgs &a, const Scratch &sc, cudaStream_t s)
+{
+    SweepParams p;
+    if (!token_map(&p.mq, a, a.q, a.HK, a.D) || !token_map(&p.mk, a, a.k, a.HK, a.D) ||
+        !token_map(&p.mv, a, BWD ? a.d_o : a.v, a.H, a.E))
+        return cudaErrorNotSupported;
+    p.a = a;
+    p.sc = sc;
+    cudaError_t e = cudaFuncSetAttribute(delta_sweep_kernel<BWD>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         SweepLayout<BWD>::DYN);
+    if (e != cudaSuccess)
+        return e;
+    delta_sweep_kernel<BWD>
+        <<<(unsigned)((int64_t)a.N * a.H), SWEEP, SweepLayout<BWD>::DYN, s>>>(p);
+    note_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool delta_tc_row_ok(const void *p, const int64_t *st, int B, int T, int heads)
+{
+    const int n[3] = {B, T, heads};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (st[i] <= 0 || st[i] % 8))
+            return false;
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+}
+
+bool delta_tc_sized(const DeltaArgs &a)
+{
+    if (!a.bf16 || a.D % 8 || a.E % 8 || a.D > 128 || a.E > 128 || a.longest <= SHORT_MAX_T)
+        return false;
+    const Tok *t[3] = {&a.q, &a.k, &a.v};
+    for (int i = 0; i < 3; ++i) {
+        const int64_t st[3] = {t[i]->sb, t[i]->st, t[i]->sh};
+        if (!delta_tc_row_ok(nullptr, st, a.B, a.T, i < 2 ? a.HK : a.H))
+            return false;
+    }
+    return tiles_of(a) <= INT_MAX;
+}
+
+size_t delta_tc_saved_bytes(const DeltaArgs &a)
+{
+    return up(prep_bytes(a) + tiles_of(a) * (STILE + ETILE));
+}
+
+size_t delta_tc_fwd_bytes(const DeltaArgs &a, bool keep) { return keep ? 0 : up(prep_bytes(a)); }
+
+size_t delta_tc_bwd_bytes(const DeltaArgs &a)
+{
+    const size_t parts = a.H == a.HK ? 0 : up((size_t)a.B * a.T * a.H * a.D * sizeof(float));
+    return up(tiles_of(a) * (STILE + ETILE)) + 2 * parts;
+}
+
+cudaError_t delta_tc_forward(const DeltaArgs &a, cudaStream_t s)
+{
+    Scratch sc{};
+    put_saved(a, a.saved ? a.saved : a.ws, a.saved != nullptr, &sc);
+    delta_prep_kernel<<<(unsigned)tiles_of(a), PREP, 0, s>>>(a, sc);
+    note_launch();
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : sweep<false>(a, sc, s);
+}
+
+cudaError_t delta_tc_backward(const DeltaArgs &a, cudaStream_t s)
+{
+    Scratch sc{};
+    const size_t t = tiles_of(a);
+    put_saved(a, a.saved, true, &sc);
+    sc.k = a.ws;
+    sc.r = a.ws + t * STILE;
+    if (a.H != a.HK) {
+        const size_t parts = up((size_t)a.B * a.T * a.H * a.D * sizeof(float));
+        sc.dqp = reinterpret_cast<float *>(a.ws + up(t * (STILE + ETILE)));
+        sc.dkp = reinterpret_cast<float *>(a.ws + up(t * (STILE + ETILE)) + parts);
+    }
+    cudaError_t e = sweep<true>(a, sc, s);
+    if (e != cudaSuccess)
+        return e;
+    GradParams p;
+    if (!token_map(&p.mq, a, a.q, a.HK, a.D) || !token_map(&p.mk, a, a.k, a.HK, a.D) ||
+        !token_map(&p.mdo, a, a.d_o, a.H, a.E))
+        return cudaErrorNotSupported;
+    p.a = a;
+    p.sc = sc;
+    e = cudaFuncSetAttribute(delta_grads_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GDYN);
+    if (e != cudaSuccess)
+        return e;
+    delta_grads_kernel<<<(unsigned)t, GRADS, GDYN, s>>>(p);
+    note_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess || a.H == a.HK)
+        return e;
+    // a shared head's gradients: the sum over its group, fp32
+    e = gqa_reduce(sc.dqp, a.dq, a.B, a.T, a.HK, a.H / a.HK, a.D, 1, s, true);
+    return e != cudaSuccess ? e
+                            : gqa_reduce(sc.dkp, a.dk, a.B, a.T, a.HK, a.H / a.HK, a.D, 1, s, true);
+}
+
+cudaError_t delta_read_and_clear_error(cudaStream_t s, int *err)
+{
+    return read_and_clear_error_word(s, err);
+}
 
 }  // namespace la

@@ -346,6 +346,7 @@ size_t delta_tc_fwd_bytes(const DeltaArgs &a, bool keep);
 size_t delta_tc_bwd_bytes(const DeltaArgs &a);
 cudaError_t delta_tc_forward(const DeltaArgs &a, cudaStream_t s);
 cudaError_t delta_tc_backward(const DeltaArgs &a, cudaStream_t s);
+cudaError_t delta_read_and_clear_error(cudaStream_t s, int *err);
 
 
 // Norms of queries and keys with the position rotation (la_qk_rope.cu).
@@ -381,6 +382,35 @@ cudaError_t rope_bwd_f32(const RopeArgs &a, bool vec, int sms, cudaStream_t s, i
 constexpr int ROPE_MOST_CTAS = 768;
 // Bytes of RopeArgs::partial.
 size_t rope_partial_bytes(int D);
+
+// The norms before and after a block with its gate and residual scale
+// (la_block_norm.cuh).
+struct NormRows {
+    const void *p;              // null: not there
+    int64_t s[3];               // element strides (batch, token, head)
+};
+struct BlockNormArgs {
+    int B, T, H, D;
+    int64_t rows;               // B T H
+    int bf16, w_bf16;
+    int activation;             // 0 none, 1 sigmoid, 2 silu
+    float eps, scale;
+    NormRows x, gate, residual;
+    NormRows h, y;              // forward
+    NormRows dh, dy, dx, dgate, dresidual;      // backward
+    const void *post, *pre;     // [D] weights, or null: no such norm
+    void *dpost, *dpre;         // their gradients, or null
+    float *partial;             // backward: [CTAs][2][D]
+};
+cudaError_t block_norm_run(bool back, const BlockNormArgs &a, cudaStream_t s);
+// Its kernels by direction and type; *ctas: the CTAs launched.
+cudaError_t block_norm_fwd_bf16(const BlockNormArgs &a, bool vec, int sms, cudaStream_t s, int *ctas);
+cudaError_t block_norm_fwd_f32(const BlockNormArgs &a, bool vec, int sms, cudaStream_t s, int *ctas);
+cudaError_t block_norm_bwd_bf16(const BlockNormArgs &a, bool vec, int sms, cudaStream_t s, int *ctas);
+cudaError_t block_norm_bwd_f32(const BlockNormArgs &a, bool vec, int sms, cudaStream_t s, int *ctas);
+constexpr int NORM_MOST_CTAS = 608;
+constexpr int NORM_MOST_DIM = 16384;
+size_t block_norm_partial_bytes(int D);
 
 // Device error word of the tensor-core kernels (bounded waits that ran out).
 cudaError_t tc_read_and_clear_error(cudaStream_t s, int *err);

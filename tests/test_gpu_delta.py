@@ -46,7 +46,6 @@ def cuda(x):
 
 
 def chunked(dt, D, E, longest):
-    return False
     return dt == BF and D % 8 == 0 and E % 8 == 0 and D <= 128 and E <= 128 and longest > 16
 
 
@@ -84,6 +83,7 @@ def check(x, cu=None, scale=None, label="", dev=None):
               cu_seqlens=cu_t.cuda() if cu is not None else None, cu_seqlens_host=cu_t)
     a = (d["q"], d["k"], d["v"], d["g"], d["beta"])
     o, fin, saved = la.gated_delta_fwd(*a, keep=True, **kw)
+    assert (saved is not None) == (tc and T > 0)
     S, K = ref["scale_S"].max() if len(spans) else 0.0, ref["scale_K"].max() if len(spans) else 0.0
     S, K = float(S), float(K)
     root = math.sqrt(max(1, v.shape[0] * T * H))
