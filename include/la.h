@@ -662,6 +662,74 @@ size_t la_gated_delta_workspace_size(const la_delta_dims *dims, int32_t dtype,
 size_t la_gated_delta_saved_size(const la_delta_dims *dims, int32_t dtype,
                                  const int32_t *cu_seqlens_host);
 
+/* Norms before and after a block with its gate and residual scale, for every
+ * row x of dim channels ([B,T,H,dim], the heads' outputs; or a stream of
+ * channels with heads = 1):
+ *     n = x * rsqrt(mean x^2 + eps) * post_weight     (x itself without it)
+ *     m = n * act(gate)                               (n without gate)
+ *     h = residual + scale * m                        (scale * m without residual)
+ *     y = h * rsqrt(mean h^2 + eps) * pre_weight      (no y without it)
+ * all in fp32, h and y rounded once (y is of h before its rounding).
+ *   batch, seq_len   as la_dims;  heads 1..65535;  dim 1..16384
+ *   activation    0: act(z) = z, 1: sigmoid, 2: silu (z * sigmoid(z))
+ *   weight_dtype  la_dtype of the weights and of their gradients
+ *   *_strides     element strides (batch, token, head); channels are contiguous.
+ *                 Inputs may repeat rows (stride 0), outputs not.  The forward
+ *                 reads those of x, gate, residual, h, y; the backward all but
+ *                 h's and y's (d_h and d_y have their own). */
+typedef struct la_block_norm_dims {
+    int32_t batch;
+    int32_t seq_len;
+    int32_t heads;
+    int32_t dim;
+    int32_t activation;
+    int32_t weight_dtype;
+    int64_t x_strides[3];
+    int64_t gate_strides[3];
+    int64_t residual_strides[3];
+    int64_t h_strides[3];
+    int64_t y_strides[3];
+    int64_t dh_strides[3];
+    int64_t dy_strides[3];
+    int64_t dx_strides[3];
+    int64_t dgate_strides[3];
+    int64_t dresidual_strides[3];
+} la_block_norm_dims;
+
+/* Forward.
+ *   x              [B,T,H,dim] of `dtype`
+ *   gate, residual [B,T,H,dim] of `dtype`, or NULL
+ *   post_weight, pre_weight  [dim] of weight_dtype, or NULL (no such norm)
+ *   h              [B,T,H,dim] of `dtype` output; may be x or residual itself
+ *                  (same pointer and strides)
+ *   y              [B,T,H,dim] of `dtype` output, with pre_weight; else NULL
+ */
+la_status la_block_norm_fwd(const la_block_norm_dims *dims, int32_t dtype, const void *x,
+                            const void *gate, const void *residual, const void *post_weight,
+                            const void *pre_weight, float eps, float scale, void *h, void *y,
+                            void *stream);
+
+/* Backward: gradients of sum(h * d_h) + sum(y * d_y); h is computed again.
+ *   x ... scale    as given to the forward call (residual is read only with
+ *                  pre_weight)
+ *   d_h            [B,T,H,dim] of `dtype`, or NULL for zeros (with pre_weight)
+ *   d_y            [B,T,H,dim] of `dtype`, with pre_weight; else NULL
+ *   dx             output;  d_gate  output, with gate;  d_residual  output or NULL
+ *                  (the gradient of h's sum: also that of a stream that is not given)
+ *   d_post_weight, d_pre_weight  [dim] of weight_dtype outputs, or NULL; the sums
+ *                  are formed in fp32 in a fixed order
+ *   workspace      256-byte aligned, la_block_norm_workspace_size bytes; needed
+ *                  when a weight's gradient is asked for */
+la_status la_block_norm_bwd(const la_block_norm_dims *dims, int32_t dtype, const void *x,
+                            const void *gate, const void *residual, const void *post_weight,
+                            const void *pre_weight, float eps, float scale, const void *d_h,
+                            const void *d_y, void *dx, void *d_gate, void *d_residual,
+                            void *d_post_weight, void *d_pre_weight, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of la_block_norm_bwd (0 for invalid sizes).  Pure host function. */
+size_t la_block_norm_workspace_size(const la_block_norm_dims *dims, int32_t dtype);
+
 /* Reads and clears the device-side error words that bounded on-device waits
  * set when they run out (LA_ERR_TIMEOUT), after synchronizing `stream`.
  * Returns LA_OK when no wait ran out, LA_ERR_TIMEOUT when one did, or

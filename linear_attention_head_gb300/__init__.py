@@ -12,9 +12,9 @@ from .api import (alibi_g_gamma, get_device_error, gla_bwd, gla_fwd, kernel_fami
                   lightning_g_gamma, recurrent, recurrent_gla)
 
 from .delta import gated_delta, gated_delta_bwd, gated_delta_fwd
-from .layer import (QkNorm, Rope, gated_scan, gated_scan_bwd, gated_scan_fwd, qk_norm_rope,
-                    qk_norm_rope_bwd, qk_norm_rope_fwd, rope_inv_freq, rotary, rotary_bwd,
-                    rotary_fwd)
+from .layer import (QkNorm, Rope, block_norm, block_norm_bwd, block_norm_fwd, gated_scan,
+                    gated_scan_bwd, gated_scan_fwd, qk_norm_rope, qk_norm_rope_bwd,
+                    qk_norm_rope_fwd, rope_inv_freq, rotary, rotary_bwd, rotary_fwd)
 
 __all__ = [
     "LaDims", "LaError", "LaInvalidArgument", "LaUnsupported", "LA_DTYPE_BF16", "LA_DTYPE_F32",
@@ -22,6 +22,7 @@ __all__ = [
     "la_bwd_dkdv", "la_bwd_dq", "la_fwd", "lightning_attn", "lightning_attn_func",
     "lightning_g_gamma", "recurrent", "recurrent_gla",
     "gated_delta", "gated_delta_bwd", "gated_delta_fwd",
-    "QkNorm", "Rope", "gated_scan", "gated_scan_bwd", "gated_scan_fwd", "qk_norm_rope",
-    "qk_norm_rope_bwd", "qk_norm_rope_fwd", "rope_inv_freq", "rotary", "rotary_bwd", "rotary_fwd",
+    "block_norm", "block_norm_bwd", "block_norm_fwd", "QkNorm", "Rope", "gated_scan",
+    "gated_scan_bwd", "gated_scan_fwd", "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_fwd",
+    "rope_inv_freq", "rotary", "rotary_bwd", "rotary_fwd",
 ]

@@ -77,6 +77,16 @@ class LaDeltaDims(ctypes.Structure):
                  "do_strides", "dq_strides", "dk_strides", "dv_strides")]
 
 
+class LaBlockNormDims(ctypes.Structure):
+    """Mirror of `la_block_norm_dims` (include/la.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("batch", "seq_len", "heads", "dim", "activation", "weight_dtype")] + \
+               [(n, _i64x3) for n in
+                ("x_strides", "gate_strides", "residual_strides", "h_strides", "y_strides",
+                 "dh_strides", "dy_strides", "dx_strides", "dgate_strides",
+                 "dresidual_strides")]
+
+
 class LaError(RuntimeError):
     def __init__(self, status, detail):
         self.status = status
@@ -99,6 +109,7 @@ _dims_p = ctypes.POINTER(LaDims)
 _scan_p = ctypes.POINTER(LaScanDims)
 _rope_p = ctypes.POINTER(LaRopeDims)
 _delta_p = ctypes.POINTER(LaDeltaDims)
+_norm_p = ctypes.POINTER(LaBlockNormDims)
 
 # name -> (restype, argtypes); mirrors include/la.h exactly (float* are passed
 # as void* addresses).
@@ -137,6 +148,11 @@ PROTOTYPES = {
                                   _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "la_gated_delta_workspace_size": (_sz, [_delta_p, _i32, _vp, _i32]),
     "la_gated_delta_saved_size": (_sz, [_delta_p, _i32, _vp]),
+    "la_block_norm_fwd": (_i32, [_norm_p, _i32, _vp, _vp, _vp, _vp, _vp, _f32, _f32, _vp, _vp,
+                                 _vp]),
+    "la_block_norm_bwd": (_i32, [_norm_p, _i32, _vp, _vp, _vp, _vp, _vp, _f32, _f32, _vp, _vp,
+                                 _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "la_block_norm_workspace_size": (_sz, [_norm_p, _i32]),
     "la_debug_withhold_next_handoff": (_i32, [_i32]),
     "la_debug_split_segments": (_i32, [_dims_p, _i32, _vp, _i32]),
     "la_fwd_noalloc": (_i32, [_dims_p, _i32, _vp, _vp, _vp, _vp, _f32, _vp, _i32, _vp, _vp,

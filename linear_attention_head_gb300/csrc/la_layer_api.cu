@@ -1,7 +1,8 @@
 // la_layer_api.cu -- the C entry points of the operators beside the attention
 // (include/la.h): the gated linear recurrence, the norms of queries and keys
-// with the position rotation, and the gated delta rule.  Argument checks, then
-// the launches of la_scan.cu, la_qk_rope.cu, la_delta_token.cu and la_delta_tc.cu.
+// with the position rotation, the gated delta rule, and the norms around a block.
+// Argument checks, then the launches of la_scan.cu, la_qk_rope.cu,
+// la_delta_token.cu, la_delta_tc.cu and la_block_norm.cu.
 
 #include <climits>
 #include <cmath>
@@ -436,6 +437,69 @@ bool delta_row(const void *p, const int64_t *st, const la::DeltaArgs &a, int hea
     return la::delta_tc_row_ok(p, st, a.B, a.T, heads);
 }
 
+// ---- norms around a block ------------------------------------------------------
+
+la_status norm_sizes(const la_block_norm_dims *d, int32_t dtype)
+{
+    if (!d)
+        return fail(LA_ERR_INVALID_ARG, "dims is NULL");
+    if (!known_dtype(dtype))
+        return fail(LA_ERR_INVALID_ARG, "dtype %d is neither LA_DTYPE_BF16 nor LA_DTYPE_F32",
+                    dtype);
+    if (!known_dtype(d->weight_dtype))
+        return fail(LA_ERR_INVALID_ARG, "weight_dtype = %d", d->weight_dtype);
+    if (d->batch < 0 || d->seq_len < 0)
+        return fail(LA_ERR_INVALID_ARG, "negative batch (%d) or seq_len (%d)", d->batch,
+                    d->seq_len);
+    if (d->heads < 1 || d->heads > 65535)
+        return fail(LA_ERR_INVALID_ARG, "heads = %d outside 1..65535", d->heads);
+    if (d->dim < 1 || d->dim > la::NORM_MOST_DIM)
+        return fail(LA_ERR_UNSUPPORTED, "dim = %d: supported range is 1..%d", d->dim,
+                    la::NORM_MOST_DIM);
+    if (d->activation < 0 || d->activation > 2)
+        return fail(LA_ERR_INVALID_ARG, "activation = %d outside 0..2", d->activation);
+    if ((double)d->batch * d->seq_len * d->heads > INT_MAX)
+        return fail(LA_ERR_UNSUPPORTED, "more than 2^31 - 1 rows");
+    return LA_OK;
+}
+
+la::NormRows norm_rows(const void *p, const int64_t *st)
+{
+    return la::NormRows{p, {st[0], st[1], st[2]}};
+}
+
+la_status norm_args(const la_block_norm_dims *d, int32_t dtype, const void *x, const void *gate,
+                    const void *residual, const void *post, const void *pre, float eps,
+                    float scale, la::BlockNormArgs *a)
+{
+    la_status e = norm_sizes(d, dtype);
+    if (e || (e = check_in(d->x_strides, "x")) ||
+        (gate && (e = check_in(d->gate_strides, "gate"))) ||
+        (residual && (e = check_in(d->residual_strides, "residual"))))
+        return e;
+    if (!(eps >= 0.f) || !std::isfinite(eps) || !std::isfinite(scale))
+        return fail(LA_ERR_INVALID_ARG, "eps must be finite and not negative, scale finite");
+    *a = la::BlockNormArgs{};
+    a->B = d->batch;
+    a->T = d->seq_len;
+    a->H = d->heads;
+    a->D = d->dim;
+    a->rows = (int64_t)d->batch * d->seq_len * d->heads;
+    if (a->rows > 0 && (e = need(x, "x")))
+        return e;
+    a->bf16 = dtype == LA_DTYPE_BF16;
+    a->w_bf16 = d->weight_dtype == LA_DTYPE_BF16;
+    a->activation = d->activation;
+    a->eps = eps;
+    a->scale = scale;
+    a->x = norm_rows(x, d->x_strides);
+    a->gate = norm_rows(gate, d->gate_strides);
+    a->residual = norm_rows(residual, d->residual_strides);
+    a->post = post;
+    a->pre = pre;
+    return LA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -763,6 +827,91 @@ la_status la_gated_delta_bwd(const la_delta_dims *dims, int32_t dtype, const voi
                 return e;
         }
         return launched(la::delta_tc_backward(a, s), "gated delta rule backward");
+    });
+}
+
+la_status la_block_norm_fwd(const la_block_norm_dims *dims, int32_t dtype, const void *x,
+                            const void *gate, const void *residual, const void *post_weight,
+                            const void *pre_weight, float eps, float scale, void *h, void *y,
+                            void *stream)
+{
+    return guarded([&]() -> la_status {
+        la::BlockNormArgs a;
+        la_status e = norm_args(dims, dtype, x, gate, residual, post_weight, pre_weight, eps,
+                                scale, &a);
+        if (e || (e = check_out(dims->h_strides, "h", a.B, a.T, a.H)) ||
+            (y && (e = check_out(dims->y_strides, "y", a.B, a.T, a.H))))
+            return e;
+        if (y && !pre_weight)
+            return fail(LA_ERR_INVALID_ARG, "y needs pre_weight");
+        if (a.rows == 0)
+            return LA_OK;
+        if ((e = need(h, "h")) || (pre_weight && (e = need(y, "y"))))
+            return e;
+        if (y == h || y == x || (gate && (y == gate || h == gate)) || (residual && y == residual))
+            return fail(LA_ERR_INVALID_ARG, "an output overlaps an input or the other output");
+        if ((h == x && !same(dims->h_strides, dims->x_strides)) ||
+            (h == residual && !same(dims->h_strides, dims->residual_strides)))
+            return fail(LA_ERR_INVALID_ARG, "h in place needs the input's strides");
+        a.h = norm_rows(h, dims->h_strides);
+        a.y = norm_rows(y, dims->y_strides);
+        return launched(la::block_norm_run(false, a, (cudaStream_t)stream), "block norm");
+    });
+}
+
+size_t la_block_norm_workspace_size(const la_block_norm_dims *dims, int32_t dtype)
+{
+    return norm_sizes(dims, dtype) == LA_OK ? la::block_norm_partial_bytes(dims->dim) : 0;
+}
+
+la_status la_block_norm_bwd(const la_block_norm_dims *dims, int32_t dtype, const void *x,
+                            const void *gate, const void *residual, const void *post_weight,
+                            const void *pre_weight, float eps, float scale, const void *d_h,
+                            const void *d_y, void *dx, void *d_gate, void *d_residual,
+                            void *d_post_weight, void *d_pre_weight, void *workspace,
+                            size_t workspace_bytes, void *stream)
+{
+    return guarded([&]() -> la_status {
+        cudaStream_t s = (cudaStream_t)stream;
+        la::BlockNormArgs a;
+        la_status e = norm_args(dims, dtype, x, gate, residual, post_weight, pre_weight, eps,
+                                scale, &a);
+        if (e || (d_h && (e = check_in(dims->dh_strides, "d_h"))) ||
+            (d_y && (e = check_in(dims->dy_strides, "d_y"))) ||
+            (e = check_out(dims->dx_strides, "dx", a.B, a.T, a.H)) ||
+            (d_gate && (e = check_out(dims->dgate_strides, "d_gate", a.B, a.T, a.H))) ||
+            (d_residual &&
+             (e = check_out(dims->dresidual_strides, "d_residual", a.B, a.T, a.H))))
+            return e;
+        if ((d_y || d_pre_weight) && !pre_weight)
+            return fail(LA_ERR_INVALID_ARG, "d_y and d_pre_weight need pre_weight");
+        if (d_post_weight && !post_weight)
+            return fail(LA_ERR_INVALID_ARG, "d_post_weight needs post_weight");
+        if (d_gate && !gate)
+            return fail(LA_ERR_INVALID_ARG, "d_gate needs gate");
+        const size_t wide = a.w_bf16 ? 2 : 4;
+        if (a.rows == 0) {  // no rows: the weights' gradients are zero
+            for (void *w : {d_post_weight, d_pre_weight})
+                if (w && (e = launched(cudaMemsetAsync(w, 0, a.D * wide, s), "weight gradient")))
+                    return e;
+            return LA_OK;
+        }
+        if ((e = need(dx, "dx")) || (gate && (e = need(d_gate, "d_gate"))) ||
+            (pre_weight ? (e = need(d_y, "d_y")) : (e = need(d_h, "d_h"))))
+            return e;
+        if ((d_post_weight || d_pre_weight) &&
+            (e = check_workspace(workspace, workspace_bytes,
+                                 la_block_norm_workspace_size(dims, dtype))))
+            return e;
+        a.dh = norm_rows(d_h, dims->dh_strides);
+        a.dy = norm_rows(d_y, dims->dy_strides);
+        a.dx = norm_rows(dx, dims->dx_strides);
+        a.dgate = norm_rows(d_gate, dims->dgate_strides);
+        a.dresidual = norm_rows(d_residual, dims->dresidual_strides);
+        a.dpost = d_post_weight;
+        a.dpre = d_pre_weight;
+        a.partial = static_cast<float *>(workspace);
+        return launched(la::block_norm_run(true, a, s), "block norm backward");
     });
 }
 

@@ -4,6 +4,8 @@
   * `qk_norm_rope`: norms of queries and keys for each head and the position
     rotation in one pass; `rotary`: the rotation alone.  `recurrent`,
     `recurrent_gla` and `lightning_attn` take them as qk_norm= and rope=.
+  * `block_norm`: the norms before and after a block, with its gate and its
+    residual scale.
   * `gated_scan`: the gated linear recurrence s_t = exp(g_t) s_{t-1} + x_t,
     elementwise, the vector-state sibling of `recurrent_gla`.
 
@@ -32,6 +34,8 @@ from .api import Tensor, _packed_batch_msg, _state, _traced
 _ref = ctypes.byref
 _scan_pack = struct.Struct("=6i18q").pack
 _rope_pack = struct.Struct("=12i21q128s").pack
+_norm_pack = struct.Struct("=6i30q").pack
+_norm_dims = N.LaBlockNormDims.from_buffer_copy
 _scan_dims = N.LaScanDims.from_buffer_copy
 _rope_dims = N.LaRopeDims.from_buffer_copy
 _current_device = torch._C._cuda_getDevice
@@ -565,3 +569,153 @@ def gated_scan(x: Tensor, g: Tensor, initial_state: Optional[Tensor] = None,
     o, fin = _GatedScan.apply(x, g, initial_state, _on_device(cu_seqlens, x.device),
                               bool(reverse), cu_seqlens_host)
     return (o[0] if squeeze else o), fin
+
+
+# ---------------------------------------------------------------------------
+# norms around a block
+
+_ACTIVATIONS = {"none": 0, "sigmoid": 1, "silu": 2}
+
+
+class _NormCall:
+    """The arguments that the forward and the backward share; 3-D tensors as one head."""
+
+    def __init__(self, x, gate, residual, post_weight, pre_weight, activation, scale, eps):
+        if activation not in _ACTIVATIONS:
+            raise ValueError("activation must be one of %s, got %r"
+                             % (sorted(_ACTIVATIONS), activation))
+        self.squeeze = x.ndim == 3
+        self.x = self.rows(x, "x")
+        self.dtype = _code(self.x.dtype)
+        dev = self.device = self.x.device
+        D = self.x.shape[3]
+        self.gate = self.like(gate, "gate")
+        self.residual = self.like(residual, "residual")
+        w_dtype, code = None, self.dtype
+        for w in (post_weight, pre_weight):
+            if w is None:
+                continue
+            if w.shape != (D,) or w.device != dev:
+                raise ValueError("weights must be [%d] on %s" % (D, dev))
+            if w.dtype != (w_dtype or w.dtype):
+                raise TypeError("the weights must share one dtype")
+            w_dtype, code = w.dtype, _code(w.dtype)
+        self.post = post_weight.contiguous() if post_weight is not None else None
+        self.pre = pre_weight.contiguous() if pre_weight is not None else None
+        self.tail = (float(eps), float(scale))
+        self._head = tuple(self.x.shape) + (_ACTIVATIONS[activation], code)
+
+    def rows(self, t, name):
+        if self.squeeze and t.ndim == 3:
+            t = t.unsqueeze(2)
+        return _token(t, name)
+
+    def like(self, t, name):
+        """t as x's rows, or None."""
+        if t is None:
+            return None
+        t = self.rows(t, name)
+        if t.shape != self.x.shape or t.dtype != self.x.dtype:
+            raise ValueError("%s must have x's shape and dtype" % name)
+        if t.device != self.device:
+            raise ValueError("all tensors must be on one device")
+        return t
+
+    def output(self, t, name):
+        if t is not None and self.squeeze and t.ndim == 3:
+            t = t.unsqueeze(2)
+        return _output(t, self.x, name)
+
+    def back(self, t):
+        return t.squeeze(2) if t is not None and self.squeeze else t
+
+    def dims(self, *outs):
+        strides = [s for t in (self.x, self.gate, self.residual) + outs for s in _strides(t)]
+        return _norm_dims(_norm_pack(*self._head, *strides))
+
+    def inputs(self):
+        return (_ptr(self.x), _ptr(self.gate), _ptr(self.residual), _ptr(self.post),
+                _ptr(self.pre)) + self.tail
+
+
+@_traced
+def block_norm_fwd(x: Tensor, gate: Optional[Tensor] = None, residual: Optional[Tensor] = None,
+                   post_weight: Optional[Tensor] = None, pre_weight: Optional[Tensor] = None,
+                   activation: str = "silu", scale: float = 1.0, eps: float = 1e-6, out=None):
+    """The norms around a block over rows x [B,T,H,D] or [B,T,C], in one pass:
+        n = rms(x) * post_weight   (x without post_weight),   m = n * act(gate),
+        h = residual + scale * m,   y = rms(h) * pre_weight,
+    rms(x) = x * rsqrt(mean(x^2) + eps).  Returns (h, y), y None without pre_weight.
+
+    A layer's end: block_norm_fwd(block_out, residual=stream, pre_weight=next_norm) gives the
+    stream and the next block's input; the heads' outputs, normalised and gated:
+    block_norm_fwd(o, gate=z, post_weight=w)[0].  activation: "none", "sigmoid" or "silu" of
+    the gate.  out: (h, y) to write to; h may be x or residual itself."""
+    c = _NormCall(x, gate, residual, post_weight, pre_weight, activation, scale, eps)
+    h, y = _pair_of(out, "out")
+    h = c.output(h, "out")
+    y = c.output(y, "out") if c.pre is not None else None
+    d = c.dims(h, y, None, None, None, None, None)
+    _call(c.device, N.lib().la_block_norm_fwd, _ref(d), c.dtype, *c.inputs(), _ptr(h), _ptr(y))
+    return c.back(h), c.back(y)
+
+
+@_traced
+def block_norm_bwd(x: Tensor, dh: Optional[Tensor], dy: Optional[Tensor] = None,
+                   gate: Optional[Tensor] = None, residual: Optional[Tensor] = None,
+                   post_weight: Optional[Tensor] = None, pre_weight: Optional[Tensor] = None,
+                   activation: str = "silu", scale: float = 1.0, eps: float = 1e-6):
+    """Backward of block_norm_fwd on the same arguments, from the gradients of h and y (either
+    may be None, not both): (dx, dgate, dresidual, dpost_weight, dpre_weight), None for what was
+    not given."""
+    c = _NormCall(x, gate, residual, post_weight, pre_weight, activation, scale, eps)
+    dh, dy = c.like(dh, "dh"), c.like(dy, "dy")
+    if dy is not None and c.pre is None:
+        raise ValueError("dy needs pre_weight")
+    if dy is None and c.pre is not None:
+        if dh is None:
+            raise ValueError("give dh, dy or both")
+        # y went unused: the same block without it
+        g = block_norm_bwd(x, c.back(dh), None, gate, residual, post_weight, None, activation,
+                           scale, eps)
+        return g[:4] + (torch.zeros_like(c.pre),)
+    if dh is None and dy is None:
+        raise ValueError("give dh, dy or both")
+    dx = _new(c.x)
+    dgate = _new(c.x) if c.gate is not None else None
+    dres = _new(c.x) if c.residual is not None else None
+    dpost = torch.empty_like(c.post) if c.post is not None else None
+    dpre = torch.empty_like(c.pre) if c.pre is not None else None
+    d = c.dims(None, None, dh, dy, dx, dgate, dres)
+    lib = N.lib()
+    ws, nbytes = None, 0
+    if dpost is not None or dpre is not None:
+        ws, nbytes = _workspace(int(lib.la_block_norm_workspace_size(_ref(d), c.dtype)), c.device)
+    _call(c.device, lib.la_block_norm_bwd, _ref(d), c.dtype, *c.inputs(), _ptr(dh), _ptr(dy),
+          _ptr(dx), _ptr(dgate), _ptr(dres), _ptr(dpost), _ptr(dpre), _ptr(ws), nbytes)
+    return c.back(dx), c.back(dgate), c.back(dres), dpost, dpre
+
+
+class _BlockNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gate, residual, post, pre, activation, scale, eps):
+        ctx.save_for_backward(x, gate, residual, post, pre)
+        ctx.args = (activation, scale, eps)
+        ctx.set_materialize_grads(False)
+        return block_norm_fwd(x, gate, residual, post, pre, activation, scale, eps)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh, dy=None):
+        x, gate, residual, post, pre = ctx.saved_tensors
+        if dh is None and dy is None:
+            return (None,) * 8
+        dh, dy = (None if t is None else t.to(x.dtype) for t in (dh, dy))
+        return block_norm_bwd(x, dh, dy, gate, residual, post, pre, *ctx.args) + (None,) * 3
+
+
+def block_norm(x: Tensor, gate: Optional[Tensor] = None, residual: Optional[Tensor] = None,
+               post_weight: Optional[Tensor] = None, pre_weight: Optional[Tensor] = None,
+               activation: str = "silu", scale: float = 1.0, eps: float = 1e-6):
+    """Differentiable block_norm_fwd: (h, y), in x, gate, residual and the weights."""
+    return _BlockNorm.apply(x, gate, residual, post_weight, pre_weight, activation, scale, eps)
