@@ -41,6 +41,7 @@
 
 #include <climits>
 
+#include "la_f32x2.cuh"
 #include "la_tc_common.cuh"
 
 namespace la {
@@ -50,7 +51,10 @@ constexpr int C = 64;                           // tokens a chunk
 constexpr int BTILE = 16384;                    // B hi, B lo: [64][64] bf16 each
 constexpr int STILE = 32768;                    // S^T or K'^T: [2][128 e][64 d] bf16
 constexpr int ETILE = 16384;                    // Eps or R: [2][64 tokens][64 e] bf16
-constexpr int TAB = C * 16;                     // {e^G, beta, kappa, G} a token
+// per token: -e^G, -beta, kappa, kappa beta, -e^G beta, beta, G / ln 2, each for a
+// chunk's 64 tokens in a row
+constexpr int TNEG = 0, TNB = 1, TKAP = 2, TKB = 3, TNGB = 4, TBETA = 5, TLOG = 6, TABS = 7;
+constexpr int TAB = TABS * C * 4;
 constexpr float LEAST_GATE = -100.f;            // e^-100 is 0 beside anything kept
 
 // Where a chunk lies.  Chunk slots: ceil(T / 64) a dense row; cu[n] / 64 + n on
@@ -98,7 +102,7 @@ __device__ __forceinline__ Seq sequence_of_slot(const int32_t *cu, int T, int N,
 
 struct Scratch {
     uint8_t *b;         // [slot][H] BTILE
-    float4 *tab;        // [slot][H][64]
+    float *tab;         // [slot][H][TABS][64]
     uint8_t *s, *e;     // [slot][H] STILE, ETILE (kept for the backward; or null)
     uint8_t *k, *r;     // backward: [slot][H] STILE, ETILE
     float *dqp, *dkp;   // backward, shared heads: [B][T][H][D] fp32
@@ -111,11 +115,56 @@ __device__ __forceinline__ float gate_at(const Tok &g, int bf16, int64_t row, in
                 : static_cast<const float *>(g.p)[at];
 }
 
-// (x0, x1) as hi + lo, each two bf16.
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo)
+// bwait, with the clock read (hundreds of cycles) only every 64th time: a chunk is
+// a dozen hand-offs one after another
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
 {
-    hi = pack_bf16x2(x0, x1);
-    lo = pack_bf16x2(x0 - bf16lo(hi), x1 - bf16hi(hi));
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity))
+            return true;
+    return bwait(bar, parity, abort_flag);
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    return un(la::mul2(f2(a.x, a.y), f2(b.x, b.y)));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    return un(la::fma2(f2(a.x, a.y), f2(b.x, b.y), f2(c.x, c.y)));
+}
+// One lane of a whole warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "elect.sync _|p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(one));
+    return one != 0;
+}
+// x as hi + lo, each two bf16.
+__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo)
+{
+    hi = pack_bf16x2(x.x, x.y);
+    const float2 rest = fma2(make_float2(bf16lo(hi), bf16hi(hi)), make_float2(-1.f, -1.f), x);
+    lo = pack_bf16x2(rest.x, rest.y);
+}
+__device__ __forceinline__ float2 pair_of(const uint32_t (&r)[32], int m)
+{
+    return make_float2(__uint_as_float(r[2 * m]), __uint_as_float(r[2 * m + 1]));
+}
+__device__ __forceinline__ void put_pair(uint32_t (&r)[32], int m, float2 x)
+{
+    r[2 * m] = __float_as_uint(x.x);
+    r[2 * m + 1] = __float_as_uint(x.y);
+}
+// 2^x, within 2^-22 of it
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
@@ -196,7 +245,9 @@ __device__ __forceinline__ void join_second(float (*A)[AP], const float *beta,
 __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, const Scratch sc)
 {
     __shared__ __align__(16) __nv_bfloat16 ks[C][KP];
-    __shared__ __align__(16) float A[C][AP], M[C / 2][AP];
+    __shared__ __align__(16) float A[C][AP];
+    float (*M)[AP] = reinterpret_cast<float (*)[AP]>(ks);   // once K K^T is done
+    static_assert(sizeof(float) * C / 2 * AP <= sizeof(ks), "M lies over K");
     __shared__ float G[C], beta[C], part[2];
     const int h = blockIdx.x % a.H;
     const int64_t slot = blockIdx.x / a.H;
@@ -211,19 +262,25 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
     const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k.p) + q.row * a.k.sb +
                              (q.bos + t0) * a.k.st + (int64_t)(h / a.k.hdiv) * a.k.sh;
     const int ksteps = (a.D + 15) / 16;
-    for (int x = tid; x < C * 2 * ksteps; x += PREP) {
-        const int i = x / (2 * ksteps), c = x % (2 * ksteps);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (i < n && 8 * c < a.D)
-            v = *reinterpret_cast<const uint4 *>(k + i * a.k.st + 8 * c);
-        *reinterpret_cast<uint4 *>(&ks[i][8 * c]) = v;
+    float g = 0.f, b = 0.f;
+    if (tid < n) {
+        g = fmaxf(gate_at(a.g, a.gate_bf16, q.row, q.bos + t0 + tid, h), LEAST_GATE);
+        b = gate_at(a.beta, a.gate_bf16, q.row, q.bos + t0 + tid, h);
+    }
+    {   // every load on its way before the first is waited for
+        uint4 v[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const int i = (tid >> 4) + 8 * x, c = tid & 15;
+            v[x] = make_uint4(0, 0, 0, 0);
+            if (i < n && 8 * c < a.D)
+                v[x] = *reinterpret_cast<const uint4 *>(k + i * a.k.st + 8 * c);
+        }
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            *reinterpret_cast<uint4 *>(&ks[(tid >> 4) + 8 * x][8 * (tid & 15)]) = v[x];
     }
     if (tid < C) {
-        float g = 0.f, b = 0.f;
-        if (tid < n) {
-            g = fmaxf(gate_at(a.g, a.gate_bf16, q.row, q.bos + t0 + tid, h), LEAST_GATE);
-            b = gate_at(a.beta, a.gate_bf16, q.row, q.bos + t0 + tid, h);
-        }
 #pragma unroll
         for (int m = 1; m < 32; m *= 2) {
             const float y = __shfl_up_sync(0xffffffffu, g, m);
@@ -237,9 +294,17 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
     }
     __syncthreads();
     if (tid < C) {
-        const float g = tid < 32 ? G[tid] : G[tid] + part[0];
+        g = tid < 32 ? g : g + part[0];
         const float all = part[0] + part[1];
-        sc.tab[tile * C + tid] = make_float4(expf(g), beta[tid], expf(all - g), g);
+        float *tab = sc.tab + tile * TABS * C + tid;
+        const float eg = expf(g), kap = expf(all - g);
+        tab[TNEG * C] = -eg;
+        tab[TNB * C] = -b;
+        tab[TKAP * C] = kap;
+        tab[TKB * C] = kap * b;
+        tab[TNGB * C] = -eg * b;
+        tab[TBETA * C] = b;
+        tab[TLOG * C] = g * 1.4426950408889634f;
         __syncwarp();
         G[tid] = g;
     }
@@ -310,7 +375,8 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 const int j = 8 * c16 + 2 * p;
-                split2(j < i ? A[i][j] : 0.f, j + 1 < i ? A[i][j + 1] : 0.f, hi[p], lo[p]);
+                split2(make_float2(j < i ? A[i][j] : 0.f, j + 1 < i ? A[i][j + 1] : 0.f), hi[p],
+                       lo[p]);
             }
             uint8_t *at = to + ((c16 ^ (i & 7)) << 4);
             *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -337,17 +403,17 @@ constexpr int Q2 = 16384;                       // bytes of one of them: [2][64]
 template <bool BWD> struct SweepLayout {
     static constexpr int TOFF = QOFF + (BWD ? 2 * Q2 : 0);
     static constexpr int MOFF = TOFF + NS * TAB;
-    static constexpr int NBAR = 4 * NS + 11;
+    static constexpr int NBAR = 4 * NS + 12;
     static constexpr int SLOT = MOFF + NBAR * 8;
     static constexpr int ABORT = SLOT + 4;
     static constexpr int RANK = ABORT + 4;
     static constexpr int DYN = RANK + 4 + 1024;
     static_assert(DYN <= 232448, "shared memory per CTA");
 };
-// TMEM columns: the state fp32, its hi and lo; the chain's accumulator; a second
-// one (O's inter term; back: P^T dO); scores, then O's intra term; the chain's
-// operand (beta X, then kappa beta Eps), hi and lo
-constexpr uint32_t TS = 0, TSH = 128, T1 = 256, T2 = 320, TR = 384, TY = 448, TCOLS = 512;
+// TMEM columns: the state fp32, its hi and lo; O's inter term (back: P^T dO) and the
+// chain's accumulator, next to each other as Q and K are in their tile; scores, then
+// O's intra term; the chain's operand (beta X, then kappa beta Eps), hi and lo
+constexpr uint32_t TS = 0, TSH = 128, T2 = 256, T1 = 320, TR = 384, TY = 448, TCOLS = 512;
 // an operand of 64 tokens in 64 columns: for each half of the tokens 16 columns of
 // hi, 16 of lo, so that the threads of a half write among columns of their own
 __device__ __forceinline__ uint32_t tok_col(int kk, int lo)
@@ -361,21 +427,35 @@ struct SweepParams {
     Scratch sc;
 };
 
-// 32 values a lane (this lane's channel, tokens 32 half ..) to bf16 rows, a token
-// a row: neighbouring lanes trade, each stores a pair of channels of every other
-// token.  at(token) gives the place of channel 0 or null.
-template <typename F>
-__device__ __forceinline__ void store_tokens(const float (&x)[32], int half, int e, int E, F at)
+// 32 values a lane (this lane's channel, 32 tokens) to bf16 rows, a token a row:
+// neighbouring lanes trade, each stores a pair of channels of every other token, the
+// even lane from the first on.  at: the lane's first row (its pair), step: bytes from
+// there to the row after next; n: rows there are, from this half's first on.
+__device__ __forceinline__ void store_rows(const float (&x)[32], bool odd, uint8_t *at, int64_t step,
+                                           int n)
 {
-    const bool odd = e & 1;
 #pragma unroll
     for (int m = 0; m < 16; ++m) {
         const float mine = odd ? x[2 * m + 1] : x[2 * m], other = odd ? x[2 * m] : x[2 * m + 1];
         const float got = __shfl_xor_sync(0xffffffffu, other, 1);
         const uint32_t pair = odd ? pack_bf16x2(got, mine) : pack_bf16x2(mine, got);
-        const int j = 32 * half + 2 * m + odd;
-        if (uint8_t *p = at(j); p && e < E)
-            *reinterpret_cast<uint32_t *>(p) = pair;
+        if (2 * m + odd < n)
+            *reinterpret_cast<uint32_t *>(at) = pair;
+        at += step;
+    }
+}
+// to a [2][64 tokens][64 channels] swizzled tile
+__device__ __forceinline__ void store_image(const float (&x)[32], int half, int e, uint8_t *tile)
+{
+    const bool odd = e & 1;
+    uint8_t *at = tile + (e >> 6) * 8192 + (32 * half + odd) * 128 + (e & 6) * 2;
+    const int c16 = (e & 63) >> 3;
+#pragma unroll
+    for (int m = 0; m < 16; ++m) {
+        const float mine = odd ? x[2 * m + 1] : x[2 * m], other = odd ? x[2 * m] : x[2 * m + 1];
+        const float got = __shfl_xor_sync(0xffffffffu, other, 1);
+        const uint32_t pair = odd ? pack_bf16x2(got, mine) : pack_bf16x2(mine, got);
+        *reinterpret_cast<uint32_t *>(at + m * 256 + ((c16 ^ ((2 * m + odd) & 7)) << 4)) = pair;
     }
 }
 // place of the pair of channels of e in row j of a [2][rows][64] swizzled tile
@@ -404,13 +484,14 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
     uint64_t *s_ready = bars + 5;       // the state's hi, lo and its decayed fp32
     uint64_t *y_ready = bars + 6;       // X and beta X
     uint64_t *w_ready = bars + 7;       // what the state takes, and beta Eps
-    uint64_t *p_ready = bars + 8;       // P (back: the Q lanes' part is q_ready)
-    uint64_t *q_ready = bars + 9;       // forward: O read; back: scale e^G Q
-    uint64_t *drain = bars + 10;
+    uint64_t *p_ready = bars + 8;       // P
+    uint64_t *q_ready = bars + 9;       // Q S read out of TMEM; back: scale e^G Q
+    uint64_t *r_ready = bars + 10;      // O's intra term read
+    uint64_t *drain = bars + 11;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::SLOT);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::ABORT);
     volatile int *rank_slot = reinterpret_cast<volatile int *>(sm + L::RANK);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -421,11 +502,12 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         }
         for (int i = 0; i < 5; ++i)
             mbar_init(&bars[i], 1);
-        mbar_init(s_ready, CHAIN);
-        mbar_init(y_ready, CHAIN);
-        mbar_init(w_ready, CHAIN);
-        mbar_init(p_ready, C);
-        mbar_init(q_ready, BWD ? C : SIDE);
+        mbar_init(s_ready, CHAIN / 32);
+        mbar_init(y_ready, CHAIN / 32);
+        mbar_init(w_ready, CHAIN / 32);
+        mbar_init(p_ready, 2);
+        mbar_init(q_ready, BWD ? 2 : SIDE / 32);
+        mbar_init(r_ready, SIDE / 32);
         mbar_init(drain, 1);
         *abort_flag = 0;
         *rank_slot = blockIdx.x / a.H;
@@ -467,7 +549,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
     auto chunk = [&](int c) { return BWD ? nc - 1 - c : c; };
     auto tokens = [&](int c) { return (int)min((int64_t)C, sq.len - (int64_t)chunk(c) * C); };
     auto tile_of = [&](int c) { return (sq.slot + chunk(c)) * a.H + h; };
-    const float4 *tabs = reinterpret_cast<const float4 *>(sm + L::TOFF);
+    const float *tabs = reinterpret_cast<const float *>(sm + L::TOFF);
 
     if (warp == 0) {
         // ------------------------------------------------------------- loads
@@ -476,7 +558,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             int issued = 0;
             for (int c = 0; c < nc; ++c) {
                 const int s = c % NS;
-                if (c >= NS && !bwait(&empty[s], (c / NS - 1) & 1, abort_flag))
+                if (c >= NS && !wait_for(&empty[s], (c / NS - 1) & 1, abort_flag))
                     break;
                 const int t = (int)(sq.bos + (int64_t)chunk(c) * C);
                 uint8_t *st = sm + s * STAGE;
@@ -487,7 +569,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                     tma_load_4d(st + QK + b * 16384 + 8192, &P.mk, &full[s], 64 * b, hq, t,
                                 (int)sq.row);
                 }
-                bulk_load(sm + L::TOFF + s * TAB, P.sc.tab + tile_of(c) * C, TAB, &full[s]);
+                bulk_load(sm + L::TOFF + s * TAB, P.sc.tab + tile_of(c) * TABS * C, TAB, &full[s]);
                 mbar_arrive_expect_tx(&fullv[s], 16384);
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
@@ -507,35 +589,67 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         // ---------------------------------------------------------- products
         const uint32_t sb = smem_u32(sm);
         constexpr uint32_t id64 = idesc_bf16_f32(128, 64, 0, 0);       // B K-major
+        constexpr uint32_t id128 = idesc_bf16_f32(128, 128, 0, 0);
         constexpr uint32_t id64mn = idesc_bf16_f32(128, 64, 0, 1);     // B MN-major
         constexpr uint32_t id128mn = idesc_bf16_f32(128, 128, 0, 1);
         constexpr uint32_t id64mm = idesc_bf16_f32(128, 64, 1, 1);     // both MN-major
         constexpr uint32_t id128mm = idesc_bf16_f32(128, 128, 1, 1);
-        const uint32_t ph = sb + POFF, pl = ph + 8192;
-        auto stage = [&](int c) { return sb + (uint32_t)((c % NS) * STAGE); };
-        // rows `row` .. of the [Q; K] tile as the K-major B operand, k-step kk of D
-        auto rows_desc = [&](uint32_t st, int row, int kk) {
-            return sdesc_sw128(st + QK + row * 128 + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024);
-        };
-        // as an MN-major operand (D along M or N), k-step kk of the tokens
-        auto cols_desc = [&](uint32_t st, int row, int kk) {
-            return sdesc_sw128(st + QK + row * 128 + kk * 2048, 16384, 1024);
-        };
+        // Descriptors of stage 0 once; another place is an addition to the address
+        // field (16-byte units): what one product costs to issue counts here.
+        const uint64_t d_rows = sdesc_sw128(sb + QK, 16, 1024);        // [Q; K] by rows
+        const uint64_t d_cols = sdesc_sw128(sb + QK, 16384, 1024);     // D along M or N
+        const uint64_t d_b = sdesc_sw128(sb + BB, 16, 1024);
+        const uint64_t d_bmn = sdesc_sw128(sb + BB, 8192, 1024);
+        const uint64_t d_do = sdesc_sw128(sb + VD, 8192, 1024);
+        const uint64_t d_p = sdesc_sw128(sb + POFF, 16, 1024);
+        const uint64_t d_pmn = sdesc_sw128(sb + POFF, 8192, 1024);
+        const uint64_t d_q2 = sdesc_sw128(sb + QOFF, 8192, 1024);
+        auto off = [](uint32_t bytes) { return (uint64_t)(bytes >> 4); };
+        auto stage = [&](int c) { return off((uint32_t)((c % NS) * STAGE)); };
+        // k-step kk of D in a tile of 128 rows
+        auto kd = [&](int kk) { return off((uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32)); };
         auto scores = [&](int c) {      // [Q; K] K^T
-            const uint32_t st = stage(c);
+            const uint64_t d = d_rows + stage(c);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-                mma_ss(tm + TR, rows_desc(st, 0, kk), rows_desc(st, 64, kk), id64, kk > 0);
+                mma_ss(tm + TR, d + kd(kk), d + off(8192) + kd(kk), id64, kk > 0);
             mma_commit(sc_full);
         };
-        auto state_times = [&](uint32_t d, int c, int row) {
-            const uint32_t st = stage(c);
+        // S^T [Q; K]^T (back: K'^T K^T)
+        auto state_times = [&](int c) {
+            const uint64_t d = d_rows + stage(c);
 #pragma unroll
             for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    mma_ts(tm + d, tm + TSH + 64 * lo + 8 * kk, rows_desc(st, row, kk), id64,
-                           lo + kk > 0);
+                    if (BWD)
+                        mma_ts(tm + T1, tm + TSH + 64 * lo + 8 * kk, d + off(8192) + kd(kk), id64,
+                               lo + kk > 0);
+                    else
+                        mma_ts(tm + T2, tm + TSH + 64 * lo + 8 * kk, d + kd(kk), id128,
+                               lo + kk > 0);
+        };
+        // T1 += (beta X)^T B^T (back: B): hi hi, lo hi, hi lo
+        auto solve = [&](int c) {
+            const uint64_t d = (BWD ? d_bmn : d_b) + stage(c);
+#pragma unroll
+            for (int x = 0; x < 3; ++x)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ts(tm + T1, tm + TY + tok_col(kk, x == 1),
+                           d + off((x == 2 ? BTILE / 2 : 0) + kk * (BWD ? 2048 : 32)),
+                           BWD ? id64mn : id64, 1);
+            mma_commit(e_full);
+        };
+        // the state += (chain's operand)^T K
+        auto update = [&](int c) {
+            const uint64_t d = d_cols + stage(c) + off(8192);
+#pragma unroll
+            for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ts(tm + TS, tm + TY + tok_col(kk, lo), d + off(kk * 2048), id128mn, 1);
+            mma_commit(s_full);
         };
         // The tokens past a packed sequence's end are another's: zeros in their
         // place (the loads fill with zeros past the tensor's end).
@@ -543,7 +657,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             const int n = tokens(c);
             if (!a.cu || n == C)
                 return true;
-            if (!warp_all(bwait(&fullv[c % NS], (c / NS) & 1, abort_flag)))
+            if (!warp_all(wait_for(&fullv[c % NS], (c / NS) & 1, abort_flag)))
                 return false;
             uint8_t *st = sm + (c % NS) * STAGE;
             const uint4 z = make_uint4(0, 0, 0, 0);
@@ -561,14 +675,14 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             return true;
         };
         auto stage_in = [&](int c) {
-            return warp_all(bwait(&full[c % NS], (c / NS) & 1, abort_flag)) && clear_tail(c);
+            return warp_all(wait_for(&full[c % NS], (c / NS) & 1, abort_flag)) && clear_tail(c);
         };
         auto both = [&](uint64_t *bar, int c) {
-            const bool ok = warp_all(bwait(bar, c & 1, abort_flag));
+            const bool ok = warp_all(wait_for(bar, c & 1, abort_flag));
             tc_fence_after();
             return ok;
         };
-        const bool one = lane == 0;
+        const bool one = elect_one();
         bool any = false;
         if (BWD && nc > 0 && stage_in(0)) {
             any = true;
@@ -577,41 +691,42 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             __syncwarp();
             auto prior = [&](int c) {   // P^T dO
                 if (!both(p_ready, c) ||
-                    !warp_all(bwait(&fullv[c % NS], (c / NS) & 1, abort_flag)))
+                    !warp_all(wait_for(&fullv[c % NS], (c / NS) & 1, abort_flag)))
                     return false;
                 if (one) {
-                    const uint32_t st = stage(c);
+                    const uint64_t d = d_do + stage(c);
 #pragma unroll
                     for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_ss(tm + T2, sdesc_sw128(st + VD + kk * 2048, 8192, 1024),
-                                   sdesc_sw128((lo ? pl : ph) + kk * 2048, 8192, 1024), id64mm,
-                                   lo + kk > 0);
+                            mma_ss(tm + T2, d + off(kk * 2048), d_pmn + off(lo * 8192 + kk * 2048),
+                                   id64mm, lo + kk > 0);
                 }
                 __syncwarp();
                 return true;
             };
             bool ok = prior(0);
             for (int c = 0; ok && c < nc; ++c) {
-                const uint32_t st = stage(c);
                 if (!(ok = both(s_ready, c)))
                     break;
                 if (one) {
-                    state_times(T1, c, 64);
+                    state_times(c);
                     mma_commit(ks_full);
                 }
                 __syncwarp();
+                // what the chain does not wait for goes between its products, while its
+                // warps work
                 if (!(ok = both(q_ready, c)))
                     break;
-                if (one)    // dO^T (scale e^G Q)
+                if (one) {  // K'^T += dO^T (scale e^G Q)
+                    const uint64_t d = d_do + stage(c);
 #pragma unroll
                     for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_ss(tm + TS, sdesc_sw128(st + VD + kk * 2048, 8192, 1024),
-                                   sdesc_sw128(sb + QOFF + lo * Q2 + kk * 2048, 8192, 1024),
+                            mma_ss(tm + TS, d + off(kk * 2048), d_q2 + off(lo * Q2 + kk * 2048),
                                    id128mm, 1);
+                }
                 __syncwarp();
                 if (c + 1 < nc) {
                     if (!(ok = stage_in(c + 1)))
@@ -620,31 +735,16 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                         scores(c + 1);
                     __syncwarp();
                 }
-                if (!(ok = warp_all(bwait(&fullb[c % NS], (c / NS) & 1, abort_flag)) &&
+                if (!(ok = warp_all(wait_for(&fullb[c % NS], (c / NS) & 1, abort_flag)) &&
                            both(y_ready, c)))
                     break;
-                if (one) {
-#pragma unroll
-                    for (int x = 0; x < 3; ++x)     // hi hi, lo hi, hi lo
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_ts(tm + T1, tm + TY + tok_col(kk, x == 1),
-                                   sdesc_sw128(st + BB + (x == 2 ? BTILE / 2 : 0) + kk * 2048, 8192,
-                                               1024),
-                                   id64mn, 1);
-                    mma_commit(e_full);
-                }
+                if (one)
+                    solve(c);
                 __syncwarp();
                 if (!(ok = both(w_ready, c)))
                     break;
                 if (one) {
-#pragma unroll
-                    for (int lo = 0; lo < 2; ++lo)
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_ts(tm + TS, tm + TY + tok_col(kk, lo), cols_desc(st, 64, kk),
-                                   id128mn, 1);
-                    mma_commit(s_full);
+                    update(c);
                     mma_commit(&empty[c % NS]);
                 }
                 __syncwarp();
@@ -653,48 +753,31 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             }
         } else if (!BWD) {
             for (int c = 0; c < nc; ++c) {
-                const uint32_t st = stage(c);
-                if (!stage_in(c) || !both(s_ready, c))
+                if (!stage_in(c) || (c > 0 && !both(q_ready, c - 1)) || !both(s_ready, c))
                     break;
                 any = true;
                 if (one) {
-                    state_times(T1, c, 64);
+                    state_times(c);
                     mma_commit(ks_full);
                 }
                 __syncwarp();
-                if (c > 0 && !both(q_ready, c - 1))     // O of the chunk before is read
+                // what the chain does not wait for goes between its products, while its
+                // warps work: the scores while X is made, O's intra term while S is
+                if (c > 0 && !both(r_ready, c - 1))
                     break;
-                if (one) {
+                if (one)
                     scores(c);
-                    state_times(T2, c, 0);
-                }
                 __syncwarp();
-                if (!warp_all(bwait(&fullb[c % NS], (c / NS) & 1, abort_flag)) ||
+                if (!warp_all(wait_for(&fullb[c % NS], (c / NS) & 1, abort_flag)) ||
                     !both(y_ready, c))
                     break;
-                if (one) {
-#pragma unroll
-                    for (int x = 0; x < 3; ++x)
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_ts(tm + T1, tm + TY + tok_col(kk, x == 1),
-                                   sdesc_sw128(st + BB + (x == 2 ? BTILE / 2 : 0) + kk * 32, 16,
-                                               1024),
-                                   id64, 1);
-                    mma_commit(e_full);
-                }
+                if (one)
+                    solve(c);
                 __syncwarp();
                 if (!both(w_ready, c))
                     break;
-                if (one) {
-#pragma unroll
-                    for (int lo = 0; lo < 2; ++lo)
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_ts(tm + TS, tm + TY + tok_col(kk, lo), cols_desc(st, 64, kk),
-                                   id128mn, 1);
-                    mma_commit(s_full);
-                }
+                if (one)
+                    update(c);
                 __syncwarp();
                 if (!both(p_ready, c))
                     break;
@@ -704,8 +787,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             mma_ts(tm + TR, tm + T1 + tok_col(kk, x == 1),
-                                   sdesc_sw128((x == 2 ? pl : ph) + kk * 32, 16, 1024), id64,
-                                   x + kk > 0);
+                                   d_p + off((x == 2 ? 8192 : 0) + kk * 32), id64, x + kk > 0);
                     mma_commit(o_full);
                     mma_commit(&empty[c % NS]);
                 }
@@ -726,24 +808,24 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         const float *in = BWD ? a.dfin : a.init;
         float *out = BWD ? a.dinit : a.fin;
         uint8_t *simg = BWD ? P.sc.k : P.sc.s, *eimg = BWD ? P.sc.r : P.sc.e;
-        const int mine = threadIdx.x - 64;
         bool ok = true;
         for (int c = 0; ok && c < nc; ++c) {
             const int s = c % NS, n = tokens(c);
             const uint8_t *st = sm + s * STAGE;
-            const float4 *tab = tabs + s * C;
+            const float *tab = tabs + s * TABS * C;
             const int64_t tile = tile_of(c);
-            if (!(ok = warp_all(bwait(&full[s], (c / NS) & 1, abort_flag))))
+            if (!(ok = warp_all(wait_for(&full[s], (c / NS) & 1, abort_flag))))
                 break;
             // ---- the state
-            if (c > 0 && !(ok = warp_all(bwait(s_full, (c - 1) & 1, abort_flag))))
+            if (c > 0 && !(ok = warp_all(wait_for(s_full, (c - 1) & 1, abort_flag))))
                 break;
             tc_fence_after();
-            const float gC = tab[C - 1].x;
+            const float2 gC = make_float2(-tab[TNEG * C + C - 1], -tab[TNEG * C + C - 1]);
+            uint32_t shi[2][16];
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 const int d0 = 64 * half + 32 * p;
-                uint32_t r[32];
+                uint32_t r[32], lo[16];
                 if (c == 0) {
 #pragma unroll
                     for (int x = 0; x < 32; ++x)
@@ -753,42 +835,48 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 } else {
                     tmem_ld32(lanes + TS + d0, r);
                 }
-                uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
-                    split2(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1]), hi[x], lo[x]);
-                    r[2 * x] = __float_as_uint(gC * __uint_as_float(r[2 * x]));
-                    r[2 * x + 1] = __float_as_uint(gC * __uint_as_float(r[2 * x + 1]));
+                    split2(pair_of(r, x), shi[p][x], lo[x]);
+                    put_pair(r, x, mul2(gC, pair_of(r, x)));
                 }
-                tmem_st16_issue(lanes + TSH + d0 / 2, hi);
+                tmem_st16_issue(lanes + TSH + d0 / 2, shi[p]);
                 tmem_st16_issue(lanes + TSH + 64 + d0 / 2, lo);
                 tmem_st32_issue(lanes + TS + d0, r);
-                if (simg) {
-                    uint8_t *to = simg + tile * STILE + half * 16384 + e * 128;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        *reinterpret_cast<uint4 *>(to + (((4 * p + x) ^ (e & 7)) << 4)) =
-                            make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
-                }
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(s_ready);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(s_ready);
+            if (simg) {
+                uint8_t *to = simg + tile * STILE + half * 16384 + e * 128;
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    *reinterpret_cast<uint4 *>(to + ((x ^ (e & 7)) << 4)) =
+                        make_uint4(shi[x >> 2][4 * (x & 3)], shi[x >> 2][4 * (x & 3) + 1],
+                                   shi[x >> 2][4 * (x & 3) + 2], shi[x >> 2][4 * (x & 3) + 3]);
+            }
             // ---- X (W)
             const int j0 = 32 * half;
+            const float *tj = tab + j0;
+            auto pair_at = [&](int which, int m) {
+                return *reinterpret_cast<const float2 *>(tj + which * C + 2 * m);
+            };
             uint32_t v[16];
             if constexpr (!BWD) {
-                if (!(ok = warp_all(bwait(&fullv[s], (c / NS) & 1, abort_flag))))
+                if (!(ok = warp_all(wait_for(&fullv[s], (c / NS) & 1, abort_flag))))
                     break;
+                const uint8_t *vr = st + VD + (e >> 6) * 8192 + j0 * 128 + (e & 7) * 2;
+                const int c16 = (e & 63) >> 3;
 #pragma unroll
                 for (int x = 0; x < 32; ++x) {
-                    const int j = j0 + x;
                     const uint32_t b = *reinterpret_cast<const uint16_t *>(
-                        st + VD + image_pair(C, j, e) + (e & 1) * 2);
+                        vr + x * 128 + ((c16 ^ (x & 7)) << 4));
                     v[x / 2] = x & 1 ? v[x / 2] | b << 16 : b;
                 }
             }
-            if (!(ok = warp_all(bwait(ks_full, c & 1, abort_flag))))
+            if (!(ok = warp_all(wait_for(ks_full, c & 1, abort_flag))))
                 break;
             tc_fence_after();
             uint32_t r[32], hi[16], lo[16];
@@ -798,16 +886,14 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 tmem_ld32_issue(lanes + T2 + j0, p);
                 tmem_wait_ld(r, p);
 #pragma unroll
-                for (int x = 0; x < 32; ++x)
-                    r[x] = __float_as_uint(fmaf(tab[j0 + x].z, __uint_as_float(r[x]),
-                                                __uint_as_float(p[x])));
+                for (int x = 0; x < 16; ++x)
+                    put_pair(r, x, fma2(pair_at(TKAP, x), pair_of(r, x), pair_of(p, x)));
             } else {
                 tmem_ld32(lanes + T1 + j0, r);
 #pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    const float vv = x & 1 ? bf16hi(v[x / 2]) : bf16lo(v[x / 2]);
-                    r[x] = __float_as_uint(fmaf(-tab[j0 + x].x, __uint_as_float(r[x]), vv));
-                }
+                for (int x = 0; x < 16; ++x)
+                    put_pair(r, x, fma2(pair_at(TNEG, x), pair_of(r, x),
+                                        make_float2(bf16lo(v[x]), bf16hi(v[x]))));
             }
             if (n < C)
 #pragma unroll
@@ -816,66 +902,52 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                         r[x] = 0u;
 #pragma unroll
             for (int x = 0; x < 16; ++x)
-                split2(-tab[j0 + 2 * x].y * __uint_as_float(r[2 * x]),
-                       -tab[j0 + 2 * x + 1].y * __uint_as_float(r[2 * x + 1]), hi[x], lo[x]);
+                split2(mul2(pair_at(TNB, x), pair_of(r, x)), hi[x], lo[x]);
             tmem_st32_issue(lanes + T1 + j0, r);
             tmem_st16_issue(lanes + TY + 32 * half, hi);
             tmem_st16_issue(lanes + TY + 32 * half + 16, lo);
             tmem_wait_st();
             tc_fence_before();
-            if (!(a.withhold_handoff && c == 0 && mine == 0))
+            __syncwarp();
+            if (lane == 0 && !(a.withhold_handoff && c == 0 && warp == 2))
                 mbar_arrive(y_ready);
             // ---- Eps (R)
-            if (!(ok = warp_all(bwait(e_full, c & 1, abort_flag))))
+            if (!(ok = warp_all(wait_for(e_full, c & 1, abort_flag))))
                 break;
             tc_fence_after();
-            float x32[32];
             tmem_ld32(lanes + T1 + j0, r);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                const float4 t0 = tab[j0 + 2 * x], t1 = tab[j0 + 2 * x + 1];
-                const float x0 = __uint_as_float(r[2 * x]), x1 = __uint_as_float(r[2 * x + 1]);
-                x32[2 * x] = x0;
-                x32[2 * x + 1] = x1;
-                split2((BWD ? -t0.x : t0.z) * t0.y * x0, (BWD ? -t1.x : t1.z) * t1.y * x1, hi[x],
-                       lo[x]);
-            }
+            for (int x = 0; x < 16; ++x)
+                split2(mul2(pair_at(BWD ? TNGB : TKB, x), pair_of(r, x)), hi[x], lo[x]);
             tmem_st16_issue(lanes + TY + 32 * half, hi);
             tmem_st16_issue(lanes + TY + 32 * half + 16, lo);
             if constexpr (!BWD) {
                 // beta Eps over this half's own columns of T1
 #pragma unroll
                 for (int x = 0; x < 16; ++x)
-                    split2(tab[j0 + 2 * x].y * x32[2 * x], tab[j0 + 2 * x + 1].y * x32[2 * x + 1],
-                           hi[x], lo[x]);
+                    split2(mul2(pair_at(TBETA, x), pair_of(r, x)), hi[x], lo[x]);
                 tmem_st16_issue(lanes + T1 + 32 * half, hi);
                 tmem_st16_issue(lanes + T1 + 32 * half + 16, lo);
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(w_ready);
-            // ---- off the chain: what delta_grads starts from, dv
-            if (eimg)
-                store_tokens(x32, half, e, 128, [&](int j) {
-                    return eimg + tile * ETILE + image_pair(C, j, e);
-                });
-            if constexpr (BWD) {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(w_ready);
+            // ---- off the chain: what delta_grads starts from
+            if (eimg) {
+                float x32[32];
 #pragma unroll
                 for (int x = 0; x < 32; ++x)
-                    x32[x] *= tab[j0 + x].y;
-                uint8_t *to = reinterpret_cast<uint8_t *>(
-                    static_cast<__nv_bfloat16 *>(a.dv.p) + sq.row * a.dv.sb +
-                    (sq.bos + (int64_t)chunk(c) * C) * a.dv.st + (int64_t)h * a.dv.sh + (e & ~1));
-                store_tokens(x32, half, e, a.E, [&](int j) -> uint8_t * {
-                    return j < n ? to + 2 * j * a.dv.st : nullptr;
-                });
+                    x32[x] = __uint_as_float(r[x]);
+                store_image(x32, half, e, eimg + tile * ETILE);
             }
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&empty[s]);
         }
         if (ok && nc > 0)
-            ok = warp_all(bwait(s_full, (nc - 1) & 1, abort_flag));
+            ok = warp_all(wait_for(s_full, (nc - 1) & 1, abort_flag));
         tc_fence_after();
         if (ok && out)
 #pragma unroll 1
@@ -898,44 +970,55 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         const uint32_t lanes = tm + ((uint32_t)(32 * q) << 16);
         for (int c = 0; c < nc; ++c) {
             const int s = c % NS, n = tokens(c);
-            const float4 *tab = tabs + s * C;
-            if (!warp_all(bwait(&full[s], (c / NS) & 1, abort_flag)) ||
-                !warp_all(bwait(sc_full, c & 1, abort_flag)))
+            const float *tab = tabs + s * TABS * C;
+            if (!warp_all(wait_for(&full[s], (c / NS) & 1, abort_flag)) ||
+                !warp_all(wait_for(sc_full, c & 1, abort_flag)))
                 break;
             tc_fence_after();
-            if (q < 2) {    // row i of P
+            if (q < 2) {    // row i of P; columns past the warp's rows are zero
                 const int i = row;
-                const float gi = tab[i].w;
+                const float gi = tab[TLOG * C + i];
+                const float2 gi2 = make_float2(gi, gi), s2 = make_float2(a.scale, a.scale);
+                const float2 minus = make_float2(-1.f, -1.f);
                 uint8_t *to = sm + POFF + i * 128;
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    uint32_t r[32];
-                    tmem_ld32(lanes + TR + 32 * p, r);
+                    uint32_t hi[16] = {}, lo[16] = {};
+                    if (p <= q) {
+                        uint32_t r[32];
+                        tmem_ld32(lanes + TR + 32 * p, r);
+                        const float *gj = tab + TLOG * C + 32 * p;
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        const int j = 32 * p + x;
-                        r[x] = j <= i ? __float_as_uint(a.scale * __expf(gi - tab[j].w) *
-                                                        __uint_as_float(r[x]))
-                                      : 0u;
+                        for (int x = 0; x < 16; ++x) {
+                            const float2 d = fma2(
+                                *reinterpret_cast<const float2 *>(gj + 2 * x), minus, gi2);
+                            float2 y = mul2(mul2(make_float2(exp2_fast(d.x), exp2_fast(d.y)), s2),
+                                            pair_of(r, x));
+                            if (p == q) {
+                                y.x = 2 * x <= lane ? y.x : 0.f;
+                                y.y = 2 * x + 1 <= lane ? y.y : 0.f;
+                            }
+                            split2(y, hi[x], lo[x]);
+                        }
                     }
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            split2(__uint_as_float(r[8 * x + 2 * y]),
-                                   __uint_as_float(r[8 * x + 2 * y + 1]), hi[y], lo[y]);
                         uint8_t *at = to + (((4 * p + x) ^ (i & 7)) << 4);
-                        *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(at + 8192) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        *reinterpret_cast<uint4 *>(at) =
+                            make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
+                        *reinterpret_cast<uint4 *>(at + 8192) =
+                            make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
                     }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(p_ready);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(p_ready);
             } else if (BWD) {   // row i of scale e^G Q
                 const int i = row - 64;
-                const float f = i < n ? a.scale * tab[i].x : 0.f;
+                const float f = i < n ? -a.scale * tab[TNEG * C + i] : 0.f;
+                const float2 f2 = make_float2(f, f);
                 const uint8_t *from = sm + s * STAGE + QK + i * 128;
                 uint8_t *to = sm + QOFF + i * 128;
 #pragma unroll 4
@@ -948,42 +1031,59 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
-                        split2(f * bf16lo(w[y]), f * bf16hi(w[y]), hi[y], lo[y]);
+                        split2(mul2(f2, make_float2(bf16lo(w[y]), bf16hi(w[y]))), hi[y], lo[y]);
                     uint8_t *at = to + (x >> 3) * 8192 + off;
                     *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(at + Q2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(q_ready);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(q_ready);
             }
             if constexpr (!BWD) {
-                if (!warp_all(bwait(o_full, c & 1, abort_flag)))
+                // the inter term leaves TMEM as soon as it is there: the next chunk's
+                // product with S takes its columns
+                if (!warp_all(wait_for(ks_full, c & 1, abort_flag)))
                     break;
                 tc_fence_after();
-                uint8_t *to = a.o.p ? reinterpret_cast<uint8_t *>(
-                                          static_cast<__nv_bfloat16 *>(a.o.p) + sq.row * a.o.sb +
-                                          (sq.bos + (int64_t)c * C) * a.o.st +
-                                          (int64_t)h * a.o.sh + (row & ~1))
-                                    : nullptr;
+                uint32_t inter[2][32];
+                tmem_ld32_issue(lanes + T2, inter[0]);
+                tmem_ld32_issue(lanes + T2 + 32, inter[1]);
+                tmem_wait_ld(inter[0], inter[1]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(q_ready);
+                if (!warp_all(wait_for(o_full, c & 1, abort_flag)))
+                    break;
+                tc_fence_after();
+                const bool odd = lane & 1;
+                uint8_t *to = reinterpret_cast<uint8_t *>(
+                    static_cast<__nv_bfloat16 *>(a.o.p) + sq.row * a.o.sb +
+                    (sq.bos + (int64_t)c * C + odd) * a.o.st + (int64_t)h * a.o.sh + (row & ~1));
+                const bool some = a.o.p && row < a.E;
+                const float2 s2 = make_float2(-a.scale, -a.scale);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    uint32_t r[32], w[32];
-                    tmem_ld32_issue(lanes + T2 + 32 * p, r);
-                    tmem_ld32_issue(lanes + TR + 32 * p, w);
-                    tmem_wait_ld(r, w);
+                    uint32_t w[32];
+                    tmem_ld32(lanes + TR + 32 * p, w);
                     if (p == 1) {
                         tc_fence_before();
-                        mbar_arrive(q_ready);
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(r_ready);
                     }
                     float y[32];
 #pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        y[x] = fmaf(a.scale * tab[32 * p + x].x, __uint_as_float(r[x]),
-                                    __uint_as_float(w[x]));
-                    if (to)
-                        store_tokens(y, p, row, a.E, [&](int j) -> uint8_t * {
-                            return j < n ? to + 2 * j * a.o.st : nullptr;
-                        });
+                    for (int x = 0; x < 16; ++x) {
+                        const float2 g = *reinterpret_cast<const float2 *>(tab + TNEG * C + 32 * p +
+                                                                           2 * x);
+                        const float2 z = fma2(mul2(g, s2), pair_of(inter[p], x), pair_of(w, x));
+                        y[2 * x] = z.x;
+                        y[2 * x + 1] = z.y;
+                    }
+                    store_rows(y, odd, to + 64 * p * a.o.st, 4 * a.o.st, some ? n - 32 * p : 0);
                 }
             }
             __syncwarp();
@@ -1073,7 +1173,7 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tm = *tslot;
     const uint32_t lanes = tm + ((uint32_t)(32 * q) << 16);
-    const float4 *tab = P.sc.tab + tile * C;
+    const float *tab = P.sc.tab + tile * TABS * C;
 
     if (tid == 0) {
         const int hq = h / a.q.hdiv, t = (int)(sq.bos + t0), row = (int)sq.row;
@@ -1089,7 +1189,7 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
         bulk_load(sm + GS, P.sc.s + tile * STILE, STILE, in_full);
     }
     __syncwarp();
-    bool ok = warp_all(bwait(in_full, 0, abort_flag));
+    bool ok = warp_all(wait_for(in_full, 0, abort_flag));
     if (a.cu && n < C) {    // another sequence's tokens: zeros
         const uint4 z = make_uint4(0, 0, 0, 0);
         for (int x = tid; x < (C - n) * 8; x += GRADS) {
@@ -1122,12 +1222,25 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
         mma_commit(one_full);
     }
     __syncwarp();
+    // dv = beta R, row by row
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int i = (tid >> 4) + 16 * x, c16 = tid & 15;
+        if (i < n && 8 * c16 < a.E) {
+            const float f = tab[TBETA * C + i];
+            const uint4 v = *reinterpret_cast<const uint4 *>(
+                sm + GD + (c16 >> 3) * 16384 + 8192 + i * 128 + (((c16 & 7) ^ (i & 7)) << 4));
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.dv.p) + sq.row * a.dv.sb +
+                                       (sq.bos + t0 + i) * a.dv.st + (int64_t)h * a.dv.sh +
+                                       8 * c16) = scale8(v, f);
+        }
+    }
     // this thread's share of S for <S, K'>
     uint4 sv[8];
 #pragma unroll
     for (int x = 0; x < 8; ++x)
         sv[x] = *reinterpret_cast<const uint4 *>(sm + GS + tid * 16 + x * 4096);
-    ok = warp_all(bwait(one_full, 0, abort_flag)) && ok;
+    ok = warp_all(wait_for(one_full, 0, abort_flag)) && ok;
     tc_fence_after();
     __syncthreads();    // S has been read, by the products and by every thread
     if (tid == 0 && ok) {
@@ -1138,12 +1251,12 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
     const int j0 = 32 * half;
     {   // W1, W2 as bf16 rows over dO and R (both read); S dO^T, S R^T scaled
         const int i = 32 * (q & 1) + lane;
-        const float4 ti = tab[i];
+        const float gi = tab[TLOG * C + i];
         uint32_t r[32];
         tmem_ld32(lanes + UW + j0, r);
         uint8_t *to = sm + GD + (q < 2 ? 0 : 8192) + i * 128;
         // one branch a warp: dO's lanes, R's lanes
-        const float f = q < 2 ? a.scale : -ti.y;
+        const float f = q < 2 ? a.scale : tab[TNB * C + i];
         const int last = q < 2 ? i : i - 1;
         if (q >= 2 && i >= j0 && i < j0 + 32 && i < n) {
             float d = 0.f;
@@ -1155,10 +1268,11 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
         }
 #pragma unroll
         for (int x = 0; x < 32; ++x) {
-            const float4 tj = tab[j0 + x];
-            r[x] = j0 + x <= last ? __float_as_uint(f * tj.y * __expf(ti.w - tj.w) *
-                                                    __uint_as_float(r[x]))
-                                  : 0u;
+            const int j = j0 + x;
+            r[x] = j <= last ? __float_as_uint(f * tab[TBETA * C + j] *
+                                               exp2_fast(gi - tab[TLOG * C + j]) *
+                                               __uint_as_float(r[x]))
+                             : 0u;
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x)
@@ -1170,15 +1284,13 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
         tmem_ld32(lanes + UQ + j0, r);
 #pragma unroll
         for (int x = 0; x < 32; ++x)
-            r[x] = __float_as_uint(a.scale * tab[j0 + x].x * __uint_as_float(r[x]));
+            r[x] = __float_as_uint(-a.scale * tab[TNEG * C + j0 + x] * __uint_as_float(r[x]));
         tmem_st32_issue(lanes + UQ + j0, r);
         uint32_t w[32];
         tmem_ld32(lanes + UR + j0, w);
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
-            const float4 tj = tab[j0 + x];
-            w[x] = __float_as_uint(-tj.x * tj.y * __uint_as_float(w[x]));
-        }
+        for (int x = 0; x < 32; ++x)
+            w[x] = __float_as_uint(tab[TNGB * C + j0 + x] * __uint_as_float(w[x]));
         tmem_st32_issue(lanes + UR + j0, w);
         tmem_wait_st();
     }
@@ -1186,7 +1298,7 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    ok = warp_all(bwait(k_full, 0, abort_flag)) && ok;
+    ok = warp_all(wait_for(k_full, 0, abort_flag)) && ok;
     if (tid == 0 && ok) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
@@ -1219,9 +1331,9 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
                 end = fmaf(bf16hi(u[y]), bf16hi(w[y]), end);
             }
         }
-        end *= tab[C - 1].x;
+        end *= -tab[TNEG * C + C - 1];
     }
-    ok = warp_all(bwait(two_full, 0, abort_flag)) && ok;
+    ok = warp_all(wait_for(two_full, 0, abort_flag)) && ok;
     tc_fence_after();
     float *red = reinterpret_cast<float *>(sm + GD + 16384);    // [4][64], then 8 sums
     const int d = 32 * q + lane;
@@ -1239,13 +1351,12 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
             float oq[16], ok_[16], t[16];
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
-                const float4 tj = tab[jp + x];
                 const uint32_t at = image_pair(C, jp + x, d) + (d & 1) * 2;
                 const float qv = __uint_as_float(
                     (uint32_t)*reinterpret_cast<const uint16_t *>(sm + GQ + at) << 16);
                 const float kv = __uint_as_float(
                     (uint32_t)*reinterpret_cast<const uint16_t *>(sm + GK + at) << 16);
-                const float into = tj.z * tj.y * __uint_as_float(dw[x]);
+                const float into = tab[TKB * C + jp + x] * __uint_as_float(dw[x]);
                 const float row = __uint_as_float(dr[x]), col = __uint_as_float(dc[x]) + into;
                 oq[x] = __uint_as_float(dq[x]);
                 ok_[x] = row + col;
@@ -1342,7 +1453,7 @@ void put_saved(const DeltaArgs &a, uint8_t *p, bool keep, Scratch *sc)
 {
     const size_t t = tiles_of(a);
     sc->b = p;
-    sc->tab = reinterpret_cast<float4 *>(p + t * BTILE);
+    sc->tab = reinterpret_cast<float *>(p + t * BTILE);
     sc->s = keep ? p + prep_bytes(a) : nullptr;
     sc->e = keep ? sc->s + t * STILE : nullptr;
 }
