@@ -46,12 +46,33 @@ bool vec_rows(const NormRows &x, int e)
            x.s[2] % m == 0;
 }
 
+// Whether x's rows in order (batch, token, head) are a constant step apart, and the step.
+bool even_rows(const BlockNormArgs &a, NormRows &x)
+{
+    const int64_t n[3] = {a.B, a.T, a.H};
+    int64_t step = 0, rows = 1;
+    bool any = false;
+    for (int i = 2; i >= 0; --i) {
+        if (n[i] == 1)
+            continue;
+        if (!any)
+            step = x.s[i];
+        else if (x.s[i] != step * rows)
+            return false;
+        any = true;
+        rows *= n[i];
+    }
+    x.step = step;
+    return true;
+}
+
 }  // namespace
 
 size_t block_norm_partial_bytes(int D) { return (size_t)NORM_MOST_CTAS * 2 * D * sizeof(float); }
 
-cudaError_t block_norm_run(bool back, const BlockNormArgs &a, cudaStream_t s)
+cudaError_t block_norm_run(bool back, const BlockNormArgs &args, cudaStream_t s)
 {
+    BlockNormArgs a = args;
     int dev = 0, sms = 0, ctas = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess)
@@ -59,11 +80,14 @@ cudaError_t block_norm_run(bool back, const BlockNormArgs &a, cudaStream_t s)
     if (e != cudaSuccess)
         return e;
     const int esz = a.bf16 ? 2 : 4;
-    const NormRows *rows[] = {&a.x, &a.gate, &a.residual, &a.h, &a.y, &a.dh, &a.dy, &a.dx,
+    NormRows *rows[] = {&a.x, &a.gate, &a.residual, &a.h, &a.y, &a.dh, &a.dy, &a.dx,
                               &a.dgate, &a.dresidual};
     bool vec = a.D % 8 == 0;
-    for (const NormRows *r : rows)
+    a.flat = 1;
+    for (NormRows *r : rows) {
         vec = vec && vec_rows(*r, esz);
+        a.flat = even_rows(a, *r) && a.flat;
+    }
     for (const void *w : {a.post, a.pre})
         vec = vec && (reinterpret_cast<uintptr_t>(w) & 15) == 0;
     if (!back)

@@ -131,12 +131,16 @@ __device__ __forceinline__ void weights8(const void *w, int bf16, int c, int n, 
     }
 }
 
-// act(z) and its slope.  bf16: by the fast exponential and reciprocal (2^-21, far
-// below the rounding of the result).
+// act(z) and its slope.  bf16: by the approximate power of two and reciprocal (2^-21
+// together, far below the rounding of the result; an infinite power gives 0).
 template <typename T> __device__ __forceinline__ float sigmoid(float z)
 {
-    if (sizeof(T) == 2)
-        return __fdividef(1.f, 1.f + __expf(fminf(-z, 80.f)));
+    if (sizeof(T) == 2) {
+        float e, r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+        return r;
+    }
     return 1.f / (1.f + expf(-z));
 }
 template <typename T> __device__ __forceinline__ float act(float z, int kind)
@@ -194,17 +198,21 @@ __device__ __forceinline__ float2 row_sum(float2 x, float2 (*red)[PL::WARPS], in
 }
 
 struct RowPlace {
-    int64_t b, t, h;
+    unsigned b, t, h, row;
 };
+// Where every tensor's rows lie a constant step apart (a.flat) nothing is divided.
 __device__ __forceinline__ RowPlace row_place(const BlockNormArgs &a, unsigned row)
 {
-    const unsigned bt = a.H == 1 ? row : row / (unsigned)a.H;
-    const unsigned b = bt / (unsigned)a.T;
-    return {b, bt - b * (unsigned)a.T, row - bt * (unsigned)a.H};
+    if (a.flat)
+        return {0u, 0u, 0u, row};
+    const unsigned bt = row / (unsigned)a.H, b = bt / (unsigned)a.T;
+    return {b, bt - b * (unsigned)a.T, row - bt * (unsigned)a.H, 0u};
 }
-template <typename T> __device__ __forceinline__ T *at(const NormRows &x, const RowPlace &p)
+template <typename T>
+__device__ __forceinline__ T *at(const BlockNormArgs &a, const NormRows &x, const RowPlace &p)
 {
-    return static_cast<T *>(const_cast<void *>(x.p)) + p.b * x.s[0] + p.t * x.s[1] + p.h * x.s[2];
+    T *q = static_cast<T *>(const_cast<void *>(x.p));
+    return a.flat ? q + p.row * x.step : q + p.b * x.s[0] + p.t * x.s[1] + p.h * x.s[2];
 }
 
 template <typename T, typename PL, bool VEC>
@@ -214,6 +222,15 @@ __global__ void __launch_bounds__(PL::CTA) block_norm_fwd_kernel(const BlockNorm
     int turn = 0;
     const int group = threadIdx.x / PL::TPR, me = threadIdx.x % PL::TPR;
     const float inv_d = 1.f / (float)a.D;
+    float post[PL::NV][8], pre[PL::NV][8];      // this thread's channels, for all its rows
+#pragma unroll
+    for (int v = 0; v < PL::NV; ++v) {
+        const int c = (v * PL::TPR + me) * 8;
+        if (a.post)
+            weights8<VEC>(a.post, a.w_bf16, c, a.D - c, post[v]);
+        if (a.pre)
+            weights8<VEC>(a.pre, a.w_bf16, c, a.D - c, pre[v]);
+    }
     for (int64_t first = (int64_t)blockIdx.x * PL::GROUPS; first < a.rows;
          first += (int64_t)gridDim.x * PL::GROUPS) {
         const bool live = first + group < a.rows;
@@ -223,11 +240,11 @@ __global__ void __launch_bounds__(PL::CTA) block_norm_fwd_kernel(const BlockNorm
 #pragma unroll
         for (int v = 0; v < PL::NV; ++v) {
             const int c = (v * PL::TPR + me) * 8, n = live ? a.D - c : 0;
-            x[v] = load8<VEC>(at<const T>(a.x, p) + c, n);
+            x[v] = load8<VEC>(at<const T>(a, a.x, p) + c, n);
             if (a.gate.p)
-                g[v] = load8<VEC>(at<const T>(a.gate, p) + c, n);
+                g[v] = load8<VEC>(at<const T>(a, a.gate, p) + c, n);
             if (a.residual.p)
-                r[v] = load8<VEC>(at<const T>(a.residual, p) + c, n);
+                r[v] = load8<VEC>(at<const T>(a, a.residual, p) + c, n);
         }
         float rx = 1.f;
         if (a.post) {
@@ -243,14 +260,11 @@ __global__ void __launch_bounds__(PL::CTA) block_norm_fwd_kernel(const BlockNorm
 #pragma unroll
         for (int v = 0; v < PL::NV; ++v) {
             const int c = (v * PL::TPR + me) * 8, n = live ? a.D - c : 0;
-            float w[8];
-            if (a.post)
-                weights8<VEC>(a.post, a.w_bf16, c, n, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float m = x[v].get(i);
                 if (a.post)
-                    m *= rx * w[i];
+                    m *= rx * post[v][i];
                 if (a.gate.p)
                     m *= act<T>(g[v].get(i), a.activation);
                 m *= a.scale;
@@ -261,7 +275,7 @@ __global__ void __launch_bounds__(PL::CTA) block_norm_fwd_kernel(const BlockNorm
                 h[v][i] = m;
                 sh.x = fmaf(m, m, sh.x);
             }
-            store8<VEC>(at<T>(a.h, p) + c, h[v], n);
+            store8<VEC>(at<T>(a, a.h, p) + c, h[v], n);
         }
         if (!a.pre)
             continue;
@@ -269,12 +283,11 @@ __global__ void __launch_bounds__(PL::CTA) block_norm_fwd_kernel(const BlockNorm
 #pragma unroll
         for (int v = 0; v < PL::NV; ++v) {
             const int c = (v * PL::TPR + me) * 8, n = live ? a.D - c : 0;
-            float w[8];
-            weights8<VEC>(a.pre, a.w_bf16, c, n, w);
+            float y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                w[i] *= h[v][i] * rh;
-            store8<VEC>(at<T>(a.y, p) + c, w, n);
+                y[i] = h[v][i] * rh * pre[v][i];
+            store8<VEC>(at<T>(a, a.y, p) + c, y, n);
         }
     }
 }
@@ -295,14 +308,14 @@ __global__ void __launch_bounds__(PL::CTA) block_norm_bwd_kernel(const BlockNorm
 #pragma unroll
         for (int v = 0; v < PL::NV; ++v) {
             const int c = (v * PL::TPR + me) * 8, n = live ? a.D - c : 0;
-            x[v] = load8<VEC>(at<const T>(a.x, p) + c, n);
+            x[v] = load8<VEC>(at<const T>(a, a.x, p) + c, n);
             if (a.gate.p)
-                g[v] = load8<VEC>(at<const T>(a.gate, p) + c, n);
+                g[v] = load8<VEC>(at<const T>(a, a.gate, p) + c, n);
             if (a.residual.p && a.pre)
-                r[v] = load8<VEC>(at<const T>(a.residual, p) + c, n);
-            dh[v] = load8<VEC>(at<const T>(a.dh, p) + c, a.dh.p ? n : 0);
+                r[v] = load8<VEC>(at<const T>(a, a.residual, p) + c, n);
+            dh[v] = load8<VEC>(at<const T>(a, a.dh, p) + c, a.dh.p ? n : 0);
             if (a.pre)
-                dy[v] = load8<VEC>(at<const T>(a.dy, p) + c, n);
+                dy[v] = load8<VEC>(at<const T>(a, a.dy, p) + c, n);
         }
         float rx = 1.f;
         if (a.post) {
@@ -367,7 +380,7 @@ __global__ void __launch_bounds__(PL::CTA) block_norm_bwd_kernel(const BlockNorm
                 out[i] = d;
             }
             if (a.dresidual.p)
-                store8<VEC>(at<T>(a.dresidual, p) + c, out, n);
+                store8<VEC>(at<T>(a, a.dresidual, p) + c, out, n);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float d = out[i] * a.scale;
@@ -386,7 +399,7 @@ __global__ void __launch_bounds__(PL::CTA) block_norm_bwd_kernel(const BlockNorm
                 h[v][i] = d;
             }
             if (a.gate.p)
-                store8<VEC>(at<T>(a.dgate, p) + c, out, n);
+                store8<VEC>(at<T>(a, a.dgate, p) + c, out, n);
         }
         const float mx = a.post ? row_sum<PL>(s, red, turn).x * inv_d * rx * rx : 0.f;
 #pragma unroll
@@ -396,7 +409,7 @@ __global__ void __launch_bounds__(PL::CTA) block_norm_bwd_kernel(const BlockNorm
             for (int i = 0; i < 8; ++i)
                 if (a.post)
                     h[v][i] = rx * (h[v][i] - x[v].get(i) * mx);
-            store8<VEC>(at<T>(a.dx, p) + c, h[v], n);
+            store8<VEC>(at<T>(a, a.dx, p) + c, h[v], n);
         }
     }
     // this CTA's part of the weights' gradients, [2][D]

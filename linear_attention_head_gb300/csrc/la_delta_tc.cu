@@ -167,6 +167,16 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+__device__ __forceinline__ void bulk_prefetch(const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+                 "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes"
@@ -201,53 +211,44 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The join of blocks of W rows: `first` is the pair's first row; M holds the second
-// blocks' rows alone.  Threads of the pair: t of n.
-template <int W>
-__device__ __forceinline__ void join_first(const float (*A)[AP], const float *beta, float (*M)[AP],
-                                           int first, int t, int n)
+// acc[r][.] -= sum over W rows k of left[r][k] right[k][.], r < R rows one after
+// another: 4 k a step, so that left and right are read 16 bytes at a time.
+template <int R, int W>
+__device__ __forceinline__ void minus_product(float4 (&acc)[R], const float *left, const float *right)
 {
-    for (int x = t; x < W * W / 4; x += n) {
-        const int i = first + W + x / (W / 4), j = first + 4 * (x % (W / 4));
-        float4 m = *reinterpret_cast<const float4 *>(&A[i][j]);
-#pragma unroll 4
-        for (int k = j + 1 - first; k < W; ++k) {       // B11 is strictly lower
-            const float f = A[i][first + k] * beta[first + k];
-            const float4 b = *reinterpret_cast<const float4 *>(&A[first + k][j]);
-            m.x = fmaf(-f, b.x, m.x);
-            m.y = fmaf(-f, b.y, m.y);
-            m.z = fmaf(-f, b.z, m.z);
-            m.w = fmaf(-f, b.w, m.w);
+#pragma unroll 2
+    for (int k4 = 0; k4 < W; k4 += 4) {
+        float4 l[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            l[r] = *reinterpret_cast<const float4 *>(left + r * AP + k4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 x = *reinterpret_cast<const float4 *>(right + (k4 + k) * AP);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float f = k == 0 ? l[r].x : k == 1 ? l[r].y : k == 2 ? l[r].z : l[r].w;
+                acc[r].x = fmaf(-f, x.x, acc[r].x);
+                acc[r].y = fmaf(-f, x.y, acc[r].y);
+                acc[r].z = fmaf(-f, x.z, acc[r].z);
+                acc[r].w = fmaf(-f, x.w, acc[r].w);
+            }
         }
-        *reinterpret_cast<float4 *>(&M[i - W - first / 2][j]) = m;
     }
 }
-template <int W>
-__device__ __forceinline__ void join_second(float (*A)[AP], const float *beta,
-                                            const float (*M)[AP], int first, int t, int n)
+__device__ __forceinline__ float4 times(float f, float4 x)
 {
-    for (int x = t; x < W * W / 4; x += n) {
-        const int ii = x / (W / 4), i = first + W + ii, j = first + 4 * (x % (W / 4));
-        float4 m = *reinterpret_cast<const float4 *>(&M[first / 2 + ii][j]);
-#pragma unroll 4
-        for (int k = 0; k < ii; ++k) {                  // B22 is strictly lower
-            const float f = A[i][first + W + k] * beta[first + W + k];
-            const float4 b = *reinterpret_cast<const float4 *>(&M[first / 2 + k][j]);
-            m.x = fmaf(-f, b.x, m.x);
-            m.y = fmaf(-f, b.y, m.y);
-            m.z = fmaf(-f, b.z, m.z);
-            m.w = fmaf(-f, b.w, m.w);
-        }
-        *reinterpret_cast<float4 *>(&A[i][j]) = m;
-    }
+    return make_float4(f * x.x, f * x.y, f * x.z, f * x.w);
 }
 
 __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, const Scratch sc)
 {
     __shared__ __align__(16) __nv_bfloat16 ks[C][KP];
     __shared__ __align__(16) float A[C][AP];
-    float (*M)[AP] = reinterpret_cast<float (*)[AP]>(ks);   // once K K^T is done
-    static_assert(sizeof(float) * C / 2 * AP <= sizeof(ks), "M lies over K");
+    // once K K^T is done: rows of beta B of the first blocks, and of beta M of the
+    // second ones (M = A21 (I - beta B11)), the right factors of the joins
+    float (*Z)[AP] = reinterpret_cast<float (*)[AP]>(ks), (*M)[AP] = Z + C / 2;
+    static_assert(sizeof(float) * C * AP <= sizeof(ks), "Z and M lie over K");
     __shared__ float G[C], beta[C], part[2];
     const int h = blockIdx.x % a.H;
     const int64_t slot = blockIdx.x / a.H;
@@ -328,41 +329,78 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
         }
 #pragma unroll
         for (int nb = 0; nb < 8; ++nb)
-            if (nb < 2 * (warp + 1))
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int i = 16 * warp + (lane >> 2) + 8 * (v >> 1);
-                    const int j = 8 * nb + 2 * (lane & 3) + (v & 1);
-                    A[i][j] = j < i ? expf(G[i] - G[j]) * acc[nb][v] : 0.f;
-                }
+            for (int v = 0; v < 4; v += 2) {
+                const int i = 16 * warp + (lane >> 2) + 4 * v, j = 8 * nb + 2 * (lane & 3);
+                float2 x = make_float2(0.f, 0.f);
+                if (j < i)
+                    x.x = expf(G[i] - G[j]) * acc[nb][v];
+                if (j + 1 < i)
+                    x.y = expf(G[i] - G[j + 1]) * acc[nb][v + 1];
+                *reinterpret_cast<float2 *>(&A[i][j]) = x;
+            }
     }
     __syncthreads();
-    // diagonal blocks: column lane of block warp
+    // diagonal blocks of 16: column lane of block warp; block 0's upper right in Z is
+    // zero, as it is in A
     {
         const int b0 = 16 * warp, c = lane & 15;
-        float x[16];
+        float z[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float s = A[b0 + i][b0 + c];
+            float x = A[b0 + i][b0 + c];
 #pragma unroll
-            for (int m = 0; m < i; ++m)
-                s = fmaf(-A[b0 + i][b0 + m] * beta[b0 + m], x[m], s);
-            x[i] = s;
+            for (int m4 = 0; m4 < i; m4 += 4) {
+                const float4 l = *reinterpret_cast<const float4 *>(&A[b0 + i][b0 + m4]);
+                x = fmaf(-l.x, z[m4], x);
+                if (m4 + 1 < i)
+                    x = fmaf(-l.y, z[m4 + 1], x);
+                if (m4 + 2 < i)
+                    x = fmaf(-l.z, z[m4 + 2], x);
+                if (m4 + 3 < i)
+                    x = fmaf(-l.w, z[m4 + 3], x);
+            }
+            z[i] = beta[b0 + i] * x;
+            __syncwarp();
+            if (lane < 16)      // row i of the block is not read again in this loop
+                A[b0 + i][b0 + c] = x;
         }
-        __syncwarp();
-        if (lane < 16)
+        if (warp < 3) {         // blocks 0 and 2 are first ones; 1 is part of one later
+            const int z0 = warp == 2 ? 16 : b0;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                A[b0 + i][b0 + c] = x[i];
+                if (lane < 16)
+                    Z[z0 + i][b0 + c] = z[i];
+                else if (warp == 0)
+                    Z[i][16 + c] = 0.f;
+        }
     }
     __syncthreads();
-    join_first<16>(A, beta, M, 32 * (tid >> 6), tid & 63, 64);
+    {   // 16 -> 32: 64 threads a pair of blocks, a row's four columns each
+        const int p = tid >> 6, t = tid & 63, first = 32 * p;
+        const int r = t >> 2, i = first + 16 + r, j = first + 4 * (t & 3);
+        float4 x[1] = {*reinterpret_cast<const float4 *>(&A[i][j])};
+        minus_product<1, 16>(x, &A[i][first], &Z[16 * p][j]);
+        *reinterpret_cast<float4 *>(&M[16 * p + r][j]) = times(beta[i], x[0]);
+        __syncthreads();
+        minus_product<1, 16>(x, &A[i][first + 16], &M[16 * p][j]);
+        *reinterpret_cast<float4 *>(&A[i][j]) = x[0];
+        if (p == 0)
+            *reinterpret_cast<float4 *>(&Z[16 + r][j]) = times(beta[i], x[0]);
+    }
     __syncthreads();
-    join_second<16>(A, beta, M, 32 * (tid >> 6), tid & 63, 64);
-    __syncthreads();
-    join_first<32>(A, beta, M, 0, tid, PREP);
-    __syncthreads();
-    join_second<32>(A, beta, M, 0, tid, PREP);
+    {   // 32 -> 64: two rows' four columns each
+        const int r = 2 * (tid >> 3), i = 32 + r, j = 4 * (tid & 7);
+        float4 x[2] = {*reinterpret_cast<const float4 *>(&A[i][j]),
+                       *reinterpret_cast<const float4 *>(&A[i + 1][j])};
+        minus_product<2, 32>(x, &A[i][0], &Z[0][j]);
+        *reinterpret_cast<float4 *>(&M[r][j]) = times(beta[i], x[0]);
+        *reinterpret_cast<float4 *>(&M[r + 1][j]) = times(beta[i + 1], x[1]);
+        __syncthreads();
+        minus_product<2, 32>(x, &A[i][32], &M[0][j]);
+        *reinterpret_cast<float4 *>(&A[i][j]) = x[0];
+        *reinterpret_cast<float4 *>(&A[i + 1][j]) = x[1];
+    }
     __syncthreads();
     // hi and lo as 128B-swizzled rows, the shared-memory image that the sweeps load
     {
@@ -387,33 +425,36 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
 
 // ---- the sweeps -----------------------------------------------------------------
 //
-// 448 threads: warp 0 loads, warp 1 issues the products, warps 2-9 ("chain") carry
+// 576 threads: warp 0 loads, warp 1 issues the products, warps 2-9 ("chain") carry
 // X, Eps (or W, R) and the state between products, each a quarter of the lanes and
-// half of the columns, warps 10-13 ("side") make P and O (or P and scale e^G Q).
+// half of the columns, warps 10-17 ("side") make P and O (or P and scale e^G Q).
 // Q and K of a chunk lie as one 128-row tile: [Q; K] K^T gives the scores in lanes
 // 0-63 (lanes 64-127, K K^T, are not used).
 
-constexpr int SWEEP = 448;
-constexpr int CHAIN = 256, SIDE = 128;
-constexpr int NS = 2;                           // stages
+constexpr int SWEEP = 576;
+constexpr int CHAIN = 256, SIDE = 256;
+constexpr int NS = 2, NT = 4;                   // stages; of the tables
 constexpr int QK = 0, VD = 32768, BB = 49152, STAGE = 65536;
 constexpr int POFF = NS * STAGE;                // P hi, lo: [64][64] bf16 each
 constexpr int QOFF = POFF + 16384;              // backward: scale e^G Q, hi, lo
 constexpr int Q2 = 16384;                       // bytes of one of them: [2][64][64] bf16
 template <bool BWD> struct SweepLayout {
-    static constexpr int TOFF = QOFF + (BWD ? 2 * Q2 : 0);
-    static constexpr int MOFF = TOFF + NS * TAB;
-    static constexpr int NBAR = 4 * NS + 12;
+    static constexpr int SOFF = QOFF + (BWD ? 2 * Q2 : 0);     // the state's image on its way out
+    static constexpr int TOFF = SOFF + STILE;
+    static constexpr int MOFF = TOFF + NT * TAB;
+    static constexpr int NBAR = 4 * NS + 2 * NT + 16;
     static constexpr int SLOT = MOFF + NBAR * 8;
     static constexpr int ABORT = SLOT + 4;
     static constexpr int RANK = ABORT + 4;
     static constexpr int DYN = RANK + 4 + 1024;
     static_assert(DYN <= 232448, "shared memory per CTA");
 };
-// TMEM columns: the state fp32, its hi and lo; O's inter term (back: P^T dO) and the
-// chain's accumulator, next to each other as Q and K are in their tile; scores, then
-// O's intra term; the chain's operand (beta X, then kappa beta Eps), hi and lo
-constexpr uint32_t TS = 0, TSH = 128, T2 = 256, T1 = 320, TR = 384, TY = 448, TCOLS = 512;
+// TMEM columns: the state fp32, its hi and lo; forward: O's inter term, the chain's
+// accumulator, scores and then O's intra term; back: scores and then P^T dO, the
+// chain's accumulator, dO^T of two chunks; the chain's operand (beta X, then kappa
+// beta Eps), hi and lo
+constexpr uint32_t TS = 0, TSH = 128, T2 = 256, T1 = 320, TR = 384, TD = 384, TY = 448,
+                   TCOLS = 512;
 // an operand of 64 tokens in 64 columns: for each half of the tokens 16 columns of
 // hi, 16 of lo, so that the threads of a half write among columns of their own
 __device__ __forceinline__ uint32_t tok_col(int kk, int lo)
@@ -458,13 +499,19 @@ __device__ __forceinline__ void store_image(const float (&x)[32], int half, int 
         *reinterpret_cast<uint32_t *>(at + m * 256 + ((c16 ^ ((2 * m + odd) & 7)) << 4)) = pair;
     }
 }
-// place of the pair of channels of e in row j of a [2][rows][64] swizzled tile
-__device__ __forceinline__ uint32_t image_pair(int rows, int j, int e)
+// Channel e of tokens 32 half .. of a [2][64 tokens][64 channels] swizzled tile,
+// pairs of tokens packed.
+__device__ __forceinline__ void channel(const uint8_t *tile, int e, int half, uint32_t (&v)[16])
 {
-    return (uint32_t)((e >> 6) * rows * 128 + j * 128 + ((((e & 63) >> 3) ^ (j & 7)) << 4) +
-                      (e & 6) * 2);
+    const uint8_t *at = tile + (e >> 6) * 8192 + 32 * half * 128 + (e & 7) * 2;
+    const int c16 = (e & 63) >> 3;
+#pragma unroll
+    for (int x = 0; x < 32; ++x) {
+        const uint32_t b =
+            *reinterpret_cast<const uint16_t *>(at + x * 128 + ((c16 ^ (x & 7)) << 4));
+        v[x / 2] = x & 1 ? v[x / 2] | b << 16 : b;
+    }
 }
-
 template <bool BWD>
 __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_constant__ SweepParams P)
 {
@@ -473,21 +520,26 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
     const DeltaArgs &a = P.a;
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::MOFF);    // Q, K, table
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::MOFF);    // Q, K
     uint64_t *fullv = full + NS, *fullb = full + 2 * NS, *empty = full + 3 * NS;
-    uint64_t *bars = full + 4 * NS;
-    uint64_t *sc_full = bars;           // scores
+    uint64_t *tfull = full + 4 * NS, *tempty = tfull + NT;          // tables
+    uint64_t *bars = tempty + NT;
+    uint64_t *sc_full = bars;           // scores (and Q S)
     uint64_t *ks_full = bars + 1;       // K S (back: K K', and P^T dO)
     uint64_t *e_full = bars + 2;        // Eps (R)
     uint64_t *s_full = bars + 3;        // the state
     uint64_t *o_full = bars + 4;        // O
     uint64_t *s_ready = bars + 5;       // the state's hi, lo and its decayed fp32
     uint64_t *y_ready = bars + 6;       // X and beta X
-    uint64_t *w_ready = bars + 7;       // what the state takes, and beta Eps
+    uint64_t *w_ready = bars + 7;       // what the state takes
     uint64_t *p_ready = bars + 8;       // P
     uint64_t *q_ready = bars + 9;       // Q S read out of TMEM; back: scale e^G Q
     uint64_t *r_ready = bars + 10;      // O's intra term read
-    uint64_t *drain = bars + 11;
+    uint64_t *d_ready = bars + 11;      // beta Eps
+    uint64_t *i_ready = bars + 12;      // the state's and Eps's (R's) images
+    uint64_t *i_free = bars + 13;       // they have been read
+    uint64_t *td_ready = bars + 14;     // back: dO^T in TMEM
+    uint64_t *drain = bars + 15;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::SLOT);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::ABORT);
     volatile int *rank_slot = reinterpret_cast<volatile int *>(sm + L::RANK);
@@ -498,15 +550,23 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             mbar_init(&full[i], 1);
             mbar_init(&fullv[i], 1);
             mbar_init(&fullb[i], 1);
-            mbar_init(&empty[i], 1 + CHAIN / 32 + SIDE / 32);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < NT; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], CHAIN / 32 + SIDE / 32);
         }
         for (int i = 0; i < 5; ++i)
             mbar_init(&bars[i], 1);
         mbar_init(s_ready, CHAIN / 32);
         mbar_init(y_ready, CHAIN / 32);
         mbar_init(w_ready, CHAIN / 32);
-        mbar_init(p_ready, 2);
-        mbar_init(q_ready, BWD ? 2 : SIDE / 32);
+        mbar_init(p_ready, SIDE / 64);
+        mbar_init(q_ready, BWD ? SIDE / 64 : SIDE / 32);
+        mbar_init(d_ready, CHAIN / 32);
+        mbar_init(i_ready, CHAIN / 32);
+        mbar_init(i_free, 1);
+        mbar_init(td_ready, SIDE / 32);
         mbar_init(r_ready, SIDE / 32);
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -555,30 +615,68 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         // ------------------------------------------------------------- loads
         if (lane == 0) {
             const int hq = h / a.q.hdiv;
+            uint8_t *simg = BWD ? P.sc.k : P.sc.s, *eimg = BWD ? P.sc.r : P.sc.e;
+            // The images that delta_grads starts from leave through shared memory: as
+            // stores of the chain's threads, a row each, they would take the chain's
+            // own way to shared memory (0.19 ms of 0.66 at b4 h32 n8192).  Eps (R) lies
+            // where V (dO) was, read by then.
+            auto images = [&](int c) {
+                if (!wait_for(i_ready, c & 1, abort_flag))
+                    return false;
+                bulk_store(simg + tile_of(c) * STILE, sm + L::SOFF, STILE);
+                bulk_store(eimg + tile_of(c) * ETILE, sm + (c % NS) * STAGE + VD, ETILE);
+                bulk_commit_group();
+                bulk_wait_read_all();
+                mbar_arrive(i_free);
+                return true;
+            };
             int issued = 0;
+            bool going = true;
             for (int c = 0; c < nc; ++c) {
                 const int s = c % NS;
-                if (c >= NS && !wait_for(&empty[s], (c / NS - 1) & 1, abort_flag))
+                if (c >= NS) {
+                    going = !simg || images(c - NS);
+                    if (!going || !(going = wait_for(&empty[s], (c / NS - 1) & 1, abort_flag)))
+                        break;
+                }
+                const int ts = c % NT;
+                if (c >= NT && !(going = wait_for(&tempty[ts], (c / NT - 1) & 1, abort_flag)))
                     break;
                 const int t = (int)(sq.bos + (int64_t)chunk(c) * C);
                 uint8_t *st = sm + s * STAGE;
-                mbar_arrive_expect_tx(&full[s], 32768 + TAB);
+                mbar_arrive_expect_tx(&tfull[ts], TAB);
+                bulk_load(sm + L::TOFF + ts * TAB, P.sc.tab + tile_of(c) * TABS * C, TAB,
+                          &tfull[ts]);
+                mbar_arrive_expect_tx(&full[s], 32768);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     tma_load_4d(st + QK + b * 16384, &P.mq, &full[s], 64 * b, hq, t, (int)sq.row);
                     tma_load_4d(st + QK + b * 16384 + 8192, &P.mk, &full[s], 64 * b, hq, t,
                                 (int)sq.row);
                 }
-                bulk_load(sm + L::TOFF + s * TAB, P.sc.tab + tile_of(c) * TABS * C, TAB, &full[s]);
                 mbar_arrive_expect_tx(&fullv[s], 16384);
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
                     tma_load_4d(st + VD + b * 8192, &P.mv, &fullv[s], 64 * b, h, t, (int)sq.row);
                 mbar_arrive_expect_tx(&fullb[s], BTILE);
                 bulk_load(st + BB, P.sc.b + tile_of(c) * BTILE, BTILE, &fullb[s]);
+                if (c + 1 < nc) {   // the next stage is free a chunk later: into L2 by then
+                    const int t1 = (int)(sq.bos + (int64_t)chunk(c + 1) * C);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        tma_prefetch_l2_4d(&P.mq, 64 * b, hq, t1, (int)sq.row);
+                        tma_prefetch_l2_4d(&P.mk, 64 * b, hq, t1, (int)sq.row);
+                        tma_prefetch_l2_4d(&P.mv, 64 * b, h, t1, (int)sq.row);
+                    }
+                    bulk_prefetch(P.sc.b + tile_of(c + 1) * BTILE, BTILE);
+                }
                 ++issued;
             }
+            if (simg)
+                for (int c = nc > NS ? nc - NS : 0; going && c < nc; ++c)
+                    going = images(c);
             for (int c = issued > NS ? issued - NS : 0; c < issued; ++c) {
+                drain_wait(&tfull[c % NT], (c / NT) & 1);
                 drain_wait(&full[c % NS], (c / NS) & 1);
                 drain_wait(&fullv[c % NS], (c / NS) & 1);
                 drain_wait(&fullb[c % NS], (c / NS) & 1);
@@ -589,18 +687,14 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         // ---------------------------------------------------------- products
         const uint32_t sb = smem_u32(sm);
         constexpr uint32_t id64 = idesc_bf16_f32(128, 64, 0, 0);       // B K-major
-        constexpr uint32_t id128 = idesc_bf16_f32(128, 128, 0, 0);
         constexpr uint32_t id64mn = idesc_bf16_f32(128, 64, 0, 1);     // B MN-major
         constexpr uint32_t id128mn = idesc_bf16_f32(128, 128, 0, 1);
-        constexpr uint32_t id64mm = idesc_bf16_f32(128, 64, 1, 1);     // both MN-major
-        constexpr uint32_t id128mm = idesc_bf16_f32(128, 128, 1, 1);
         // Descriptors of stage 0 once; another place is an addition to the address
         // field (16-byte units): what one product costs to issue counts here.
         const uint64_t d_rows = sdesc_sw128(sb + QK, 16, 1024);        // [Q; K] by rows
         const uint64_t d_cols = sdesc_sw128(sb + QK, 16384, 1024);     // D along M or N
         const uint64_t d_b = sdesc_sw128(sb + BB, 16, 1024);
         const uint64_t d_bmn = sdesc_sw128(sb + BB, 8192, 1024);
-        const uint64_t d_do = sdesc_sw128(sb + VD, 8192, 1024);
         const uint64_t d_p = sdesc_sw128(sb + POFF, 16, 1024);
         const uint64_t d_pmn = sdesc_sw128(sb + POFF, 8192, 1024);
         const uint64_t d_q2 = sdesc_sw128(sb + QOFF, 8192, 1024);
@@ -612,22 +706,17 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             const uint64_t d = d_rows + stage(c);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-                mma_ss(tm + TR, d + kd(kk), d + off(8192) + kd(kk), id64, kk > 0);
+                mma_ss(tm + (BWD ? T2 : TR), d + kd(kk), d + off(8192) + kd(kk), id64, kk > 0);
             mma_commit(sc_full);
         };
-        // S^T [Q; K]^T (back: K'^T K^T)
-        auto state_times = [&](int c) {
-            const uint64_t d = d_rows + stage(c);
+        // the state's rows times those of the [Q; K] tile from `row` on
+        auto state_times = [&](uint32_t to, int c, int row) {
+            const uint64_t d = d_rows + stage(c) + off(row * 128);
 #pragma unroll
             for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    if (BWD)
-                        mma_ts(tm + T1, tm + TSH + 64 * lo + 8 * kk, d + off(8192) + kd(kk), id64,
-                               lo + kk > 0);
-                    else
-                        mma_ts(tm + T2, tm + TSH + 64 * lo + 8 * kk, d + kd(kk), id128,
-                               lo + kk > 0);
+                    mma_ts(tm + to, tm + TSH + 64 * lo + 8 * kk, d + kd(kk), id64, lo + kk > 0);
         };
         // T1 += (beta X)^T B^T (back: B): hi hi, lo hi, hi lo
         auto solve = [&](int c) {
@@ -689,19 +778,18 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             if (one)
                 scores(0);
             __syncwarp();
-            auto prior = [&](int c) {   // P^T dO
-                if (!both(p_ready, c) ||
-                    !warp_all(wait_for(&fullv[c % NS], (c / NS) & 1, abort_flag)))
+            // dO^T goes in from TMEM: as an A operand in shared memory it would lie
+            // MN-major, and such a product took 200 cycles for 34
+            auto prior = [&](int c) {   // dO^T P
+                if (!both(p_ready, c) || !both(td_ready, c))
                     return false;
-                if (one) {
-                    const uint64_t d = d_do + stage(c);
+                if (one)
 #pragma unroll
                     for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_ss(tm + T2, d + off(kk * 2048), d_pmn + off(lo * 8192 + kk * 2048),
-                                   id64mm, lo + kk > 0);
-                }
+                            mma_ts(tm + T2, tm + TD + 32 * (c & 1) + 8 * kk,
+                                   d_pmn + off(lo * 8192 + kk * 2048), id64mn, lo + kk > 0);
                 __syncwarp();
                 return true;
             };
@@ -710,7 +798,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 if (!(ok = both(s_ready, c)))
                     break;
                 if (one) {
-                    state_times(c);
+                    state_times(T1, c, 64);
                     mma_commit(ks_full);
                 }
                 __syncwarp();
@@ -718,29 +806,27 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 // warps work
                 if (!(ok = both(q_ready, c)))
                     break;
-                if (one) {  // K'^T += dO^T (scale e^G Q)
-                    const uint64_t d = d_do + stage(c);
+                if (one)    // K'^T += dO^T (scale e^G Q)
 #pragma unroll
                     for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_ss(tm + TS, d + off(kk * 2048), d_q2 + off(lo * Q2 + kk * 2048),
-                                   id128mm, 1);
-                }
+                            mma_ts(tm + TS, tm + TD + 32 * (c & 1) + 8 * kk,
+                                   d_q2 + off(lo * Q2 + kk * 2048), id128mn, 1);
                 __syncwarp();
-                if (c + 1 < nc) {
-                    if (!(ok = stage_in(c + 1)))
-                        break;
-                    if (one)
-                        scores(c + 1);
-                    __syncwarp();
-                }
                 if (!(ok = warp_all(wait_for(&fullb[c % NS], (c / NS) & 1, abort_flag)) &&
                            both(y_ready, c)))
                     break;
                 if (one)
                     solve(c);
                 __syncwarp();
+                if (c + 1 < nc) {   // over dO^T P, which W has taken
+                    if (!(ok = stage_in(c + 1)))
+                        break;
+                    if (one)
+                        scores(c + 1);
+                    __syncwarp();
+                }
                 if (!(ok = both(w_ready, c)))
                     break;
                 if (one) {
@@ -753,20 +839,23 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             }
         } else if (!BWD) {
             for (int c = 0; c < nc; ++c) {
-                if (!stage_in(c) || (c > 0 && !both(q_ready, c - 1)) || !both(s_ready, c))
+                if (!stage_in(c) || !both(s_ready, c))
                     break;
                 any = true;
                 if (one) {
-                    state_times(c);
+                    state_times(T1, c, 64);
                     mma_commit(ks_full);
                 }
                 __syncwarp();
                 // what the chain does not wait for goes between its products, while its
-                // warps work: the scores while X is made, O's intra term while S is
-                if (c > 0 && !both(r_ready, c - 1))
+                // warps work: Q S and the scores while X is made, O's intra term while
+                // S is
+                if (c > 0 && (!both(q_ready, c - 1) || !both(r_ready, c - 1)))
                     break;
-                if (one)
+                if (one) {
+                    state_times(T2, c, 0);
                     scores(c);
+                }
                 __syncwarp();
                 if (!warp_all(wait_for(&fullb[c % NS], (c / NS) & 1, abort_flag)) ||
                     !both(y_ready, c))
@@ -776,10 +865,12 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 __syncwarp();
                 if (!both(w_ready, c))
                     break;
-                if (one)
+                if (one) {
                     update(c);
+                    mma_commit(&empty[c % NS]);
+                }
                 __syncwarp();
-                if (!both(p_ready, c))
+                if (!both(p_ready, c) || !both(d_ready, c))
                     break;
                 if (one) {  // (beta Eps)^T P^T; beta Eps lies in T1, as tok_col
 #pragma unroll
@@ -789,7 +880,6 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                             mma_ts(tm + TR, tm + T1 + tok_col(kk, x == 1),
                                    d_p + off((x == 2 ? 8192 : 0) + kk * 32), id64, x + kk > 0);
                     mma_commit(o_full);
-                    mma_commit(&empty[c % NS]);
                 }
                 __syncwarp();
             }
@@ -807,14 +897,13 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         const int64_t sbase = ((int64_t)sq.n * a.H + h) * a.D * a.E;
         const float *in = BWD ? a.dfin : a.init;
         float *out = BWD ? a.dinit : a.fin;
-        uint8_t *simg = BWD ? P.sc.k : P.sc.s, *eimg = BWD ? P.sc.r : P.sc.e;
+        const bool keep = BWD || P.sc.s;
         bool ok = true;
         for (int c = 0; ok && c < nc; ++c) {
             const int s = c % NS, n = tokens(c);
             const uint8_t *st = sm + s * STAGE;
-            const float *tab = tabs + s * TABS * C;
-            const int64_t tile = tile_of(c);
-            if (!(ok = warp_all(wait_for(&full[s], (c / NS) & 1, abort_flag))))
+            const float *tab = tabs + (c % NT) * TABS * C;
+            if (!(ok = warp_all(wait_for(&tfull[c % NT], (c / NT) & 1, abort_flag))))
                 break;
             // ---- the state
             if (c > 0 && !(ok = warp_all(wait_for(s_full, (c - 1) & 1, abort_flag))))
@@ -849,8 +938,10 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(s_ready);
-            if (simg) {
-                uint8_t *to = simg + tile * STILE + half * 16384 + e * 128;
+            if (keep) {
+                if (c > 0 && !(ok = warp_all(wait_for(i_free, (c - 1) & 1, abort_flag))))
+                    break;
+                uint8_t *to = sm + L::SOFF + half * 16384 + e * 128;
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
                     *reinterpret_cast<uint4 *>(to + ((x ^ (e & 7)) << 4)) =
@@ -867,14 +958,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             if constexpr (!BWD) {
                 if (!(ok = warp_all(wait_for(&fullv[s], (c / NS) & 1, abort_flag))))
                     break;
-                const uint8_t *vr = st + VD + (e >> 6) * 8192 + j0 * 128 + (e & 7) * 2;
-                const int c16 = (e & 63) >> 3;
-#pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    const uint32_t b = *reinterpret_cast<const uint16_t *>(
-                        vr + x * 128 + ((c16 ^ (x & 7)) << 4));
-                    v[x / 2] = x & 1 ? v[x / 2] | b << 16 : b;
-                }
+                channel(st + VD, e, half, v);
             }
             if (!(ok = warp_all(wait_for(ks_full, c & 1, abort_flag))))
                 break;
@@ -921,30 +1005,39 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 split2(mul2(pair_at(BWD ? TNGB : TKB, x), pair_of(r, x)), hi[x], lo[x]);
             tmem_st16_issue(lanes + TY + 32 * half, hi);
             tmem_st16_issue(lanes + TY + 32 * half + 16, lo);
-            if constexpr (!BWD) {
-                // beta Eps over this half's own columns of T1
-#pragma unroll
-                for (int x = 0; x < 16; ++x)
-                    split2(mul2(pair_at(TBETA, x), pair_of(r, x)), hi[x], lo[x]);
-                tmem_st16_issue(lanes + T1 + 32 * half, hi);
-                tmem_st16_issue(lanes + T1 + 32 * half + 16, lo);
-            }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(w_ready);
-            // ---- off the chain: what delta_grads starts from
-            if (eimg) {
+            // ---- off the chain: beta Eps over this half's own columns of T1, for O
+            if constexpr (!BWD) {
+#pragma unroll
+                for (int x = 0; x < 16; ++x)
+                    split2(mul2(pair_at(TBETA, x), pair_of(r, x)), hi[x], lo[x]);
+                tmem_st16_issue(lanes + T1 + 32 * half, hi);
+                tmem_st16_issue(lanes + T1 + 32 * half + 16, lo);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(d_ready);
+            }
+            // what delta_grads starts from
+            if (keep) {
                 float x32[32];
 #pragma unroll
                 for (int x = 0; x < 32; ++x)
                     x32[x] = __uint_as_float(r[x]);
-                store_image(x32, half, e, eimg + tile * ETILE);
+                store_image(x32, half, e, sm + s * STAGE + VD);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(i_ready);
             }
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&empty[s]);
+                mbar_arrive(&tempty[c % NT]);
         }
         if (ok && nc > 0)
             ok = warp_all(wait_for(s_full, (nc - 1) & 1, abort_flag));
@@ -965,66 +1058,66 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             }
     } else {
         // -------------------------------------------------------------- side
-        const int q = warp & 3;
+        const int q = warp & 3, half = (warp - 10) >> 2;
         const int row = 32 * q + lane;
         const uint32_t lanes = tm + ((uint32_t)(32 * q) << 16);
+        const int j0 = 32 * half;
         for (int c = 0; c < nc; ++c) {
             const int s = c % NS, n = tokens(c);
-            const float *tab = tabs + s * TABS * C;
-            if (!warp_all(wait_for(&full[s], (c / NS) & 1, abort_flag)) ||
+            const float *tab = tabs + (c % NT) * TABS * C;
+            if (!warp_all(wait_for(&tfull[c % NT], (c / NT) & 1, abort_flag)) ||
                 !warp_all(wait_for(sc_full, c & 1, abort_flag)))
                 break;
             tc_fence_after();
-            if (q < 2) {    // row i of P; columns past the warp's rows are zero
+            if (q < 2) {    // row i of P, this half's columns; those past the warp's rows are zero
                 const int i = row;
-                const float gi = tab[TLOG * C + i];
-                const float2 gi2 = make_float2(gi, gi), s2 = make_float2(a.scale, a.scale);
-                const float2 minus = make_float2(-1.f, -1.f);
                 uint8_t *to = sm + POFF + i * 128;
+                uint32_t hi[16] = {}, lo[16] = {};
+                if (half <= q) {
+                    const float gi = tab[TLOG * C + i];
+                    const float2 gi2 = make_float2(gi, gi), s2 = make_float2(a.scale, a.scale);
+                    const float2 minus = make_float2(-1.f, -1.f);
+                    uint32_t r[32];
+                    tmem_ld32(lanes + (BWD ? T2 : TR) + j0, r);
+                    const float *gj = tab + TLOG * C + j0;
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    uint32_t hi[16] = {}, lo[16] = {};
-                    if (p <= q) {
-                        uint32_t r[32];
-                        tmem_ld32(lanes + TR + 32 * p, r);
-                        const float *gj = tab + TLOG * C + 32 * p;
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) {
-                            const float2 d = fma2(
-                                *reinterpret_cast<const float2 *>(gj + 2 * x), minus, gi2);
-                            float2 y = mul2(mul2(make_float2(exp2_fast(d.x), exp2_fast(d.y)), s2),
-                                            pair_of(r, x));
-                            if (p == q) {
-                                y.x = 2 * x <= lane ? y.x : 0.f;
-                                y.y = 2 * x + 1 <= lane ? y.y : 0.f;
-                            }
-                            split2(y, hi[x], lo[x]);
+                    for (int x = 0; x < 16; ++x) {
+                        const float2 d =
+                            fma2(*reinterpret_cast<const float2 *>(gj + 2 * x), minus, gi2);
+                        float2 y = mul2(mul2(make_float2(exp2_fast(d.x), exp2_fast(d.y)), s2),
+                                        pair_of(r, x));
+                        if (half == q) {
+                            y.x = 2 * x <= lane ? y.x : 0.f;
+                            y.y = 2 * x + 1 <= lane ? y.y : 0.f;
                         }
+                        split2(y, hi[x], lo[x]);
                     }
+                }
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        uint8_t *at = to + (((4 * p + x) ^ (i & 7)) << 4);
-                        *reinterpret_cast<uint4 *>(at) =
-                            make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
-                        *reinterpret_cast<uint4 *>(at + 8192) =
-                            make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
-                    }
+                for (int x = 0; x < 4; ++x) {
+                    uint8_t *at = to + (((4 * half + x) ^ (i & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(at) =
+                        make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
+                    *reinterpret_cast<uint4 *>(at + 8192) =
+                        make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(p_ready);
-            } else if (BWD) {   // row i of scale e^G Q
+            } else if (BWD) {   // row i of scale e^G Q, this half's channels
+                if (!warp_all(wait_for(&full[s], (c / NS) & 1, abort_flag)))
+                    break;
                 const int i = row - 64;
                 const float f = i < n ? -a.scale * tab[TNEG * C + i] : 0.f;
                 const float2 f2 = make_float2(f, f);
-                const uint8_t *from = sm + s * STAGE + QK + i * 128;
-                uint8_t *to = sm + QOFF + i * 128;
+                const uint8_t *from = sm + s * STAGE + QK + half * 16384 + i * 128;
+                uint8_t *to = sm + QOFF + half * 8192 + i * 128;
 #pragma unroll 4
-                for (int x = 0; x < 16; ++x) {
-                    const int off = ((x & 7) ^ (i & 7)) << 4;
-                    uint4 v = *reinterpret_cast<const uint4 *>(from + (x >> 3) * 16384 + off);
+                for (int x = 0; x < 8; ++x) {
+                    const int off = (x ^ (i & 7)) << 4;
+                    uint4 v = *reinterpret_cast<const uint4 *>(from + off);
                     if (i >= n)
                         v = make_uint4(0, 0, 0, 0);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -1032,25 +1125,38 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
                         split2(mul2(f2, make_float2(bf16lo(w[y]), bf16hi(w[y]))), hi[y], lo[y]);
-                    uint8_t *at = to + (x >> 3) * 8192 + off;
-                    *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(at + Q2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    *reinterpret_cast<uint4 *>(to + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(to + off + Q2) =
+                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(q_ready);
             }
-            if constexpr (!BWD) {
-                // the inter term leaves TMEM as soon as it is there: the next chunk's
-                // product with S takes its columns
-                if (!warp_all(wait_for(ks_full, c & 1, abort_flag)))
+            if constexpr (BWD) {    // dO^T: this lane's channel, this half's tokens
+                if (!warp_all(wait_for(&fullv[s], (c / NS) & 1, abort_flag)))
                     break;
-                tc_fence_after();
-                uint32_t inter[2][32];
-                tmem_ld32_issue(lanes + T2, inter[0]);
-                tmem_ld32_issue(lanes + T2 + 32, inter[1]);
-                tmem_wait_ld(inter[0], inter[1]);
+                uint32_t v[16];
+                channel(sm + s * STAGE + VD, row, half, v);
+                if (n < C)
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        if (j0 + 2 * x >= n)
+                            v[x] = 0u;
+                        else if (j0 + 2 * x + 1 >= n)
+                            v[x] &= 0xFFFFu;
+                    }
+                tmem_st16_issue(lanes + TD + 32 * (c & 1) + 16 * half, v);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(td_ready);
+            }
+            if constexpr (!BWD) {
+                uint32_t inter[32], w[32];
+                tmem_ld32(lanes + T2 + j0, inter);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
@@ -1058,37 +1164,31 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 if (!warp_all(wait_for(o_full, c & 1, abort_flag)))
                     break;
                 tc_fence_after();
+                tmem_ld32(lanes + TR + j0, w);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(r_ready);
+                const float2 s2 = make_float2(-a.scale, -a.scale);
+                float y[32];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const float2 g =
+                        *reinterpret_cast<const float2 *>(tab + TNEG * C + j0 + 2 * x);
+                    const float2 z = fma2(mul2(g, s2), pair_of(inter, x), pair_of(w, x));
+                    y[2 * x] = z.x;
+                    y[2 * x + 1] = z.y;
+                }
                 const bool odd = lane & 1;
                 uint8_t *to = reinterpret_cast<uint8_t *>(
                     static_cast<__nv_bfloat16 *>(a.o.p) + sq.row * a.o.sb +
-                    (sq.bos + (int64_t)c * C + odd) * a.o.st + (int64_t)h * a.o.sh + (row & ~1));
-                const bool some = a.o.p && row < a.E;
-                const float2 s2 = make_float2(-a.scale, -a.scale);
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    uint32_t w[32];
-                    tmem_ld32(lanes + TR + 32 * p, w);
-                    if (p == 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(r_ready);
-                    }
-                    float y[32];
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                        const float2 g = *reinterpret_cast<const float2 *>(tab + TNEG * C + 32 * p +
-                                                                           2 * x);
-                        const float2 z = fma2(mul2(g, s2), pair_of(inter[p], x), pair_of(w, x));
-                        y[2 * x] = z.x;
-                        y[2 * x + 1] = z.y;
-                    }
-                    store_rows(y, odd, to + 64 * p * a.o.st, 4 * a.o.st, some ? n - 32 * p : 0);
-                }
+                    (sq.bos + (int64_t)c * C + j0 + odd) * a.o.st + (int64_t)h * a.o.sh +
+                    (row & ~1));
+                store_rows(y, odd, to, 4 * a.o.st, a.o.p && row < a.E ? n - j0 : 0);
             }
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&empty[s]);
+                mbar_arrive(&tempty[c % NT]);
         }
     }
 
@@ -1100,17 +1200,23 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
     }
 }
 
-// ---- dQ, dK, dg, dbeta -----------------------------------------------------------
+// ---- dQ, dK, dV, dg, dbeta ----------------------------------------------------------
 //
-// A CTA a (chunk, head), two of them an SM: 112 KB of tiles, 256 TMEM columns.
-// Transposed as the sweeps: lanes are key channels, columns tokens.  [dO; R] lie as
-// one 128-row tile, so one product with Eps^T gives dO Eps^T in lanes 0-63 and
-// R Eps^T in lanes 64-127.  K'^T takes S^T's place once the products with S are done.
+// A CTA a (chunk, head), two of them an SM: 112 KB of tiles, 256 TMEM columns.  Lanes
+// are tokens here: [dO; R] lie as one 128-row tile, as [Q; K] do, so that one product
+// serves dQ (lanes 0-63) and dK's row part (lanes 64-127):
+//     D1 = [scale e^G dO S^T; -e^G beta R S^T] + [W1; W2] K
+//     DC = kappa beta Eps K'^T + [W1^T, W2^T] [Q; K]         (lanes 64-127)
+// Every A operand is read along its rows (MN-major ones took 200 cycles a product, not
+// 68: 0.80 ms in all at b4 h32 n8192): W1 and W2 are written both ways, and DC's
+// operands start 64 rows early, so that their rows meet lanes 64-127 where dK's other
+// part is (lanes 0-63 of DC hold products of whatever lies before, read by nobody).
 
 constexpr int GRADS = 256;
-constexpr int GQ = 0, GK = 16384, GE = 32768, GD = 49152, GS = 81920, GBAR = 114688;
+constexpr int GQ = 0, GE = 32768, GD = 49152, GS = 81920, GBAR = 114688;
+constexpr int GW = GD, GWT = GD + 16384;        // over dO and R
 constexpr int GDYN = GBAR + 64;
-constexpr uint32_t UW = 0, UQ = 64, UR = 128, UC = 192, UCOLS = 256;
+constexpr uint32_t U1 = 0, UC = 128, UW = 128, UCOLS = 256;
 
 struct GradParams {
     CUtensorMap mq, mk, mdo;
@@ -1118,19 +1224,31 @@ struct GradParams {
     Scratch sc;
 };
 
-// 16 tokens' values of this lane's channel to rows of bf16 or, f32, fp32.
-template <typename F>
-__device__ __forceinline__ void store_16(const float (&x)[16], int j0, int d, int D, F at)
+// 32 numbers of a bf16 row (half a 128-byte row, 16-byte units c16 ..), as loaded
+__device__ __forceinline__ float row_dot(const uint8_t *row, int i, int c0, const float (&x)[32])
 {
-    const bool odd = d & 1;
+    float t = 0.f;
 #pragma unroll
-    for (int m = 0; m < 8; ++m) {
-        const float mine = odd ? x[2 * m + 1] : x[2 * m], other = odd ? x[2 * m] : x[2 * m + 1];
-        const float got = __shfl_xor_sync(0xffffffffu, other, 1);
-        const uint32_t pair = odd ? pack_bf16x2(got, mine) : pack_bf16x2(mine, got);
-        if (uint32_t *p = at(j0 + 2 * m + odd); p && d < D)
-            *p = pair;
+    for (int c = 0; c < 4; ++c) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(row + (((c0 + c) ^ (i & 7)) << 4));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            t = fmaf(bf16lo(w[y]), x[8 * c + 2 * y], t);
+            t = fmaf(bf16hi(w[y]), x[8 * c + 2 * y + 1], t);
+        }
     }
+    return t;
+}
+// 32 values to half of a swizzled 128-byte bf16 row
+__device__ __forceinline__ void put_half_row(uint8_t *row, int i, int c0, const float (&x)[32])
+{
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4 *>(row + (((c0 + c) ^ (i & 7)) << 4)) =
+            make_uint4(pack_bf16x2(x[8 * c], x[8 * c + 1]), pack_bf16x2(x[8 * c + 2], x[8 * c + 3]),
+                       pack_bf16x2(x[8 * c + 4], x[8 * c + 5]),
+                       pack_bf16x2(x[8 * c + 6], x[8 * c + 7]));
 }
 
 __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_constant__ GradParams P)
@@ -1152,14 +1270,16 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
     }
     const int n = (int)min((int64_t)C, sq.len - t0);
     const int64_t tile = slot * a.H + h;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int q = warp & 3, half = warp >> 2;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + GBAR);
-    uint64_t *in_full = bars, *one_full = bars + 1, *k_full = bars + 2, *two_full = bars + 3;
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 4);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 5);
+    uint64_t *in_full = bars, *one_full = bars + 1, *k_full = bars + 2, *c_full = bars + 3,
+             *two_full = bars + 4;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 5);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 6);
     if (tid == 0) {
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 5; ++i)
             mbar_init(&bars[i], 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -1178,47 +1298,44 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
     if (tid == 0) {
         const int hq = h / a.q.hdiv, t = (int)(sq.bos + t0), row = (int)sq.row;
         mbar_arrive_expect_tx(in_full, 3 * 16384 + 2 * ETILE + STILE);
+        bulk_load(sm + GS, P.sc.s + tile * STILE, STILE, in_full);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             tma_load_4d(sm + GD + b * 16384, &P.mdo, in_full, 64 * b, h, t, row);
             bulk_load(sm + GD + b * 16384 + 8192, P.sc.r + tile * ETILE + b * 8192, 8192, in_full);
-            tma_load_4d(sm + GQ + b * 8192, &P.mq, in_full, 64 * b, hq, t, row);
-            tma_load_4d(sm + GK + b * 8192, &P.mk, in_full, 64 * b, hq, t, row);
+            tma_load_4d(sm + GQ + b * 16384, &P.mq, in_full, 64 * b, hq, t, row);
+            tma_load_4d(sm + GQ + b * 16384 + 8192, &P.mk, in_full, 64 * b, hq, t, row);
         }
         bulk_load(sm + GE, P.sc.e + tile * ETILE, ETILE, in_full);
-        bulk_load(sm + GS, P.sc.s + tile * STILE, STILE, in_full);
+        bulk_prefetch(P.sc.k + tile * STILE, STILE);
     }
     __syncwarp();
-    bool ok = warp_all(wait_for(in_full, 0, abort_flag));
+    bool ok = warp_all(bwait(in_full, 0, abort_flag));
     if (a.cu && n < C) {    // another sequence's tokens: zeros
         const uint4 z = make_uint4(0, 0, 0, 0);
         for (int x = tid; x < (C - n) * 8; x += GRADS) {
             const int off = (n + x / 8) * 128 + (x % 8) * 16;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < 4; ++b)
                 *reinterpret_cast<uint4 *>(sm + GQ + b * 8192 + off) = z;
-                *reinterpret_cast<uint4 *>(sm + GK + b * 8192 + off) = z;
-                *reinterpret_cast<uint4 *>(sm + GD + b * 16384 + off) = z;
-            }
+            *reinterpret_cast<uint4 *>(sm + GD + off) = z;
+            *reinterpret_cast<uint4 *>(sm + GD + 16384 + off) = z;
         }
         fence_proxy_async_smem();
     }
     __syncthreads();
     const uint32_t sb = smem_u32(sm);
-    constexpr uint32_t id_kk = idesc_bf16_f32(128, 64, 0, 0), id_mk = idesc_bf16_f32(128, 64, 1, 0),
-                       id_mm = idesc_bf16_f32(128, 64, 1, 1);
-    if (tid == 0 && ok) {
+    constexpr uint32_t id64 = idesc_bf16_f32(128, 64, 0, 0), id128 = idesc_bf16_f32(128, 128, 0, 1);
+    if (warp == 0 && ok && elect_one()) {
+        const uint64_t d_d = sdesc_sw128(sb + GD, 16, 1024), d_e = sdesc_sw128(sb + GE, 16, 1024);
+        const uint64_t d_s = sdesc_sw128(sb + GS, 16384, 1024);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t rows = (kk >> 2) * 16384 + (kk & 3) * 32;
-            const uint64_t de = sdesc_sw128(sb + GE + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024);
-            const uint64_t ddo = sdesc_sw128(sb + GD + rows, 16, 1024);
-            const uint64_t dr = sdesc_sw128(sb + GD + 8192 + rows, 16, 1024);
-            const uint64_t ds = sdesc_sw128(sb + GS + kk * 2048, 16384, 1024);
-            mma_ss(tm + UW, ddo, de, id_kk, kk > 0);        // [dO; R] Eps^T
-            mma_ss(tm + UQ, ds, ddo, id_mk, kk > 0);        // S dO^T
-            mma_ss(tm + UR, ds, dr, id_mk, kk > 0);         // S R^T
-        }
+        for (int kk = 0; kk < 8; ++kk)      // [dO; R] Eps^T
+            mma_ss(tm + UW, d_d + ((kk >> 2) * 1024 + (kk & 3) * 2),
+                   d_e + ((kk >> 2) * 512 + (kk & 3) * 2), id64, kk > 0);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)      // [dO; R] S^T
+            mma_ss(tm + U1, d_d + ((kk >> 2) * 1024 + (kk & 3) * 2), d_s + kk * 128, id128, kk > 0);
         mma_commit(one_full);
     }
     __syncwarp();
@@ -1240,25 +1357,22 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
 #pragma unroll
     for (int x = 0; x < 8; ++x)
         sv[x] = *reinterpret_cast<const uint4 *>(sm + GS + tid * 16 + x * 4096);
-    ok = warp_all(wait_for(one_full, 0, abort_flag)) && ok;
+    ok = warp_all(bwait(one_full, 0, abort_flag)) && ok;
     tc_fence_after();
-    __syncthreads();    // S has been read, by the products and by every thread
+    __syncthreads();    // S and R have been read, by the products and by every thread
     if (tid == 0 && ok) {
         mbar_arrive_expect_tx(k_full, STILE);
         bulk_load(sm + GS, P.sc.k + tile * STILE, STILE, k_full);
     }
     __syncwarp();
-    const int j0 = 32 * half;
-    {   // W1, W2 as bf16 rows over dO and R (both read); S dO^T, S R^T scaled
-        const int i = 32 * (q & 1) + lane;
-        const float gi = tab[TLOG * C + i];
+    const int i = 32 * (q & 1) + lane;              // this lane's token
+    const bool key = q >= 2;                        // R's lanes: dK's row part
+    const float eg = -tab[TNEG * C + i], beta = tab[TBETA * C + i];
+    {   // W1 (W2), row i, columns 32 half .., as rows and as columns
+        const int j0 = 32 * half;
         uint32_t r[32];
         tmem_ld32(lanes + UW + j0, r);
-        uint8_t *to = sm + GD + (q < 2 ? 0 : 8192) + i * 128;
-        // one branch a warp: dO's lanes, R's lanes
-        const float f = q < 2 ? a.scale : tab[TNB * C + i];
-        const int last = q < 2 ? i : i - 1;
-        if (q >= 2 && i >= j0 && i < j0 + 32 && i < n) {
+        if (key && i >= j0 && i < j0 + 32 && i < n) {
             float d = 0.f;
 #pragma unroll
             for (int x = 0; x < 32; ++x)
@@ -1266,56 +1380,66 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
             static_cast<__nv_bfloat16 *>(a.dbeta)[((sq.row * a.T) + sq.bos + t0 + i) * a.H + h] =
                 __float2bfloat16_rn(d);
         }
+        const float f = key ? -beta : a.scale, gi = tab[TLOG * C + i];
+        const int last = key ? i - 1 : i;
+        float w[32];
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
-            const int j = j0 + x;
-            r[x] = j <= last ? __float_as_uint(f * tab[TBETA * C + j] *
-                                               exp2_fast(gi - tab[TLOG * C + j]) *
-                                               __uint_as_float(r[x]))
-                             : 0u;
+        for (int x4 = 0; x4 < 8; ++x4) {
+            const float4 b = *reinterpret_cast<const float4 *>(tab + TBETA * C + j0 + 4 * x4);
+            const float4 g = *reinterpret_cast<const float4 *>(tab + TLOG * C + j0 + 4 * x4);
+            const float bb[4] = {b.x, b.y, b.z, b.w}, gg[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int x = 4 * x4 + y;
+                w[x] = j0 + x <= last
+                           ? f * bb[y] * exp2_fast(gi - gg[y]) * __uint_as_float(r[x])
+                           : 0.f;
+            }
         }
+        put_half_row(sm + GW + (key ? 8192 : 0) + i * 128, i, 4 * half, w);
+        uint8_t *to = sm + GWT + (key ? 8192 : 0) + (i & 6) * 2;
+        const bool odd = lane & 1;
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<uint4 *>(to + (((4 * half + x) ^ (i & 7)) << 4)) = make_uint4(
-                pack_bf16x2(__uint_as_float(r[8 * x]), __uint_as_float(r[8 * x + 1])),
-                pack_bf16x2(__uint_as_float(r[8 * x + 2]), __uint_as_float(r[8 * x + 3])),
-                pack_bf16x2(__uint_as_float(r[8 * x + 4]), __uint_as_float(r[8 * x + 5])),
-                pack_bf16x2(__uint_as_float(r[8 * x + 6]), __uint_as_float(r[8 * x + 7])));
-        tmem_ld32(lanes + UQ + j0, r);
+        for (int m = 0; m < 16; ++m) {
+            const float mine = odd ? w[2 * m + 1] : w[2 * m], other = odd ? w[2 * m] : w[2 * m + 1];
+            const float got = __shfl_xor_sync(0xffffffffu, other, 1);
+            const int j = j0 + 2 * m + odd;
+            *reinterpret_cast<uint32_t *>(to + j * 128 + (((i >> 3) ^ (j & 7)) << 4)) =
+                odd ? pack_bf16x2(got, mine) : pack_bf16x2(mine, got);
+        }
+    }
+    {   // the products with S, scaled
+        const float f = key ? -eg * beta : a.scale * eg;
+        const float2 f2 = make_float2(f, f);
 #pragma unroll
-        for (int x = 0; x < 32; ++x)
-            r[x] = __float_as_uint(-a.scale * tab[TNEG * C + j0 + x] * __uint_as_float(r[x]));
-        tmem_st32_issue(lanes + UQ + j0, r);
-        uint32_t w[32];
-        tmem_ld32(lanes + UR + j0, w);
+        for (int p = 0; p < 2; ++p) {
+            uint32_t r[32];
+            tmem_ld32(lanes + U1 + 64 * half + 32 * p, r);
 #pragma unroll
-        for (int x = 0; x < 32; ++x)
-            w[x] = __float_as_uint(tab[TNGB * C + j0 + x] * __uint_as_float(w[x]));
-        tmem_st32_issue(lanes + UR + j0, w);
+            for (int x = 0; x < 16; ++x)
+                put_pair(r, x, mul2(f2, pair_of(r, x)));
+            tmem_st32_issue(lanes + U1 + 64 * half + 32 * p, r);
+        }
         tmem_wait_st();
     }
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    ok = warp_all(wait_for(k_full, 0, abort_flag)) && ok;
-    if (tid == 0 && ok) {
+    ok = warp_all(bwait(k_full, 0, abort_flag)) && ok;
+    const bool issuer = warp == 0 && ok && elect_one();
+    if (issuer) {
+        const uint64_t d_e = sdesc_sw128(sb + GE - 8192, 16, 1024);
+        const uint64_t d_s = sdesc_sw128(sb + GS, 16384, 1024);
+        const uint64_t d_w = sdesc_sw128(sb + GW, 16, 1024);
+        const uint64_t d_k = sdesc_sw128(sb + GQ + 8192, 16384, 1024);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t kt = sdesc_sw128(sb + GK + kk * 2048, 8192, 1024);
-            const uint64_t qt = sdesc_sw128(sb + GQ + kk * 2048, 8192, 1024);
-            const uint32_t w1 = sb + GD, w2 = sb + GD + 8192;
-            mma_ss(tm + UQ, kt, sdesc_sw128(w1 + kk * 32, 16, 1024), id_mk, 1);     // K^T W1^T
-            mma_ss(tm + UR, kt, sdesc_sw128(w2 + kk * 32, 16, 1024), id_mk, 1);     // K^T W2^T
-            mma_ss(tm + UC, qt, sdesc_sw128(w1 + kk * 2048, 8192, 1024), id_mm, kk > 0);
-            mma_ss(tm + UC, kt, sdesc_sw128(w2 + kk * 2048, 8192, 1024), id_mm, 1);
-        }
+        for (int kk = 0; kk < 8; ++kk)      // Eps K'^T
+            mma_ss(tm + UC, d_e + ((kk >> 2) * 512 + (kk & 3) * 2), d_s + kk * 128, id128, kk > 0);
+        mma_commit(c_full);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)      // K' Eps^T
-            mma_ss(tm + UW, sdesc_sw128(sb + GS + kk * 2048, 16384, 1024),
-                   sdesc_sw128(sb + GE + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024), id_mk,
-                   kk > 0);
-        mma_commit(two_full);
+        for (int kk = 0; kk < 4; ++kk)      // [W1; W2] K
+            mma_ss(tm + U1, d_w + kk * 2, d_k + kk * 128, id128, 1);
     }
     __syncwarp();
     float end = 0.f;    // <S', K'>
@@ -1333,73 +1457,77 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
         }
         end *= -tab[TNEG * C + C - 1];
     }
-    ok = warp_all(wait_for(two_full, 0, abort_flag)) && ok;
+    // row i of Q (K): this half's 64 channels
+    const uint8_t *own = sm + GQ + half * 16384 + (key ? 8192 : 0) + i * 128;
+    ok = warp_all(bwait(c_full, 0, abort_flag)) && ok;
     tc_fence_after();
-    float *red = reinterpret_cast<float *>(sm + GD + 16384);    // [4][64], then 8 sums
-    const int d = 32 * q + lane;
-    if (ok) {
+    if (key) {
+        const float f = tab[TKB * C + i];
 #pragma unroll 1
         for (int p = 0; p < 2; ++p) {
-            const int jp = j0 + 16 * p;
-            uint32_t dq[16], dr[16], dc[16], dw[16];
-            tmem_ld16_issue(lanes + UQ + jp, dq);
-            tmem_ld16_issue(lanes + UR + jp, dr);
-            tmem_wait_ld16x2(dq, dr);
-            tmem_ld16_issue(lanes + UC + jp, dc);
-            tmem_ld16_issue(lanes + UW + jp, dw);
-            tmem_wait_ld16x2(dc, dw);
-            float oq[16], ok_[16], t[16];
+            uint32_t r[32];
+            float x32[32];
+            tmem_ld32(lanes + UC + 64 * half + 32 * p, r);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                const uint32_t at = image_pair(C, jp + x, d) + (d & 1) * 2;
-                const float qv = __uint_as_float(
-                    (uint32_t)*reinterpret_cast<const uint16_t *>(sm + GQ + at) << 16);
-                const float kv = __uint_as_float(
-                    (uint32_t)*reinterpret_cast<const uint16_t *>(sm + GK + at) << 16);
-                const float into = tab[TKB * C + jp + x] * __uint_as_float(dw[x]);
-                const float row = __uint_as_float(dr[x]), col = __uint_as_float(dc[x]) + into;
-                oq[x] = __uint_as_float(dq[x]);
-                ok_[x] = row + col;
-                t[x] = fmaf(qv, oq[x], kv * (row - col));
-                end = fmaf(kv, into, end);
+            for (int x = 0; x < 32; ++x) {
+                x32[x] = f * __uint_as_float(r[x]);
+                r[x] = __float_as_uint(x32[x]);
             }
-            if (P.sc.dqp) {
-                float *pq = P.sc.dqp + ((sq.row * a.T + sq.bos + t0) * a.H + h) * a.D + d;
-                float *pk = P.sc.dkp + (pq - P.sc.dqp);
-#pragma unroll
-                for (int x = 0; x < 16; ++x)
-                    if (jp + x < n && d < a.D) {
-                        pq[(int64_t)(jp + x) * a.H * a.D] = oq[x];
-                        pk[(int64_t)(jp + x) * a.H * a.D] = ok_[x];
-                    }
-            } else {
-                auto rows = [&](const TokOut &o) {
-                    return static_cast<__nv_bfloat16 *>(o.p) + sq.row * o.sb +
-                           (sq.bos + t0) * o.st + (int64_t)h * o.sh + (d & ~1);
-                };
-                __nv_bfloat16 *pq = rows(a.dq), *pk = rows(a.dk);
-                store_16(oq, jp, d, a.D, [&](int j) {
-                    return j < n ? reinterpret_cast<uint32_t *>(pq + j * a.dq.st) : nullptr;
-                });
-                store_16(ok_, jp, d, a.D, [&](int j) {
-                    return j < n ? reinterpret_cast<uint32_t *>(pk + j * a.dk.st) : nullptr;
-                });
-            }
-            // t summed over the lanes: halves traded, each lane ends with one token
-#pragma unroll
-            for (int m = 16, w = 8; w >= 1; m /= 2, w /= 2) {
-                const bool up = lane & m;
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    if (x < w) {
-                        const float keep = up ? t[x + w] : t[x], send = up ? t[x] : t[x + w];
-                        t[x] = keep + __shfl_xor_sync(0xffffffffu, send, m);
-                    }
-            }
-            t[0] += __shfl_xor_sync(0xffffffffu, t[0], 1);
-            if (!(lane & 1))
-                red[64 * q + jp + (lane >> 1)] = t[0];
+            tmem_st32_issue(lanes + UC + 64 * half + 32 * p, r);
+            end += row_dot(own, i, 4 * p, x32);
         }
+        tmem_wait_st();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (issuer) {
+        const uint64_t d_wt = sdesc_sw128(sb + GWT - 8192, 16, 1024);
+        const uint64_t d_q = sdesc_sw128(sb + GQ, 16384, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)      // [W1^T, W2^T] [Q; K]
+            mma_ss(tm + UC, d_wt + ((kk >> 2) * 512 + (kk & 3) * 2), d_q + kk * 128, id128, 1);
+        mma_commit(two_full);
+    }
+    __syncwarp();
+    ok = warp_all(bwait(two_full, 0, abort_flag)) && ok;
+    tc_fence_after();
+    float *red = reinterpret_cast<float *>(sm + GS);        // [4][64], then 8 sums
+    if (ok) {
+        float t = 0.f;
+        // dq (dk) of token i, 64 channels: out through the tile of Eps (of dO)
+        uint8_t *stage = sm + (key ? GD : GE) + half * 8192 + i * 128;
+        float *part = P.sc.dqp ? (key ? P.sc.dkp : P.sc.dqp) +
+                                     ((sq.row * a.T + sq.bos + t0 + i) * a.H + h) * a.D + 64 * half
+                               : nullptr;
+#pragma unroll 1
+        for (int p = 0; p < 2; ++p) {
+            uint32_t r[32];
+            float x32[32], y32[32];
+            tmem_ld32(lanes + U1 + 64 * half + 32 * p, r);
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+                x32[x] = y32[x] = __uint_as_float(r[x]);
+            if (key) {
+                tmem_ld32(lanes + UC + 64 * half + 32 * p, r);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                    const float col = __uint_as_float(r[x]);
+                    y32[x] = x32[x] - col;
+                    x32[x] += col;
+                }
+            }
+            t += row_dot(own, i, 4 * p, y32);
+            if (!part)
+                put_half_row(stage, i, 4 * p, x32);
+            else if (i < n)
+#pragma unroll
+                for (int x = 0; x < 32; x += 4)
+                    if (64 * half + 32 * p + x < a.D)
+                        *reinterpret_cast<float4 *>(part + 32 * p + x) =
+                            make_float4(x32[x], x32[x + 1], x32[x + 2], x32[x + 3]);
+        }
+        red[64 * (2 * (q >> 1) + half) + i] = t;
 #pragma unroll
         for (int m = 1; m < 32; m *= 2)
             end += __shfl_xor_sync(0xffffffffu, end, m);
@@ -1410,30 +1538,43 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
         drain_wait(in_full, 0);
         drain_wait(one_full, 0);
         drain_wait(k_full, 0);
+        drain_wait(c_full, 0);
         drain_wait(two_full, 0);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) {
+    if (warp == 0)
         tmem_dealloc(tm, UCOLS);
-        // dg: running sums from the chunk's last token
+    if (!P.sc.dqp && ok)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const int j = ((tid >> 4) + 16 * x) & 63, c16 = tid & 15;
+            const TokOut &o = x < 4 ? a.dq : a.dk;
+            if (j < n && 8 * c16 < a.D)
+                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(o.p) + sq.row * o.sb +
+                                           (sq.bos + t0 + j) * o.st + (int64_t)h * o.sh +
+                                           8 * c16) =
+                    *reinterpret_cast<const uint4 *>(sm + (x < 4 ? GE : GD) + (c16 >> 3) * 8192 +
+                                                     j * 128 + (((c16 & 7) ^ (j & 7)) << 4));
+        }
+    if (warp == 7) {    // dg: running sums from the chunk's last token
         float run = 0.f;
 #pragma unroll
         for (int w = 0; w < 8; ++w)
             run += red[256 + w];
 #pragma unroll
         for (int p = 1; p >= 0; --p) {
-            const int i = 32 * p + 31 - lane;
-            float x = red[i] + red[64 + i] + red[128 + i] + red[192 + i];
+            const int j = 32 * p + 31 - lane;
+            float x = red[j] + red[64 + j] + red[128 + j] + red[192 + j];
 #pragma unroll
             for (int m = 1; m < 32; m *= 2) {
                 const float y = __shfl_up_sync(0xffffffffu, x, m);
                 if (lane >= m)
                     x += y;
             }
-            if (i < n && ok)
-                static_cast<__nv_bfloat16 *>(a.dg)[((sq.row * a.T) + sq.bos + t0 + i) * a.H + h] =
+            if (j < n && ok)
+                static_cast<__nv_bfloat16 *>(a.dg)[((sq.row * a.T) + sq.bos + t0 + j) * a.H + h] =
                     __float2bfloat16_rn(run + x);
             run += __shfl_sync(0xffffffffu, x, 31);
         }

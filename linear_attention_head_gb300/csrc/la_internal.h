@@ -388,10 +388,12 @@ size_t rope_partial_bytes(int D);
 struct NormRows {
     const void *p;              // null: not there
     int64_t s[3];               // element strides (batch, token, head)
+    int64_t step;               // from row to row, where BlockNormArgs::flat
 };
 struct BlockNormArgs {
     int B, T, H, D;
     int64_t rows;               // B T H
+    int flat;                   // every tensor's rows are a constant step apart
     int bf16, w_bf16;
     int activation;             // 0 none, 1 sigmoid, 2 silu
     float eps, scale;
