@@ -187,17 +187,30 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 
 // ---- B of every chunk -----------------------------------------------------------
 //
-// K K^T by mma.sync (bf16 exact, fp32 sums), then the triangular system in fp32:
-// diagonal blocks of 16 by substitution, a thread a column, then blocks joined
-// 16 -> 32 -> 64:  B21 = (I - B22 beta) A21 (I - beta B11).
+// K K^T by mma.sync (bf16 exact, fp32 sums), then the triangular system: diagonal
+// blocks of 16 by substitution in fp32, a thread a column, and blocks joined
+// 16 -> 32 -> 64 on the tensor cores,
+//     M = A21 - A21 (beta B11),   B21 = M - B22 (beta M),
+// the factors as hi + lo (hi hi, hi lo, lo hi), A21 and M in the fp32 fragments that
+// K K^T left in registers.  The left factors (A21, then B) end as B itself, hi and lo:
+// what is written out.  (The joins by fp32 FMAs read 180 times 16 bytes a thread from
+// shared memory, which bound them: 0.30 ms for the 16384 chunks of b4 h32 n8192.)
 
 constexpr int PREP = 128;
 constexpr int KP = 136;         // bf16 a row of K in shared memory
-constexpr int AP = 68;          // floats a row of A
+constexpr int LP = 72;          // bf16 a row of the factors: eight rows, eight banks of 16 bytes
+constexpr int DP = 20;          // floats a row of the diagonal blocks
 
 __device__ __forceinline__ void ldm_x4(uint32_t (&r)[4], const void *p)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_u32(p))
+                 : "memory");
+}
+__device__ __forceinline__ void ldm_x4_trans(uint32_t (&r)[4], const void *p)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(smem_u32(p))
                  : "memory");
@@ -211,44 +224,67 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// acc[r][.] -= sum over W rows k of left[r][k] right[k][.], r < R rows one after
-// another: 4 k a step, so that left and right are read 16 bytes at a time.
-template <int R, int W>
-__device__ __forceinline__ void minus_product(float4 (&acc)[R], const float *left, const float *right)
+typedef __nv_bfloat16 Factor[2][C][LP];         // hi, lo
+
+// acc (16 rows from r0, 8 N columns from c0) -= left[r0 ..][k0 .. k0 + K) right[k0 ..][c0 ..]
+template <int K, int N>
+__device__ __forceinline__ void minus_product(float (*acc)[4], const Factor &left,
+                                              const Factor &right, int r0, int k0, int c0)
 {
-#pragma unroll 2
-    for (int k4 = 0; k4 < W; k4 += 4) {
-        float4 l[R];
+    const int lane = threadIdx.x & 31, r = lane & 15, half = 8 * (lane >> 4);
+    float sum[N][4] = {};
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-            l[r] = *reinterpret_cast<const float4 *>(left + r * AP + k4);
+    for (int kk = 0; kk < K; kk += 16) {
+        uint32_t l[2][4];
+        ldm_x4(l[0], &left[0][r0 + r][k0 + kk + half]);
+        ldm_x4(l[1], &left[1][r0 + r][k0 + kk + half]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float4 x = *reinterpret_cast<const float4 *>(right + (k4 + k) * AP);
+        for (int n = 0; n < N; n += 2) {
+            uint32_t x[2][4];
+            ldm_x4_trans(x[0], &right[0][k0 + kk + r][c0 + 8 * n + half]);
+            ldm_x4_trans(x[1], &right[1][k0 + kk + r][c0 + 8 * n + half]);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float f = k == 0 ? l[r].x : k == 1 ? l[r].y : k == 2 ? l[r].z : l[r].w;
-                acc[r].x = fmaf(-f, x.x, acc[r].x);
-                acc[r].y = fmaf(-f, x.y, acc[r].y);
-                acc[r].z = fmaf(-f, x.z, acc[r].z);
-                acc[r].w = fmaf(-f, x.w, acc[r].w);
+            for (int y = 0; y < 2; ++y) {
+                mma_16816(sum[n + y], l[0], x[0][2 * y], x[0][2 * y + 1]);
+                mma_16816(sum[n + y], l[1], x[0][2 * y], x[0][2 * y + 1]);
+                mma_16816(sum[n + y], l[0], x[1][2 * y], x[1][2 * y + 1]);
             }
         }
     }
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            acc[n][v] -= sum[n][v];
 }
-__device__ __forceinline__ float4 times(float f, float4 x)
+// the fragments of 16 rows from r0, 8 N columns from c0, times f[row] (null: 1), as hi + lo
+template <int N>
+__device__ __forceinline__ void put_factor(Factor &to, const float (*acc)[4], int r0, int c0,
+                                           const float *f)
 {
-    return make_float4(f * x.x, f * x.y, f * x.z, f * x.w);
+    const int lane = threadIdx.x & 31, r = r0 + (lane >> 2), c = c0 + 2 * (lane & 3);
+#pragma unroll
+    for (int v = 0; v < 4; v += 2) {
+        const float s = f ? f[r + 4 * v] : 1.f;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            uint32_t hi, lo;
+            split2(make_float2(s * acc[n][v], s * acc[n][v + 1]), hi, lo);
+            *reinterpret_cast<uint32_t *>(&to[0][r + 4 * v][c + 8 * n]) = hi;
+            *reinterpret_cast<uint32_t *>(&to[1][r + 4 * v][c + 8 * n]) = lo;
+        }
+    }
 }
 
 __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, const Scratch sc)
 {
-    __shared__ __align__(16) __nv_bfloat16 ks[C][KP];
-    __shared__ __align__(16) float A[C][AP];
-    // once K K^T is done: rows of beta B of the first blocks, and of beta M of the
-    // second ones (M = A21 (I - beta B11)), the right factors of the joins
-    float (*Z)[AP] = reinterpret_cast<float (*)[AP]>(ks), (*M)[AP] = Z + C / 2;
-    static_assert(sizeof(float) * C * AP <= sizeof(ks), "Z and M lie over K");
+    // K, then the right factors: beta B of the first blocks, beta M of the second ones
+    __shared__ __align__(16) uint8_t over[sizeof(Factor)];
+    static_assert(sizeof(Factor) >= C * KP * sizeof(__nv_bfloat16), "the right factors lie over K");
+    __nv_bfloat16 (*ks)[KP] = reinterpret_cast<__nv_bfloat16 (*)[KP]>(over);
+    Factor &R = *reinterpret_cast<Factor *>(over);
+    __shared__ __align__(16) Factor L;
+    __shared__ __align__(16) float diag[4][16][DP];
     __shared__ float G[C], beta[C], part[2];
     const int h = blockIdx.x % a.H;
     const int64_t slot = blockIdx.x / a.H;
@@ -290,7 +326,6 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
         }
         if (lane == 31)
             part[warp] = g;
-        G[tid] = g;
         beta[tid] = b;
     }
     __syncthreads();
@@ -306,15 +341,12 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
         tab[TNGB * C] = -eg * b;
         tab[TBETA * C] = b;
         tab[TLOG * C] = g * 1.4426950408889634f;
-        __syncwarp();
         G[tid] = g;
     }
-    __syncthreads();
-
     // rows 16 warp .. of K K^T, columns up to the diagonal block
+    float acc[8][4] = {};
     {
         const int r = lane & 15, half = lane >> 4;
-        float acc[8][4] = {};
         for (int kk = 0; kk < ksteps; ++kk) {
             uint32_t x[4];
             ldm_x4(x, &ks[16 * warp + r][16 * kk + 8 * half]);
@@ -327,31 +359,44 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
                     mma_16816(acc[2 * jb + 1], x, y[1], y[3]);
                 }
         }
+    }
+    __syncthreads();    // K has been read, G written
+    {   // A in place of K K^T; zeros from the diagonal on
+        const int i0 = 16 * warp + (lane >> 2), j0 = 2 * (lane & 3);
+        const float g0 = G[i0], g1 = G[i0 + 8];
 #pragma unroll
         for (int nb = 0; nb < 8; ++nb)
-#pragma unroll
-            for (int v = 0; v < 4; v += 2) {
-                const int i = 16 * warp + (lane >> 2) + 4 * v, j = 8 * nb + 2 * (lane & 3);
-                float2 x = make_float2(0.f, 0.f);
-                if (j < i)
-                    x.x = expf(G[i] - G[j]) * acc[nb][v];
-                if (j + 1 < i)
-                    x.y = expf(G[i] - G[j + 1]) * acc[nb][v + 1];
-                *reinterpret_cast<float2 *>(&A[i][j]) = x;
+            if (nb < 2 * (warp + 1)) {
+                const int j = 8 * nb + j0;
+                const float h0 = G[j], h1 = G[j + 1];
+                acc[nb][0] = j < i0 ? expf(g0 - h0) * acc[nb][0] : 0.f;
+                acc[nb][1] = j + 1 < i0 ? expf(g0 - h1) * acc[nb][1] : 0.f;
+                acc[nb][2] = j < i0 + 8 ? expf(g1 - h0) * acc[nb][2] : 0.f;
+                acc[nb][3] = j + 1 < i0 + 8 ? expf(g1 - h1) * acc[nb][3] : 0.f;
             }
+        put_factor<8>(L, acc, 16 * warp, 0, nullptr);
+#pragma unroll
+        for (int jb = 0; jb < 4; ++jb)
+            if (jb == warp)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int v = 0; v < 4; v += 2)
+                        *reinterpret_cast<float2 *>(
+                            &diag[warp][(lane >> 2) + 4 * v][8 * x + j0]) =
+                            make_float2(acc[2 * jb + x][v], acc[2 * jb + x][v + 1]);
     }
-    __syncthreads();
-    // diagonal blocks of 16: column lane of block warp; block 0's upper right in Z is
-    // zero, as it is in A
+    __syncwarp();
+    // diagonal blocks of 16: column lane of block warp; L takes B, R beta B
     {
         const int b0 = 16 * warp, c = lane & 15;
         float z[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float x = A[b0 + i][b0 + c];
+            float x = diag[warp][i][c];
 #pragma unroll
             for (int m4 = 0; m4 < i; m4 += 4) {
-                const float4 l = *reinterpret_cast<const float4 *>(&A[b0 + i][b0 + m4]);
+                const float4 l = *reinterpret_cast<const float4 *>(&diag[warp][i][m4]);
                 x = fmaf(-l.x, z[m4], x);
                 if (m4 + 1 < i)
                     x = fmaf(-l.y, z[m4 + 1], x);
@@ -361,65 +406,59 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
                     x = fmaf(-l.w, z[m4 + 3], x);
             }
             z[i] = beta[b0 + i] * x;
-            __syncwarp();
-            if (lane < 16)      // row i of the block is not read again in this loop
-                A[b0 + i][b0 + c] = x;
+            // lanes 0-15 write hi, 16-31 lo; block 0's upper right in R is zero
+            const __nv_bfloat16 xh = __float2bfloat16_rn(x), zh = __float2bfloat16_rn(z[i]);
+            const bool low = lane >= 16;
+            L[low][b0 + i][b0 + c] =
+                low ? __float2bfloat16_rn(x - __bfloat162float(xh)) : xh;
+            if (warp < 3)
+                R[low][b0 + i][b0 + c] =
+                    low ? __float2bfloat16_rn(z[i] - __bfloat162float(zh)) : zh;
+            if (warp == 0)
+                R[low][i][16 + c] = __float2bfloat16_rn(0.f);
         }
-        if (warp < 3) {         // blocks 0 and 2 are first ones; 1 is part of one later
-            const int z0 = warp == 2 ? 16 : b0;
+    }
+    __syncthreads();
+    if (warp & 1) {     // 16 -> 32: this warp's rows, the 16 columns before its diagonal block
+        const int r0 = 16 * warp, c0 = r0 - 16;
+        float m[2][4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (lane < 16)
-                    Z[z0 + i][b0 + c] = z[i];
-                else if (warp == 0)
-                    Z[i][16 + c] = 0.f;
-        }
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                m[x][v] = warp == 1 ? acc[x][v] : acc[4 + x][v];
+        minus_product<16, 2>(m, L, R, r0, c0, c0);
+        put_factor<2>(R, m, r0, c0, beta);
+        __syncwarp();
+        minus_product<16, 2>(m, L, R, r0, r0, c0);
+        put_factor<2>(L, m, r0, c0, nullptr);
+        __syncwarp();
+        if (warp == 1)  // beta B in place of beta M
+            put_factor<2>(R, m, r0, c0, beta);
     }
     __syncthreads();
-    {   // 16 -> 32: 64 threads a pair of blocks, a row's four columns each
-        const int p = tid >> 6, t = tid & 63, first = 32 * p;
-        const int r = t >> 2, i = first + 16 + r, j = first + 4 * (t & 3);
-        float4 x[1] = {*reinterpret_cast<const float4 *>(&A[i][j])};
-        minus_product<1, 16>(x, &A[i][first], &Z[16 * p][j]);
-        *reinterpret_cast<float4 *>(&M[16 * p + r][j]) = times(beta[i], x[0]);
-        __syncthreads();
-        minus_product<1, 16>(x, &A[i][first + 16], &M[16 * p][j]);
-        *reinterpret_cast<float4 *>(&A[i][j]) = x[0];
-        if (p == 0)
-            *reinterpret_cast<float4 *>(&Z[16 + r][j]) = times(beta[i], x[0]);
-    }
-    __syncthreads();
-    {   // 32 -> 64: two rows' four columns each
-        const int r = 2 * (tid >> 3), i = 32 + r, j = 4 * (tid & 7);
-        float4 x[2] = {*reinterpret_cast<const float4 *>(&A[i][j]),
-                       *reinterpret_cast<const float4 *>(&A[i + 1][j])};
-        minus_product<2, 32>(x, &A[i][0], &Z[0][j]);
-        *reinterpret_cast<float4 *>(&M[r][j]) = times(beta[i], x[0]);
-        *reinterpret_cast<float4 *>(&M[r + 1][j]) = times(beta[i + 1], x[1]);
-        __syncthreads();
-        minus_product<2, 32>(x, &A[i][32], &M[0][j]);
-        *reinterpret_cast<float4 *>(&A[i][j]) = x[0];
-        *reinterpret_cast<float4 *>(&A[i + 1][j]) = x[1];
+    if (warp >= 2) {    // 32 -> 64: this warp's rows, columns 0-31
+        const int r0 = 16 * warp;
+        float m[4][4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                m[x][v] = acc[x][v];
+        minus_product<32, 4>(m, L, R, r0, 0, 0);
+        put_factor<4>(R, m, r0, 0, beta);
+        asm volatile("bar.sync 1, 64;" ::: "memory");
+        minus_product<32, 4>(m, L, R, r0, 32, 0);
+        put_factor<4>(L, m, r0, 0, nullptr);
     }
     __syncthreads();
     // hi and lo as 128B-swizzled rows, the shared-memory image that the sweeps load
-    {
-        const int i = tid >> 1, half = tid & 1;
-        uint8_t *to = sc.b + tile * BTILE + i * 128;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int c16 = 4 * half + x;
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const int j = 8 * c16 + 2 * p;
-                split2(make_float2(j < i ? A[i][j] : 0.f, j + 1 < i ? A[i][j + 1] : 0.f), hi[p],
-                       lo[p]);
-            }
-            uint8_t *at = to + ((c16 ^ (i & 7)) << 4);
-            *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(at + BTILE / 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
+    for (int x = 0; x < 8; ++x) {
+        const int lo = x >> 2, i = (tid >> 3) + 16 * (x & 3), c16 = tid & 7;
+        *reinterpret_cast<uint4 *>(sc.b + tile * BTILE + lo * (BTILE / 2) + i * 128 +
+                                   ((c16 ^ (i & 7)) << 4)) =
+            *reinterpret_cast<const uint4 *>(&L[lo][i][8 * c16]);
     }
 }
 
@@ -630,23 +669,34 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 mbar_arrive(i_free);
                 return true;
             };
-            int issued = 0;
+            int issued = 0, tables = 0;
             bool going = true;
+            auto tables_in = [&]() {
+                const int ts = tables % NT;
+                if (tables >= NT &&
+                    !(going = wait_for(&tempty[ts], (tables / NT - 1) & 1, abort_flag)))
+                    return false;
+                mbar_arrive_expect_tx(&tfull[ts], TAB);
+                bulk_load(sm + L::TOFF + ts * TAB, P.sc.tab + tile_of(tables) * TABS * C, TAB,
+                          &tfull[ts]);
+                ++tables;
+                return true;
+            };
             for (int c = 0; c < nc; ++c) {
                 const int s = c % NS;
+                // tables a chunk ahead, the tiles of the chunk after this into L2: its
+                // stage is free a chunk later
+                while (tables < nc && tables < c + 2 && tables_in())
+                    ;
+                if (!going)
+                    break;
                 if (c >= NS) {
                     going = !simg || images(c - NS);
                     if (!going || !(going = wait_for(&empty[s], (c / NS - 1) & 1, abort_flag)))
                         break;
                 }
-                const int ts = c % NT;
-                if (c >= NT && !(going = wait_for(&tempty[ts], (c / NT - 1) & 1, abort_flag)))
-                    break;
                 const int t = (int)(sq.bos + (int64_t)chunk(c) * C);
                 uint8_t *st = sm + s * STAGE;
-                mbar_arrive_expect_tx(&tfull[ts], TAB);
-                bulk_load(sm + L::TOFF + ts * TAB, P.sc.tab + tile_of(c) * TABS * C, TAB,
-                          &tfull[ts]);
                 mbar_arrive_expect_tx(&full[s], 32768);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
@@ -660,15 +710,15 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                     tma_load_4d(st + VD + b * 8192, &P.mv, &fullv[s], 64 * b, h, t, (int)sq.row);
                 mbar_arrive_expect_tx(&fullb[s], BTILE);
                 bulk_load(st + BB, P.sc.b + tile_of(c) * BTILE, BTILE, &fullb[s]);
-                if (c + 1 < nc) {   // the next stage is free a chunk later: into L2 by then
-                    const int t1 = (int)(sq.bos + (int64_t)chunk(c + 1) * C);
+                if (const int c1 = c + (c == 0 ? 1 : 2); c1 < nc) {
+                    const int t1 = (int)(sq.bos + (int64_t)chunk(c1) * C);
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         tma_prefetch_l2_4d(&P.mq, 64 * b, hq, t1, (int)sq.row);
                         tma_prefetch_l2_4d(&P.mk, 64 * b, hq, t1, (int)sq.row);
                         tma_prefetch_l2_4d(&P.mv, 64 * b, h, t1, (int)sq.row);
                     }
-                    bulk_prefetch(P.sc.b + tile_of(c + 1) * BTILE, BTILE);
+                    bulk_prefetch(P.sc.b + tile_of(c1) * BTILE, BTILE);
                 }
                 ++issued;
             }
@@ -676,11 +726,12 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 for (int c = nc > NS ? nc - NS : 0; going && c < nc; ++c)
                     going = images(c);
             for (int c = issued > NS ? issued - NS : 0; c < issued; ++c) {
-                drain_wait(&tfull[c % NT], (c / NT) & 1);
                 drain_wait(&full[c % NS], (c / NS) & 1);
                 drain_wait(&fullv[c % NS], (c / NS) & 1);
                 drain_wait(&fullb[c % NS], (c / NS) & 1);
             }
+            for (int c = tables > NT ? tables - NT : 0; c < tables; ++c)
+                drain_wait(&tfull[c % NT], (c / NT) & 1);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -764,7 +815,9 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             return true;
         };
         auto stage_in = [&](int c) {
-            return warp_all(wait_for(&full[c % NS], (c / NS) & 1, abort_flag)) && clear_tail(c);
+            return warp_all(wait_for(&full[c % NS], (c / NS) & 1, abort_flag) &&
+                            wait_for(&fullb[c % NS], (c / NS) & 1, abort_flag)) &&
+                   clear_tail(c);
         };
         auto both = [&](uint64_t *bar, int c) {
             const bool ok = warp_all(wait_for(bar, c & 1, abort_flag));
@@ -814,8 +867,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                             mma_ts(tm + TS, tm + TD + 32 * (c & 1) + 8 * kk,
                                    d_q2 + off(lo * Q2 + kk * 2048), id128mn, 1);
                 __syncwarp();
-                if (!(ok = warp_all(wait_for(&fullb[c % NS], (c / NS) & 1, abort_flag)) &&
-                           both(y_ready, c)))
+                if (!(ok = both(y_ready, c)))
                     break;
                 if (one)
                     solve(c);
@@ -857,8 +909,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                     scores(c);
                 }
                 __syncwarp();
-                if (!warp_all(wait_for(&fullb[c % NS], (c / NS) & 1, abort_flag)) ||
-                    !both(y_ready, c))
+                if (!both(y_ready, c))
                     break;
                 if (one)
                     solve(c);
@@ -1215,7 +1266,8 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
 constexpr int GRADS = 256;
 constexpr int GQ = 0, GE = 32768, GD = 49152, GS = 81920, GBAR = 114688;
 constexpr int GW = GD, GWT = GD + 16384;        // over dO and R
-constexpr int GDYN = GBAR + 64;
+constexpr int GTAB = GBAR + 64, GDYN = GTAB + 2 * C * 4;     // beta, G / ln 2
+static_assert(TLOG == TBETA + 1 && 2 * (GDYN + 1024) <= 228 * 1024, "two CTAs an SM");
 constexpr uint32_t U1 = 0, UC = 128, UW = 128, UCOLS = 256;
 
 struct GradParams {
@@ -1293,11 +1345,12 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tm = *tslot;
     const uint32_t lanes = tm + ((uint32_t)(32 * q) << 16);
-    const float *tab = P.sc.tab + tile * TABS * C;
+    const float *betas = reinterpret_cast<const float *>(sm + GTAB), *logs = betas + C;
 
     if (tid == 0) {
         const int hq = h / a.q.hdiv, t = (int)(sq.bos + t0), row = (int)sq.row;
-        mbar_arrive_expect_tx(in_full, 3 * 16384 + 2 * ETILE + STILE);
+        mbar_arrive_expect_tx(in_full, 3 * 16384 + 2 * ETILE + STILE + 2 * C * 4);
+        bulk_load(sm + GTAB, P.sc.tab + (tile * TABS + TBETA) * C, 2 * C * 4, in_full);
         bulk_load(sm + GS, P.sc.s + tile * STILE, STILE, in_full);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -1344,7 +1397,7 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
     for (int x = 0; x < 4; ++x) {
         const int i = (tid >> 4) + 16 * x, c16 = tid & 15;
         if (i < n && 8 * c16 < a.E) {
-            const float f = tab[TBETA * C + i];
+            const float f = betas[i];
             const uint4 v = *reinterpret_cast<const uint4 *>(
                 sm + GD + (c16 >> 3) * 16384 + 8192 + i * 128 + (((c16 & 7) ^ (i & 7)) << 4));
             *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.dv.p) + sq.row * a.dv.sb +
@@ -1367,7 +1420,7 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
     __syncwarp();
     const int i = 32 * (q & 1) + lane;              // this lane's token
     const bool key = q >= 2;                        // R's lanes: dK's row part
-    const float eg = -tab[TNEG * C + i], beta = tab[TBETA * C + i];
+    const float gi = logs[i], eg = exp2_fast(gi), beta = betas[i];
     {   // W1 (W2), row i, columns 32 half .., as rows and as columns
         const int j0 = 32 * half;
         uint32_t r[32];
@@ -1380,13 +1433,13 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
             static_cast<__nv_bfloat16 *>(a.dbeta)[((sq.row * a.T) + sq.bos + t0 + i) * a.H + h] =
                 __float2bfloat16_rn(d);
         }
-        const float f = key ? -beta : a.scale, gi = tab[TLOG * C + i];
+        const float f = key ? -beta : a.scale;
         const int last = key ? i - 1 : i;
         float w[32];
 #pragma unroll
         for (int x4 = 0; x4 < 8; ++x4) {
-            const float4 b = *reinterpret_cast<const float4 *>(tab + TBETA * C + j0 + 4 * x4);
-            const float4 g = *reinterpret_cast<const float4 *>(tab + TLOG * C + j0 + 4 * x4);
+            const float4 b = *reinterpret_cast<const float4 *>(betas + j0 + 4 * x4);
+            const float4 g = *reinterpret_cast<const float4 *>(logs + j0 + 4 * x4);
             const float bb[4] = {b.x, b.y, b.z, b.w}, gg[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
@@ -1455,14 +1508,14 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
                 end = fmaf(bf16hi(u[y]), bf16hi(w[y]), end);
             }
         }
-        end *= -tab[TNEG * C + C - 1];
+        end *= exp2_fast(logs[C - 1]);
     }
     // row i of Q (K): this half's 64 channels
     const uint8_t *own = sm + GQ + half * 16384 + (key ? 8192 : 0) + i * 128;
     ok = warp_all(bwait(c_full, 0, abort_flag)) && ok;
     tc_fence_after();
     if (key) {
-        const float f = tab[TKB * C + i];
+        const float f = beta * exp2_fast(logs[C - 1] - gi);
 #pragma unroll 1
         for (int p = 0; p < 2; ++p) {
             uint32_t r[32];
