@@ -87,8 +87,8 @@ __device__ __forceinline__ Seq sequence(const int32_t *cu, int T, int n)
 // The sequence that slot belongs to (the last one whose first slot is not above).
 __device__ __forceinline__ Seq sequence_of_slot(const int32_t *cu, int T, int N, int64_t slot)
 {
-    if (!cu)
-        return sequence(nullptr, T, (int)(slot / ((T + C - 1) / C)));
+    if (!cu)    // slots of all heads together are below 2^31
+        return sequence(nullptr, T, (int)slot / ((T + C - 1) / C));
     int lo = 0, hi = N - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
@@ -115,14 +115,29 @@ __device__ __forceinline__ float gate_at(const Tok &g, int bf16, int64_t row, in
                 : static_cast<const float *>(g.p)[at];
 }
 
-// bwait, with the clock read (hundreds of cycles) only every 64th time: a chunk is
-// a dozen hand-offs one after another
+// bwait in few instructions, the clock read only every 64th time: a chunk is a dozen
+// hand-offs one after another, and a kernel that outgrows the instruction cache waits
+// for its code (0.19 MB of it: 0.62 ms a sweep at b4 h32 n8192)
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
 {
-    for (int i = 0; i < 64; ++i)
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (int i = 1;; ++i) {
         if (mbar_try_wait(bar, parity))
             return true;
-    return bwait(bar, parity, abort_flag);
+        if (i & 63)
+            continue;
+        if (*abort_flag)
+            return false;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0)
+            t0 = now;
+        if (now - t0 > TC_WAIT_NS) {
+            *abort_flag = 1;
+            atomicExch(&g_tc_error, TC_ERR_TIMEOUT);
+            return false;
+        }
+    }
 }
 
 __device__ __forceinline__ float2 mul2(float2 a, float2 b)
@@ -286,8 +301,8 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
     __shared__ __align__(16) Factor L;
     __shared__ __align__(16) float diag[4][16][DP];
     __shared__ float G[C], beta[C], part[2];
-    const int h = blockIdx.x % a.H;
-    const int64_t slot = blockIdx.x / a.H;
+    const int64_t slot = (int)blockIdx.x / a.H;
+    const int h = (int)blockIdx.x - (int)slot * a.H;
     const Seq q = sequence_of_slot(a.cu, a.T, a.N, slot);
     const int64_t t0 = (slot - q.slot) * C;
     if (t0 >= q.len)
@@ -340,7 +355,8 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
         tab[TKB * C] = kap * b;
         tab[TNGB * C] = -eg * b;
         tab[TBETA * C] = b;
-        tab[TLOG * C] = g * 1.4426950408889634f;
+        g *= 1.4426950408889634f;
+        tab[TLOG * C] = g;
         G[tid] = g;
     }
     // rows 16 warp .. of K K^T, columns up to the diagonal block
@@ -369,10 +385,10 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
             if (nb < 2 * (warp + 1)) {
                 const int j = 8 * nb + j0;
                 const float h0 = G[j], h1 = G[j + 1];
-                acc[nb][0] = j < i0 ? expf(g0 - h0) * acc[nb][0] : 0.f;
-                acc[nb][1] = j + 1 < i0 ? expf(g0 - h1) * acc[nb][1] : 0.f;
-                acc[nb][2] = j < i0 + 8 ? expf(g1 - h0) * acc[nb][2] : 0.f;
-                acc[nb][3] = j + 1 < i0 + 8 ? expf(g1 - h1) * acc[nb][3] : 0.f;
+                acc[nb][0] = j < i0 ? exp2_fast(g0 - h0) * acc[nb][0] : 0.f;
+                acc[nb][1] = j + 1 < i0 ? exp2_fast(g0 - h1) * acc[nb][1] : 0.f;
+                acc[nb][2] = j < i0 + 8 ? exp2_fast(g1 - h0) * acc[nb][2] : 0.f;
+                acc[nb][3] = j + 1 < i0 + 8 ? exp2_fast(g1 - h1) * acc[nb][3] : 0.f;
             }
         put_factor<8>(L, acc, 16 * warp, 0, nullptr);
 #pragma unroll
@@ -464,13 +480,16 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
 
 // ---- the sweeps -----------------------------------------------------------------
 //
-// 576 threads: warp 0 loads, warp 1 issues the products, warps 2-9 ("chain") carry
-// X, Eps (or W, R) and the state between products, each a quarter of the lanes and
-// half of the columns, warps 10-17 ("side") make P and O (or P and scale e^G Q).
+// 608 threads: warp 0 loads, warp 1 issues the products, warps 2-9 ("chain") carry X,
+// the state's operand and the state between products, each a quarter of the lanes and
+// half of the columns, warps 10-17 ("side") do what the chain does not wait for (P,
+// beta Eps, O; back: P, scale e^G Q, dO^T) and warp 18 sends out what they leave in
+// shared memory: as stores of these warps it would stand before the chain's own
+// accesses to shared memory and TMEM (0.1 ms of 0.5 at b4 h32 n8192).
 // Q and K of a chunk lie as one 128-row tile: [Q; K] K^T gives the scores in lanes
 // 0-63 (lanes 64-127, K K^T, are not used).
 
-constexpr int SWEEP = 576;
+constexpr int SWEEP = 608;
 constexpr int CHAIN = 256, SIDE = 256;
 constexpr int NS = 2, NT = 4;                   // stages; of the tables
 constexpr int QK = 0, VD = 32768, BB = 49152, STAGE = 65536;
@@ -479,9 +498,10 @@ constexpr int QOFF = POFF + 16384;              // backward: scale e^G Q, hi, lo
 constexpr int Q2 = 16384;                       // bytes of one of them: [2][64][64] bf16
 template <bool BWD> struct SweepLayout {
     static constexpr int SOFF = QOFF + (BWD ? 2 * Q2 : 0);     // the state's image on its way out
-    static constexpr int TOFF = SOFF + STILE;
+    static constexpr int OOFF = SOFF + STILE;                       // O on its way out
+    static constexpr int TOFF = OOFF + (BWD ? 0 : 16384);
     static constexpr int MOFF = TOFF + NT * TAB;
-    static constexpr int NBAR = 4 * NS + 2 * NT + 16;
+    static constexpr int NBAR = 4 * NS + 2 * NT + 20;
     static constexpr int SLOT = MOFF + NBAR * 8;
     static constexpr int ABORT = SLOT + 4;
     static constexpr int RANK = ABORT + 4;
@@ -502,7 +522,7 @@ __device__ __forceinline__ uint32_t tok_col(int kk, int lo)
 }
 
 struct SweepParams {
-    CUtensorMap mq, mk, mv;     // mv: v, or back: do
+    CUtensorMap mq, mk, mv, mo;     // mv: v, or back: do; mo: o, where a.o is given
     DeltaArgs a;
     Scratch sc;
 };
@@ -574,11 +594,15 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
     uint64_t *p_ready = bars + 8;       // P
     uint64_t *q_ready = bars + 9;       // Q S read out of TMEM; back: scale e^G Q
     uint64_t *r_ready = bars + 10;      // O's intra term read
-    uint64_t *d_ready = bars + 11;      // beta Eps
-    uint64_t *i_ready = bars + 12;      // the state's and Eps's (R's) images
-    uint64_t *i_free = bars + 13;       // they have been read
+    uint64_t *d_ready = bars + 11;      // beta Eps (back: R read out of TMEM)
+    uint64_t *i_ready = bars + 12;      // the state's image
+    uint64_t *i_free = bars + 13;       // it has been read
     uint64_t *td_ready = bars + 14;     // back: dO^T in TMEM
-    uint64_t *drain = bars + 15;
+    uint64_t *o_ready = bars + 15;      // O in shared memory
+    uint64_t *o_free = bars + 16;       // it has been read
+    uint64_t *e_ready = bars + 17;      // Eps's (R's) image
+    uint64_t *e_free = bars + 18;       // it has been read
+    uint64_t *drain = bars + 19;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::SLOT);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::ABORT);
     volatile int *rank_slot = reinterpret_cast<volatile int *>(sm + L::RANK);
@@ -602,8 +626,12 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         mbar_init(w_ready, CHAIN / 32);
         mbar_init(p_ready, SIDE / 64);
         mbar_init(q_ready, BWD ? SIDE / 64 : SIDE / 32);
-        mbar_init(d_ready, CHAIN / 32);
+        mbar_init(d_ready, SIDE / 32);
         mbar_init(i_ready, CHAIN / 32);
+        mbar_init(e_ready, SIDE / 32);
+        mbar_init(e_free, 1);
+        mbar_init(o_ready, SIDE / 32);
+        mbar_init(o_free, 1);
         mbar_init(i_free, 1);
         mbar_init(td_ready, SIDE / 32);
         mbar_init(r_ready, SIDE / 32);
@@ -620,6 +648,8 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         prefetch_tmap(&P.mq);
         prefetch_tmap(&P.mk);
         prefetch_tmap(&P.mv);
+        if (!BWD && a.o.p)
+            prefetch_tmap(&P.mo);
     }
     tc_fence_before();
     __syncthreads();
@@ -649,26 +679,16 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
     auto tokens = [&](int c) { return (int)min((int64_t)C, sq.len - (int64_t)chunk(c) * C); };
     auto tile_of = [&](int c) { return (sq.slot + chunk(c)) * a.H + h; };
     const float *tabs = reinterpret_cast<const float *>(sm + L::TOFF);
+    const bool keep = BWD || P.sc.s;        // the images are wanted
+    // O leaves tile by tile; the last rows of a packed sequence row by row, the rows
+    // after them are another's
+    const bool some_o = !BWD && a.o.p;
+    auto o_tile = [&](int c) { return !a.cu || tokens(c) == C; };
 
     if (warp == 0) {
         // ------------------------------------------------------------- loads
         if (lane == 0) {
             const int hq = h / a.q.hdiv;
-            uint8_t *simg = BWD ? P.sc.k : P.sc.s, *eimg = BWD ? P.sc.r : P.sc.e;
-            // The images that delta_grads starts from leave through shared memory: as
-            // stores of the chain's threads, a row each, they would take the chain's
-            // own way to shared memory (0.19 ms of 0.66 at b4 h32 n8192).  Eps (R) lies
-            // where V (dO) was, read by then.
-            auto images = [&](int c) {
-                if (!wait_for(i_ready, c & 1, abort_flag))
-                    return false;
-                bulk_store(simg + tile_of(c) * STILE, sm + L::SOFF, STILE);
-                bulk_store(eimg + tile_of(c) * ETILE, sm + (c % NS) * STAGE + VD, ETILE);
-                bulk_commit_group();
-                bulk_wait_read_all();
-                mbar_arrive(i_free);
-                return true;
-            };
             int issued = 0, tables = 0;
             bool going = true;
             auto tables_in = [&]() {
@@ -682,6 +702,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 ++tables;
                 return true;
             };
+#pragma unroll 1
             for (int c = 0; c < nc; ++c) {
                 const int s = c % NS;
                 // tables a chunk ahead, the tiles of the chunk after this into L2: its
@@ -691,8 +712,9 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 if (!going)
                     break;
                 if (c >= NS) {
-                    going = !simg || images(c - NS);
-                    if (!going || !(going = wait_for(&empty[s], (c / NS - 1) & 1, abort_flag)))
+                    // Eps's (R's) image lies where V (dO) was
+                    if (!(going = (!keep || wait_for(e_free, (c - NS) & 1, abort_flag)) &&
+                                  wait_for(&empty[s], (c / NS - 1) & 1, abort_flag)))
                         break;
                 }
                 const int t = (int)(sq.bos + (int64_t)chunk(c) * C);
@@ -722,9 +744,6 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 }
                 ++issued;
             }
-            if (simg)
-                for (int c = nc > NS ? nc - NS : 0; going && c < nc; ++c)
-                    going = images(c);
             for (int c = issued > NS ? issued - NS : 0; c < issued; ++c) {
                 drain_wait(&full[c % NS], (c / NS) & 1);
                 drain_wait(&fullv[c % NS], (c / NS) & 1);
@@ -847,8 +866,9 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 return true;
             };
             bool ok = prior(0);
+#pragma unroll 1
             for (int c = 0; ok && c < nc; ++c) {
-                if (!(ok = both(s_ready, c)))
+                if (!(ok = (c == 0 || both(d_ready, c - 1)) && both(s_ready, c)))
                     break;
                 if (one) {
                     state_times(T1, c, 64);
@@ -890,6 +910,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                     ok = prior(c + 1);
             }
         } else if (!BWD) {
+#pragma unroll 1
             for (int c = 0; c < nc; ++c) {
                 if (!stage_in(c) || !both(s_ready, c))
                     break;
@@ -940,6 +961,44 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             drain_wait(drain, 0);
         }
         __syncwarp();
+    } else if (warp == 18) {
+        // ------------------------------------------------------------ stores
+        if (lane == 0) {
+            uint8_t *simg = BWD ? P.sc.k : P.sc.s, *eimg = BWD ? P.sc.r : P.sc.e;
+#pragma unroll 1
+            for (int c = 0; c < nc; ++c) {
+                if (keep) {
+                    if (!wait_for(i_ready, c & 1, abort_flag))
+                        break;
+                    bulk_store(simg + tile_of(c) * STILE, sm + L::SOFF, STILE);
+                    bulk_commit_group();
+                    bulk_wait_read_all();
+                    mbar_arrive(i_free);
+                    if (!wait_for(e_ready, c & 1, abort_flag))
+                        break;
+                    bulk_store(eimg + tile_of(c) * ETILE, sm + (c % NS) * STAGE + VD, ETILE);
+                    bulk_commit_group();
+                    bulk_wait_read_all();
+                    mbar_arrive(e_free);
+                }
+                if (some_o) {
+                    if (!wait_for(o_ready, c & 1, abort_flag))
+                        break;
+                    if (o_tile(c)) {
+                        const int t = (int)(sq.bos + (int64_t)c * C);
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+                            if (64 * b < a.E)
+                                tma_store_4d(&P.mo, sm + L::OOFF + b * 8192, 64 * b, h, t,
+                                             (int)sq.row);
+                        bulk_commit_group();
+                        bulk_wait_read_all();
+                    }
+                    mbar_arrive(o_free);
+                }
+            }
+        }
+        __syncwarp();
     } else if (warp < 10) {
         // ------------------------------------------------------------- chain
         const int q = warp & 3, half = (warp - 2) >> 2;
@@ -948,8 +1007,19 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         const int64_t sbase = ((int64_t)sq.n * a.H + h) * a.D * a.E;
         const float *in = BWD ? a.dfin : a.init;
         float *out = BWD ? a.dinit : a.fin;
-        const bool keep = BWD || P.sc.s;
         bool ok = true;
+        if (nc > 0)
+#pragma unroll 1
+            for (int d0 = 64 * half; d0 < 64 * half + 64; d0 += 8) {
+                uint32_t r[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    r[x] = in && e < a.E && d0 + x < a.D
+                               ? __float_as_uint(in[sbase + (int64_t)(d0 + x) * a.E + e])
+                               : 0u;
+                tmem_st8(lanes + TS + d0, r);
+            }
+#pragma unroll 1
         for (int c = 0; ok && c < nc; ++c) {
             const int s = c % NS, n = tokens(c);
             const uint8_t *st = sm + s * STAGE;
@@ -961,26 +1031,16 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 break;
             tc_fence_after();
             const float2 gC = make_float2(-tab[TNEG * C + C - 1], -tab[TNEG * C + C - 1]);
-            uint32_t shi[2][16];
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const int d0 = 64 * half + 32 * p;
-                uint32_t r[32], lo[16];
-                if (c == 0) {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        r[x] = in && e < a.E && d0 + x < a.D
-                                   ? __float_as_uint(in[sbase + (int64_t)(d0 + x) * a.E + e])
-                                   : 0u;
-                } else {
-                    tmem_ld32(lanes + TS + d0, r);
-                }
+#pragma unroll 1
+            for (int d0 = 64 * half; d0 < 64 * half + 64; d0 += 32) {
+                uint32_t r[32], hi[16], lo[16];
+                tmem_ld32(lanes + TS + d0, r);
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
-                    split2(pair_of(r, x), shi[p][x], lo[x]);
+                    split2(pair_of(r, x), hi[x], lo[x]);
                     put_pair(r, x, mul2(gC, pair_of(r, x)));
                 }
-                tmem_st16_issue(lanes + TSH + d0 / 2, shi[p]);
+                tmem_st16_issue(lanes + TSH + d0 / 2, hi);
                 tmem_st16_issue(lanes + TSH + 64 + d0 / 2, lo);
                 tmem_st32_issue(lanes + TS + d0, r);
             }
@@ -992,12 +1052,21 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             if (keep) {
                 if (c > 0 && !(ok = warp_all(wait_for(i_free, (c - 1) & 1, abort_flag))))
                     break;
+                // hi, back from TMEM
                 uint8_t *to = sm + L::SOFF + half * 16384 + e * 128;
+#pragma unroll 1
+                for (int p = 0; p < 2; ++p) {
+                    uint32_t hi[16];
+                    tmem_ld16(lanes + TSH + 32 * half + 16 * p, hi);
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    *reinterpret_cast<uint4 *>(to + ((x ^ (e & 7)) << 4)) =
-                        make_uint4(shi[x >> 2][4 * (x & 3)], shi[x >> 2][4 * (x & 3) + 1],
-                                   shi[x >> 2][4 * (x & 3) + 2], shi[x >> 2][4 * (x & 3) + 3]);
+                    for (int x = 0; x < 4; ++x)
+                        *reinterpret_cast<uint4 *>(to + (((4 * p + x) ^ (e & 7)) << 4)) =
+                            make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(i_ready);
             }
             // ---- X (W)
             const int j0 = 32 * half;
@@ -1061,31 +1130,6 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(w_ready);
-            // ---- off the chain: beta Eps over this half's own columns of T1, for O
-            if constexpr (!BWD) {
-#pragma unroll
-                for (int x = 0; x < 16; ++x)
-                    split2(mul2(pair_at(TBETA, x), pair_of(r, x)), hi[x], lo[x]);
-                tmem_st16_issue(lanes + T1 + 32 * half, hi);
-                tmem_st16_issue(lanes + T1 + 32 * half + 16, lo);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(d_ready);
-            }
-            // what delta_grads starts from
-            if (keep) {
-                float x32[32];
-#pragma unroll
-                for (int x = 0; x < 32; ++x)
-                    x32[x] = __uint_as_float(r[x]);
-                store_image(x32, half, e, sm + s * STAGE + VD);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(i_ready);
-            }
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&tempty[c % NT]);
@@ -1095,13 +1139,12 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         tc_fence_after();
         if (ok && out)
 #pragma unroll 1
-            for (int p = 0; p < 2; ++p) {
-                const int d0 = 64 * half + 32 * p;
-                uint32_t r[32];
+            for (int d0 = 64 * half; d0 < 64 * half + 64; d0 += 8) {
+                uint32_t r[8];
                 if (nc > 0)
-                    tmem_ld32(lanes + TS + d0, r);
+                    tmem_ld8(lanes + TS + d0, r);
 #pragma unroll
-                for (int x = 0; x < 32; ++x)
+                for (int x = 0; x < 8; ++x)
                     if (e < a.E && d0 + x < a.D) {
                         const int64_t at = sbase + (int64_t)(d0 + x) * a.E + e;
                         out[at] = nc > 0 ? __uint_as_float(r[x]) : in ? in[at] : 0.f;
@@ -1113,6 +1156,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         const int row = 32 * q + lane;
         const uint32_t lanes = tm + ((uint32_t)(32 * q) << 16);
         const int j0 = 32 * half;
+#pragma unroll 1
         for (int c = 0; c < nc; ++c) {
             const int s = c % NS, n = tokens(c);
             const float *tab = tabs + (c % NT) * TABS * C;
@@ -1205,6 +1249,44 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 if (lane == 0)
                     mbar_arrive(td_ready);
             }
+            // ---- Eps (R): beta Eps for O, over this half's own columns; the image that
+            // delta_grads starts from
+            if (!warp_all(wait_for(e_full, c & 1, abort_flag)))
+                break;
+            tc_fence_after();
+            {
+                uint32_t r[32];
+                tmem_ld32(lanes + T1 + j0, r);
+                if constexpr (!BWD) {
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        split2(mul2(*reinterpret_cast<const float2 *>(tab + TBETA * C + j0 + 2 * x),
+                                    pair_of(r, x)),
+                               hi[x], lo[x]);
+                    // the chain has read all of Eps before it is overwritten
+                    if (!warp_all(wait_for(w_ready, c & 1, abort_flag)))
+                        break;
+                    tmem_st16_issue(lanes + T1 + 32 * half, hi);
+                    tmem_st16_issue(lanes + T1 + 32 * half + 16, lo);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(d_ready);
+                if (keep) {
+                    float x32[32];
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        x32[x] = __uint_as_float(r[x]);
+                    store_image(x32, half, row, sm + s * STAGE + VD);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(e_ready);
+                }
+            }
             if constexpr (!BWD) {
                 uint32_t inter[32], w[32];
                 tmem_ld32(lanes + T2 + j0, inter);
@@ -1230,12 +1312,24 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                     y[2 * x] = z.x;
                     y[2 * x + 1] = z.y;
                 }
-                const bool odd = lane & 1;
-                uint8_t *to = reinterpret_cast<uint8_t *>(
-                    static_cast<__nv_bfloat16 *>(a.o.p) + sq.row * a.o.sb +
-                    (sq.bos + (int64_t)c * C + j0 + odd) * a.o.st + (int64_t)h * a.o.sh +
-                    (row & ~1));
-                store_rows(y, odd, to, 4 * a.o.st, a.o.p && row < a.E ? n - j0 : 0);
+                if (some_o) {
+                    if (c > 0 && !warp_all(wait_for(o_free, (c - 1) & 1, abort_flag)))
+                        break;
+                    if (o_tile(c)) {
+                        store_image(y, half, row, sm + L::OOFF);
+                        fence_proxy_async_smem();
+                    } else {
+                        const bool odd = lane & 1;
+                        uint8_t *to = reinterpret_cast<uint8_t *>(
+                            static_cast<__nv_bfloat16 *>(a.o.p) + sq.row * a.o.sb +
+                            (sq.bos + (int64_t)c * C + j0 + odd) * a.o.st +
+                            (int64_t)h * a.o.sh + (row & ~1));
+                        store_rows(y, odd, to, 4 * a.o.st, row < a.E ? n - j0 : 0);
+                    }
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(o_ready);
+                }
             }
             __syncwarp();
             if (lane == 0)
@@ -1307,8 +1401,8 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
 {
     extern __shared__ __align__(1024) uint8_t sm[];
     const DeltaArgs &a = P.a;
-    const int h = blockIdx.x % a.H;
-    const int64_t slot = blockIdx.x / a.H;
+    const int64_t slot = (int)blockIdx.x / a.H;
+    const int h = (int)blockIdx.x - (int)slot * a.H;
     const Seq sq = sequence_of_slot(a.cu, a.T, a.N, slot);
     const int64_t t0 = (slot - sq.slot) * C;
     if (t0 >= sq.len)
@@ -1666,6 +1760,9 @@ template <bool BWD> cudaError_t sweep(const DeltaArgs &a, const Scratch &sc, cud
     SweepParams p;
     if (!token_map(&p.mq, a, a.q, a.HK, a.D) || !token_map(&p.mk, a, a.k, a.HK, a.D) ||
         !token_map(&p.mv, a, BWD ? a.d_o : a.v, a.H, a.E))
+        return cudaErrorNotSupported;
+    if (!BWD && a.o.p &&
+        !token_map(&p.mo, a, Tok{a.o.p, a.o.sb, a.o.st, a.o.sh, 1}, a.H, a.E))
         return cudaErrorNotSupported;
     p.a = a;
     p.sc = sc;
