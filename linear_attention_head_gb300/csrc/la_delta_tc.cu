@@ -501,7 +501,7 @@ template <bool BWD> struct SweepLayout {
     static constexpr int OOFF = SOFF + STILE;                       // O on its way out
     static constexpr int TOFF = OOFF + (BWD ? 0 : 16384);
     static constexpr int MOFF = TOFF + NT * TAB;
-    static constexpr int NBAR = 4 * NS + 2 * NT + 20;
+    static constexpr int NBAR = 4 * NS + 2 * NT + 21;
     static constexpr int SLOT = MOFF + NBAR * 8;
     static constexpr int ABORT = SLOT + 4;
     static constexpr int RANK = ABORT + 4;
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
     uint64_t *p_ready = bars + 8;       // P
     uint64_t *q_ready = bars + 9;       // Q S read out of TMEM; back: scale e^G Q
     uint64_t *r_ready = bars + 10;      // O's intra term read
-    uint64_t *d_ready = bars + 11;      // beta Eps (back: R read out of TMEM)
+    uint64_t *d_ready = bars + 11;      // beta Eps
     uint64_t *i_ready = bars + 12;      // the state's image
     uint64_t *i_free = bars + 13;       // it has been read
     uint64_t *td_ready = bars + 14;     // back: dO^T in TMEM
@@ -602,7 +602,8 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
     uint64_t *o_free = bars + 16;       // it has been read
     uint64_t *e_ready = bars + 17;      // Eps's (R's) image
     uint64_t *e_free = bars + 18;       // it has been read
-    uint64_t *drain = bars + 19;
+    uint64_t *x_read = bars + 19;       // Eps (R) read by the side warps
+    uint64_t *drain = bars + 20;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::SLOT);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::ABORT);
     volatile int *rank_slot = reinterpret_cast<volatile int *>(sm + L::RANK);
@@ -626,7 +627,8 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         mbar_init(w_ready, CHAIN / 32);
         mbar_init(p_ready, SIDE / 64);
         mbar_init(q_ready, BWD ? SIDE / 64 : SIDE / 32);
-        mbar_init(d_ready, SIDE / 32);
+        mbar_init(d_ready, CHAIN / 32);
+        mbar_init(x_read, SIDE / 32);
         mbar_init(i_ready, CHAIN / 32);
         mbar_init(e_ready, SIDE / 32);
         mbar_init(e_free, 1);
@@ -813,9 +815,9 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         // The tokens past a packed sequence's end are another's: zeros in their
         // place (the loads fill with zeros past the tensor's end).
         auto clear_tail = [&](int c) {
-            const int n = tokens(c);
-            if (!a.cu || n == C)
+            if (!a.cu || chunk(c) != nc - 1)
                 return true;
+            const int n = tokens(c);
             if (!warp_all(wait_for(&fullv[c % NS], (c / NS) & 1, abort_flag)))
                 return false;
             uint8_t *st = sm + (c % NS) * STAGE;
@@ -868,7 +870,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             bool ok = prior(0);
 #pragma unroll 1
             for (int c = 0; ok && c < nc; ++c) {
-                if (!(ok = (c == 0 || both(d_ready, c - 1)) && both(s_ready, c)))
+                if (!(ok = (c == 0 || both(x_read, c - 1)) && both(s_ready, c)))
                     break;
                 if (one) {
                     state_times(T1, c, 64);
@@ -909,12 +911,12 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 if (c + 1 < nc)
                     ok = prior(c + 1);
             }
-        } else if (!BWD) {
+        } else if (!BWD && nc > 0 && stage_in(0)) {
+            any = true;
 #pragma unroll 1
             for (int c = 0; c < nc; ++c) {
-                if (!stage_in(c) || !both(s_ready, c))
+                if (!both(s_ready, c))
                     break;
-                any = true;
                 if (one) {
                     state_times(T1, c, 64);
                     mma_commit(ks_full);
@@ -935,7 +937,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 if (one)
                     solve(c);
                 __syncwarp();
-                if (!both(w_ready, c))
+                if ((c + 1 < nc && !stage_in(c + 1)) || !both(w_ready, c))
                     break;
                 if (one) {
                     update(c);
@@ -1130,6 +1132,23 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(w_ready);
+            // off the chain: beta Eps over this half's own columns of T1, for O
+            if constexpr (!BWD) {
+                // r is Eps still
+#pragma unroll
+                for (int x = 0; x < 16; ++x)
+                    split2(mul2(pair_at(TBETA, x), pair_of(r, x)), hi[x], lo[x]);
+                // the side warps have read Eps, where they want it
+                if (keep && !(ok = warp_all(wait_for(x_read, c & 1, abort_flag))))
+                    break;
+                tmem_st16_issue(lanes + T1 + 32 * half, hi);
+                tmem_st16_issue(lanes + T1 + 32 * half + 16, lo);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(d_ready);
+            }
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&tempty[c % NT]);
@@ -1249,43 +1268,26 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 if (lane == 0)
                     mbar_arrive(td_ready);
             }
-            // ---- Eps (R): beta Eps for O, over this half's own columns; the image that
-            // delta_grads starts from
-            if (!warp_all(wait_for(e_full, c & 1, abort_flag)))
-                break;
-            tc_fence_after();
-            {
+            // ---- the image of Eps (R), which delta_grads starts from
+            if (keep) {
+                if (!warp_all(wait_for(e_full, c & 1, abort_flag)))
+                    break;
+                tc_fence_after();
                 uint32_t r[32];
                 tmem_ld32(lanes + T1 + j0, r);
-                if constexpr (!BWD) {
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int x = 0; x < 16; ++x)
-                        split2(mul2(*reinterpret_cast<const float2 *>(tab + TBETA * C + j0 + 2 * x),
-                                    pair_of(r, x)),
-                               hi[x], lo[x]);
-                    // the chain has read all of Eps before it is overwritten
-                    if (!warp_all(wait_for(w_ready, c & 1, abort_flag)))
-                        break;
-                    tmem_st16_issue(lanes + T1 + 32 * half, hi);
-                    tmem_st16_issue(lanes + T1 + 32 * half + 16, lo);
-                    tmem_wait_st();
-                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(d_ready);
-                if (keep) {
-                    float x32[32];
+                    mbar_arrive(x_read);
+                float x32[32];
 #pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        x32[x] = __uint_as_float(r[x]);
-                    store_image(x32, half, row, sm + s * STAGE + VD);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(e_ready);
-                }
+                for (int x = 0; x < 32; ++x)
+                    x32[x] = __uint_as_float(r[x]);
+                store_image(x32, half, row, sm + s * STAGE + VD);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(e_ready);
             }
             if constexpr (!BWD) {
                 uint32_t inter[32], w[32];
