@@ -12,9 +12,9 @@
 //     dresidual = dH,  dm = scale dH,  dgate = dm n act'(gate),  dn = dm act(gate)
 //     dw_post = sum dn x r_x,  dx = r_x (dn w_post - x r_x^2 mean(dn w_post x))
 //
-// One pass: a row lives in the registers of a group of threads (8 to 32 lanes, or a
-// CTA for long rows), as it was loaded, 16 bytes at a time; the row's sums are fp32
-// shuffles.  Bytes bound it.  The weights' gradients are summed by each thread over
+// One pass: a row lives in the registers of a group of threads, 8 channels each (8 to
+// 32 lanes, or a CTA for long rows); the row's sums are fp32 shuffles.  While a row is
+// worked on the group's next one is on its way.  Bytes bound it.  The weights' gradients are summed by each thread over
 // the rows that it takes, then over a CTA's groups, then over CTAs by a last kernel:
 // a fixed order.
 #pragma once
@@ -22,6 +22,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "la_f32x2.cuh"
 #include "la_internal.h"
 
 namespace la {
@@ -161,14 +162,14 @@ template <typename T> __device__ __forceinline__ float act(float z, int kind, fl
     return z * s;
 }
 
-// TPR threads a row (8, 16, 32, or a whole CTA of 256 or 512), NV times 8 channels
+// TPR threads a row (8, 16, 32, or a whole CTA of 128 to 512), NV times 8 channels
 // each.
 template <int TPR_, int NV_> struct Plan {
     static constexpr int TPR = TPR_, NV = NV_;
     static constexpr int CTA = TPR > 32 ? TPR : 256;
     static constexpr int GROUPS = CTA / TPR;
     static constexpr int WARPS = CTA / 32;
-    static constexpr int CHANNELS = TPR * NV * 8;
+    static constexpr int BLOCKS = 512 / CTA > 0 ? 512 / CTA : 1;    // 128 registers a thread
 };
 
 // Sums over the row's threads, in a fixed order.  turn: alternates, so that one
@@ -215,201 +216,271 @@ __device__ __forceinline__ T *at(const BlockNormArgs &a, const NormRows &x, cons
     return a.flat ? q + p.row * x.step : q + p.b * x.s[0] + p.t * x.s[1] + p.h * x.s[2];
 }
 
-template <typename T, typename PL, bool VEC>
-__global__ void __launch_bounds__(PL::CTA) block_norm_fwd_kernel(const BlockNormArgs a)
+// Pair m of eight channels as loaded.
+__device__ __forceinline__ F2 pair_of(const Raw<__nv_bfloat16> &r, int m)
 {
+    const uint32_t w = m == 0 ? r.v.x : m == 1 ? r.v.y : m == 2 ? r.v.z : r.v.w;
+    return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ F2 pair_of(const Raw<float> &r, int m)
+{
+    const float4 &f = m < 2 ? r.a : r.b;
+    return m & 1 ? f2(f.z, f.w) : f2(f.x, f.y);
+}
+template <bool VEC, typename T> __device__ __forceinline__ void store_pairs(T *p, const F2 (&x)[4], int n)
+{
+    float y[8];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const float2 u = un(x[m]);
+        y[2 * m] = u.x;
+        y[2 * m + 1] = u.y;
+    }
+    store8<VEC>(p, y, n);
+}
+__device__ __forceinline__ float sum_of(F2 x)
+{
+    const float2 u = un(x);
+    return u.x + u.y;
+}
+template <typename T> __device__ __forceinline__ F2 act2(F2 z, int kind)
+{
+    const float2 u = un(z);
+    return f2(act<T>(u.x, kind), act<T>(u.y, kind));
+}
+
+template <typename T, typename PL, bool VEC>
+__global__ void __launch_bounds__(PL::CTA, PL::BLOCKS) block_norm_fwd_kernel(const BlockNormArgs a)
+{
+    constexpr int NV = PL::NV;
     __shared__ float2 red[2][PL::WARPS];
     int turn = 0;
     const int group = threadIdx.x / PL::TPR, me = threadIdx.x % PL::TPR;
     const float inv_d = 1.f / (float)a.D;
-    float post[PL::NV][8], pre[PL::NV][8];      // this thread's channels, for all its rows
+    const bool post = a.post, pre = a.pre, gated = a.gate.p, stream = a.residual.p;
+    F2 wpost[NV][4], wpre[NV][4];       // this thread's channels, for all its rows
 #pragma unroll
-    for (int v = 0; v < PL::NV; ++v) {
+    for (int v = 0; v < NV; ++v) {
         const int c = (v * PL::TPR + me) * 8;
-        if (a.post)
-            weights8<VEC>(a.post, a.w_bf16, c, a.D - c, post[v]);
-        if (a.pre)
-            weights8<VEC>(a.pre, a.w_bf16, c, a.D - c, pre[v]);
-    }
-    for (int64_t first = (int64_t)blockIdx.x * PL::GROUPS; first < a.rows;
-         first += (int64_t)gridDim.x * PL::GROUPS) {
-        const bool live = first + group < a.rows;
-        const RowPlace p = row_place(a, live ? (unsigned)(first + group) : 0u);
-        Raw<T> x[PL::NV], g[PL::NV], r[PL::NV];
-        float h[PL::NV][8];
+        float w[8];
+        weights8<VEC>(post ? a.post : a.x.p, post ? a.w_bf16 : a.bf16, c, post ? a.D - c : 0, w);
 #pragma unroll
-        for (int v = 0; v < PL::NV; ++v) {
+        for (int m = 0; m < 4; ++m)     // the scale once and for all
+            wpost[v][m] = mul2(f2(a.scale), post ? f2(w[2 * m], w[2 * m + 1]) : f2(1.f));
+        weights8<VEC>(pre ? a.pre : a.x.p, pre ? a.w_bf16 : a.bf16, c, pre ? a.D - c : 0, w);
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            wpre[v][m] = f2(w[2 * m], w[2 * m + 1]);
+    }
+    Raw<T> x[NV], g[NV], r[NV];
+    const int64_t step = (int64_t)gridDim.x * PL::GROUPS;
+    int64_t row = (int64_t)blockIdx.x * PL::GROUPS + group;
+    auto load = [&](int64_t at_row) {
+        const bool live = at_row < a.rows;
+        const RowPlace p = row_place(a, live ? (unsigned)at_row : 0u);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
             const int c = (v * PL::TPR + me) * 8, n = live ? a.D - c : 0;
             x[v] = load8<VEC>(at<const T>(a, a.x, p) + c, n);
-            if (a.gate.p)
+            if (gated)
                 g[v] = load8<VEC>(at<const T>(a, a.gate, p) + c, n);
-            if (a.residual.p)
+            if (stream)
                 r[v] = load8<VEC>(at<const T>(a, a.residual, p) + c, n);
         }
-        float rx = 1.f;
-        if (a.post) {
-            float2 s = make_float2(0.f, 0.f);
+    };
+    load(row);
+    for (int64_t first = (int64_t)blockIdx.x * PL::GROUPS; first < a.rows; first += step) {
+        const bool live = row < a.rows;
+        const RowPlace p = row_place(a, live ? (unsigned)row : 0u);
+        F2 h[NV][4];
+        F2 sx = f2(0.f), sh = f2(0.f);
+        // n times the scale and the gate, but for the row's factor; what was loaded is
+        // free for the next row's loads then
+        F2 res[NV][4];
 #pragma unroll
-            for (int v = 0; v < PL::NV; ++v)
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    s.x = fmaf(x[v].get(i), x[v].get(i), s.x);
-            rx = rsqrtf(row_sum<PL>(s, red, turn).x * inv_d + a.eps);
-        }
-        float2 sh = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int v = 0; v < PL::NV; ++v) {
-            const int c = (v * PL::TPR + me) * 8, n = live ? a.D - c : 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float m = x[v].get(i);
-                if (a.post)
-                    m *= rx * post[v][i];
-                if (a.gate.p)
-                    m *= act<T>(g[v].get(i), a.activation);
-                m *= a.scale;
-                if (a.residual.p)
-                    m += r[v].get(i);
-                if (!VEC && i >= n)
-                    m = 0.f;
-                h[v][i] = m;
-                sh.x = fmaf(m, m, sh.x);
+            for (int m = 0; m < 4; ++m) {
+                const F2 u = pair_of(x[v], m);
+                sx = fma2(u, u, sx);
+                h[v][m] = mul2(u, wpost[v][m]);
+                if (gated)
+                    h[v][m] = mul2(h[v][m], act2<T>(pair_of(g[v], m), a.activation));
+                res[v][m] = stream ? pair_of(r[v], m) : f2(0.f);
             }
-            store8<VEC>(at<T>(a, a.h, p) + c, h[v], n);
-        }
-        if (!a.pre)
-            continue;
-        const float rh = rsqrtf(row_sum<PL>(sh, red, turn).x * inv_d + a.eps);
+        row += step;
+        if (first + step < a.rows)
+            load(row);
+        float rx = 1.f;
+        if (post)
+            rx = rsqrtf(row_sum<PL>(make_float2(sum_of(sx), 0.f), red, turn).x * inv_d + a.eps);
 #pragma unroll
-        for (int v = 0; v < PL::NV; ++v) {
+        for (int v = 0; v < NV; ++v) {
             const int c = (v * PL::TPR + me) * 8, n = live ? a.D - c : 0;
-            float y[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                y[i] = h[v][i] * rh * pre[v][i];
-            store8<VEC>(at<T>(a, a.y, p) + c, y, n);
+            for (int m = 0; m < 4; ++m) {
+                h[v][m] = fma2(h[v][m], f2(rx), res[v][m]);
+                sh = fma2(h[v][m], h[v][m], sh);
+            }
+            store_pairs<VEC>(at<T>(a, a.h, p) + c, h[v], n);
+        }
+        if (!pre)
+            continue;
+        const float rh = rsqrtf(row_sum<PL>(make_float2(sum_of(sh), 0.f), red, turn).x * inv_d +
+                                a.eps);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * PL::TPR + me) * 8, n = live ? a.D - c : 0;
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                h[v][m] = mul2(mul2(h[v][m], f2(rh)), wpre[v][m]);
+            store_pairs<VEC>(at<T>(a, a.y, p) + c, h[v], n);
         }
     }
 }
 
 template <typename T, typename PL, bool VEC>
-__global__ void __launch_bounds__(PL::CTA) block_norm_bwd_kernel(const BlockNormArgs a)
+__global__ void __launch_bounds__(PL::CTA, PL::BLOCKS) block_norm_bwd_kernel(const BlockNormArgs a)
 {
+    constexpr int NV = PL::NV;
     __shared__ float2 red[2][PL::WARPS];
     int turn = 0;
     const int group = threadIdx.x / PL::TPR, me = threadIdx.x % PL::TPR;
     const float inv_d = 1.f / (float)a.D;
-    float wpost[PL::NV][8] = {}, wpre[PL::NV][8] = {};
-    for (int64_t first = (int64_t)blockIdx.x * PL::GROUPS; first < a.rows;
-         first += (int64_t)gridDim.x * PL::GROUPS) {
-        const bool live = first + group < a.rows;
-        const RowPlace p = row_place(a, live ? (unsigned)(first + group) : 0u);
-        Raw<T> x[PL::NV], g[PL::NV], r[PL::NV], dh[PL::NV], dy[PL::NV];
+    const bool post = a.post, pre = a.pre, gated = a.gate.p, stream = a.residual.p && pre;
+    F2 wpost[NV][4], wpre[NV][4], dpost[NV][4], dpre[NV][4];
 #pragma unroll
-        for (int v = 0; v < PL::NV; ++v) {
+    for (int v = 0; v < NV; ++v) {
+        const int c = (v * PL::TPR + me) * 8;
+        float w[8];
+        weights8<VEC>(post ? a.post : a.x.p, post ? a.w_bf16 : a.bf16, c, post ? a.D - c : 0, w);
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            wpost[v][m] = post ? f2(w[2 * m], w[2 * m + 1]) : f2(1.f);
+        weights8<VEC>(pre ? a.pre : a.x.p, pre ? a.w_bf16 : a.bf16, c, pre ? a.D - c : 0, w);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            wpre[v][m] = f2(w[2 * m], w[2 * m + 1]);
+            dpost[v][m] = dpre[v][m] = f2(0.f);
+        }
+    }
+    Raw<T> x[NV], g[NV], r[NV], dh[NV], dy[NV];
+    const int64_t step = (int64_t)gridDim.x * PL::GROUPS;
+    int64_t row = (int64_t)blockIdx.x * PL::GROUPS + group;
+    auto load = [&](int64_t at_row) {
+        const bool live = at_row < a.rows;
+        const RowPlace p = row_place(a, live ? (unsigned)at_row : 0u);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
             const int c = (v * PL::TPR + me) * 8, n = live ? a.D - c : 0;
             x[v] = load8<VEC>(at<const T>(a, a.x, p) + c, n);
-            if (a.gate.p)
+            if (gated)
                 g[v] = load8<VEC>(at<const T>(a, a.gate, p) + c, n);
-            if (a.residual.p && a.pre)
+            if (stream)
                 r[v] = load8<VEC>(at<const T>(a, a.residual, p) + c, n);
             dh[v] = load8<VEC>(at<const T>(a, a.dh, p) + c, a.dh.p ? n : 0);
-            if (a.pre)
+            if (pre)
                 dy[v] = load8<VEC>(at<const T>(a, a.dy, p) + c, n);
         }
+    };
+    load(row);
+    for (int64_t first = (int64_t)blockIdx.x * PL::GROUPS; first < a.rows; first += step) {
+        const bool live = row < a.rows;
+        const RowPlace p = row_place(a, live ? (unsigned)row : 0u);
+        // x and the gate as loaded, the gate's factor made where it is wanted (twice with
+        // pre): registers are what the next row's loads need
+        Raw<T> xc[NV], gc[NV];
+        F2 d[NV][4];
         float rx = 1.f;
-        if (a.post) {
-            float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int v = 0; v < PL::NV; ++v)
+        for (int v = 0; v < NV; ++v) {
+            xc[v] = x[v];
+            gc[v] = g[v];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    s.x = fmaf(x[v].get(i), x[v].get(i), s.x);
-            rx = rsqrtf(row_sum<PL>(s, red, turn).x * inv_d + a.eps);
+            for (int m = 0; m < 4; ++m)
+                d[v][m] = pair_of(dh[v], m);
         }
-        // h again, and its two sums
-        float h[PL::NV][8], rh = 0.f, mean = 0.f;
-        if (a.pre) {
-            float2 s = make_float2(0.f, 0.f);
+        if (post) {
+            F2 sx = f2(0.f);
 #pragma unroll
-            for (int v = 0; v < PL::NV; ++v) {
-                const int c = (v * PL::TPR + me) * 8, n = live ? a.D - c : 0;
-                float w[8], u[8];
-                if (a.post)
-                    weights8<VEC>(a.post, a.w_bf16, c, n, w);
-                weights8<VEC>(a.pre, a.w_bf16, c, n, u);
+            for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float m = x[v].get(i);
-                    if (a.post)
-                        m *= rx * w[i];
-                    if (a.gate.p)
-                        m *= act<T>(g[v].get(i), a.activation);
-                    m *= a.scale;
-                    if (a.residual.p)
-                        m += r[v].get(i);
-                    if (!VEC && i >= n)
-                        m = 0.f;
-                    h[v][i] = m;
-                    s.x = fmaf(m, m, s.x);
-                    s.y = fmaf(m, dy[v].get(i) * u[i], s.y);
+                for (int m = 0; m < 4; ++m) {
+                    const F2 t = pair_of(xc[v], m);
+                    sx = fma2(t, t, sx);
                 }
-            }
-            s = row_sum<PL>(s, red, turn);
-            rh = rsqrtf(s.x * inv_d + a.eps);
-            mean = s.y * inv_d * rh * rh;
+            rx = rsqrtf(row_sum<PL>(make_float2(sum_of(sx), 0.f), red, turn).x * inv_d + a.eps);
         }
-        // h turns into dn: the gradient before the gate and the scale
-        float2 s = make_float2(0.f, 0.f);
+        if (pre) {      // h again, and its two sums
+            F2 h[NV][4], sh = f2(0.f), su = f2(0.f);
 #pragma unroll
-        for (int v = 0; v < PL::NV; ++v) {
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    h[v][m] = mul2(mul2(pair_of(xc[v], m), f2(rx * a.scale)), wpost[v][m]);
+                    if (gated)
+                        h[v][m] = mul2(h[v][m], act2<T>(pair_of(gc[v], m), a.activation));
+                    if (stream)
+                        h[v][m] = add2(h[v][m], pair_of(r[v], m));
+                    sh = fma2(h[v][m], h[v][m], sh);
+                    su = fma2(h[v][m], mul2(pair_of(dy[v], m), wpre[v][m]), su);
+                }
+            const float2 s = row_sum<PL>(make_float2(sum_of(sh), sum_of(su)), red, turn);
+            const float rh = rsqrtf(s.x * inv_d + a.eps);
+            const float mean = -s.y * inv_d * rh * rh;
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const F2 y = pair_of(dy[v], m);
+                    const F2 t = fma2(h[v][m], f2(mean), mul2(y, wpre[v][m]));
+                    d[v][m] = fma2(t, f2(rh), d[v][m]);
+                    dpre[v][m] = fma2(y, mul2(h[v][m], f2(rh)), dpre[v][m]);
+                }
+        }
+        row += step;
+        if (first + step < a.rows)
+            load(row);
+        F2 sd = f2(0.f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
             const int c = (v * PL::TPR + me) * 8, n = live ? a.D - c : 0;
-            float w[8], u[8], out[8];
-            if (a.post)
-                weights8<VEC>(a.post, a.w_bf16, c, n, w);
-            if (a.pre)
-                weights8<VEC>(a.pre, a.w_bf16, c, n, u);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float d = dh[v].get(i);
-                if (a.pre) {
-                    const float y = dy[v].get(i);
-                    d += rh * (y * u[i] - h[v][i] * mean);
-                    wpre[v][i] = fmaf(y, h[v][i] * rh, wpre[v][i]);
-                }
-                out[i] = d;
-            }
             if (a.dresidual.p)
-                store8<VEC>(at<T>(a, a.dresidual, p) + c, out, n);
+                store_pairs<VEC>(at<T>(a, a.dresidual, p) + c, d[v], n);
+            F2 dg[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float d = out[i] * a.scale;
-                const float xi = x[v].get(i);
-                if (a.gate.p) {
-                    float slope;
-                    const float f = act<T>(g[v].get(i), a.activation, slope);
-                    out[i] = d * slope * (a.post ? xi * rx * w[i] : xi);
-                    d *= f;
+            for (int m = 0; m < 4; ++m) {
+                const F2 u = mul2(pair_of(xc[v], m), f2(rx));
+                d[v][m] = mul2(d[v][m], f2(a.scale));
+                if (gated) {
+                    const float2 z = un(pair_of(gc[v], m));
+                    float s0, s1;
+                    const float f0 = act<T>(z.x, a.activation, s0);
+                    const float f1 = act<T>(z.y, a.activation, s1);
+                    dg[m] = mul2(mul2(d[v][m], f2(s0, s1)), mul2(u, wpost[v][m]));
+                    d[v][m] = mul2(d[v][m], f2(f0, f1));
                 }
-                if (a.post) {
-                    wpost[v][i] = fmaf(d, xi * rx, wpost[v][i]);
-                    d *= w[i];
-                    s.x = fmaf(d, xi, s.x);
+                if (post) {
+                    dpost[v][m] = fma2(d[v][m], u, dpost[v][m]);
+                    d[v][m] = mul2(d[v][m], wpost[v][m]);
+                    sd = fma2(d[v][m], u, sd);
                 }
-                h[v][i] = d;
             }
-            if (a.gate.p)
-                store8<VEC>(at<T>(a, a.dgate, p) + c, out, n);
+            if (gated)
+                store_pairs<VEC>(at<T>(a, a.dgate, p) + c, dg, n);
         }
-        const float mx = a.post ? row_sum<PL>(s, red, turn).x * inv_d * rx * rx : 0.f;
+        if (post) {
+            const float mean = -row_sum<PL>(make_float2(sum_of(sd), 0.f), red, turn).x * inv_d * rx;
 #pragma unroll
-        for (int v = 0; v < PL::NV; ++v) {
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    d[v][m] = mul2(fma2(pair_of(xc[v], m), f2(mean), d[v][m]), f2(rx));
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
             const int c = (v * PL::TPR + me) * 8, n = live ? a.D - c : 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (a.post)
-                    h[v][i] = rx * (h[v][i] - x[v].get(i) * mx);
-            store8<VEC>(at<T>(a, a.dx, p) + c, h[v], n);
+            store_pairs<VEC>(at<T>(a, a.dx, p) + c, d[v], n);
         }
     }
     // this CTA's part of the weights' gradients, [2][D]
@@ -419,19 +490,26 @@ __global__ void __launch_bounds__(PL::CTA) block_norm_bwd_kernel(const BlockNorm
             continue;
         float *to = a.partial + ((int64_t)blockIdx.x * 2 + which) * a.D;
 #pragma unroll
-        for (int v = 0; v < PL::NV; ++v) {
+        for (int v = 0; v < NV; ++v) {
             const int c0 = v * PL::TPR * 8;
+            float w[8];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const float2 t = un(which ? dpre[v][m] : dpost[v][m]);
+                w[2 * m] = t.x;
+                w[2 * m + 1] = t.y;
+            }
             if (PL::GROUPS == 1) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (c0 + me * 8 + i < a.D)
-                        to[c0 + me * 8 + i] = which ? wpre[v][i] : wpost[v][i];
+                        to[c0 + me * 8 + i] = w[i];
                 continue;
             }
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                sums[group][me * 8 + i] = which ? wpre[v][i] : wpost[v][i];
+                sums[group][me * 8 + i] = w[i];
             __syncthreads();
             for (int c = threadIdx.x; c < PL::TPR * 8; c += PL::CTA) {
                 float t = 0.f;
@@ -475,9 +553,8 @@ cudaError_t norm_by_access(const BlockNormArgs &a, bool vec, int sms, cudaStream
                    : norm_launch<PL>(block_norm_fwd_kernel<T, PL, false>, a, sms, s, ctas);
 }
 
-// The fewest threads that hold a row at 8 to 32 channels each: several rows a warp
-// where rows are short, a CTA a row where a warp would hold more than 32 channels a
-// lane (spills in the backward, and too few bytes in flight with few rows).
+// Eight channels a thread: several rows a warp where rows are short, a CTA a row where
+// they are longer than a warp's 256 channels.  (More channels a thread above 4096.)
 template <bool BWD, typename T>
 cudaError_t norm_by_width(const BlockNormArgs &a, bool vec, int sms, cudaStream_t s, int *ctas)
 {
@@ -488,12 +565,12 @@ cudaError_t norm_by_width(const BlockNormArgs &a, bool vec, int sms, cudaStream_
         return norm_by_access<BWD, T, Plan<16, 1>>(a, vec, sms, s, ctas);
     if (chunks <= 32)
         return norm_by_access<BWD, T, Plan<32, 1>>(a, vec, sms, s, ctas);
-    if (chunks <= 64)
-        return norm_by_access<BWD, T, Plan<32, 2>>(a, vec, sms, s, ctas);
+    if (chunks <= 128)
+        return norm_by_access<BWD, T, Plan<128, 1>>(a, vec, sms, s, ctas);
     if (chunks <= 256)
         return norm_by_access<BWD, T, Plan<256, 1>>(a, vec, sms, s, ctas);
     if (chunks <= 512)
-        return norm_by_access<BWD, T, Plan<256, 2>>(a, vec, sms, s, ctas);
+        return norm_by_access<BWD, T, Plan<512, 1>>(a, vec, sms, s, ctas);
     if (chunks <= 1024)
         return norm_by_access<BWD, T, Plan<512, 2>>(a, vec, sms, s, ctas);
     return norm_by_access<BWD, T, Plan<512, 4>>(a, vec, sms, s, ctas);
