@@ -8,12 +8,14 @@
 namespace la {
 namespace {
 
-// dw[c] = sum over the CTAs' parts, a warp a channel group of 32, 8 warps sharing the
-// CTAs, joined in order.
-__global__ void __launch_bounds__(256) weights_sum_kernel(const float *partial, int ctas, int D,
-                                                          void *post, void *pre, int bf16)
+// dw[c] = sum over the CTAs' parts: 32 channels a CTA, 16 warps sharing the parts,
+// joined in order.
+constexpr int SUM_WARPS = 16;
+__global__ void __launch_bounds__(32 * SUM_WARPS) weights_sum_kernel(const float *partial, int ctas,
+                                                                    int D, void *post, void *pre,
+                                                                    int bf16)
 {
-    __shared__ float part[8][32];
+    __shared__ float part[SUM_WARPS][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int which = blockIdx.y, c = blockIdx.x * 32 + lane;
     void *out = which ? pre : post;
@@ -21,7 +23,8 @@ __global__ void __launch_bounds__(256) weights_sum_kernel(const float *partial, 
         return;
     float s = 0.f;
     if (c < D)
-        for (int k = w; k < ctas; k += 8)
+#pragma unroll 8
+        for (int k = w; k < ctas; k += SUM_WARPS)
             s += partial[((int64_t)k * 2 + which) * D + c];
     part[w][lane] = s;
     __syncthreads();
@@ -29,7 +32,7 @@ __global__ void __launch_bounds__(256) weights_sum_kernel(const float *partial, 
         return;
     s = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < SUM_WARPS; ++k)
         s += part[k][lane];
     if (bf16)
         static_cast<__nv_bfloat16 *>(out)[c] = __float2bfloat16_rn(s);
@@ -97,7 +100,7 @@ cudaError_t block_norm_run(bool back, const BlockNormArgs &args, cudaStream_t s)
                : block_norm_bwd_f32(a, vec, sms, s, &ctas);
     if (e != cudaSuccess || !(a.dpost || a.dpre))
         return e;
-    weights_sum_kernel<<<dim3((unsigned)(a.D + 31) / 32, 2), 256, 0, s>>>(
+    weights_sum_kernel<<<dim3((unsigned)(a.D + 31) / 32, 2), 32 * SUM_WARPS, 0, s>>>(
         a.partial, ctas, a.D, a.dpost, a.dpre, a.w_bf16);
     note_launch();
     return cudaGetLastError();

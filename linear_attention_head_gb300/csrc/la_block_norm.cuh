@@ -14,7 +14,9 @@
 //
 // One pass: a row lives in the registers of a group of threads, 8 channels each (8 to
 // 32 lanes, or a CTA for long rows); the row's sums are fp32 shuffles.  While a row is
-// worked on the group's next one is on its way.  Bytes bound it.  The weights' gradients are summed by each thread over
+// worked on the group's next two are on their way: aligned rows by asynchronous copies
+// into places of shared memory that the thread that asks for them reads alone, so that
+// no barrier stands between.  Bytes bound it.  The weights' gradients are summed by each thread over
 // the rows that it takes, then over a CTA's groups, then over CTAs by a last kernel:
 // a fixed order.
 #pragma once
@@ -169,7 +171,8 @@ template <int TPR_, int NV_> struct Plan {
     static constexpr int CTA = TPR > 32 ? TPR : 256;
     static constexpr int GROUPS = CTA / TPR;
     static constexpr int WARPS = CTA / 32;
-    static constexpr int BLOCKS = 512 / CTA > 0 ? 512 / CTA : 1;    // 128 registers a thread
+    // CTAs an SM at 128 registers a thread, and at 64 (the forward's are enough there)
+    static constexpr int BLOCKS = 512 / CTA, FWD_BLOCKS = NV == 1 ? 1024 / CTA : 512 / CTA;
 };
 
 // Sums over the row's threads, in a fixed order.  turn: alternates, so that one
@@ -196,6 +199,49 @@ __device__ __forceinline__ float2 row_sum(float2 x, float2 (*red)[PL::WARPS], in
         }
     }
     return x;
+}
+
+// The rows on their way: K tensors, NV times 8 channels a thread, AHEAD rows beside
+// the one worked on: two, or one where two would take more than 128 KB, or (AHEAD 0,
+// as for rows that are not aligned) the next one in registers.
+template <typename T, typename PL, bool VEC, int K> struct Ring {
+    static constexpr int UNITS = sizeof(Raw<T>) / 16;   // of 16 bytes
+    static constexpr int ROW = K * PL::NV * UNITS * PL::CTA * 16;
+    static constexpr int AHEAD = !VEC || 2 * ROW > 224 * 1024 ? 0 : 3 * ROW > 128 * 1024 ? 1 : 2;
+    static constexpr size_t BYTES = AHEAD ? (size_t)(AHEAD + 1) * ROW : 0;
+    // unit u of tensor k, part v in slot s: a thread's units lie CTA apart, so that
+    // neighbours' are neighbours
+    static __device__ __forceinline__ uint4 *place(uint4 *ring, int s, int k, int v, int u)
+    {
+        return ring + (((s * K + k) * PL::NV + v) * UNITS + u) * PL::CTA + threadIdx.x;
+    }
+    // n: channels left of the row; none: zeros
+    static __device__ __forceinline__ void ask(uint4 *ring, int s, int k, int v, const T *p, int n)
+    {
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            const uint32_t to = (uint32_t)__cvta_generic_to_shared(place(ring, s, k, v, u));
+            const int bytes = n > 0 ? 16 : 0;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                         "l"(reinterpret_cast<const char *>(p) + 16 * u), "r"(bytes)
+                         : "memory");
+        }
+    }
+    static __device__ __forceinline__ Raw<T> get(uint4 *ring, int s, int k, int v)
+    {
+        Raw<T> r;
+        uint4 *w = reinterpret_cast<uint4 *>(&r);
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u)
+            w[u] = *place(ring, s, k, v, u);
+        return r;
+    }
+};
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// until all but the youngest `younger` rows asked for are there
+template <int younger> __device__ __forceinline__ void ring_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(younger) : "memory");
 }
 
 struct RowPlace {
@@ -250,7 +296,7 @@ template <typename T> __device__ __forceinline__ F2 act2(F2 z, int kind)
 }
 
 template <typename T, typename PL, bool VEC>
-__global__ void __launch_bounds__(PL::CTA, PL::BLOCKS) block_norm_fwd_kernel(const BlockNormArgs a)
+__global__ void __launch_bounds__(PL::CTA, PL::FWD_BLOCKS) block_norm_fwd_kernel(const BlockNormArgs a)
 {
     constexpr int NV = PL::NV;
     __shared__ float2 red[2][PL::WARPS];
@@ -275,25 +321,55 @@ __global__ void __launch_bounds__(PL::CTA, PL::BLOCKS) block_norm_fwd_kernel(con
     Raw<T> x[NV], g[NV], r[NV];
     const int64_t step = (int64_t)gridDim.x * PL::GROUPS;
     int64_t row = (int64_t)blockIdx.x * PL::GROUPS + group;
-    auto load = [&](int64_t at_row) {
+    using R = Ring<T, PL, VEC, 3>;
+    constexpr int AHEAD = R::AHEAD;
+    extern __shared__ uint4 ring[];
+    int slot = 0, ahead = AHEAD;        // slots of the row worked on, and of the one asked for
+    auto load = [&](int64_t at_row, int s) {
         const bool live = at_row < a.rows;
         const RowPlace p = row_place(a, live ? (unsigned)at_row : 0u);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * PL::TPR + me) * 8, n = live ? a.D - c : 0;
-            x[v] = load8<VEC>(at<const T>(a, a.x, p) + c, n);
-            if (gated)
-                g[v] = load8<VEC>(at<const T>(a, a.gate, p) + c, n);
-            if (stream)
-                r[v] = load8<VEC>(at<const T>(a, a.residual, p) + c, n);
+            // past the row's end an address that is there
+            const int cc = n > 0 ? c : 0;
+            if constexpr (AHEAD > 0) {
+                R::ask(ring, s, 0, v, at<const T>(a, a.x, p) + cc, n);
+                if (gated)
+                    R::ask(ring, s, 1, v, at<const T>(a, a.gate, p) + cc, n);
+                if (stream)
+                    R::ask(ring, s, 2, v, at<const T>(a, a.residual, p) + cc, n);
+            } else {
+                x[v] = load8<VEC>(at<const T>(a, a.x, p) + c, n);
+                if (gated)
+                    g[v] = load8<VEC>(at<const T>(a, a.gate, p) + c, n);
+                if (stream)
+                    r[v] = load8<VEC>(at<const T>(a, a.residual, p) + c, n);
+            }
         }
+        if constexpr (AHEAD > 0)
+            ring_commit();
     };
-    load(row);
+    load(row, 0);
+    if constexpr (AHEAD > 1)
+        load(row + step, 1);
     for (int64_t first = (int64_t)blockIdx.x * PL::GROUPS; first < a.rows; first += step) {
         const bool live = row < a.rows;
         const RowPlace p = row_place(a, live ? (unsigned)row : 0u);
         F2 h[NV][4];
         F2 sx = f2(0.f), sh = f2(0.f);
+        if constexpr (AHEAD > 0) {
+            ring_wait<AHEAD - 1>();
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                x[v] = R::get(ring, slot, 0, v);
+                g[v] = R::get(ring, slot, 1, v);
+                r[v] = R::get(ring, slot, 2, v);
+            }
+            load(row + AHEAD * step, ahead);
+            slot = slot == AHEAD ? 0 : slot + 1;
+            ahead = ahead == AHEAD ? 0 : ahead + 1;
+        }
         // n times the scale and the gate, but for the row's factor; what was loaded is
         // free for the next row's loads then
         F2 res[NV][4];
@@ -309,8 +385,8 @@ __global__ void __launch_bounds__(PL::CTA, PL::BLOCKS) block_norm_fwd_kernel(con
                 res[v][m] = stream ? pair_of(r[v], m) : f2(0.f);
             }
         row += step;
-        if (first + step < a.rows)
-            load(row);
+        if (AHEAD == 0 && first + step < a.rows)
+            load(row, 0);
         float rx = 1.f;
         if (post)
             rx = rsqrtf(row_sum<PL>(make_float2(sum_of(sx), 0.f), red, turn).x * inv_d + a.eps);
@@ -367,23 +443,44 @@ __global__ void __launch_bounds__(PL::CTA, PL::BLOCKS) block_norm_bwd_kernel(con
     Raw<T> x[NV], g[NV], r[NV], dh[NV], dy[NV];
     const int64_t step = (int64_t)gridDim.x * PL::GROUPS;
     int64_t row = (int64_t)blockIdx.x * PL::GROUPS + group;
-    auto load = [&](int64_t at_row) {
+    using R = Ring<T, PL, VEC, 5>;
+    constexpr int AHEAD = R::AHEAD;
+    extern __shared__ uint4 ring[];
+    int slot = 0, ahead = AHEAD;
+    auto load = [&](int64_t at_row, int s) {
         const bool live = at_row < a.rows;
         const RowPlace p = row_place(a, live ? (unsigned)at_row : 0u);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * PL::TPR + me) * 8, n = live ? a.D - c : 0;
-            x[v] = load8<VEC>(at<const T>(a, a.x, p) + c, n);
-            if (gated)
-                g[v] = load8<VEC>(at<const T>(a, a.gate, p) + c, n);
-            if (stream)
-                r[v] = load8<VEC>(at<const T>(a, a.residual, p) + c, n);
-            dh[v] = load8<VEC>(at<const T>(a, a.dh, p) + c, a.dh.p ? n : 0);
-            if (pre)
-                dy[v] = load8<VEC>(at<const T>(a, a.dy, p) + c, n);
+            const int cc = n > 0 ? c : 0;
+            if constexpr (AHEAD > 0) {
+                R::ask(ring, s, 0, v, at<const T>(a, a.x, p) + cc, n);
+                if (gated)
+                    R::ask(ring, s, 1, v, at<const T>(a, a.gate, p) + cc, n);
+                if (stream)
+                    R::ask(ring, s, 2, v, at<const T>(a, a.residual, p) + cc, n);
+                if (a.dh.p)
+                    R::ask(ring, s, 3, v, at<const T>(a, a.dh, p) + cc, n);
+                if (pre)
+                    R::ask(ring, s, 4, v, at<const T>(a, a.dy, p) + cc, n);
+            } else {
+                x[v] = load8<VEC>(at<const T>(a, a.x, p) + c, n);
+                if (gated)
+                    g[v] = load8<VEC>(at<const T>(a, a.gate, p) + c, n);
+                if (stream)
+                    r[v] = load8<VEC>(at<const T>(a, a.residual, p) + c, n);
+                dh[v] = load8<VEC>(at<const T>(a, a.dh, p) + c, a.dh.p ? n : 0);
+                if (pre)
+                    dy[v] = load8<VEC>(at<const T>(a, a.dy, p) + c, n);
+            }
         }
+        if constexpr (AHEAD > 0)
+            ring_commit();
     };
-    load(row);
+    load(row, 0);
+    if constexpr (AHEAD > 1)
+        load(row + step, 1);
     for (int64_t first = (int64_t)blockIdx.x * PL::GROUPS; first < a.rows; first += step) {
         const bool live = row < a.rows;
         const RowPlace p = row_place(a, live ? (unsigned)row : 0u);
@@ -392,6 +489,20 @@ __global__ void __launch_bounds__(PL::CTA, PL::BLOCKS) block_norm_bwd_kernel(con
         Raw<T> xc[NV], gc[NV];
         F2 d[NV][4];
         float rx = 1.f;
+        if constexpr (AHEAD > 0) {
+            ring_wait<AHEAD - 1>();
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                x[v] = R::get(ring, slot, 0, v);
+                g[v] = R::get(ring, slot, 1, v);
+                r[v] = R::get(ring, slot, 2, v);
+                dh[v] = a.dh.p ? R::get(ring, slot, 3, v) : Raw<T>{};
+                dy[v] = R::get(ring, slot, 4, v);
+            }
+            load(row + AHEAD * step, ahead);
+            slot = slot == AHEAD ? 0 : slot + 1;
+            ahead = ahead == AHEAD ? 0 : ahead + 1;
+        }
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             xc[v] = x[v];
@@ -439,8 +550,8 @@ __global__ void __launch_bounds__(PL::CTA, PL::BLOCKS) block_norm_bwd_kernel(con
                 }
         }
         row += step;
-        if (first + step < a.rows)
-            load(row);
+        if (AHEAD == 0 && first + step < a.rows)
+            load(row, 0);
         F2 sd = f2(0.f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -525,10 +636,15 @@ __global__ void __launch_bounds__(PL::CTA, PL::BLOCKS) block_norm_bwd_kernel(con
 // Rows a CTA takes at once, and the CTAs that one wave holds; a CTA more than there
 // are rows for is not launched.
 template <typename PL, typename K>
-cudaError_t norm_launch(K kernel, const BlockNormArgs &a, int sms, cudaStream_t s, int *ctas)
+cudaError_t norm_launch(K kernel, size_t ring, const BlockNormArgs &a, int sms, cudaStream_t s,
+                        int *ctas)
 {
     int per_sm = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, PL::CTA, 0);
+    cudaError_t e = ring > 0 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                    (int)ring)
+                             : cudaSuccess;
+    if (e == cudaSuccess)
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, PL::CTA, ring);
     if (e != cudaSuccess)
         return e;
     const int64_t want = (a.rows + PL::GROUPS - 1) / PL::GROUPS;
@@ -537,7 +653,7 @@ cudaError_t norm_launch(K kernel, const BlockNormArgs &a, int sms, cudaStream_t 
     if (n > NORM_MOST_CTAS && (a.dpost || a.dpre))
         n = NORM_MOST_CTAS;
     *ctas = (int)n;
-    kernel<<<(unsigned)n, PL::CTA, 0, s>>>(a);
+    kernel<<<(unsigned)n, PL::CTA, ring, s>>>(a);
     note_launch();
     return cudaGetLastError();
 }
@@ -546,11 +662,13 @@ template <bool BWD, typename T, typename PL>
 cudaError_t norm_by_access(const BlockNormArgs &a, bool vec, int sms, cudaStream_t s, int *ctas)
 {
     if constexpr (BWD)
-        return vec ? norm_launch<PL>(block_norm_bwd_kernel<T, PL, true>, a, sms, s, ctas)
-                   : norm_launch<PL>(block_norm_bwd_kernel<T, PL, false>, a, sms, s, ctas);
+        return vec ? norm_launch<PL>(block_norm_bwd_kernel<T, PL, true>,
+                                     Ring<T, PL, true, 5>::BYTES, a, sms, s, ctas)
+                   : norm_launch<PL>(block_norm_bwd_kernel<T, PL, false>, 0, a, sms, s, ctas);
     else
-        return vec ? norm_launch<PL>(block_norm_fwd_kernel<T, PL, true>, a, sms, s, ctas)
-                   : norm_launch<PL>(block_norm_fwd_kernel<T, PL, false>, a, sms, s, ctas);
+        return vec ? norm_launch<PL>(block_norm_fwd_kernel<T, PL, true>,
+                                     Ring<T, PL, true, 3>::BYTES, a, sms, s, ctas)
+                   : norm_launch<PL>(block_norm_fwd_kernel<T, PL, false>, 0, a, sms, s, ctas);
 }
 
 // Eight channels a thread: several rows a warp where rows are short, a CTA a row where
