@@ -25,6 +25,11 @@
 //   delta_sweep    <false>: the forward, a CTA a (sequence, head), chunk by chunk
 //                  <true>: the backward's K', from the last chunk to the first
 //   delta_grads    dQ, dK, dg, dbeta, all chunks in parallel
+// and where (sequence, head) pairs are few, long sequences in segments that run at
+// once: S' = Phi S + H over a segment, Phi (D x D) and H by sweeps without outputs that
+// start from the identity without values and from zero, then a scan over the segments
+// (delta_scan) and the sweeps proper from the states that it gives.  Back the same with
+// Phi^T, which the forward's sweeps have left.
 //
 // The sweeps work transposed: the 128 TMEM lanes are the value channels, the
 // columns tokens or key channels.  So S^T, X^T, Eps^T come out of one product and
@@ -105,6 +110,8 @@ struct Scratch {
     float *tab;         // [slot][H][TABS][64]
     uint8_t *s, *e;     // [slot][H] STILE, ETILE (kept for the backward; or null)
     uint8_t *k, *r;     // backward: [slot][H] STILE, ETILE
+    // segments: [N segs][H][D][D], and [N segs][H][D][E] each: Phi, H, entering states
+    float *phi, *own, *enter;
     float *dqp, *dkp;   // backward, shared heads: [B][T][H][D] fp32
 };
 
@@ -525,6 +532,8 @@ struct SweepParams {
     CUtensorMap mq, mk, mv, mo;     // mv: v, or back: do; mo: o, where a.o is given
     DeltaArgs a;
     Scratch sc;
+    int segs, seg_len;  // segments of a sequence (1: whole), their tokens: whole chunks
+    int states;         // the states alone, of a segment from zero, and (forward) Phi
 };
 
 // 32 values a lane (this lane's channel, 32 tokens) to bf16 rows, a token a row:
@@ -618,7 +627,8 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         }
         for (int i = 0; i < NT; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], CHAIN / 32 + SIDE / 32);
+            // the forward's side warps have nothing to do for the states alone
+            mbar_init(&tempty[i], CHAIN / 32 + (!BWD && P.states ? 0 : SIDE / 32));
         }
         for (int i = 0; i < 5; ++i)
             mbar_init(&bars[i], 1);
@@ -658,9 +668,12 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tm = *tslot;
     const int h = blockIdx.x % a.H;
+    const bool states = P.states;
+    // Phi's sweep: no values, from the identity, D columns
+    const bool phi = !BWD && states && blockIdx.y == 1;
     // packed sequences the longest first: a late long one would run alone.  Each
-    // CTA counts for itself which it is (N * N compares over 448 threads).
-    if (a.cu && a.N > 1 && a.N <= 256) {
+    // CTA counts for itself which it is (N * N compares over 608 threads).
+    if (a.cu && a.N > 1 && a.N <= 256 && P.segs == 1) {
         const int rank = blockIdx.x / a.H;
         for (int n = threadIdx.x; n < a.N; n += SWEEP) {
             const int len = a.cu[n + 1] - a.cu[n];
@@ -674,17 +687,33 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         }
         __syncthreads();
     }
-    const Seq sq = sequence(a.cu, a.T, *rank_slot);
-    const int nc = (int)((sq.len + C - 1) / C);
+    const int seg = *rank_slot % P.segs;
+    Seq sq = sequence(a.cu, a.T, *rank_slot / P.segs);
+    // whether the sequence's state leaves this segment (back: its first one)
+    bool last = true;
+    if (P.segs > 1) {
+        const int64_t from = (int64_t)seg * P.seg_len;
+        last = BWD ? seg == 0 : from + P.seg_len >= sq.len;
+        // nothing to do: past the end (segment 0 carries an empty sequence's state on),
+        // or a state that no segment takes (the last Phi is the backward's)
+        if ((seg > 0 && from >= sq.len) || (states && last && !(phi && P.sc.s)))
+            sq.len = -1;
+        else
+            sq.len = min(sq.len - from, (int64_t)P.seg_len);
+        sq.bos += from;
+        sq.slot += from / C;
+    }
+    const bool idle = sq.len < 0;
+    const int nc = idle ? 0 : (int)((sq.len + C - 1) / C);
     // c counts chunks in the order of the sweep
     auto chunk = [&](int c) { return BWD ? nc - 1 - c : c; };
     auto tokens = [&](int c) { return (int)min((int64_t)C, sq.len - (int64_t)chunk(c) * C); };
     auto tile_of = [&](int c) { return (sq.slot + chunk(c)) * a.H + h; };
     const float *tabs = reinterpret_cast<const float *>(sm + L::TOFF);
-    const bool keep = BWD || P.sc.s;        // the images are wanted
+    const bool keep = !states && (BWD || P.sc.s);   // the images are wanted
     // O leaves tile by tile; the last rows of a packed sequence row by row, the rows
     // after them are another's
-    const bool some_o = !BWD && a.o.p;
+    const bool some_o = !BWD && a.o.p && !states;
     auto o_tile = [&](int c) { return !a.cu || tokens(c) == C; };
 
     if (warp == 0) {
@@ -870,7 +899,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             bool ok = prior(0);
 #pragma unroll 1
             for (int c = 0; ok && c < nc; ++c) {
-                if (!(ok = (c == 0 || both(x_read, c - 1)) && both(s_ready, c)))
+                if (!(ok = (c == 0 || !keep || both(x_read, c - 1)) && both(s_ready, c)))
                     break;
                 if (one) {
                     state_times(T1, c, 64);
@@ -925,13 +954,15 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 // what the chain does not wait for goes between its products, while its
                 // warps work: Q S and the scores while X is made, O's intra term while
                 // S is
-                if (c > 0 && (!both(q_ready, c - 1) || !both(r_ready, c - 1)))
-                    break;
-                if (one) {
-                    state_times(T2, c, 0);
-                    scores(c);
+                if (!states) {
+                    if (c > 0 && (!both(q_ready, c - 1) || !both(r_ready, c - 1)))
+                        break;
+                    if (one) {
+                        state_times(T2, c, 0);
+                        scores(c);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
                 if (!both(y_ready, c))
                     break;
                 if (one)
@@ -944,6 +975,8 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                     mma_commit(&empty[c % NS]);
                 }
                 __syncwarp();
+                if (states)
+                    continue;
                 if (!both(p_ready, c) || !both(d_ready, c))
                     break;
                 if (one) {  // (beta Eps)^T P^T; beta Eps lies in T1, as tok_col
@@ -1006,9 +1039,26 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         const int q = warp & 3, half = (warp - 2) >> 2;
         const int e = 32 * q + lane;
         const uint32_t lanes = tm + ((uint32_t)(32 * q) << 16);
-        const int64_t sbase = ((int64_t)sq.n * a.H + h) * a.D * a.E;
+        // states [.][H][D][E], of sequences or of segments (Phi: [.][H][D][D])
+        const int E = phi ? a.D : a.E;
+        const int64_t one_state = (int64_t)a.D * E;
+        const int64_t at_seq = ((int64_t)sq.n * a.H + h) * one_state;
+        const int64_t at_seg = ((int64_t)blockIdx.x / a.H * a.H + h) * one_state;
         const float *in = BWD ? a.dfin : a.init;
         float *out = BWD ? a.dinit : a.fin;
+        if (in)
+            in += at_seq;
+        if (out)
+            out += at_seq;
+        if (states) {
+            in = nullptr;
+            out = (phi ? P.sc.phi : P.sc.own) + at_seg;
+        } else if (P.segs > 1) {
+            in = P.sc.enter + at_seg;
+            out = last ? out : nullptr;
+        }
+        if (idle)
+            out = nullptr;
         bool ok = true;
         if (nc > 0)
 #pragma unroll 1
@@ -1016,9 +1066,9 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 uint32_t r[8];
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
-                    r[x] = in && e < a.E && d0 + x < a.D
-                               ? __float_as_uint(in[sbase + (int64_t)(d0 + x) * a.E + e])
-                               : 0u;
+                    r[x] = in && e < E && d0 + x < a.D
+                               ? __float_as_uint(in[(int64_t)(d0 + x) * E + e])
+                               : phi && e == d0 + x && e < a.D ? __float_as_uint(1.f) : 0u;
                 tmem_st8(lanes + TS + d0, r);
             }
 #pragma unroll 1
@@ -1081,6 +1131,10 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 if (!(ok = warp_all(wait_for(&fullv[s], (c / NS) & 1, abort_flag))))
                     break;
                 channel(st + VD, e, half, v);
+                if (phi)
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        v[x] = 0u;
             }
             if (!(ok = warp_all(wait_for(ks_full, c & 1, abort_flag))))
                 break;
@@ -1133,7 +1187,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             if (lane == 0)
                 mbar_arrive(w_ready);
             // off the chain: beta Eps over this half's own columns of T1, for O
-            if constexpr (!BWD) {
+            if (!BWD && !states) {
                 // r is Eps still
 #pragma unroll
                 for (int x = 0; x < 16; ++x)
@@ -1164,8 +1218,8 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                     tmem_ld8(lanes + TS + d0, r);
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
-                    if (e < a.E && d0 + x < a.D) {
-                        const int64_t at = sbase + (int64_t)(d0 + x) * a.E + e;
+                    if (e < E && d0 + x < a.D) {
+                        const int64_t at = (int64_t)(d0 + x) * E + e;
                         out[at] = nc > 0 ? __uint_as_float(r[x]) : in ? in[at] : 0.f;
                     }
             }
@@ -1175,8 +1229,9 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         const int row = 32 * q + lane;
         const uint32_t lanes = tm + ((uint32_t)(32 * q) << 16);
         const int j0 = 32 * half;
+        const int todo = !BWD && states ? 0 : nc;
 #pragma unroll 1
-        for (int c = 0; c < nc; ++c) {
+        for (int c = 0; c < todo; ++c) {
             const int s = c % NS, n = tokens(c);
             const float *tab = tabs + (c % NT) * TABS * C;
             if (!warp_all(wait_for(&tfull[c % NT], (c / NT) & 1, abort_flag)) ||
@@ -1730,7 +1785,86 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
     }
 }
 
+// ---- scan over segments -------------------------------------------------------------
+//
+// The states that enter a sequence's segments: S_0 the initial state, S_j+1 = Phi_j S_j +
+// H_j; back K'_last = dL/dfinal, K'_j-1 = Phi_j^T K'_j + H_j.  A CTA takes 8 columns of a
+// (sequence, head)'s state, two threads a row, in fp32.
+constexpr int SCAN_COLS = 8, SCAN = 256;
+template <bool BWD>
+__global__ void __launch_bounds__(SCAN) delta_scan_kernel(const DeltaArgs a, const Scratch sc,
+                                                          int segs, int seg_len)
+{
+    __shared__ __align__(16) float S[2][128][SCAN_COLS];
+    const int cols = (a.E + SCAN_COLS - 1) / SCAN_COLS;
+    const int h = blockIdx.x / cols % a.H, n = blockIdx.x / cols / a.H;
+    const int e0 = blockIdx.x % cols * SCAN_COLS + 4 * (threadIdx.x & 1), d = threadIdx.x >> 1;
+    const Seq sq = sequence(a.cu, a.T, n);
+    const int count = sq.len > 0 ? (int)((sq.len + seg_len - 1) / seg_len) : 1;
+    const float *first = BWD ? a.dfin : a.init;
+    const bool row = d < a.D;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);     // E is a multiple of 8
+    if (first && row)
+        x = make_float4(first[(((int64_t)n * a.H + h) * a.D + d) * a.E + e0],
+                        first[(((int64_t)n * a.H + h) * a.D + d) * a.E + e0 + 1],
+                        first[(((int64_t)n * a.H + h) * a.D + d) * a.E + e0 + 2],
+                        first[(((int64_t)n * a.H + h) * a.D + d) * a.E + e0 + 3]);
+    for (int i = 0;; ++i) {
+        const int j = BWD ? count - 1 - i : i;
+        const int64_t at = ((int64_t)n * segs + j) * a.H + h;
+        if (row)
+            *reinterpret_cast<float4 *>(sc.enter + (at * a.D + d) * a.E + e0) = x;
+        if (i == count - 1)
+            return;
+        *reinterpret_cast<float4 *>(&S[i & 1][d][4 * (threadIdx.x & 1)]) = x;
+        __syncthreads();
+        if (row) {
+            x = *reinterpret_cast<const float4 *>(sc.own + (at * a.D + d) * a.E + e0);
+            const float *m = sc.phi + at * a.D * a.D + (BWD ? d : d * a.D);
+#pragma unroll 8
+            for (int k = 0; k < a.D; ++k) {     // D is a multiple of 8
+                const float f = BWD ? m[k * a.D] : m[k];
+                const float4 s = *reinterpret_cast<const float4 *>(
+                    &S[i & 1][k][4 * (threadIdx.x & 1)]);
+                x.x = fmaf(f, s.x, x.x);
+                x.y = fmaf(f, s.y, x.y);
+                x.z = fmaf(f, s.z, x.z);
+                x.w = fmaf(f, s.w, x.w);
+            }
+        }
+    }
+}
+
 // ---- host -------------------------------------------------------------------------
+
+// Segments of a sequence: the count with the least time by this model, of a chunk's time
+// in a sweep of states (2.6 us) and in one with outputs (3.2), rounds of CTAs on the
+// 152 SMs of a GB300, and 4 us a step of the scan with its launches: one sequence of
+// 65536 tokens with 8 heads 0.6 ms in 19 segments, 3.1 whole.
+struct Segments {
+    int count, tokens;
+};
+Segments segments_of(const DeltaArgs &a)
+{
+    const int64_t pairs = (int64_t)a.N * a.H, chunks = (a.longest + C - 1) / C;
+    const int64_t sms = 152;
+    Segments best{1, (int)(chunks * C)};
+    if (pairs == 0 || pairs > sms / 2)
+        return best;
+    double least = 0.9 * 3.2 * (double)chunks;      // a split has to be worth it
+    for (int64_t n = 2; n <= 64 && 4 * n <= chunks; ++n) {
+        const int64_t len = (chunks + n - 1) / n, count = (chunks + len - 1) / len;
+        const int64_t first = (2 * pairs * (count - 1) + sms - 1) / sms;
+        const int64_t second = (pairs * count + sms - 1) / sms;
+        const double t = (2.6 * (double)first + 3.2 * (double)second) * (double)len +
+                         4.0 * (double)count + 10.0;
+        if (t < least) {
+            least = t;
+            best = Segments{(int)count, (int)(len * C)};
+        }
+    }
+    return best;
+}
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 size_t tiles_of(const DeltaArgs &a)
@@ -1739,9 +1873,28 @@ size_t tiles_of(const DeltaArgs &a)
 }
 size_t prep_bytes(const DeltaArgs &a) { return tiles_of(a) * (BTILE + TAB); }
 
+// Phi, and the states of segments (each of two buffers); 0 for whole sequences
+size_t phi_bytes(const DeltaArgs &a)
+{
+    const int n = segments_of(a).count;
+    return n > 1 ? up((size_t)a.N * n * a.H * a.D * a.D * sizeof(float)) : 0;
+}
+size_t segment_bytes(const DeltaArgs &a)
+{
+    const int n = segments_of(a).count;
+    return n > 1 ? up((size_t)a.N * n * a.H * a.D * a.E * sizeof(float)) : 0;
+}
+void put_segments(const DeltaArgs &a, uint8_t *p, Scratch *sc)
+{
+    sc->own = reinterpret_cast<float *>(p);
+    sc->enter = reinterpret_cast<float *>(p + segment_bytes(a));
+}
+
 void put_saved(const DeltaArgs &a, uint8_t *p, bool keep, Scratch *sc)
 {
     const size_t t = tiles_of(a);
+    sc->phi = reinterpret_cast<float *>(
+        p + up(prep_bytes(a) + (keep ? t * (STILE + ETILE) : 0)));
     sc->b = p;
     sc->tab = reinterpret_cast<float *>(p + t * BTILE);
     sc->s = keep ? p + prep_bytes(a) : nullptr;
@@ -1768,13 +1921,32 @@ template <bool BWD> cudaError_t sweep(const DeltaArgs &a, const Scratch &sc, cud
         return cudaErrorNotSupported;
     p.a = a;
     p.sc = sc;
+    const Segments seg = segments_of(a);
+    p.segs = seg.count;
+    p.seg_len = seg.tokens;
+    p.states = 0;
     cudaError_t e = cudaFuncSetAttribute(delta_sweep_kernel<BWD>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          SweepLayout<BWD>::DYN);
     if (e != cudaSuccess)
         return e;
-    delta_sweep_kernel<BWD>
-        <<<(unsigned)((int64_t)a.N * a.H), SWEEP, SweepLayout<BWD>::DYN, s>>>(p);
+    const unsigned ctas = (unsigned)((int64_t)a.N * seg.count * a.H);
+    if (seg.count > 1) {
+        SweepParams first = p;
+        first.states = 1;
+        delta_sweep_kernel<BWD><<<dim3(ctas, BWD ? 1 : 2), SWEEP, SweepLayout<BWD>::DYN, s>>>(first);
+        note_launch();
+        if ((e = cudaGetLastError()) != cudaSuccess)
+            return e;
+        const unsigned cols = (unsigned)((a.E + SCAN_COLS - 1) / SCAN_COLS);
+        delta_scan_kernel<BWD>
+            <<<(unsigned)(a.N * a.H) * cols, SCAN, 0, s>>>(a, sc, seg.count, seg.tokens);
+        note_launch();
+        if ((e = cudaGetLastError()) != cudaSuccess)
+            return e;
+        p.a.withhold_handoff = 0;
+    }
+    delta_sweep_kernel<BWD><<<ctas, SWEEP, SweepLayout<BWD>::DYN, s>>>(p);
     note_launch();
     return cudaGetLastError();
 }
@@ -1805,21 +1977,26 @@ bool delta_tc_sized(const DeltaArgs &a)
 
 size_t delta_tc_saved_bytes(const DeltaArgs &a)
 {
-    return up(prep_bytes(a) + tiles_of(a) * (STILE + ETILE));
+    return up(prep_bytes(a) + tiles_of(a) * (STILE + ETILE)) + phi_bytes(a);
 }
 
-size_t delta_tc_fwd_bytes(const DeltaArgs &a, bool keep) { return keep ? 0 : up(prep_bytes(a)); }
+size_t delta_tc_fwd_bytes(const DeltaArgs &a, bool keep)
+{
+    return 2 * segment_bytes(a) + (keep ? 0 : up(prep_bytes(a)) + phi_bytes(a));
+}
 
 size_t delta_tc_bwd_bytes(const DeltaArgs &a)
 {
     const size_t parts = a.H == a.HK ? 0 : up((size_t)a.B * a.T * a.H * a.D * sizeof(float));
-    return up(tiles_of(a) * (STILE + ETILE)) + 2 * parts;
+    return up(tiles_of(a) * (STILE + ETILE)) + 2 * parts + 2 * segment_bytes(a);
 }
 
 cudaError_t delta_tc_forward(const DeltaArgs &a, cudaStream_t s)
 {
     Scratch sc{};
-    put_saved(a, a.saved ? a.saved : a.ws, a.saved != nullptr, &sc);
+    // the workspace: the segments' states, then what is not saved
+    put_segments(a, a.ws, &sc);
+    put_saved(a, a.saved ? a.saved : a.ws + 2 * segment_bytes(a), a.saved != nullptr, &sc);
     delta_prep_kernel<<<(unsigned)tiles_of(a), PREP, 0, s>>>(a, sc);
     note_launch();
     const cudaError_t e = cudaGetLastError();
@@ -1833,10 +2010,13 @@ cudaError_t delta_tc_backward(const DeltaArgs &a, cudaStream_t s)
     put_saved(a, a.saved, true, &sc);
     sc.k = a.ws;
     sc.r = a.ws + t * STILE;
+    const size_t images = up(t * (STILE + ETILE));
+    put_segments(a, a.ws + images, &sc);
     if (a.H != a.HK) {
         const size_t parts = up((size_t)a.B * a.T * a.H * a.D * sizeof(float));
-        sc.dqp = reinterpret_cast<float *>(a.ws + up(t * (STILE + ETILE)));
-        sc.dkp = reinterpret_cast<float *>(a.ws + up(t * (STILE + ETILE)) + parts);
+        uint8_t *at = a.ws + images + 2 * segment_bytes(a);
+        sc.dqp = reinterpret_cast<float *>(at);
+        sc.dkp = reinterpret_cast<float *>(at + parts);
     }
     cudaError_t e = sweep<true>(a, sc, s);
     if (e != cudaSuccess)

@@ -156,6 +156,20 @@ def test_packed(pack, dt):
     check(x, cu=cu, label="pack %s" % cu)
 
 
+@pytest.mark.parametrize("size", [(1, 2100, 1, 1, 128, 128), (2, 1601, 2, 1, 64, 40)])
+def test_segments(size):
+    # few heads, long sequences: segments at once, joined by a scan over their states
+    for state in (True, False):
+        x = inputs(*size, BF, F32, size[0], 9, state)
+        check(x, label="%s state %d" % (size, state))
+
+
+def test_segments_packed():
+    # one long sequence among short and empty ones: segments past a sequence's end
+    cu = [0, 0, 30, 1700, 1700, 1764]
+    check(inputs(1, cu[-1], 1, 1, 32, 24, BF, F32, len(cu) - 1, 4), cu=cu)
+
+
 def test_scale():
     check(inputs(1, 100, 2, 1, 64, 64, BF, F32, 1, 3), scale=1.0)
     check(inputs(1, 10, 2, 1, 64, 64, BF, F32, 1, 3), scale=0.0)
