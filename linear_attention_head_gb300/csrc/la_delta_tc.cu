@@ -1789,49 +1789,83 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
 //
 // The states that enter a sequence's segments: S_0 the initial state, S_j+1 = Phi_j S_j +
 // H_j; back K'_last = dL/dfinal, K'_j-1 = Phi_j^T K'_j + H_j.  A CTA takes 8 columns of a
-// (sequence, head)'s state, two threads a row, in fp32.
+// (sequence, head)'s state, two threads a row, in fp32; the next Phi is on its way into
+// shared memory meanwhile.  Its steps are one after another: 128 x 128 x 8 products each.
 constexpr int SCAN_COLS = 8, SCAN = 256;
+constexpr int PP = 132;         // floats a row of Phi: neighbouring rows, other banks
+constexpr int SCAN_DYN = (2 * 128 * PP + 2 * 128 * SCAN_COLS) * 4;
 template <bool BWD>
 __global__ void __launch_bounds__(SCAN) delta_scan_kernel(const DeltaArgs a, const Scratch sc,
                                                           int segs, int seg_len)
 {
-    __shared__ __align__(16) float S[2][128][SCAN_COLS];
+    extern __shared__ __align__(16) float scan_sm[];
+    float *M[2] = {scan_sm, scan_sm + 128 * PP};
+    float(*S)[128][SCAN_COLS] = reinterpret_cast<float(*)[128][SCAN_COLS]>(scan_sm + 2 * 128 * PP);
     const int cols = (a.E + SCAN_COLS - 1) / SCAN_COLS;
     const int h = blockIdx.x / cols % a.H, n = blockIdx.x / cols / a.H;
-    const int e0 = blockIdx.x % cols * SCAN_COLS + 4 * (threadIdx.x & 1), d = threadIdx.x >> 1;
+    const int c0 = 4 * (threadIdx.x & 1), d = threadIdx.x >> 1;
+    const int e0 = blockIdx.x % cols * SCAN_COLS + c0;
     const Seq sq = sequence(a.cu, a.T, n);
     const int count = sq.len > 0 ? (int)((sq.len + seg_len - 1) / seg_len) : 1;
-    const float *first = BWD ? a.dfin : a.init;
     const bool row = d < a.D;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);     // E is a multiple of 8
-    if (first && row)
-        x = make_float4(first[(((int64_t)n * a.H + h) * a.D + d) * a.E + e0],
-                        first[(((int64_t)n * a.H + h) * a.D + d) * a.E + e0 + 1],
-                        first[(((int64_t)n * a.H + h) * a.D + d) * a.E + e0 + 2],
-                        first[(((int64_t)n * a.H + h) * a.D + d) * a.E + e0 + 3]);
-    for (int i = 0;; ++i) {
-        const int j = BWD ? count - 1 - i : i;
-        const int64_t at = ((int64_t)n * segs + j) * a.H + h;
-        if (row)
-            *reinterpret_cast<float4 *>(sc.enter + (at * a.D + d) * a.E + e0) = x;
-        if (i == count - 1)
-            return;
-        *reinterpret_cast<float4 *>(&S[i & 1][d][4 * (threadIdx.x & 1)]) = x;
-        __syncthreads();
-        if (row) {
-            x = *reinterpret_cast<const float4 *>(sc.own + (at * a.D + d) * a.E + e0);
-            const float *m = sc.phi + at * a.D * a.D + (BWD ? d : d * a.D);
-#pragma unroll 8
-            for (int k = 0; k < a.D; ++k) {     // D is a multiple of 8
-                const float f = BWD ? m[k * a.D] : m[k];
-                const float4 s = *reinterpret_cast<const float4 *>(
-                    &S[i & 1][k][4 * (threadIdx.x & 1)]);
-                x.x = fmaf(f, s.x, x.x);
-                x.y = fmaf(f, s.y, x.y);
-                x.z = fmaf(f, s.z, x.z);
-                x.w = fmaf(f, s.w, x.w);
+    auto at = [&](int i) {      // the i-th segment in the scan's order
+        return ((int64_t)n * segs + (BWD ? count - 1 - i : i)) * a.H + h;
+    };
+    auto ask = [&](int i) {
+        if (i < count - 1) {
+            const float *from = sc.phi + at(i) * a.D * a.D;
+            for (int u = threadIdx.x; u < a.D * a.D / 4; u += SCAN) {
+                const int r = u / (a.D / 4), c = 4 * (u - r * (a.D / 4));
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 smem_u32(M[i & 1] + r * PP + c)),
+                             "l"(from + r * a.D + c)
+                             : "memory");
             }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    ask(0);
+    const float *first = BWD ? a.dfin : a.init;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);     // E is a multiple of 8
+    if (first && row) {
+        first += (((int64_t)n * a.H + h) * a.D + d) * a.E + e0;
+        x = make_float4(first[0], first[1], first[2], first[3]);
+    }
+    for (int i = 0;; ++i) {
+        if (row)
+            *reinterpret_cast<float4 *>(sc.enter + (at(i) * a.D + d) * a.E + e0) = x;
+        if (i == count - 1)
+            return;
+        ask(i + 1);
+        *reinterpret_cast<float4 *>(&S[i & 1][d][c0]) = x;
+        if (row)
+            x = *reinterpret_cast<const float4 *>(sc.own + (at(i) * a.D + d) * a.E + e0);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();
+        if (row) {
+            const float *m = M[i & 1] + (BWD ? d : d * PP);
+#pragma unroll 4
+            for (int k = 0; k < a.D; k += 4) {      // D is a multiple of 8
+                float f[4];
+                if (BWD) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        f[y] = m[(k + y) * PP];
+                } else {
+                    const float4 v = *reinterpret_cast<const float4 *>(m + k);
+                    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+                }
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float4 s = *reinterpret_cast<const float4 *>(&S[i & 1][k + y][c0]);
+                    x.x = fmaf(f[y], s.x, x.x);
+                    x.y = fmaf(f[y], s.y, x.y);
+                    x.z = fmaf(f[y], s.z, x.z);
+                    x.w = fmaf(f[y], s.w, x.w);
+                }
+            }
+        }
+        __syncthreads();        // M[i & 1] is asked for again in the next round
     }
 }
 
@@ -1939,8 +1973,12 @@ template <bool BWD> cudaError_t sweep(const DeltaArgs &a, const Scratch &sc, cud
         if ((e = cudaGetLastError()) != cudaSuccess)
             return e;
         const unsigned cols = (unsigned)((a.E + SCAN_COLS - 1) / SCAN_COLS);
+        e = cudaFuncSetAttribute(delta_scan_kernel<BWD>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, SCAN_DYN);
+        if (e != cudaSuccess)
+            return e;
         delta_scan_kernel<BWD>
-            <<<(unsigned)(a.N * a.H) * cols, SCAN, 0, s>>>(a, sc, seg.count, seg.tokens);
+            <<<(unsigned)(a.N * a.H) * cols, SCAN, SCAN_DYN, s>>>(a, sc, seg.count, seg.tokens);
         note_launch();
         if ((e = cudaGetLastError()) != cudaSuccess)
             return e;
