@@ -147,6 +147,30 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatil
     }
 }
 
+// Without a clock: for the chain's and the side warps, which wait for what the other
+// warps do or give up.  Those raise abort_flag when a wait of theirs runs out, and end
+// only with everything done that is waited for here.
+__device__ __forceinline__ bool wait_here(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
+{
+    int i = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity))
+        if ((++i & 63) == 0 && *abort_flag)     // seldom: it is shared memory's time too
+            return false;
+    return true;
+}
+// (The backward's sweep was slower with it, 45 us to 67 at b2 h8 n2047 d64.)
+template <bool BWD>
+__device__ __forceinline__ bool wait_role(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
+{
+    return BWD ? wait_for(bar, parity, abort_flag) : wait_here(bar, parity, abort_flag);
+}
+// the same as a call: for the warps that hold little in registers
+__device__ __noinline__ bool wait_call(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
+{
+    return wait_for(bar, parity, abort_flag);
+}
+
 __device__ __forceinline__ float2 mul2(float2 a, float2 b)
 {
     return un(la::mul2(f2(a.x, a.y), f2(b.x, b.y)));
@@ -725,7 +749,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             auto tables_in = [&]() {
                 const int ts = tables % NT;
                 if (tables >= NT &&
-                    !(going = wait_for(&tempty[ts], (tables / NT - 1) & 1, abort_flag)))
+                    !(going = wait_call(&tempty[ts], (tables / NT - 1) & 1, abort_flag)))
                     return false;
                 mbar_arrive_expect_tx(&tfull[ts], TAB);
                 bulk_load(sm + L::TOFF + ts * TAB, P.sc.tab + tile_of(tables) * TABS * C, TAB,
@@ -744,8 +768,8 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                     break;
                 if (c >= NS) {
                     // Eps's (R's) image lies where V (dO) was
-                    if (!(going = (!keep || wait_for(e_free, (c - NS) & 1, abort_flag)) &&
-                                  wait_for(&empty[s], (c / NS - 1) & 1, abort_flag)))
+                    if (!(going = (!keep || wait_call(e_free, (c - NS) & 1, abort_flag)) &&
+                                  wait_call(&empty[s], (c / NS - 1) & 1, abort_flag)))
                         break;
                 }
                 const int t = (int)(sq.bos + (int64_t)chunk(c) * C);
@@ -805,24 +829,28 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         auto kd = [&](int kk) { return off((uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32)); };
         auto scores = [&](int c) {      // [Q; K] K^T
             const uint64_t d = d_rows + stage(c);
+#pragma unroll 1
+            for (int k4 = 0; k4 < 2; ++k4)
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-                mma_ss(tm + (BWD ? T2 : TR), d + kd(kk), d + off(8192) + kd(kk), id64, kk > 0);
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ss(tm + (BWD ? T2 : TR), d + kd(4 * k4 + kk),
+                           d + off(8192) + kd(4 * k4 + kk), id64, k4 + kk > 0);
             mma_commit(sc_full);
         };
         // the state's rows times those of the [Q; K] tile from `row` on
         auto state_times = [&](uint32_t to, int c, int row) {
             const uint64_t d = d_rows + stage(c) + off(row * 128);
+#pragma unroll 1
+            for (int k4 = 0; k4 < 4; ++k4)      // hi's D, then lo's
 #pragma unroll
-            for (int lo = 0; lo < 2; ++lo)
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ts(tm + to, tm + TSH + 64 * lo + 8 * kk, d + kd(kk), id64, lo + kk > 0);
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ts(tm + to, tm + TSH + 32 * k4 + 8 * kk, d + kd((4 * k4 + kk) & 7), id64,
+                           k4 + kk > 0);
         };
         // T1 += (beta X)^T B^T (back: B): hi hi, lo hi, hi lo
         auto solve = [&](int c) {
             const uint64_t d = (BWD ? d_bmn : d_b) + stage(c);
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < 3; ++x)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
@@ -834,7 +862,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         // the state += (chain's operand)^T K
         auto update = [&](int c) {
             const uint64_t d = d_cols + stage(c) + off(8192);
-#pragma unroll
+#pragma unroll 1
             for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
@@ -847,7 +875,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             if (!a.cu || chunk(c) != nc - 1)
                 return true;
             const int n = tokens(c);
-            if (!warp_all(wait_for(&fullv[c % NS], (c / NS) & 1, abort_flag)))
+            if (!warp_all(wait_call(&fullv[c % NS], (c / NS) & 1, abort_flag)))
                 return false;
             uint8_t *st = sm + (c % NS) * STAGE;
             const uint4 z = make_uint4(0, 0, 0, 0);
@@ -865,12 +893,12 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             return true;
         };
         auto stage_in = [&](int c) {
-            return warp_all(wait_for(&full[c % NS], (c / NS) & 1, abort_flag) &&
-                            wait_for(&fullb[c % NS], (c / NS) & 1, abort_flag)) &&
+            return warp_all(wait_call(&full[c % NS], (c / NS) & 1, abort_flag) &&
+                            wait_call(&fullb[c % NS], (c / NS) & 1, abort_flag)) &&
                    clear_tail(c);
         };
         auto both = [&](uint64_t *bar, int c) {
-            const bool ok = warp_all(wait_for(bar, c & 1, abort_flag));
+            const bool ok = warp_all(wait_call(bar, c & 1, abort_flag));
             tc_fence_after();
             return ok;
         };
@@ -887,7 +915,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 if (!both(p_ready, c) || !both(td_ready, c))
                     return false;
                 if (one)
-#pragma unroll
+#pragma unroll 1
                     for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
@@ -911,7 +939,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 if (!(ok = both(q_ready, c)))
                     break;
                 if (one)    // K'^T += dO^T (scale e^G Q)
-#pragma unroll
+#pragma unroll 1
                     for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
@@ -980,7 +1008,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 if (!both(p_ready, c) || !both(d_ready, c))
                     break;
                 if (one) {  // (beta Eps)^T P^T; beta Eps lies in T1, as tok_col
-#pragma unroll
+#pragma unroll 1
                     for (int x = 0; x < 3; ++x)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
@@ -1003,13 +1031,13 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
 #pragma unroll 1
             for (int c = 0; c < nc; ++c) {
                 if (keep) {
-                    if (!wait_for(i_ready, c & 1, abort_flag))
+                    if (!wait_call(i_ready, c & 1, abort_flag))
                         break;
                     bulk_store(simg + tile_of(c) * STILE, sm + L::SOFF, STILE);
                     bulk_commit_group();
                     bulk_wait_read_all();
                     mbar_arrive(i_free);
-                    if (!wait_for(e_ready, c & 1, abort_flag))
+                    if (!wait_call(e_ready, c & 1, abort_flag))
                         break;
                     bulk_store(eimg + tile_of(c) * ETILE, sm + (c % NS) * STAGE + VD, ETILE);
                     bulk_commit_group();
@@ -1017,7 +1045,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                     mbar_arrive(e_free);
                 }
                 if (some_o) {
-                    if (!wait_for(o_ready, c & 1, abort_flag))
+                    if (!wait_call(o_ready, c & 1, abort_flag))
                         break;
                     if (o_tile(c)) {
                         const int t = (int)(sq.bos + (int64_t)c * C);
@@ -1076,10 +1104,10 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             const int s = c % NS, n = tokens(c);
             const uint8_t *st = sm + s * STAGE;
             const float *tab = tabs + (c % NT) * TABS * C;
-            if (!(ok = warp_all(wait_for(&tfull[c % NT], (c / NT) & 1, abort_flag))))
+            if (!(ok = warp_all(wait_role<BWD>(&tfull[c % NT], (c / NT) & 1, abort_flag))))
                 break;
             // ---- the state
-            if (c > 0 && !(ok = warp_all(wait_for(s_full, (c - 1) & 1, abort_flag))))
+            if (c > 0 && !(ok = warp_all(wait_role<BWD>(s_full, (c - 1) & 1, abort_flag))))
                 break;
             tc_fence_after();
             const float2 gC = make_float2(-tab[TNEG * C + C - 1], -tab[TNEG * C + C - 1]);
@@ -1102,7 +1130,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             if (lane == 0)
                 mbar_arrive(s_ready);
             if (keep) {
-                if (c > 0 && !(ok = warp_all(wait_for(i_free, (c - 1) & 1, abort_flag))))
+                if (c > 0 && !(ok = warp_all(wait_role<BWD>(i_free, (c - 1) & 1, abort_flag))))
                     break;
                 // hi, back from TMEM
                 uint8_t *to = sm + L::SOFF + half * 16384 + e * 128;
@@ -1128,7 +1156,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             };
             uint32_t v[16];
             if constexpr (!BWD) {
-                if (!(ok = warp_all(wait_for(&fullv[s], (c / NS) & 1, abort_flag))))
+                if (!(ok = warp_all(wait_role<BWD>(&fullv[s], (c / NS) & 1, abort_flag))))
                     break;
                 channel(st + VD, e, half, v);
                 if (phi)
@@ -1136,7 +1164,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                     for (int x = 0; x < 16; ++x)
                         v[x] = 0u;
             }
-            if (!(ok = warp_all(wait_for(ks_full, c & 1, abort_flag))))
+            if (!(ok = warp_all(wait_role<BWD>(ks_full, c & 1, abort_flag))))
                 break;
             tc_fence_after();
             uint32_t r[32], hi[16], lo[16];
@@ -1172,7 +1200,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             if (lane == 0 && !(a.withhold_handoff && c == 0 && warp == 2))
                 mbar_arrive(y_ready);
             // ---- Eps (R)
-            if (!(ok = warp_all(wait_for(e_full, c & 1, abort_flag))))
+            if (!(ok = warp_all(wait_role<BWD>(e_full, c & 1, abort_flag))))
                 break;
             tc_fence_after();
             tmem_ld32(lanes + T1 + j0, r);
@@ -1193,7 +1221,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 for (int x = 0; x < 16; ++x)
                     split2(mul2(pair_at(TBETA, x), pair_of(r, x)), hi[x], lo[x]);
                 // the side warps have read Eps, where they want it
-                if (keep && !(ok = warp_all(wait_for(x_read, c & 1, abort_flag))))
+                if (keep && !(ok = warp_all(wait_role<BWD>(x_read, c & 1, abort_flag))))
                     break;
                 tmem_st16_issue(lanes + T1 + 32 * half, hi);
                 tmem_st16_issue(lanes + T1 + 32 * half + 16, lo);
@@ -1208,7 +1236,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 mbar_arrive(&tempty[c % NT]);
         }
         if (ok && nc > 0)
-            ok = warp_all(wait_for(s_full, (nc - 1) & 1, abort_flag));
+            ok = warp_all(wait_role<BWD>(s_full, (nc - 1) & 1, abort_flag));
         tc_fence_after();
         if (ok && out)
 #pragma unroll 1
@@ -1234,8 +1262,8 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         for (int c = 0; c < todo; ++c) {
             const int s = c % NS, n = tokens(c);
             const float *tab = tabs + (c % NT) * TABS * C;
-            if (!warp_all(wait_for(&tfull[c % NT], (c / NT) & 1, abort_flag)) ||
-                !warp_all(wait_for(sc_full, c & 1, abort_flag)))
+            if (!warp_all(wait_role<BWD>(&tfull[c % NT], (c / NT) & 1, abort_flag)) ||
+                !warp_all(wait_role<BWD>(sc_full, c & 1, abort_flag)))
                 break;
             tc_fence_after();
             if (q < 2) {    // row i of P, this half's columns; those past the warp's rows are zero
@@ -1276,7 +1304,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 if (lane == 0)
                     mbar_arrive(p_ready);
             } else if (BWD) {   // row i of scale e^G Q, this half's channels
-                if (!warp_all(wait_for(&full[s], (c / NS) & 1, abort_flag)))
+                if (!warp_all(wait_role<BWD>(&full[s], (c / NS) & 1, abort_flag)))
                     break;
                 const int i = row - 64;
                 const float f = i < n ? -a.scale * tab[TNEG * C + i] : 0.f;
@@ -1304,7 +1332,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                     mbar_arrive(q_ready);
             }
             if constexpr (BWD) {    // dO^T: this lane's channel, this half's tokens
-                if (!warp_all(wait_for(&fullv[s], (c / NS) & 1, abort_flag)))
+                if (!warp_all(wait_role<BWD>(&fullv[s], (c / NS) & 1, abort_flag)))
                     break;
                 uint32_t v[16];
                 channel(sm + s * STAGE + VD, row, half, v);
@@ -1325,7 +1353,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             }
             // ---- the image of Eps (R), which delta_grads starts from
             if (keep) {
-                if (!warp_all(wait_for(e_full, c & 1, abort_flag)))
+                if (!warp_all(wait_role<BWD>(e_full, c & 1, abort_flag)))
                     break;
                 tc_fence_after();
                 uint32_t r[32];
@@ -1351,7 +1379,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(q_ready);
-                if (!warp_all(wait_for(o_full, c & 1, abort_flag)))
+                if (!warp_all(wait_role<BWD>(o_full, c & 1, abort_flag)))
                     break;
                 tc_fence_after();
                 tmem_ld32(lanes + TR + j0, w);
@@ -1370,7 +1398,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                     y[2 * x + 1] = z.y;
                 }
                 if (some_o) {
-                    if (c > 0 && !warp_all(wait_for(o_free, (c - 1) & 1, abort_flag)))
+                    if (c > 0 && !warp_all(wait_role<BWD>(o_free, (c - 1) & 1, abort_flag)))
                         break;
                     if (o_tile(c)) {
                         store_image(y, half, row, sm + L::OOFF);
