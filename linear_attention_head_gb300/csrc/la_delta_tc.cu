@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
     uint64_t *o_free = bars + 16;       // it has been read
     uint64_t *e_ready = bars + 17;      // Eps's (R's) image
     uint64_t *e_free = bars + 18;       // it has been read
-    uint64_t *x_read = bars + 19;       // Eps (R) read by the side warps
+    uint64_t *x_read = bars + 19;       // forward: Eps read by the side warps
     uint64_t *drain = bars + 20;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::SLOT);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::ABORT);
@@ -927,7 +927,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             bool ok = prior(0);
 #pragma unroll 1
             for (int c = 0; ok && c < nc; ++c) {
-                if (!(ok = (c == 0 || !keep || both(x_read, c - 1)) && both(s_ready, c)))
+                if (!(ok = both(s_ready, c)))
                     break;
                 if (one) {
                     state_times(T1, c, 64);
@@ -1214,7 +1214,19 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(w_ready);
-            // off the chain: beta Eps over this half's own columns of T1, for O
+            // off the chain, while the state is made.  Back: R's image
+            if (BWD && keep) {
+                float x32[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                    x32[x] = __uint_as_float(r[x]);
+                store_image(x32, half, e, sm + s * STAGE + VD);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(e_ready);
+            }
+            // forward: beta Eps over this half's own columns of T1, for O
             if (!BWD && !states) {
                 // r is Eps still
 #pragma unroll
@@ -1262,6 +1274,26 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         for (int c = 0; c < todo; ++c) {
             const int s = c % NS, n = tokens(c);
             const float *tab = tabs + (c % NT) * TABS * C;
+            if constexpr (BWD) {    // dO^T: this lane's channel, this half's tokens
+                if (!warp_all(wait_role<BWD>(&fullv[s], (c / NS) & 1, abort_flag)))
+                    break;
+                uint32_t v[16];
+                channel(sm + s * STAGE + VD, row, half, v);
+                if (n < C)
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        if (j0 + 2 * x >= n)
+                            v[x] = 0u;
+                        else if (j0 + 2 * x + 1 >= n)
+                            v[x] &= 0xFFFFu;
+                    }
+                tmem_st16_issue(lanes + TD + 32 * (c & 1) + 16 * half, v);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(td_ready);
+            }
             if (!warp_all(wait_role<BWD>(&tfull[c % NT], (c / NT) & 1, abort_flag)) ||
                 !warp_all(wait_role<BWD>(sc_full, c & 1, abort_flag)))
                 break;
@@ -1331,28 +1363,8 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 if (lane == 0)
                     mbar_arrive(q_ready);
             }
-            if constexpr (BWD) {    // dO^T: this lane's channel, this half's tokens
-                if (!warp_all(wait_role<BWD>(&fullv[s], (c / NS) & 1, abort_flag)))
-                    break;
-                uint32_t v[16];
-                channel(sm + s * STAGE + VD, row, half, v);
-                if (n < C)
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                        if (j0 + 2 * x >= n)
-                            v[x] = 0u;
-                        else if (j0 + 2 * x + 1 >= n)
-                            v[x] &= 0xFFFFu;
-                    }
-                tmem_st16_issue(lanes + TD + 32 * (c & 1) + 16 * half, v);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(td_ready);
-            }
-            // ---- the image of Eps (R), which delta_grads starts from
-            if (keep) {
+            // ---- the image of Eps, which delta_grads starts from
+            if (!BWD && keep) {
                 if (!warp_all(wait_role<BWD>(e_full, c & 1, abort_flag)))
                     break;
                 tc_fence_after();
