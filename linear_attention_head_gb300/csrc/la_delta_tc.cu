@@ -1090,14 +1090,15 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         bool ok = true;
         if (nc > 0)
 #pragma unroll 1
-            for (int d0 = 64 * half; d0 < 64 * half + 64; d0 += 8) {
-                uint32_t r[8];
+            for (int d0 = 64 * half; d0 < 64 * half + 64; d0 += 32) {
+                uint32_t r[32];     // the loads all at once
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
+                for (int x = 0; x < 32; ++x)
                     r[x] = in && e < E && d0 + x < a.D
                                ? __float_as_uint(in[(int64_t)(d0 + x) * E + e])
                                : phi && e == d0 + x && e < a.D ? __float_as_uint(1.f) : 0u;
-                tmem_st8(lanes + TS + d0, r);
+                tmem_st32_issue(lanes + TS + d0, r);
+                tmem_wait_st();
             }
 #pragma unroll 1
         for (int c = 0; ok && c < nc; ++c) {

@@ -28,6 +28,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "la_f32x2.cuh"
 #include "la_internal.h"
 
 namespace la {
@@ -111,47 +112,57 @@ template <int RG> __device__ __forceinline__ float4 over_rows(float4 x)
     return x;
 }
 
-// x[r] summed over the warp's column quads; lane quad 0 of each row group has it.
-template <int RG> __device__ __forceinline__ void over_quads(float (&x)[ROWS])
+// x[r] summed over the warp's column quads: halves traded, so that lane quad qw ends
+// with rows first .. first + ROWS / QW - 1, in x[0] ..
+template <int RG> __device__ __forceinline__ int over_quads(float (&x)[ROWS], int qw)
 {
+    constexpr int QW = 32 / RG;
+    int first = 0;
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r)
+    for (int m = QW / 2, w = ROWS / 2; m >= 1; m /= 2, w /= 2) {
+        const bool up = qw & m;
 #pragma unroll
-        for (int m = 1; m < 32 / RG; m *= 2)
-            x[r] += __shfl_xor_sync(0xffffffffu, x[r], m);
+        for (int r = 0; r < ROWS / 2; ++r)
+            if (r < w) {
+                const float mine = up ? x[r + w] : x[r], other = up ? x[r] : x[r + w];
+                x[r] = mine + __shfl_xor_sync(0xffffffffu, other, m);
+            }
+        first += up ? w : 0;
+    }
+    return first;
 }
 
+// The packed instructions do two columns at once.
 template <int RG> __device__ __forceinline__ float4 dot_rows(const float4 (&S)[ROWS], const float *x)
 {
-    float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+    F2 u0 = f2(0.f), u1 = f2(0.f);
 #pragma unroll
     for (int r4 = 0; r4 < ROWS; r4 += 4) {
         const float4 k = *reinterpret_cast<const float4 *>(x + r4);
         const float kk[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            u.x = fmaf(S[r4 + j].x, kk[j], u.x);
-            u.y = fmaf(S[r4 + j].y, kk[j], u.y);
-            u.z = fmaf(S[r4 + j].z, kk[j], u.z);
-            u.w = fmaf(S[r4 + j].w, kk[j], u.w);
+            u0 = fma2(f2(S[r4 + j].x, S[r4 + j].y), f2(kk[j]), u0);
+            u1 = fma2(f2(S[r4 + j].z, S[r4 + j].w), f2(kk[j]), u1);
         }
     }
-    return over_rows<RG>(u);
+    const float2 a = un(u0), b = un(u1);
+    return over_rows<RG>(make_float4(a.x, a.y, b.x, b.y));
 }
 
 // S = f S + x y^T
 __device__ __forceinline__ void rank_one(float4 (&S)[ROWS], float f, const float *x, float4 y)
 {
+    const F2 y0 = f2(y.x, y.y), y1 = f2(y.z, y.w), f0 = f2(f);
 #pragma unroll
     for (int r4 = 0; r4 < ROWS; r4 += 4) {
         const float4 k = *reinterpret_cast<const float4 *>(x + r4);
         const float kk[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            S[r4 + j].x = fmaf(kk[j], y.x, f * S[r4 + j].x);
-            S[r4 + j].y = fmaf(kk[j], y.y, f * S[r4 + j].y);
-            S[r4 + j].z = fmaf(kk[j], y.z, f * S[r4 + j].z);
-            S[r4 + j].w = fmaf(kk[j], y.w, f * S[r4 + j].w);
+            const float2 a = un(fma2(f2(kk[j]), y0, mul2(f0, f2(S[r4 + j].x, S[r4 + j].y))));
+            const float2 b = un(fma2(f2(kk[j]), y1, mul2(f0, f2(S[r4 + j].z, S[r4 + j].w))));
+            S[r4 + j] = make_float4(a.x, a.y, b.x, b.y);
         }
     }
 }
@@ -280,15 +291,14 @@ __global__ void __launch_bounds__(32 * WARPS, 4) delta_token_kernel(const Params
 #pragma unroll
                 for (int r = 0; r < ROWS; ++r)
                     dk[r] = beta * (S[r].x * e.x + S[r].y * e.y + S[r].z * e.z + S[r].w * e.w);
-                over_quads<RG>(dk);
+                const int rq = over_quads<RG>(dk, qw);
                 float db = w.x * e.x + w.y * e.y + w.z * e.z + w.w * e.w;
 #pragma unroll
                 for (int m = 1; m < L::QW; m *= 2)
                     db += __shfl_xor_sync(0xffffffffu, db, m);
-                if (qw == 0)
 #pragma unroll
-                    for (int r = 0; r < ROWS; ++r)
-                        red[j][warp][r0 + r] = dk[r];
+                for (int r = 0; r < ROWS / L::QW; ++r)
+                    red[j][warp][r0 + rq + r] = dk[r];
                 if (lane == 0)
                     redb[j][warp] = db;
                 rank_one(S, 1.f, kr, make_float4(-dv.x, -dv.y, -dv.z, -dv.w));
@@ -319,14 +329,13 @@ __global__ void __launch_bounds__(32 * WARPS, 4) delta_token_kernel(const Params
                 for (int r = 0; r < ROWS; ++r)
                     dq[r] = a.scale * (S[r].x * col.x + S[r].y * col.y + S[r].z * col.z +
                                        S[r].w * col.w);
-                over_quads<RG>(dk);
-                over_quads<RG>(dq);
-                if (qw == 0)
+                const int rq = over_quads<RG>(dk, qw);
+                over_quads<RG>(dq, qw);
 #pragma unroll
-                    for (int r = 0; r < ROWS; ++r) {
-                        red[j][warp][r0 + r] = dk[r];
-                        red[TB + j][warp][r0 + r] = dq[r];
-                    }
+                for (int r = 0; r < ROWS / L::QW; ++r) {
+                    red[j][warp][r0 + rq + r] = dk[r];
+                    red[TB + j][warp][r0 + rq + r] = dq[r];
+                }
             }
         }
         if constexpr (M >= BACK) {
