@@ -619,10 +619,13 @@ typedef struct la_delta_dims {
  * Kernels: bf16 with D and E multiples of 8 up to 128, strides of q, k, v that
  * are multiples of 8 elements (and positive where the axis is longer than 1),
  * and a sequence of more than 16 tokens: chunks of 64 tokens on the tensor
- * cores, in which every operand that is not an input is split in two bf16
- * (16 bits of it: the states come out as fp32 arithmetic gives them).  Then q, k,
- * v and o must start on 16-byte boundaries, or (without saved) the call runs as
- * every other one: token by token in fp32. */
+ * cores, in which every operand that is not an input is split in two bf16 (16
+ * bits of it: the states are within some 1e-5 of those of exact arithmetic).
+ * Where (sequence, head) pairs are at most 76, long sequences are cut in
+ * segments that run at once.  Then q, k, v and o must start on 16-byte
+ * boundaries, or (without saved) the call runs as every other one: token by
+ * token in fp32.  A token that is not finite makes its whole chunk so, also the
+ * up to 63 tokens before it; other sequences never. */
 la_status la_gated_delta_fwd(const la_delta_dims *dims, int32_t dtype, const void *q,
                              const void *k, const void *v, const void *g, const void *beta,
                              float scale, const float *initial_state, const int32_t *cu_seqlens,
@@ -744,7 +747,8 @@ la_status la_get_device_error(void *stream);
 
 /* Diagnostic, for testing error reporting: with on != 0, the next launch of
  * a kernel with internal hand-offs (the tensor-core sweeps, the streamed
- * decode kernel, the tiles of la_gated_scan_fwd and _bwd) made from this host
+ * decode kernel, the tiles of la_gated_scan_fwd and _bwd, the chunks of
+ * la_gated_delta_fwd and _bwd) made from this host
  * thread withholds one of them -- between its warps, or the copy of a state
  * block -- so that a bounded on-device wait runs out (after about 2 s); the
  * kernel then stops, frees what it holds and returns, its outputs are

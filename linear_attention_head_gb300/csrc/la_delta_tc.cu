@@ -122,7 +122,7 @@ __device__ __forceinline__ float gate_at(const Tok &g, int bf16, int64_t row, in
                 : static_cast<const float *>(g.p)[at];
 }
 
-// bwait in few instructions, the clock read only every 64th time: a chunk is a dozen
+// bwait in few instructions, the clock read only every 16th time: a chunk is a dozen
 // hand-offs one after another, and a kernel that outgrows the instruction cache waits
 // for its code (0.19 MB of it: 0.62 ms a sweep at b4 h32 n8192)
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
@@ -132,7 +132,7 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatil
     for (int i = 1;; ++i) {
         if (mbar_try_wait(bar, parity))
             return true;
-        if (i & 63)
+        if (i & 15)
             continue;
         if (*abort_flag)
             return false;
@@ -155,7 +155,7 @@ __device__ __forceinline__ bool wait_here(uint64_t *bar, uint32_t parity, volati
     int i = 0;
 #pragma unroll 1
     while (!mbar_try_wait(bar, parity))
-        if ((++i & 63) == 0 && *abort_flag)     // seldom: it is shared memory's time too
+        if ((++i & 15) == 0 && *abort_flag)     // seldom: it is shared memory's time too
             return false;
     return true;
 }
@@ -2072,6 +2072,8 @@ size_t delta_tc_bwd_bytes(const DeltaArgs &a)
 
 cudaError_t delta_tc_forward(const DeltaArgs &a, cudaStream_t s)
 {
+    if (a.N == 0)
+        return cudaSuccess;
     Scratch sc{};
     // the workspace: the segments' states, then what is not saved
     put_segments(a, a.ws, &sc);
@@ -2084,6 +2086,8 @@ cudaError_t delta_tc_forward(const DeltaArgs &a, cudaStream_t s)
 
 cudaError_t delta_tc_backward(const DeltaArgs &a, cudaStream_t s)
 {
+    if (a.N == 0)
+        return cudaSuccess;
     Scratch sc{};
     const size_t t = tiles_of(a);
     put_saved(a, a.saved, true, &sc);
