@@ -633,23 +633,23 @@ __global__ void __launch_bounds__(PL::CTA, PL::BLOCKS) block_norm_bwd_kernel(con
     }
 }
 
-// Rows a CTA takes at once, and the CTAs that one wave holds; a CTA more than there
-// are rows for is not launched.
-template <typename PL, typename K>
+// One wave of CTAs (as many an SM as the launch bounds and shared memory let be; asking
+// the runtime costs 5 us of a call), no more than there are rows for.
+template <typename PL, int BLOCKS, typename K>
 cudaError_t norm_launch(K kernel, size_t ring, const BlockNormArgs &a, int sms, cudaStream_t s,
                         int *ctas)
 {
-    int per_sm = 0;
-    cudaError_t e = ring > 0 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                    (int)ring)
-                             : cudaSuccess;
-    if (e == cudaSuccess)
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, PL::CTA, ring);
-    if (e != cudaSuccess)
-        return e;
+    if (ring > 32 * 1024) {     // with what the kernels have of their own above 48 KB
+        const cudaError_t e = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring);
+        if (e != cudaSuccess)
+            return e;
+    }
+    const int fit = (int)(228 * 1024 / (ring + 12 * 1024));
+    const int per_sm = fit < 1 ? 1 : fit < BLOCKS ? fit : BLOCKS;
     const int64_t want = (a.rows + PL::GROUPS - 1) / PL::GROUPS;
-    const int64_t wave = (int64_t)sms * (per_sm > 0 ? per_sm : 1);
-    int64_t n = want < wave ? want : wave;
+    int64_t n = (int64_t)sms * per_sm;
+    n = want < n ? want : n;
     if (n > NORM_MOST_CTAS && (a.dpost || a.dpre))
         n = NORM_MOST_CTAS;
     *ctas = (int)n;
@@ -662,13 +662,15 @@ template <bool BWD, typename T, typename PL>
 cudaError_t norm_by_access(const BlockNormArgs &a, bool vec, int sms, cudaStream_t s, int *ctas)
 {
     if constexpr (BWD)
-        return vec ? norm_launch<PL>(block_norm_bwd_kernel<T, PL, true>,
-                                     Ring<T, PL, true, 5>::BYTES, a, sms, s, ctas)
-                   : norm_launch<PL>(block_norm_bwd_kernel<T, PL, false>, 0, a, sms, s, ctas);
+        return vec ? norm_launch<PL, PL::BLOCKS>(block_norm_bwd_kernel<T, PL, true>,
+                                                 Ring<T, PL, true, 5>::BYTES, a, sms, s, ctas)
+                   : norm_launch<PL, PL::BLOCKS>(block_norm_bwd_kernel<T, PL, false>, 0, a, sms, s,
+                                                 ctas);
     else
-        return vec ? norm_launch<PL>(block_norm_fwd_kernel<T, PL, true>,
-                                     Ring<T, PL, true, 3>::BYTES, a, sms, s, ctas)
-                   : norm_launch<PL>(block_norm_fwd_kernel<T, PL, false>, 0, a, sms, s, ctas);
+        return vec ? norm_launch<PL, PL::FWD_BLOCKS>(block_norm_fwd_kernel<T, PL, true>,
+                                                     Ring<T, PL, true, 3>::BYTES, a, sms, s, ctas)
+                   : norm_launch<PL, PL::FWD_BLOCKS>(block_norm_fwd_kernel<T, PL, false>, 0, a, sms,
+                                                     s, ctas);
 }
 
 // Eight channels a thread: several rows a warp where rows are short, a CTA a row where

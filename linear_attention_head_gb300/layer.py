@@ -578,59 +578,58 @@ _ACTIVATIONS = {"none": 0, "sigmoid": 1, "silu": 2}
 
 
 class _NormCall:
-    """The arguments that the forward and the backward share; 3-D tensors as one head."""
+    """The arguments that the forward and the backward share; [B,T,C] as one head."""
 
     def __init__(self, x, gate, residual, post_weight, pre_weight, activation, scale, eps):
-        if activation not in _ACTIVATIONS:
+        kind = _ACTIVATIONS.get(activation)
+        if kind is None:
             raise ValueError("activation must be one of %s, got %r"
                              % (sorted(_ACTIVATIONS), activation))
-        self.squeeze = x.ndim == 3
-        self.x = self.rows(x, "x")
-        self.dtype = _code(self.x.dtype)
-        dev = self.device = self.x.device
-        D = self.x.shape[3]
+        if x.ndim not in (3, 4):
+            raise ValueError("x must be [B, T, H, D] or [B, T, C], got %s" % (tuple(x.shape),))
+        if not x.is_cuda:
+            raise ValueError("token tensors must be CUDA tensors")
+        self.x = x = self.channels(x)
+        self.dtype = code = _code(x.dtype)
+        self.device = x.device
         self.gate = self.like(gate, "gate")
         self.residual = self.like(residual, "residual")
-        w_dtype, code = None, self.dtype
+        shape = x.shape
+        w_dtype = None
         for w in (post_weight, pre_weight):
             if w is None:
                 continue
-            if w.shape != (D,) or w.device != dev:
-                raise ValueError("weights must be [%d] on %s" % (D, dev))
+            if w.shape != shape[-1:] or w.device != self.device:
+                raise ValueError("weights must be [%d] on %s" % (shape[-1], self.device))
             if w.dtype != (w_dtype or w.dtype):
                 raise TypeError("the weights must share one dtype")
             w_dtype, code = w.dtype, _code(w.dtype)
         self.post = post_weight.contiguous() if post_weight is not None else None
         self.pre = pre_weight.contiguous() if pre_weight is not None else None
         self.tail = (float(eps), float(scale))
-        self._head = tuple(self.x.shape) + (_ACTIVATIONS[activation], code)
+        self._head = (tuple(shape) if len(shape) == 4 else (shape[0], shape[1], 1, shape[2])) + \
+            (kind, code)
 
-    def rows(self, t, name):
-        if self.squeeze and t.ndim == 3:
-            t = t.unsqueeze(2)
-        return _token(t, name)
+    @staticmethod
+    def channels(t):
+        return t if t.is_contiguous() or t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
 
     def like(self, t, name):
-        """t as x's rows, or None."""
+        """t with x's rows, or None."""
         if t is None:
             return None
-        t = self.rows(t, name)
         if t.shape != self.x.shape or t.dtype != self.x.dtype:
             raise ValueError("%s must have x's shape and dtype" % name)
         if t.device != self.device:
             raise ValueError("all tensors must be on one device")
-        return t
-
-    def output(self, t, name):
-        if t is not None and self.squeeze and t.ndim == 3:
-            t = t.unsqueeze(2)
-        return _output(t, self.x, name)
-
-    def back(self, t):
-        return t.squeeze(2) if t is not None and self.squeeze else t
+        return self.channels(t)
 
     def dims(self, *outs):
-        strides = [s for t in (self.x, self.gate, self.residual) + outs for s in _strides(t)]
+        strides = []
+        for t in (self.x, self.gate, self.residual) + outs:
+            strides += (0, 0, 0) if t is None else t.stride()[:-1]
+            if t is not None and t.ndim == 3:
+                strides.append(0)
         return _norm_dims(_norm_pack(*self._head, *strides))
 
     def inputs(self):
@@ -653,11 +652,11 @@ def block_norm_fwd(x: Tensor, gate: Optional[Tensor] = None, residual: Optional[
     the gate.  out: (h, y) to write to; h may be x or residual itself."""
     c = _NormCall(x, gate, residual, post_weight, pre_weight, activation, scale, eps)
     h, y = _pair_of(out, "out")
-    h = c.output(h, "out")
-    y = c.output(y, "out") if c.pre is not None else None
+    h = _output(h, c.x, "out")
+    y = _output(y, c.x, "out") if c.pre is not None else None
     d = c.dims(h, y, None, None, None, None, None)
     _call(c.device, N.lib().la_block_norm_fwd, _ref(d), c.dtype, *c.inputs(), _ptr(h), _ptr(y))
-    return c.back(h), c.back(y)
+    return h, y
 
 
 @_traced
@@ -676,7 +675,7 @@ def block_norm_bwd(x: Tensor, dh: Optional[Tensor], dy: Optional[Tensor] = None,
         if dh is None:
             raise ValueError("give dh, dy or both")
         # y went unused: the same block without it
-        g = block_norm_bwd(x, c.back(dh), None, gate, residual, post_weight, None, activation,
+        g = block_norm_bwd(x, dh, None, gate, residual, post_weight, None, activation,
                            scale, eps)
         return g[:4] + (torch.zeros_like(c.pre),)
     if dh is None and dy is None:
@@ -693,7 +692,7 @@ def block_norm_bwd(x: Tensor, dh: Optional[Tensor], dy: Optional[Tensor] = None,
         ws, nbytes = _workspace(int(lib.la_block_norm_workspace_size(_ref(d), c.dtype)), c.device)
     _call(c.device, lib.la_block_norm_bwd, _ref(d), c.dtype, *c.inputs(), _ptr(dh), _ptr(dy),
           _ptr(dx), _ptr(dgate), _ptr(dres), _ptr(dpost), _ptr(dpre), _ptr(ws), nbytes)
-    return c.back(dx), c.back(dgate), c.back(dres), dpost, dpre
+    return dx, dgate, dres, dpost, dpre
 
 
 class _BlockNorm(torch.autograd.Function):

@@ -56,7 +56,7 @@ def test_neighbours_that_are_not_finite(dt, bad):
 @pytest.mark.parametrize("dt,T", [(BF, 200), (F32, 60)])
 def test_gates_that_forget_all(dt, T):
     x = inputs(1, T, 2, 2, 64, 64, dt, F32, 1, 5)
-    for t in (0, 17, 18, 63, 64, T - 1):
+    for t in {0, 17, 18, min(63, T - 2), min(64, T - 2), T - 1}:
         x["g"][:, t] = -math.inf
     x["g"][:, 40] = -1e4
     check(x, label="resets")
