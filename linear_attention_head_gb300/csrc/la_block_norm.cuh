@@ -177,25 +177,28 @@ template <int TPR_, int NV_> struct Plan {
 
 // Sums over the row's threads, in a fixed order.  turn: alternates, so that one
 // barrier a sum is enough.
-template <typename PL>
+// TWO: x.y is wanted too.
+template <typename PL, bool TWO = false>
 __device__ __forceinline__ float2 row_sum(float2 x, float2 (*red)[PL::WARPS], int &turn)
 {
 #pragma unroll
     for (int m = 1; m < (PL::TPR < 32 ? PL::TPR : 32); m *= 2) {
         x.x += __shfl_xor_sync(0xffffffffu, x.x, m);
-        x.y += __shfl_xor_sync(0xffffffffu, x.y, m);
+        if (TWO)
+            x.y += __shfl_xor_sync(0xffffffffu, x.y, m);
     }
     if (PL::TPR > 32) {
         turn ^= 1;
         if ((threadIdx.x & 31) == 0)
             red[turn][threadIdx.x >> 5] = x;
         __syncthreads();
-        x = make_float2(0.f, 0.f);
+        // a warp's sum a lane (again and again where there are fewer), traded likewise
+        x = red[turn][threadIdx.x & (PL::WARPS - 1)];
 #pragma unroll
-        for (int w = 0; w < PL::WARPS; ++w) {
-            const float2 y = red[turn][w];
-            x.x += y.x;
-            x.y += y.y;
+        for (int m = 1; m < PL::WARPS; m *= 2) {
+            x.x += __shfl_xor_sync(0xffffffffu, x.x, m);
+            if (TWO)
+                x.y += __shfl_xor_sync(0xffffffffu, x.y, m);
         }
     }
     return x;
@@ -536,7 +539,7 @@ __global__ void __launch_bounds__(PL::CTA, PL::BLOCKS) block_norm_bwd_kernel(con
                     sh = fma2(h[v][m], h[v][m], sh);
                     su = fma2(h[v][m], mul2(pair_of(dy[v], m), wpre[v][m]), su);
                 }
-            const float2 s = row_sum<PL>(make_float2(sum_of(sh), sum_of(su)), red, turn);
+            const float2 s = row_sum<PL, true>(make_float2(sum_of(sh), sum_of(su)), red, turn);
             const float rh = rsqrtf(s.x * inv_d + a.eps);
             const float mean = -s.y * inv_d * rh * rh;
 #pragma unroll
