@@ -527,6 +527,8 @@ __global__ void __launch_bounds__(PL::CTA, PL::BLOCKS) block_norm_bwd_kernel(con
                     sx = fma2(t, t, sx);
                 }
             rx = rsqrtf(row_sum<PL>(make_float2(sum_of(sx), 0.f), red, turn).x * inv_d + a.eps);
+            // a group without a row: 0 times what eps 0 makes infinite is no 0
+            rx = PL::GROUPS > 1 && !live ? 0.f : rx;
         }
         if (pre) {      // h again, and its two sums
             F2 h[NV][4], sh = f2(0.f), su = f2(0.f);
@@ -543,7 +545,7 @@ __global__ void __launch_bounds__(PL::CTA, PL::BLOCKS) block_norm_bwd_kernel(con
                     su = fma2(h[v][m], mul2(pair_of(dy[v], m), wpre[v][m]), su);
                 }
             const float2 s = row_sum<PL, true>(make_float2(sum_of(sh), sum_of(su)), red, turn);
-            const float rh = rsqrtf(s.x * inv_d + a.eps);
+            const float rh = PL::GROUPS > 1 && !live ? 0.f : rsqrtf(s.x * inv_d + a.eps);
             const float mean = -s.y * inv_d * rh * rh;
 #pragma unroll
             for (int v = 0; v < NV; ++v)

@@ -214,3 +214,18 @@ def test_captured():
     graph.replay()
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("shape", [(1, 5, 2, 64), (1, 3, 250), (2, 3, 7), (1, 1, 16)])
+def test_no_eps_and_fewer_rows_than_groups(shape, dt):
+    # eps 0: the groups of a CTA that have no row add nothing to the weights' gradients
+    x = make(shape, dt, F32, 1, 1, 1, 1, 21)
+    d = {n: t.cuda() if t is not None else None for n, t in x.items()}
+    ref = R.block_norm(**x, eps=0.0)
+    got = la.block_norm_bwd(d["x"], d["dh"], d["dy"], **call(d, eps=0.0))
+    rows = x["x"].numel() // shape[-1]
+    for name, t in zip(("dx", "dgate", "dres", "dpost", "dpre"), got):
+        weight = name in ("dpost", "dpre")
+        near(t, ref[name], ref[name + "_s"], F32 if weight else dt, "%s %s" % (shape, name),
+             (256 + (rows if weight else 0)) * U)
