@@ -351,7 +351,8 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
     const int ksteps = (a.D + 15) / 16;
     float g = 0.f, b = 0.f;
     if (tid < n) {
-        g = fmaxf(gate_at(a.g, a.gate_bf16, q.row, q.bos + t0 + tid, h), LEAST_GATE);
+        g = gate_at(a.g, a.gate_bf16, q.row, q.bos + t0 + tid, h);
+        g = g < LEAST_GATE ? LEAST_GATE : g;    // (a NaN stays one)
         b = gate_at(a.beta, a.gate_bf16, q.row, q.bos + t0 + tid, h);
     }
     {   // every load on its way before the first is waited for

@@ -252,6 +252,19 @@ def test_withheld_handoff(T):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T,at", [(12, 5), (300, 100)])
+def test_a_gate_that_is_not_a_number(T, at):
+    # it shows: in every output of its head from its token on, and in no other head
+    x = cuda(inputs(1, T, 2, 2, 64, 64, BF, F32, 1, 17))
+    want = la.gated_delta_fwd(*args(x), initial_state=x["init"])
+    x["g"][0, at, 1] = math.nan
+    o, fin = la.gated_delta_fwd(*args(x), initial_state=x["init"])
+    assert torch.equal(o[:, :, 0], want[0][:, :, 0]) and torch.equal(fin[:, 0], want[1][:, 0])
+    assert o[:, at:, 1].isnan().all() and fin[:, 1].isnan().all()
+    before = at // 64 * 64 if T > 16 else at
+    assert torch.equal(o[:, :before, 1], want[0][:, :before, 1])
+
+
 def test_refused_tensors():
     x = cuda(inputs(1, 20, 4, 2, 64, 64, BF, F32, 1, 1))
     with pytest.raises(ValueError, match="divide"):
