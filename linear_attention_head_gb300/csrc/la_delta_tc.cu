@@ -1852,7 +1852,8 @@ __global__ void __launch_bounds__(SCAN) delta_scan_kernel(const DeltaArgs a, con
     const int c0 = 4 * (threadIdx.x & 1), d = threadIdx.x >> 1;
     const int e0 = blockIdx.x % cols * SCAN_COLS + c0;
     const Seq sq = sequence(a.cu, a.T, n);
-    const int count = sq.len > 0 ? (int)((sq.len + seg_len - 1) / seg_len) : 1;
+    // never more than there is room for, whatever the table on the device says
+    const int count = sq.len > 0 ? (int)min((sq.len + seg_len - 1) / seg_len, (int64_t)segs) : 1;
     const bool row = d < a.D;
     auto at = [&](int i) {      // the i-th segment in the scan's order
         return ((int64_t)n * segs + (BWD ? count - 1 - i : i)) * a.H + h;
