@@ -646,7 +646,8 @@ la_status la_gated_delta_fwd(const la_delta_dims *dims, int32_t dtype, const voi
  *   workspace      256-byte aligned, la_gated_delta_workspace_size bytes with
  *                  backward = 1 (saved given) or 2 (saved NULL)
  * Where the forward's sizes and strides give the tensor-core kernels, so do the
- * backward's; the strides of d_o, dq, dk, dv must then be multiples of 8 too and
+ * backward's (dq, dk, dg, dbeta are then within some 3e-3 of exact arithmetic, their
+ * operands being rounded to bf16 once; dv and d_initial_state are as the forward's); the strides of d_o, dq, dk, dv must then be multiples of 8 too and
  * every token tensor start on a 16-byte boundary (LA_ERR_INVALID_ARG). */
 la_status la_gated_delta_bwd(const la_delta_dims *dims, int32_t dtype, const void *q,
                              const void *k, const void *v, const void *g, const void *beta,
