@@ -537,7 +537,7 @@ template <bool BWD> struct SweepLayout {
     static constexpr int OOFF = SOFF + STILE;                       // O on its way out
     static constexpr int TOFF = OOFF + (BWD ? 0 : 16384);
     static constexpr int MOFF = TOFF + NT * TAB;
-    static constexpr int NBAR = 4 * NS + 2 * NT + 21;
+    static constexpr int NBAR = 4 * NS + 2 * NT + 18 + 2 * NS + 2;
     static constexpr int SLOT = MOFF + NBAR * 8;
     static constexpr int ABORT = SLOT + 4;
     static constexpr int RANK = ABORT + 4;
@@ -635,13 +635,15 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
     uint64_t *d_ready = bars + 11;      // beta Eps
     uint64_t *i_ready = bars + 12;      // the state's image
     uint64_t *i_free = bars + 13;       // it has been read
-    uint64_t *td_ready = bars + 14;     // back: dO^T in TMEM
-    uint64_t *o_ready = bars + 15;      // O in shared memory
-    uint64_t *o_free = bars + 16;       // it has been read
-    uint64_t *e_ready = bars + 17;      // Eps's (R's) image
-    uint64_t *e_free = bars + 18;       // it has been read
-    uint64_t *x_read = bars + 19;       // forward: Eps read by the side warps
-    uint64_t *drain = bars + 20;
+    uint64_t *o_ready = bars + 14;      // O in shared memory
+    uint64_t *o_free = bars + 15;       // it has been read
+    uint64_t *x_read = bars + 16;       // forward: Eps read by the side warps
+    uint64_t *drain = bars + 17;
+    // These take turns by chunk: what arrives for the next chunk does not wait until its
+    // waiter has seen this one, and a waiter that comes a phase late waits for good.
+    uint64_t *e_ready = bars + 18;              // [NS] Eps's (R's) image
+    uint64_t *e_free = bars + 18 + NS;          // [NS] it has been read
+    uint64_t *td_ready = bars + 18 + 2 * NS;    // [2] back: dO^T in TMEM
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::SLOT);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::ABORT);
     volatile int *rank_slot = reinterpret_cast<volatile int *>(sm + L::RANK);
@@ -653,6 +655,8 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             mbar_init(&fullv[i], 1);
             mbar_init(&fullb[i], 1);
             mbar_init(&empty[i], 1);
+            mbar_init(&e_ready[i], SIDE / 32);
+            mbar_init(&e_free[i], 1);
         }
         for (int i = 0; i < NT; ++i) {
             mbar_init(&tfull[i], 1);
@@ -669,12 +673,11 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         mbar_init(d_ready, CHAIN / 32);
         mbar_init(x_read, SIDE / 32);
         mbar_init(i_ready, CHAIN / 32);
-        mbar_init(e_ready, SIDE / 32);
-        mbar_init(e_free, 1);
         mbar_init(o_ready, SIDE / 32);
         mbar_init(o_free, 1);
         mbar_init(i_free, 1);
-        mbar_init(td_ready, SIDE / 32);
+        mbar_init(&td_ready[0], SIDE / 32);
+        mbar_init(&td_ready[1], SIDE / 32);
         mbar_init(r_ready, SIDE / 32);
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -773,7 +776,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                     break;
                 if (c >= NS) {
                     // Eps's (R's) image lies where V (dO) was
-                    if (!(going = (!keep || wait_call(e_free, (c - NS) & 1, abort_flag)) &&
+                    if (!(going = (!keep || wait_call(&e_free[s], (c / NS - 1) & 1, abort_flag)) &&
                                   wait_call(&empty[s], (c / NS - 1) & 1, abort_flag)))
                         break;
                 }
@@ -917,7 +920,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             // dO^T goes in from TMEM: as an A operand in shared memory it would lie
             // MN-major (delta_grads was slower with such operands)
             auto prior = [&](int c) {   // dO^T P
-                if (!both(p_ready, c) || !both(td_ready, c))
+                if (!both(p_ready, c) || !both(&td_ready[c & 1], c >> 1))
                     return false;
                 if (one)
 #pragma unroll 1
@@ -1042,12 +1045,12 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                     bulk_commit_group();
                     bulk_wait_read_all();
                     mbar_arrive(i_free);
-                    if (!wait_call(e_ready, c & 1, abort_flag))
+                    if (!wait_call(&e_ready[c % NS], (c / NS) & 1, abort_flag))
                         break;
                     bulk_store(eimg + tile_of(c) * ETILE, sm + (c % NS) * STAGE + VD, ETILE);
                     bulk_commit_group();
                     bulk_wait_read_all();
-                    mbar_arrive(e_free);
+                    mbar_arrive(&e_free[c % NS]);
                 }
                 if (some_o) {
                     if (!wait_call(o_ready, c & 1, abort_flag))
@@ -1230,7 +1233,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(e_ready);
+                    mbar_arrive(&e_ready[s]);
             }
             // forward: beta Eps over this half's own columns of T1, for O
             if (!BWD && !states) {
@@ -1298,7 +1301,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(td_ready);
+                    mbar_arrive(&td_ready[c & 1]);
             }
             if (!warp_all(wait_role<BWD>(&tfull[c % NT], (c / NT) & 1, abort_flag)) ||
                 !warp_all(wait_role<BWD>(sc_full, c & 1, abort_flag)))
@@ -1388,7 +1391,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(e_ready);
+                    mbar_arrive(&e_ready[s]);
             }
             if constexpr (!BWD) {
                 uint32_t inter[32], w[32];
