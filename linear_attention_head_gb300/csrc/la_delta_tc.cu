@@ -60,9 +60,10 @@ constexpr int C = 64;                           // tokens a chunk
 constexpr int BTILE = 16384;                    // B hi, B lo: [64][64] bf16 each
 constexpr int STILE = 32768;                    // S^T or K'^T: [2][128 e][64 d] bf16
 constexpr int ETILE = 16384;                    // Eps or R: [2][64 tokens][64 e] bf16
-// per token: -e^G, -beta, kappa, kappa beta, -e^G beta, beta, G / ln 2, each for a
-// chunk's 64 tokens in a row
-constexpr int TNEG = 0, TNB = 1, TKAP = 2, TKB = 3, TNGB = 4, TBETA = 5, TLOG = 6, TABS = 7;
+// per token: -e^G, -beta, kappa, kappa beta, -e^G beta, beta, G / ln 2 as two floats,
+// each for a chunk's 64 tokens in a row
+constexpr int TNEG = 0, TNB = 1, TKAP = 2, TKB = 3, TNGB = 4, TBETA = 5, TLOG = 6, TLOW = 7,
+              TABS = 8;
 constexpr int TAB = TABS * C * 4;
 constexpr float LEAST_GATE = -100.f;            // e^-100 is 0 beside anything kept
 
@@ -179,6 +180,10 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
 {
     return un(la::mul2(f2(a.x, a.y), f2(b.x, b.y)));
 }
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    return un(la::add2(f2(a.x, a.y), f2(b.x, b.y)));
+}
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
     return un(la::fma2(f2(a.x, a.y), f2(b.x, b.y), f2(c.x, c.y)));
@@ -215,6 +220,28 @@ __device__ __forceinline__ float exp2_fast(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Running sums of gates as two floats (hi, lo; 2^-46 or so): strong gates leave sums of
+// thousands, and the decays between slow ones after them are differences of such sums.
+// In one float a decay was off by up to 2.4e-4 (32 resets in a chunk), so now by 2^-24 a
+// unit of the difference itself.
+__device__ __forceinline__ float2 sum_two(float2 a, float2 b)
+{
+    const float s = a.x + b.x, t = s - a.x;
+    const float e = (a.x - (s - t)) + (b.x - t) + (a.y + b.y);
+    const float hi = s + e;
+    return make_float2(hi, e - (hi - s));
+}
+__device__ __forceinline__ float less_two(float2 a, float2 b) { return (a.x - b.x) + (a.y - b.y); }
+// times log2 e
+__device__ __forceinline__ float2 to_log2(float2 a)
+{
+    constexpr float H = 1.4426950408889634f, LO = (float)(1.4426950408889634 - (double)H);
+    const float p = a.x * H;
+    const float e = fmaf(a.x, LO, fmaf(a.y, H, fmaf(a.x, H, -p)));
+    const float hi = p + e;
+    return make_float2(hi, e - (hi - p));
 }
 
 __device__ __forceinline__ void bulk_prefetch(const void *src, uint32_t bytes)
@@ -335,7 +362,8 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
     Factor &R = *reinterpret_cast<Factor *>(over);
     __shared__ __align__(16) Factor L;
     __shared__ __align__(16) float diag[4][16][DP];
-    __shared__ float G[C], beta[C], part[2];
+    __shared__ float2 G[C], part[2];
+    __shared__ float beta[C];
     const int64_t slot = (int)blockIdx.x / a.H;
     const int h = (int)blockIdx.x - (int)slot * a.H;
     const Seq q = sequence_of_slot(a.cu, a.T, a.N, slot);
@@ -349,10 +377,11 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
     const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k.p) + q.row * a.k.sb +
                              (q.bos + t0) * a.k.st + (int64_t)(h / a.k.hdiv) * a.k.sh;
     const int ksteps = (a.D + 15) / 16;
-    float g = 0.f, b = 0.f;
+    float2 g = make_float2(0.f, 0.f);
+    float b = 0.f;
     if (tid < n) {
-        g = gate_at(a.g, a.gate_bf16, q.row, q.bos + t0 + tid, h);
-        g = g < LEAST_GATE ? LEAST_GATE : g;    // (a NaN stays one)
+        g.x = gate_at(a.g, a.gate_bf16, q.row, q.bos + t0 + tid, h);
+        g.x = g.x < LEAST_GATE ? LEAST_GATE : g.x;      // (a NaN stays one)
         b = gate_at(a.beta, a.gate_bf16, q.row, q.bos + t0 + tid, h);
     }
     {   // every load on its way before the first is waited for
@@ -371,9 +400,10 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
     if (tid < C) {
 #pragma unroll
         for (int m = 1; m < 32; m *= 2) {
-            const float y = __shfl_up_sync(0xffffffffu, g, m);
+            const float2 y = make_float2(__shfl_up_sync(0xffffffffu, g.x, m),
+                                         __shfl_up_sync(0xffffffffu, g.y, m));
             if (lane >= m)
-                g += y;
+                g = sum_two(g, y);
         }
         if (lane == 31)
             part[warp] = g;
@@ -381,18 +411,18 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
     }
     __syncthreads();
     if (tid < C) {
-        g = tid < 32 ? g : g + part[0];
-        const float all = part[0] + part[1];
+        g = tid < 32 ? g : sum_two(g, part[0]);
         float *tab = sc.tab + tile * TABS * C + tid;
-        const float eg = expf(g), kap = expf(all - g);
+        const float eg = expf(g.x), kap = expf(less_two(sum_two(part[1], part[0]), g));
         tab[TNEG * C] = -eg;
         tab[TNB * C] = -b;
         tab[TKAP * C] = kap;
         tab[TKB * C] = kap * b;
         tab[TNGB * C] = -eg * b;
         tab[TBETA * C] = b;
-        g *= 1.4426950408889634f;
-        tab[TLOG * C] = g;
+        g = to_log2(g);
+        tab[TLOG * C] = g.x;
+        tab[TLOW * C] = g.y;
         G[tid] = g;
     }
     // rows 16 warp .. of K K^T, columns up to the diagonal block
@@ -415,16 +445,16 @@ __global__ void __launch_bounds__(PREP) delta_prep_kernel(const DeltaArgs a, con
     __syncthreads();    // K has been read, G written
     {   // A in place of K K^T; zeros from the diagonal on
         const int i0 = 16 * warp + (lane >> 2), j0 = 2 * (lane & 3);
-        const float g0 = G[i0], g1 = G[i0 + 8];
+        const float2 g0 = G[i0], g1 = G[i0 + 8];
 #pragma unroll
         for (int nb = 0; nb < 8; ++nb)
             if (nb < 2 * (warp + 1)) {
                 const int j = 8 * nb + j0;
-                const float h0 = G[j], h1 = G[j + 1];
-                acc[nb][0] = j < i0 ? exp2_fast(g0 - h0) * acc[nb][0] : 0.f;
-                acc[nb][1] = j + 1 < i0 ? exp2_fast(g0 - h1) * acc[nb][1] : 0.f;
-                acc[nb][2] = j < i0 + 8 ? exp2_fast(g1 - h0) * acc[nb][2] : 0.f;
-                acc[nb][3] = j + 1 < i0 + 8 ? exp2_fast(g1 - h1) * acc[nb][3] : 0.f;
+                const float2 h0 = G[j], h1 = G[j + 1];
+                acc[nb][0] = j < i0 ? exp2_fast(less_two(g0, h0)) * acc[nb][0] : 0.f;
+                acc[nb][1] = j + 1 < i0 ? exp2_fast(less_two(g0, h1)) * acc[nb][1] : 0.f;
+                acc[nb][2] = j < i0 + 8 ? exp2_fast(less_two(g1, h0)) * acc[nb][2] : 0.f;
+                acc[nb][3] = j + 1 < i0 + 8 ? exp2_fast(less_two(g1, h1)) * acc[nb][3] : 0.f;
             }
         put_factor<8>(L, acc, 16 * warp, 0, nullptr);
 #pragma unroll
@@ -1312,16 +1342,18 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 uint8_t *to = sm + POFF + i * 128;
                 uint32_t hi[16] = {}, lo[16] = {};
                 if (half <= q) {
-                    const float gi = tab[TLOG * C + i];
-                    const float2 gi2 = make_float2(gi, gi), s2 = make_float2(a.scale, a.scale);
+                    const float gi = tab[TLOG * C + i], li = tab[TLOW * C + i];
+                    const float2 gi2 = make_float2(gi, gi), li2 = make_float2(li, li);
+                    const float2 s2 = make_float2(a.scale, a.scale);
                     const float2 minus = make_float2(-1.f, -1.f);
                     uint32_t r[32];
                     tmem_ld32(lanes + (BWD ? T2 : TR) + j0, r);
-                    const float *gj = tab + TLOG * C + j0;
+                    const float *gj = tab + TLOG * C + j0, *lj = tab + TLOW * C + j0;
 #pragma unroll
                     for (int x = 0; x < 16; ++x) {
-                        const float2 d =
-                            fma2(*reinterpret_cast<const float2 *>(gj + 2 * x), minus, gi2);
+                        const float2 d = add2(
+                            fma2(*reinterpret_cast<const float2 *>(gj + 2 * x), minus, gi2),
+                            fma2(*reinterpret_cast<const float2 *>(lj + 2 * x), minus, li2));
                         float2 y = mul2(mul2(make_float2(exp2_fast(d.x), exp2_fast(d.y)), s2),
                                         pair_of(r, x));
                         if (half == q) {
@@ -1466,8 +1498,9 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
 constexpr int GRADS = 256;
 constexpr int GQ = 0, GE = 32768, GD = 49152, GS = 81920, GBAR = 114688;
 constexpr int GW = GD, GWT = GD + 16384;        // over dO and R
-constexpr int GTAB = GBAR + 64, GDYN = GTAB + 2 * C * 4;     // beta, G / ln 2
-static_assert(TLOG == TBETA + 1 && 2 * (GDYN + 1024) <= 228 * 1024, "two CTAs an SM");
+constexpr int GTAB = GBAR + 64, GDYN = GTAB + 3 * C * 4;     // beta, G / ln 2
+static_assert(TLOG == TBETA + 1 && TLOW == TLOG + 1 && 2 * (GDYN + 1024) <= 228 * 1024,
+              "two CTAs an SM");
 constexpr uint32_t U1 = 0, UC = 128, UW = 128, UCOLS = 256;
 
 struct GradParams {
@@ -1545,12 +1578,13 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tm = *tslot;
     const uint32_t lanes = tm + ((uint32_t)(32 * q) << 16);
-    const float *betas = reinterpret_cast<const float *>(sm + GTAB), *logs = betas + C;
+    const float *betas = reinterpret_cast<const float *>(sm + GTAB), *logs = betas + C,
+                *lows = logs + C;
 
     if (tid == 0) {
         const int hq = h / a.q.hdiv, t = (int)(sq.bos + t0), row = (int)sq.row;
-        mbar_arrive_expect_tx(in_full, 3 * 16384 + 2 * ETILE + STILE + 2 * C * 4);
-        bulk_load(sm + GTAB, P.sc.tab + (tile * TABS + TBETA) * C, 2 * C * 4, in_full);
+        mbar_arrive_expect_tx(in_full, 3 * 16384 + 2 * ETILE + STILE + 3 * C * 4);
+        bulk_load(sm + GTAB, P.sc.tab + (tile * TABS + TBETA) * C, 3 * C * 4, in_full);
         bulk_load(sm + GS, P.sc.s + tile * STILE, STILE, in_full);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -1621,6 +1655,7 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
     const int i = 32 * (q & 1) + lane;              // this lane's token
     const bool key = q >= 2;                        // R's lanes: dK's row part
     const float gi = logs[i], eg = exp2_fast(gi), beta = betas[i];
+    const float li = lows[i];
     {   // W1 (W2), row i, columns 32 half .., as rows and as columns
         const int j0 = 32 * half;
         uint32_t r[32];
@@ -1634,20 +1669,21 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
                 __float2bfloat16_rn(d);
         }
         const float f = key ? -beta : a.scale;
+        const float2 f2 = make_float2(f, f), gi2 = make_float2(gi, gi), li2 = make_float2(li, li);
+        const float2 minus = make_float2(-1.f, -1.f);
         const int last = key ? i - 1 : i;
         float w[32];
 #pragma unroll
-        for (int x4 = 0; x4 < 8; ++x4) {
-            const float4 b = *reinterpret_cast<const float4 *>(betas + j0 + 4 * x4);
-            const float4 g = *reinterpret_cast<const float4 *>(logs + j0 + 4 * x4);
-            const float bb[4] = {b.x, b.y, b.z, b.w}, gg[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const int x = 4 * x4 + y;
-                w[x] = j0 + x <= last
-                           ? f * bb[y] * exp2_fast(gi - gg[y]) * __uint_as_float(r[x])
-                           : 0.f;
-            }
+        for (int x = 0; x < 16; ++x) {
+            auto pair = [&](const float *t) {
+                return *reinterpret_cast<const float2 *>(t + j0 + 2 * x);
+            };
+            const float2 d = add2(fma2(pair(logs), minus, gi2), fma2(pair(lows), minus, li2));
+            const float2 y = mul2(mul2(mul2(f2, pair(betas)),
+                                       make_float2(exp2_fast(d.x), exp2_fast(d.y))),
+                                  pair_of(r, x));
+            w[2 * x] = j0 + 2 * x <= last ? y.x : 0.f;
+            w[2 * x + 1] = j0 + 2 * x + 1 <= last ? y.y : 0.f;
         }
         put_half_row(sm + GW + (key ? 8192 : 0) + i * 128, i, 4 * half, w);
         uint8_t *to = sm + GWT + (key ? 8192 : 0) + (i & 6) * 2;
@@ -1715,7 +1751,7 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
     ok = warp_all(bwait(c_full, 0, abort_flag)) && ok;
     tc_fence_after();
     if (key) {
-        const float f = beta * exp2_fast(logs[C - 1] - gi);
+        const float f = beta * exp2_fast((logs[C - 1] - gi) + (lows[C - 1] - li));
 #pragma unroll 1
         for (int p = 0; p < 2; ++p) {
             uint32_t r[32];
