@@ -588,7 +588,7 @@ __device__ __forceinline__ uint32_t tok_col(int kk, int lo)
 }
 
 struct SweepParams {
-    CUtensorMap mq, mk, mv, mo;     // mv: v, or back: do; mo: o, where a.o is given
+    CUtensorMap mq, mk, mv, mo;     // mv: v, or back: do; mo: o, where a.o is given, or back: dv
     DeltaArgs a;
     Scratch sc;
     int segs, seg_len;  // segments of a sequence (1: whole), their tokens: whole chunks
@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         prefetch_tmap(&P.mq);
         prefetch_tmap(&P.mk);
         prefetch_tmap(&P.mv);
-        if (!BWD && a.o.p)
+        if (BWD || a.o.p)
             prefetch_tmap(&P.mo);
     }
     tc_fence_before();
@@ -773,10 +773,17 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
     auto tile_of = [&](int c) { return (sq.slot + chunk(c)) * a.H + h; };
     const float *tabs = reinterpret_cast<const float *>(sm + L::TOFF);
     const bool keep = !states && (BWD || P.sc.s);   // the images are wanted
-    // O leaves tile by tile; the last rows of a packed sequence row by row, the rows
+    // O (dV) leaves tile by tile; the last rows of a packed sequence row by row, the rows
     // after them are another's
     const bool some_o = !BWD && a.o.p && !states;
     auto o_tile = [&](int c) { return !a.cu || tokens(c) == C; };
+    // this lane's first row of 32 from token j0 of the chunk, at its pair of channels
+    auto token_rows = [&](const TokOut &o, int c, int j0, int e) {
+        return reinterpret_cast<uint8_t *>(
+            static_cast<__nv_bfloat16 *>(o.p) + sq.row * o.sb +
+            (sq.bos + (int64_t)chunk(c) * C + j0 + (lane & 1)) * o.st + (int64_t)h * o.sh +
+            (e & ~1));
+    };
 
     if (warp == 0) {
         // ------------------------------------------------------------- loads
@@ -805,7 +812,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                 if (!going)
                     break;
                 if (c >= NS) {
-                    // Eps's (R's) image lies where V (dO) was
+                    // Eps's (R's) image lies where V (dO) was, dV's where Q was
                     if (!(going = (!keep || wait_call(&e_free[s], (c / NS - 1) & 1, abort_flag)) &&
                                   wait_call(&empty[s], (c / NS - 1) & 1, abort_flag)))
                         break;
@@ -1077,7 +1084,15 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                     mbar_arrive(i_free);
                     if (!wait_call(&e_ready[c % NS], (c / NS) & 1, abort_flag))
                         break;
-                    bulk_store(eimg + tile_of(c) * ETILE, sm + (c % NS) * STAGE + VD, ETILE);
+                    const uint8_t *st = sm + (c % NS) * STAGE;
+                    bulk_store(eimg + tile_of(c) * ETILE, st + VD, ETILE);
+                    if (BWD && o_tile(c)) {
+                        const int t = (int)(sq.bos + (int64_t)chunk(c) * C);
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+                            if (64 * b < a.E)
+                                tma_store_4d(&P.mo, st + QK + b * 16384, 64 * b, h, t, (int)sq.row);
+                    }
                     bulk_commit_group();
                     bulk_wait_read_all();
                     mbar_arrive(&e_free[c % NS]);
@@ -1253,13 +1268,25 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(w_ready);
-            // off the chain, while the state is made.  Back: R's image
+            // off the chain, while the state is made.  Back: R's image, and dV from R before
+            // its rounding, where Q was: the scores and scale e^G Q are done with it
             if (BWD && keep) {
                 float x32[32];
 #pragma unroll
                 for (int x = 0; x < 32; ++x)
                     x32[x] = __uint_as_float(r[x]);
                 store_image(x32, half, e, sm + s * STAGE + VD);
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const float2 y = mul2(pair_at(TBETA, x), pair_of(r, x));
+                    x32[2 * x] = y.x;
+                    x32[2 * x + 1] = y.y;
+                }
+                if (o_tile(c))
+                    store_image(x32, half, e, sm + s * STAGE + QK + (e >> 6) * 8192);
+                else
+                    store_rows(x32, lane & 1, token_rows(a.dv, c, j0, e), 4 * a.dv.st,
+                               e < a.E ? n - j0 : 0);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
@@ -1457,12 +1484,8 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
                         store_image(y, half, row, sm + L::OOFF);
                         fence_proxy_async_smem();
                     } else {
-                        const bool odd = lane & 1;
-                        uint8_t *to = reinterpret_cast<uint8_t *>(
-                            static_cast<__nv_bfloat16 *>(a.o.p) + sq.row * a.o.sb +
-                            (sq.bos + (int64_t)c * C + j0 + odd) * a.o.st +
-                            (int64_t)h * a.o.sh + (row & ~1));
-                        store_rows(y, odd, to, 4 * a.o.st, row < a.E ? n - j0 : 0);
+                        store_rows(y, lane & 1, token_rows(a.o, c, j0, row), 4 * a.o.st,
+                                   row < a.E ? n - j0 : 0);
                     }
                     __syncwarp();
                     if (lane == 0)
@@ -1483,7 +1506,7 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
     }
 }
 
-// ---- dQ, dK, dV, dg, dbeta ----------------------------------------------------------
+// ---- dQ, dK, dg, dbeta --------------------------------------------------------------
 //
 // A CTA a (chunk, head), two of them an SM: 112 KB of tiles, 256 TMEM columns.  Lanes
 // are tokens here: [dO; R] lie as one 128-row tile, as [Q; K] do, so that one product
@@ -1626,19 +1649,6 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
         mma_commit(one_full);
     }
     __syncwarp();
-    // dv = beta R, row by row
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        const int i = (tid >> 4) + 16 * x, c16 = tid & 15;
-        if (i < n && 8 * c16 < a.E) {
-            const float f = betas[i];
-            const uint4 v = *reinterpret_cast<const uint4 *>(
-                sm + GD + (c16 >> 3) * 16384 + 8192 + i * 128 + (((c16 & 7) ^ (i & 7)) << 4));
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.dv.p) + sq.row * a.dv.sb +
-                                       (sq.bos + t0 + i) * a.dv.st + (int64_t)h * a.dv.sh +
-                                       8 * c16) = scale8(v, f);
-        }
-    }
     // this thread's share of S for <S, K'>
     uint4 sv[8];
 #pragma unroll
@@ -1646,7 +1656,7 @@ __global__ void __launch_bounds__(GRADS, 2) delta_grads_kernel(const __grid_cons
         sv[x] = *reinterpret_cast<const uint4 *>(sm + GS + tid * 16 + x * 4096);
     ok = warp_all(bwait(one_full, 0, abort_flag)) && ok;
     tc_fence_after();
-    __syncthreads();    // S and R have been read, by the products and by every thread
+    __syncthreads();    // S has been read, by the products and by every thread
     if (tid == 0 && ok) {
         mbar_arrive_expect_tx(k_full, STILE);
         bulk_load(sm + GS, P.sc.k + tile * STILE, STILE, k_full);
@@ -2036,8 +2046,8 @@ template <bool BWD> cudaError_t sweep(const DeltaArgs &a, const Scratch &sc, cud
     if (!token_map(&p.mq, a, a.q, a.HK, a.D) || !token_map(&p.mk, a, a.k, a.HK, a.D) ||
         !token_map(&p.mv, a, BWD ? a.d_o : a.v, a.H, a.E))
         return cudaErrorNotSupported;
-    if (!BWD && a.o.p &&
-        !token_map(&p.mo, a, Tok{a.o.p, a.o.sb, a.o.st, a.o.sh, 1}, a.H, a.E))
+    const TokOut &out = BWD ? a.dv : a.o;
+    if (out.p && !token_map(&p.mo, a, Tok{out.p, out.sb, out.st, out.sh, 1}, a.H, a.E))
         return cudaErrorNotSupported;
     p.a = a;
     p.sc = sc;

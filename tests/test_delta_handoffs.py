@@ -213,8 +213,8 @@ def sweep(bwd, keep, states, some_o, nc, turns):
             g.touch(w, False, ("T1", w))
             g.touch(w, True, ("TY", w))
             g.arrive(w, "w_ready", c)
-            if bwd and keep:
-                g.touch(w, True, (stage("VD", c), w))
+            if bwd and keep:    # R's image, and dV's
+                g.touch(w, True, (stage("VD", c), w), (stage("Q", c), w))
                 g.arrive(w, *of("e_ready", n_er, c))
             if not bwd and not states:
                 if keep:
@@ -273,7 +273,7 @@ def sweep(bwd, keep, states, some_o, nc, turns):
             g.touch("stores", False, "SOFF")
             g.arrive("stores", "i_free", c)
             g.wait("stores", *of("e_ready", n_er, c))
-            g.touch("stores", False, stage("VD", c))
+            g.touch("stores", False, stage("VD", c), *([stage("Q", c)] if bwd else []))
             g.arrive("stores", *of("e_free", n_ef, c))
         if some_o:
             g.wait("stores", "o_ready", c)
