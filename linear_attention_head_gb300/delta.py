@@ -175,14 +175,18 @@ class _GatedDelta(torch.autograd.Function):
         y = gated_delta_fwd(q, k, v, g, beta, scale, init, cu, cu_host, keep=grad)
         ctx.save_for_backward(q, k, v, g, beta, init, cu, cu_host, y[2] if grad else None)
         ctx.scale = scale
+        ctx.set_materialize_grads(False)    # a final state that went unused has no gradient
         return y[0], y[1]
 
     @staticmethod
     @once_differentiable
     def backward(ctx, do, dfin):
+        if do is None and dfin is None:
+            return (None,) * 9
         q, k, v, g, beta, init, cu, cu_host, saved = ctx.saved_tensors
+        do = torch.zeros_like(v) if do is None else do.to(v.dtype)
         dq, dk, dv, dg, db, dinit = gated_delta_bwd(
-            q, k, v, g, beta, do.to(v.dtype), ctx.scale, init, dfin, cu, cu_host,
+            q, k, v, g, beta, do, ctx.scale, init, dfin, cu, cu_host,
             want_d_initial_state=init is not None, saved=saved)
         return (dq, dk, dv, dg.to(g.dtype), db.to(beta.dtype),
                 None if dinit is None else dinit.to(init.dtype), None, None, None)
