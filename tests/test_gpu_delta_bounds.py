@@ -9,9 +9,10 @@ below 20 such errors over four chunks, at 6 sigma 20 * 6 * 2^-18 = 4.6e-4 of the
 import pytest
 import torch
 
+import delta_bounds as DB
 import delta_reference as R
 import linear_attention_head_gb300 as la
-from test_gpu_delta import BF, F32, cuda, inputs
+from test_gpu_delta import BF, F32, chunked, cuda, inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -34,5 +35,43 @@ def test_dv_is_rounded_once(size, cu):
     off = (dv.cpu().double() - ref).abs()
     rms = float(ref.square().mean().sqrt())
     over = off - (2.0 ** -8 * ref.abs() + 4.6e-4 * rms)
-    assert float(over.max()) <= 0.0, "%d of %d numbers beyond one rounding, the worst by %.3g rms" % (
+    assert float(over.max()) <= 0.0, "%d of %d numbers beyond one rounding, by up to %.3g rms" % (
         int((over > 0).sum()), over.numel(), float(over.max()) / rms)
+
+
+SIZES = [  # dtype, gates' dtype, (B, T, H, H_qk, D, E), cu
+    (F32, F32, (1, 150, 2, 2, 40, 24), None), (F32, F32, (2, 77, 3, 1, 128, 128), None),
+    (F32, F32, (1, 60, 2, 1, 33, 200), None), (F32, F32, (1, 40, 2, 2, 256, 130), None),
+    (F32, F32, (1, 100, 2, 1, 32, 40), [0, 1, 2, 3, 60, 60, 100]),
+    (BF, BF, (3, 1, 4, 2, 128, 128), None), (BF, F32, (2, 16, 4, 2, 64, 96), None),
+    (BF, F32, (1, 70, 2, 2, 12, 20), None), (BF, F32, (1, 50, 2, 1, 130, 256), None),
+    (BF, BF, (2, 63, 2, 1, 128, 128), None), (BF, F32, (2, 256, 4, 2, 128, 128), None),
+    (BF, F32, (1, 333, 2, 2, 96, 120), None), (BF, F32, (1, 200, 1, 1, 8, 16), None),
+    (BF, F32, (1, 300, 2, 1, 32, 40), [0, 20, 21, 21, 300]),
+    (BF, F32, (1, 2100, 1, 1, 128, 128), None), (BF, F32, (2, 1601, 2, 1, 64, 40), None),
+    (BF, F32, (1, 1764, 1, 1, 32, 24), [0, 0, 30, 1700, 1700, 1764])]
+
+
+@pytest.mark.parametrize("case", range(len(SIZES)))
+@pytest.mark.parametrize("state", [True, False])
+def test_every_output_within_its_bound(case, state):
+    dt, gt, size, cu = SIZES[case]
+    n = size[0] if cu is None else len(cu) - 1
+    x = inputs(*size, dt, gt, n, 41 + case, state)
+    ref = R.delta(x["q"], x["k"], x["v"], x["g"], x["beta"], size[4] ** -0.5, x["init"], cu,
+                  x["do"], x["dfin"])
+    longest = max(hi - lo for _, lo, hi in R.spans(size[0], size[1], cu))
+    tc = chunked(dt, size[4], size[5], longest)
+    d = cuda(x)
+    cu_t = torch.tensor(cu, dtype=torch.int32) if cu is not None else None
+    a = (d["q"], d["k"], d["v"], d["g"], d["beta"])
+    kw = dict(initial_state=d["init"], cu_seqlens=cu_t)
+    o, fin, saved = la.gated_delta_fwd(*a, keep=True, **kw)
+    assert (saved is not None) == tc
+    got = dict(zip(("dq", "dk", "dv", "dg", "dbeta", "dinit"),
+                   la.gated_delta_bwd(*a, d["do"], d_final_state=d["dfin"], saved=saved, **kw)))
+    got.update(o=o, final=fin)
+    terms = DB.terms_of(x["v"], ref["dv"])
+    bad = [t for name, y in got.items()
+           for t in DB.faults(name, y, ref[name], dt, tc, longest, terms)]
+    assert not bad, bad
