@@ -153,8 +153,8 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatil
 }
 
 // Without a clock: for the chain's and the side warps, which wait for what the other
-// warps do or give up.  Those raise abort_flag when a wait of theirs runs out, and end
-// only with everything done that is waited for here.
+// warps do or give up.  Those raise abort_flag when a wait of theirs runs out, the last
+// products' too, and otherwise end only with everything done that is waited for here.
 __device__ __forceinline__ bool wait_here(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
 {
     int i = 0;
@@ -1067,6 +1067,8 @@ __global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_cons
         if (any && one) {   // every product is done before TMEM is released
             mma_commit(drain);
             drain_wait(drain, 0);
+            if (!mbar_try_wait(drain, 0))   // it never came: waits without a clock end too
+                *abort_flag = 1;
         }
         __syncwarp();
     } else if (warp == 18) {

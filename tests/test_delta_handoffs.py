@@ -186,6 +186,9 @@ def sweep(bwd, keep, states, some_o, nc, turns):
             product("P Eps", ["TR"], "T1", "P")
             commit("o_full", c)
 
+    commit("drain", 0)
+    g.wait(mma, "drain", 0)
+
     # chain
     for w in CHAIN:
         for c in range(nc):
@@ -320,6 +323,33 @@ def test_one_barrier_for_both_stages_can_be_missed():
     assert faults(sweep(True, True, False, False, 9, turns=(2, NS, 1)))[0] == {"e_free"}
 
 
+def unclocked(g, drain):
+    """Barriers that the chain or the side warps wait for although no wait with a clock (of the
+    other roles; the last products' where drain is set) would run out if an arrival at them
+    never came."""
+    g.close()
+    clocked = [n for n, bar, _ in g.waits
+               if g.label[n][0] in ("loads", "products", "stores") and (drain or bar != "drain")]
+    return {bar for n, bar, phase in g.waits if g.label[n][0] in CHAIN + SIDE
+            for a in g.arrivals[bar, phase] if not any(g.before(a, c) for c in clocked)}
+
+
+@pytest.mark.parametrize("nc", [1, 2, 9])
+@pytest.mark.parametrize("mode", MODES)
+def test_every_wait_ends(mode, nc):
+    g = sweep(*mode, nc, turns=(2, NS, NS))
+    assert unclocked(g, True) == set()
+    # what the last products' wait is needed for: where no O goes to the stores' waits
+    assert ("s_full" in unclocked(g, False)) == (not mode[3])
+
+
+def test_the_last_products_raise_the_flag():
+    with open(SOURCE) as f:
+        text = f.read()
+    assert re.search(r"drain_wait\(drain, 0\);\s+if \(!mbar_try_wait\(drain, 0\)\)[^\n]*\n"
+                     r"\s+\*abort_flag = 1;", text)
+
+
 def test_the_kernel_has_these_barriers():
     with open(SOURCE) as f:
         text = f.read()
@@ -328,7 +358,7 @@ def test_the_kernel_has_these_barriers():
         assert len(re.findall(r"&%s\[" % name, text)) >= uses, name
         assert not re.search(r"(wait_\w+(<BWD>)?|both|mbar_arrive)\(%s\b" % name, text), name
     # the model knows every barrier of the sweep
-    names = set(re.findall(r"uint64_t \*(\w+) = bars", text)) - {"in_full", "drain"}
+    names = set(re.findall(r"uint64_t \*(\w+) = bars", text)) - {"in_full"}
     model = set()
     for mode in MODES:
         model |= {re.sub(r"\[.*", "", bar) for bar, _ in sweep(*mode, 3, (2, NS, NS)).arrivals}
