@@ -611,7 +611,8 @@ typedef struct la_delta_dims {
  *   cu_seqlens, cu_seqlens_host   as la_fwd
  *   o              [B,T,H,E] of `dtype` (output)
  *   final_state    [N,H,D,E] fp32 output, or NULL; may be initial_state itself
- *   saved          la_gated_delta_saved_size bytes, 256-byte aligned, or NULL:
+ *   saved          la_gated_delta_saved_size bytes (66 KB a chunk and head and,
+ *                  where sequences are cut, 4 D^2 a segment), 256-byte aligned, or NULL:
  *                  what la_gated_delta_bwd starts from, to be passed to it once
  *                  or more; then o's rows must lie as v's (below)
  *   workspace      256-byte aligned, la_gated_delta_workspace_size(..., 0) bytes,
@@ -620,7 +621,8 @@ typedef struct la_delta_dims {
  * are multiples of 8 elements (and positive where the axis is longer than 1),
  * and a sequence of more than 16 tokens: chunks of 64 tokens on the tensor
  * cores, in which every operand that is not an input is split in two bf16 (16
- * bits of it: the states are within some 1e-5 of those of exact arithmetic).
+ * bits of it: the states are within some 1e-5 of those of exact arithmetic,
+ * whatever the gates: their sums are kept in two floats).
  * Where (sequence, head) pairs are at most 76, long sequences are cut in
  * segments that run at once.  Then q, k, v and o must start on 16-byte
  * boundaries, or (without saved) the call runs as every other one: token by
@@ -646,9 +648,11 @@ la_status la_gated_delta_fwd(const la_delta_dims *dims, int32_t dtype, const voi
  *   workspace      256-byte aligned, la_gated_delta_workspace_size bytes with
  *                  backward = 1 (saved given) or 2 (saved NULL)
  * Where the forward's sizes and strides give the tensor-core kernels, so do the
- * backward's (dq, dk, dg, dbeta are then within some 3e-3 of exact arithmetic, their
- * operands being rounded to bf16 once; dv and d_initial_state are as the forward's); the strides of d_o, dq, dk, dv must then be multiples of 8 too and
- * every token tensor start on a 16-byte boundary (LA_ERR_INVALID_ARG). */
+ * backward's; the strides of d_o, dq, dk, dv must then be multiples of 8 too and
+ * every token tensor start on a 16-byte boundary (LA_ERR_INVALID_ARG).  dq, dk,
+ * dg, dbeta are then within some 3e-3 of exact arithmetic (in the norm), their
+ * operands being rounded to bf16 once; dv, rounded once, and d_initial_state are
+ * as the forward's o and final_state. */
 la_status la_gated_delta_bwd(const la_delta_dims *dims, int32_t dtype, const void *q,
                              const void *k, const void *v, const void *g, const void *beta,
                              const void *d_o, float scale, const float *initial_state,

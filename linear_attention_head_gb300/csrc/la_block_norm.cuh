@@ -19,7 +19,16 @@
 // no barrier stands between (gated heads, b4 n8192 32 x 128, forward and backward: 0.40 ms
 // on one GB300, 0.45 with the next row in registers).  There the forward takes 139 us, 0.87
 // of the copy rate, and the backward 255, 0.79; rows of 4096 with all parts, 16380 of them:
-// 107 and 255, the backward bound by its sums over a CTA.  The weights' gradients are summed by each thread over
+// 107 and 255, the backward bound by its sums over a CTA.  Above 4096 channels a thread
+// holds 16 or 32 of a row and no longer keeps them all in registers (spill stores a
+// thread, bf16 and fp32: backward to 8192 channels 488 and 984 bytes, to 16384 3240 and
+// 3968; forward fp32 to 16384 2420).  All parts, 2^26 numbers a tensor, of the copy rate:
+//     channels          1024  2048  4096  5120  7168  8192  12288  16384
+//     bf16 forward      0.87  0.91  0.90  0.60  0.80  0.89  0.70   0.81
+//     bf16 backward     0.67  0.64  0.61  0.33  0.45  0.50  0.13   0.16
+//     fp32 forward      0.65  0.69  0.69  0.51  0.56  0.57  0.32   0.37
+//     fp32 backward     0.57  0.41  0.52  0.26  0.33  0.36  0.15   0.19
+// The weights' gradients are summed by each thread over
 // the rows that it takes, then over a CTA's groups, then over CTAs by a last kernel:
 // a fixed order.
 #pragma once

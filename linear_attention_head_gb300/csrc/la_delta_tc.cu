@@ -21,9 +21,10 @@
 //     dg_t = sum over i >= t in the chunk of (q_i.dq_i + k_i.(row_i - col_i)) + <S', K'>.
 //
 // B needs neither S nor a division by beta.  Four kernels:
-//   delta_prep     B of every chunk, all chunks in parallel (fp32 diagonal blocks, mma.sync between)
+//   delta_prep     B of every chunk, all chunks in parallel (fp32 diagonal blocks, mma.sync
+//                  between)
 //   delta_sweep    <false>: the forward, a CTA a (sequence, head), chunk by chunk
-//                  <true>: the backward's K', from the last chunk to the first
+//                  <true>: the backward's K' and dV, from the last chunk to the first
 //   delta_grads    dQ, dK, dg, dbeta, all chunks in parallel
 // and where (sequence, head) pairs are few, long sequences in segments that run at
 // once: S' = Phi S + H over a segment, Phi (D x D) and H by sweeps without outputs that
@@ -42,11 +43,14 @@
 // hi hi + hi lo + lo hi with fp32 sums: the states stay within 2^-17 a factor
 // instead of 2^-9.  The tensor cores have room: the chain's latency is what a
 // chunk takes.  delta_grads rounds its operands (S, K', Eps, R, W1, W2) to bf16
-// once: its outputs are bf16 gradients that no later chunk depends on.
+// once: its outputs are bf16 gradients that no later chunk depends on.  dV leaves the
+// sweep, which has R in fp32.  The gates' running sums are two floats each.
 //
-// On one GB300, b4 h32 n8192 d128, forward and backward 1.76 ms: delta_prep 0.20, the
-// sweeps 0.50 and 0.51 (DRAM busy 46% and 40%, the tensor pipe 25%: the chain's latency,
-// 4 us a chunk), delta_grads 0.55 (3.2 GB, 0.88 of the copy rate).
+// On one GB300, b4 h32 n8192 d128, forward and backward 1.80 ms: delta_prep 0.21, the
+// sweeps 0.51 and 0.55 (DRAM busy 46% and 41%, the tensor pipe 25% and 21%: the chain's
+// latency, 4 us a chunk), delta_grads 0.52 (3.0 GB, 0.85 of the copy rate).  With 16
+// query and key heads for the 32 value heads it is 2.80: delta_grads 0.73, which writes
+// fp32 parts of dq and dk a value head, and 0.40 for each of their sums over a group.
 
 #include <climits>
 
@@ -271,7 +275,7 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 // the factors as hi + lo (hi hi, hi lo, lo hi), A21 and M in the fp32 fragments that
 // K K^T left in registers.  The left factors (A21, then B) end as B itself, hi and lo:
 // what is written out.  (The joins by fp32 FMAs read their factors again and again from
-// shared memory: 0.30 ms for the 16384 chunks of b4 h32 n8192, then 0.22, now 0.20.)
+// shared memory: 0.30 ms for the 16384 chunks of b4 h32 n8192, then 0.22, now 0.21.)
 
 constexpr int PREP = 128;
 constexpr int KP = 136;         // bf16 a row of K in shared memory
@@ -599,8 +603,8 @@ struct SweepParams {
 // neighbouring lanes trade, each stores a pair of channels of every other token, the
 // even lane from the first on.  at: the lane's first row (its pair), step: bytes from
 // there to the row after next; n: rows there are, from this half's first on.
-__device__ __forceinline__ void store_rows(const float (&x)[32], bool odd, uint8_t *at, int64_t step,
-                                           int n)
+__device__ __forceinline__ void store_rows(const float (&x)[32], bool odd, uint8_t *at,
+                                           int64_t step, int n)
 {
 #pragma unroll
     for (int m = 0; m < 16; ++m) {
@@ -640,7 +644,8 @@ __device__ __forceinline__ void channel(const uint8_t *tile, int e, int half, ui
     }
 }
 template <bool BWD>
-__global__ void __launch_bounds__(SWEEP, 1) delta_sweep_kernel(const __grid_constant__ SweepParams P)
+__global__ void __launch_bounds__(SWEEP, 1)
+    delta_sweep_kernel(const __grid_constant__ SweepParams P)
 {
     using L = SweepLayout<BWD>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1970,9 +1975,16 @@ __global__ void __launch_bounds__(SCAN) delta_scan_kernel(const DeltaArgs a, con
 // ---- host -------------------------------------------------------------------------
 
 // Segments of a sequence: the count with the least time by this model, of a chunk's time
-// in a sweep of states (2.6 us) and in one with outputs (3.2), rounds of CTAs on the
-// 152 SMs of a GB300, and 4 us a step of the scan with its launches: one sequence of
-// 65536 tokens with 8 heads 0.69 ms in 19 segments, 3.1 whole (before the last steps).
+// in a sweep of states (2.6 us) and in one with outputs (3.2), rounds of CTAs on a GB300's
+// 152 SMs, and 4 us a step of the scan with its launches.  The times are those of 128 x
+// 128; narrower states take less in the scan alone.  Forward, one sequence, us, whole and
+// in the segments taken (D = E = 128; 64):
+//     1 head n2048     131, 80;      130, 66        1 head n65536    3570, 328;   3560, 258
+//     16 heads n2047   134, 104;     131, 81        16 heads n65536  3730, 1350;  3710, 1220
+//     32 heads n4096   266, 224;     261, 195       32 heads n32768  1980, 1330;  1960, 1220
+// and where it stays whole (the best count, forced): 1 head n1024 74 (68; 54), 48 heads
+// n16384 1050 (984; 940), 76 heads n16384 1150 (1110; 1056), 128 heads n16384 1330 (2100).
+// The query of the sizes is a host function, so the SMs are not asked of the device.
 struct Segments {
     int count, tokens;
 };
@@ -2066,7 +2078,8 @@ template <bool BWD> cudaError_t sweep(const DeltaArgs &a, const Scratch &sc, cud
     if (seg.count > 1) {
         SweepParams first = p;
         first.states = 1;
-        delta_sweep_kernel<BWD><<<dim3(ctas, BWD ? 1 : 2), SWEEP, SweepLayout<BWD>::DYN, s>>>(first);
+        delta_sweep_kernel<BWD>
+            <<<dim3(ctas, BWD ? 1 : 2), SWEEP, SweepLayout<BWD>::DYN, s>>>(first);
         note_launch();
         if ((e = cudaGetLastError()) != cudaSuccess)
             return e;

@@ -105,7 +105,8 @@ def gated_delta_fwd(q: Tensor, k: Tensor, v: Tensor, g: Tensor, beta: Tensor,
     """The gated delta rule over q, k [B,T,H_qk,D] and v [B,T,H,E] (H a multiple of H_qk), with
     the log-decay g and the write strength beta [B,T,H], both of the tokens' dtype or fp32.
     Returns (o, final_state [N,H,D,E] fp32), and with keep=True (o, final_state, saved): what
-    gated_delta_bwd starts from (None where it needs nothing).
+    gated_delta_bwd starts from (None where it needs nothing), 66 KB for every 64 tokens of a
+    head: 1.1 GB at 4 x 8192 tokens of 32 heads.
 
     scale: D^-1/2 when None.  q and k come normalised (QkNorm with weights D^-1/2 does it).
     final_state may be the initial_state tensor itself.  cu_seqlens packs the sequences in one
@@ -140,7 +141,7 @@ def gated_delta_bwd(q: Tensor, k: Tensor, v: Tensor, g: Tensor, beta: Tensor, do
     """Backward of gated_delta_fwd: (dq, dk, dv, dg, dbeta, d_initial_state) of
     sum(o * do) + sum(final_state * d_final_state).  dg and dbeta have the tokens' dtype.
     saved: what gated_delta_fwd(..., keep=True) returned for the same arguments; without it it
-    is computed again."""
+    is computed again, in a workspace that lives for the call alone."""
     c = _Call(q, k, v, g, beta, scale, initial_state, cu_seqlens, cu_seqlens_host, True)
     dev = c.device
     do = _token(do, "do", c.v)
@@ -197,7 +198,8 @@ def gated_delta(q: Tensor, k: Tensor, v: Tensor, g: Tensor, beta: Tensor,
                 cu_seqlens=None, cu_seqlens_host: Optional[Tensor] = None):
     """Differentiable gated_delta_fwd: (o, final_state), in q, k, v, g, beta and initial_state.
     Accepts [B,T,H,D] or packed [T_total,H,D] (g and beta [T_total,H]) with cu_seqlens, as
-    `recurrent`."""
+    `recurrent`.  Between forward and backward the graph holds gated_delta_fwd's `saved`; who
+    would rather have it made again calls gated_delta_fwd and gated_delta_bwd."""
     squeeze = v.ndim == 3
     if squeeze:
         if cu_seqlens is None:
