@@ -12,6 +12,7 @@ import torch
 import delta_bounds as DB
 import delta_reference as R
 import linear_attention_head_gb300 as la
+from linear_attention_head_gb300 import delta
 from test_gpu_delta import BF, F32, chunked, cuda, inputs
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +76,31 @@ def test_every_output_within_its_bound(case, state):
     bad = [t for name, y in got.items()
            for t in DB.faults(name, y, ref[name], dt, tc, longest, terms)]
     assert not bad, bad
+
+
+@pytest.mark.parametrize("cu", [None, [0, 70, 70, 201]])
+def test_dv_in_a_place_with_strides_of_its_own(cu):
+    # heads before tokens, rows with room behind them: what lies between stays
+    B, T, H, E = (2, 201, 3, 40) if cu is None else (1, 201, 3, 40)
+    n = B if cu is None else len(cu) - 1
+    d = cuda(inputs(B, T, H, 1, 64, E, BF, F32, n, 51))
+    cu_t = torch.tensor(cu, dtype=torch.int32) if cu is not None else None
+    a = (d["q"], d["k"], d["v"], d["g"], d["beta"])
+    want = la.gated_delta_bwd(*a, d["do"], initial_state=d["init"], d_final_state=d["dfin"],
+                              cu_seqlens=cu_t)
+    c = delta._Call(*a, None, d["init"], cu_t, cu_t, True)
+    room = torch.full((B, H, T + 1, E + 8), 7.0, dtype=BF, device="cuda")
+    dv = room.transpose(1, 2)[:, :T, :, :E]
+    dq, dk = torch.empty_like(d["q"]), torch.empty_like(d["k"])
+    dg, db = (torch.empty(B, T, H, dtype=BF, device="cuda") for _ in range(2))
+    dinit = torch.empty_like(d["init"])
+    dims = c.dims(do=d["do"], dq=dq, dk=dk, dv=dv)
+    ws, nbytes = c.workspace(dims, 2)
+    delta._call(c.device, delta.N.lib().la_gated_delta_bwd, delta._ref(dims), c.code, *c.inputs(),
+                *(delta._ptr(t) if torch.is_tensor(t) else t for t in (
+                    d["do"], c.scale, c.init, d["dfin"], c.cu.dev, c.cu.host, None, dq, dk, dv, dg,
+                    db, dinit, ws)), nbytes)
+    for x, y in zip((dq, dk, dv, dg, db, dinit), want):
+        assert torch.equal(x, y)
+    room.transpose(1, 2)[:, :T, :, :E] = 7.0
+    assert (room == 7.0).all()
